@@ -74,7 +74,8 @@ extern "C" {
 #define MOE4_DEVERR_WAIT 1u   /* a bounded wait between workgroups gave up: that
                                  call's results are wrong                       */
 #define MOE4_DEVERR_INDEX 2u  /* a routed row index outside its range was
-                                 clamped (gather, combine, un-permute, dgates)  */
+                                 clamped (gather, combine, un-permute, dgates,  \
+                                 balance counts) or dropped (mxfp4_quant)       */
 
 #define MOE4_BF16 0
 #define MOE4_F32 1
@@ -317,6 +318,61 @@ int mxfp8_quant_rows_T(const void* x, int dtype, int64_t rows, int64_t cols,
                        uint8_t* row_codes, uint8_t* row_sf, uint8_t* t_codes, uint8_t* t_sf,
                        void* stream);
 
+/*
+ * mxfp8_requant_mx4_sr_T - as mxfp8_requant_sr_T for a forward operand in
+ * MXFP4 (mxfp4_quant: codes [rows, cols/2], scales [rows, cols/32], no tensor
+ * scale): exact values q * 2**(scale - 127) -> transpose -> MXFP8 with
+ * stochastic rounding (same exponent rule, random words and layouts).  The
+ * backward operands of an MXFP4 forward (lhc.media page, the paragraphs on
+ * transposition and on requantising with stochastic rounding).  A source row
+ * whose scale byte is 255 (NaN) gives each column block that meets it the
+ * scale byte 255.
+ */
+int mxfp8_requant_mx4_sr_T(const uint8_t* codes, const uint8_t* sf, int64_t rows, int64_t cols,
+                           const int32_t* group_row_off, const int32_t* group_off_pad, int32_t n_groups,
+                           int64_t max_padded_rows, uint64_t seed, uint32_t stream_id, int sf_layout,
+                           uint8_t* out_codes, uint8_t* out_sf, void* stream);
+
+/* ---------------------------------------------------------------- MXFP4 */
+/*
+ * MXFP4: codes [R, C/2] uint8 (E2M1, as NVFP4: element 2j of a row in the low
+ * nibble of byte j); scales [R, C/32] uint8 E8M0, one per 32 consecutive
+ * elements of a row.  The 4-bit format whose scales gfx950's block-scaled
+ * MFMA applies itself, as the pages' 4-bit hardware does NVFP4's
+ * (fourweekmba.com page, the hardware table): a forward operand format of the
+ * expert layer beside NVFP4 (exact E4M3 scales, dequantised to f16 for the
+ * MFMA) and MXFP8.
+ *
+ * mxfp4_quant - x [rows, cols] bf16 or float32 (dtype) -> MXFP4, ties to even.
+ * Per block of 32: e = least integer with amax <= 6 * 2**e, clamped to
+ * [-127, 127] (e = -127 for an all-zero block), scale byte e + 127, code =
+ * E2M1(x * 2**-e) (signs kept).  A block with an infinity or a NaN gets the
+ * scale byte 255 (E8M0's NaN) and zero codes.
+ * pre_op   MOE4_PRE_NONE, or MOE4_PRE_SILU (bf16 x): the correctly rounded
+ *          float32 silu(x) is quantised.
+ * out_map  NULL: row r goes to output row r (copies = 1, out_rows = rows).
+ *          Else [rows * copies] int32: row r goes to the output rows
+ *          out_map[r * copies + j], j < copies: the dispatch of a token's
+ *          codes to its routed rows (moe_route_topk's inv_perm), each token
+ *          quantised once.  Output rows that no entry names are not written;
+ *          entries outside [0, out_rows) are dropped and reported
+ *          (MOE4_DEVERR_INDEX); rows named twice by different tokens hold
+ *          either one's values, block by block.
+ * codes [out_rows, cols/2], sf [out_rows, cols/32]; cols % 32 == 0; x and
+ * codes 16-byte aligned.
+ */
+int mxfp4_quant(const void* x, int dtype, int64_t rows, int64_t cols, const int32_t* out_map, int32_t copies,
+                int64_t out_rows, int pre_op, uint8_t* codes, uint8_t* sf, void* stream);
+
+/*
+ * mxfp4_dequant - the values q * 2**(scale - 127), exact in bf16 and float32
+ * (out_dtype): a test and debugging aid, as nvfp4_dequant.  NaN for the scale
+ * byte 255; a value of 2**128 is an infinity.  out [rows, cols]; codes and
+ * out 16-byte aligned.
+ */
+int mxfp4_dequant(const uint8_t* codes, const uint8_t* sf, int64_t rows, int64_t cols, void* out, int out_dtype,
+                  void* stream);
+
 /* ------------------------------------------------------------- routing */
 /*
  * moe_route_topk - top-k routing and the stable expert permutation.  The pages
@@ -464,6 +520,20 @@ int moe_grouped_gemm_bwd(const uint8_t* dy_codes, const uint8_t* dy_sf,         
                          int64_t M_total, int64_t Nin, int64_t Nout,
                          float* dx, float* dw, float beta, int flags, void* stream);
 
+/*
+ * moe_grouped_gemm_mx4 - C[rows of e] = A[rows of e] . B[e]^T with MXFP4 A
+ * [M_total, K] (+ scales [M_total, K/32]) and MXFP4 B [E, N, K] (+ [E, N,
+ * K/32]) on the block-scaled FP4 MFMA: exact products, float32 accumulation,
+ * C [M_total, N] float32 or bf16 (rounded once, c_dtype).  The forward GEMMs
+ * of an MXFP4 layer (fourweekmba.com page, the hardware table's 4-bit rate).
+ * A scale byte of 255 makes the results it enters NaN.  Rows of C outside
+ * [expert_off[0], expert_off[E]) are not written.  K % 32 == 0, N % 32 == 0;
+ * each expert's B below 2 GiB; a_codes, b_codes and c 16-byte aligned.
+ */
+int moe_grouped_gemm_mx4(const uint8_t* a_codes, const uint8_t* a_sf, const uint8_t* b_codes, const uint8_t* b_sf,
+                         const int32_t* expert_off, int32_t E, int64_t M_total, int64_t N, int64_t K,
+                         void* c, int c_dtype, void* stream);
+
 /* ----------------------------------------------------- combine / scatter */
 /*
  * moe_combine - the gate-weighted return of the expert outputs to their
@@ -607,6 +677,77 @@ int moe_unpermute_sum_router(const float* dxp, const int32_t* inv_perm, int64_t 
 int moe_router_wgrad(const uint16_t* x, const float* dlogits, const int32_t* perm, const int32_t* expert_off,
                      int64_t T, int32_t E, int32_t k, int64_t d, float* dw, void* ws, size_t ws_bytes, void* stream);
 size_t moe_router_wgrad_ws_bytes(int64_t T, int32_t E, int32_t k, int64_t d);
+
+/*
+ * The router's load balance: the pages route each token to 8 of 384 experts
+ * (fourweekmba.com page, "Update") and do not say how the load is kept even;
+ * this is the usual auxiliary loss on the router's probabilities, per segment
+ * of tokens (a batch, or its sequences).
+ *
+ * moe_balance_loss - with z = fl(logits + bias) (bias [E] or NULL), p[t] =
+ * softmax(z[t]) over all E experts, and per segment s, over its n_s unmasked
+ * tokens t:
+ *   counts[s, e] = number of (t, j) with topk_idx[t, j] == e,
+ *   probs[s, e]  = mean of p[t, e],
+ *   loss[s]      = E / (k * n_s) * sum_e counts[s, e] * probs[s, e]
+ * (1 for an even router).  A segment without unmasked tokens has loss, probs
+ * and counts 0.  A row of z that is -infinity throughout has probabilities 0;
+ * -infinity elsewhere is a probability of 0.
+ * token_mask [T] uint8 or NULL: 0 = a padding token, whose logits and topk_idx
+ *          are not read.
+ * seg_off  NULL (n_seg = 1: one segment of all T tokens) or [n_seg + 1]
+ *          ascending token offsets in [0, T]; tokens outside
+ *          [seg_off[0], seg_off[n_seg]) belong to no segment.
+ * loss [n_seg], counts [n_seg, E] int32, tokens [n_seg] int32 (n_s), probs
+ * [n_seg, E].  Sums over tokens in float32 in a fixed order (deterministic).
+ * Indices outside [0, E) are clamped and reported (MOE4_DEVERR_INDEX).
+ * 1 <= k <= min(E, 16), E <= 1024.  ws: moe_balance_loss_ws_bytes(T, E, n_seg),
+ * the caller's, overwritten.
+ */
+int moe_balance_loss(const float* logits, const float* bias, const int32_t* topk_idx, const uint8_t* token_mask,
+                     const int32_t* seg_off, int32_t n_seg, int64_t T, int32_t E, int32_t k, float* loss,
+                     int32_t* counts, int32_t* tokens, float* probs, void* ws, size_t ws_bytes, void* stream);
+size_t moe_balance_loss_ws_bytes(int64_t T, int32_t E, int32_t n_seg);
+
+/*
+ * moe_balance_loss_backward - gradient of sum_s dloss[s] * loss[s] in the
+ * logits, the counts being constants:
+ *   dlogits[t, e] = dlogits_in[t, e] + dloss[s] * E / (k * n_s^2) * p[t, e]
+ *                   * (counts[s, e] - sum_e' p[t, e'] * counts[s, e'])
+ * for the unmasked tokens t of segment s; dlogits_in[t, e] for every other
+ * token.  dlogits_in [T, E] (e.g. moe_route_backward's output) may be NULL
+ * (zeros) and may be dlogits itself.  counts and tokens as moe_balance_loss
+ * wrote them; the other arguments as there.
+ */
+int moe_balance_loss_backward(const float* dloss, const float* logits, const float* bias, const int32_t* counts,
+                              const int32_t* tokens, const uint8_t* token_mask, const int32_t* seg_off, int32_t n_seg,
+                              int64_t T, int32_t E, int32_t k, const float* dlogits_in, float* dlogits, void* stream);
+
+/*
+ * moe_unpermute_sum_router_dense - moe_unpermute_sum_router for a logit
+ * gradient that is not confined to the selected experts (a balance loss):
+ *   dx[t, c] = bf16(sum_j dxp[inv_perm[t*k+j], c] + sum_e dlogits[t, e] * w[e, c])
+ * with float32 sums (the k rows in slot order; the products exact, from three
+ * bf16 parts of each dlogits value, accumulated in float32 by the MFMA).
+ * dxp [T*k, d] float32, dlogits [T, E] float32, w [E, d] bf16, dx [T, d] bf16,
+ * all 16-byte aligned.  1 <= k <= 16, d % 4 == 0.  Out-of-range rows are
+ * clamped and reported (MOE4_DEVERR_INDEX).
+ */
+int moe_unpermute_sum_router_dense(const float* dxp, const int32_t* inv_perm, int64_t T, int32_t k, int64_t d,
+                                   const float* dlogits, int32_t E, const uint16_t* w, uint16_t* dx, void* stream);
+
+/*
+ * moe_router_wgrad_dense - dw [E, d] float32 = sum over all tokens t of
+ * dlogits[t, e] * x[t, c]: the router's weight gradient for a dense logit
+ * gradient.  Exact products as above, float32 accumulation, tokens cut into
+ * shares whose sums are added in order (deterministic).  x [T, d] bf16,
+ * dlogits [T, E], dw: 16-byte aligned; d % 4 == 0; zeros for T = 0.
+ * ws: moe_router_wgrad_dense_ws_bytes(T, E, d) bytes (0 for few tokens, then
+ * ws may be NULL), the caller's, overwritten.
+ */
+int moe_router_wgrad_dense(const uint16_t* x, const float* dlogits, int64_t T, int32_t E, int64_t d, float* dw,
+                           void* ws, size_t ws_bytes, void* stream);
+size_t moe_router_wgrad_dense_ws_bytes(int64_t T, int32_t E, int64_t d);
 
 /*
  * moe_silu_eval - correctly rounded float32 silu(u) and silu'(u) of bf16 u

@@ -32,6 +32,8 @@ route     top-k routing, gates and the stable expert permutation
 silu      correctly rounded SiLU and SiLU' tables over all bf16 inputs
 gemm      float64 grouped GEMMs on exactly dequantised operands
 layer     the whole expert layer, forward and backward
+mxfp4     MXFP4 quantisation and its transposed requantisation to MXFP8
+balance   the router's balance loss and its gradient
 combine_q the combine-path quantiser (block Hadamard + 8-bit fixed-point MX)
 
 Parity pins: every function here is pinned in ``tests/test_oracle_*.py``

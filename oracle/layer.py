@@ -49,6 +49,7 @@ import numpy as np
 
 from . import formats as fmt
 from . import gemm
+from . import mxfp4 as m4
 from . import mxfp8 as mx
 from . import nvfp4 as nv
 from . import route
@@ -212,4 +213,38 @@ def backward_mx(fw, dy_bf16, seed=1, layer=0):
     SR requantisations reading MXFP8 forward operands."""
     def req(q, off, ts_per_group, role, layout):
         return mx.requant_mx_sr_t(q["codes"], q["sf"], off, seed, 16 * layer + role, layout)
+    return _backward(fw, dy_bf16, req)
+
+
+# ------------------------------------------------ MXFP4-forward variant
+#
+# The forward in MXFP4 (mxfp4.py) instead of NVFP4: x quantised once before
+# dispatch, the weights and H along the forward contraction, no tensor scale;
+# U in bf16; the backward the same, with the transposed SR requantisations
+# reading MXFP4 forward operands.
+
+def forward_mx4(x_bf16, W_up, W_down, logits, k, bias=None):
+    T, d = x_bf16.shape
+    E, F, _ = W_up.shape
+    q = lambda x: dict(zip(("codes", "sf"), m4.quantize(x)))
+    wu, wd = q(W_up.reshape(E * F, d)), q(W_down.reshape(E * d, F))
+    idx, gates = route.topk_gates(logits, k, bias)
+    P = route.permutation(idx, E)
+    off, perm, inv = P["off"], P["perm"], P["inv_perm"]
+    xq = q(fmt.bf16_to_f32(x_bf16))
+    src = perm.astype(np.int64) // k
+    xp = dict(codes=xq["codes"][src], sf=xq["sf"][src])
+    Bup = m4.dequant(wu["codes"], wu["sf"]).reshape(E, F, d)
+    U = fmt.f64_to_bf16(gemm.grouped_nt(m4.dequant(xp["codes"], xp["sf"]), Bup, off))
+    hq = q(silu.silu_f32(U))
+    Bdn = m4.dequant(wd["codes"], wd["sf"]).reshape(E, d, F)
+    Yp = gemm.grouped_nt(m4.dequant(hq["codes"], hq["sf"]), Bdn, off).astype(np.float32)
+    return dict(wu=wu, wd=wd, idx=idx, gates=gates, perm=P, xq_perm=xp, U=U, hq=hq, Yp=Yp,
+                y=combine(Yp, gates, inv, k), dims=(T, d, F, E, k))
+
+
+def backward_mx4(fw, dy_bf16, seed=1, layer=0):
+    """The backward of ``forward_mx4``: the requantisations read MXFP4 operands."""
+    def req(q, off, ts_per_group, role, layout):
+        return m4.requant_sr_t(q["codes"], q["sf"], off, seed, 16 * layer + role, layout)
     return _backward(fw, dy_bf16, req)

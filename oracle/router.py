@@ -21,6 +21,10 @@ token's k selected experts:
   (bit-exact against the GPU);
 * weight gradient: dW_r[e] = sum over the tokens routed to e of dz[t, e] * x[t]
   (float32 output of an exact sum; the GEMM tolerance rule).
+
+A balance loss (balance.py) gives every expert's logit a gradient; the dense
+forms at the end sum over all experts (input gradient) and all tokens (weight
+gradient), in float64.
 """
 import numpy as np
 
@@ -78,3 +82,19 @@ def weight_grad(x_bf16, dlogits, idx):
 
 def weight_grad_abs_bound(x_bf16, dlogits, idx):
     return weight_grad(np.asarray(x_bf16) & np.uint16(0x7FFF), np.abs(np.asarray(dlogits, np.float64)), idx)
+
+
+def unpermute_sum_dense(dXp, inv, T, k, dlogits, w_bf16):
+    """dx [T, d] float64 = sum_j dXp[row(t, j)] + sum_e dz[t, e] * W_r[e], and the
+    sum of the terms' magnitudes (the tolerance's scale)."""
+    rows = np.asarray(dXp, dtype=np.float64)[np.asarray(inv, dtype=np.int64).reshape(T, k)]
+    dz = np.asarray(dlogits, dtype=np.float64)
+    w = fmt.bf16_to_f32(w_bf16).astype(np.float64)
+    return rows.sum(axis=1) + dz @ w, np.abs(rows).sum(axis=1) + np.abs(dz) @ np.abs(w)
+
+
+def weight_grad_dense(x_bf16, dlogits):
+    """dW_r [E, d] float64 = dz^T x, and the sum of the terms' magnitudes."""
+    x = fmt.bf16_to_f32(x_bf16).astype(np.float64)
+    dz = np.asarray(dlogits, dtype=np.float64)
+    return dz.T @ x, np.abs(dz).T @ np.abs(x)

@@ -90,6 +90,21 @@ _SIGS = {
     "moe_hmx8_dequant": (_int, [_c_void_p, _c_void_p, _i64, _i64, _c_void_p, _c_void_p]),
     "moe_combine_hmx8": (_int, [_c_void_p, _c_void_p, _c_void_p, _c_void_p, _i64, _i32, _i64, _c_void_p,
                                 _c_void_p]),
+    "mxfp4_quant": (_int, [_c_void_p, _int, _i64, _i64, _c_void_p, _i32, _i64, _int, _c_void_p, _c_void_p, _c_void_p]),
+    "mxfp4_dequant": (_int, [_c_void_p, _c_void_p, _i64, _i64, _c_void_p, _int, _c_void_p]),
+    "mxfp8_requant_mx4_sr_T": (_int, [_c_void_p, _c_void_p, _i64, _i64, _c_void_p, _c_void_p, _i32, _i64, _u64,
+                                      _u32, _int, _c_void_p, _c_void_p, _c_void_p]),
+    "moe_grouped_gemm_mx4": (_int, [_c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _i32, _i64, _i64, _i64,
+                                    _c_void_p, _int, _c_void_p]),
+    "moe_balance_loss": (_int, [_c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _i32, _i64, _i32, _i32,
+                                _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _size, _c_void_p]),
+    "moe_balance_loss_ws_bytes": (_size, [_i64, _i32, _i32]),
+    "moe_balance_loss_backward": (_int, [_c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p, _c_void_p,
+                                         _i32, _i64, _i32, _i32, _c_void_p, _c_void_p, _c_void_p]),
+    "moe_unpermute_sum_router_dense": (_int, [_c_void_p, _c_void_p, _i64, _i32, _i64, _c_void_p, _i32, _c_void_p,
+                                              _c_void_p, _c_void_p]),
+    "moe_router_wgrad_dense": (_int, [_c_void_p, _c_void_p, _i64, _i32, _i64, _c_void_p, _c_void_p, _size, _c_void_p]),
+    "moe_router_wgrad_dense_ws_bytes": (_size, [_i64, _i32, _i64]),
     "moe_grouped_gemm_fwd_hmx8": (_int, [_c_void_p, _c_void_p, _c_void_p, _int, _c_void_p, _c_void_p, _c_void_p,
                                          _c_void_p, _i32, _i64, _i64, _i64, _c_void_p, _c_void_p, _c_void_p,
                                          _c_void_p]),
@@ -154,6 +169,26 @@ def _empty(shape, dtype, like):
 
 def _ws(nbytes, like):
     return torch.empty(max(int(nbytes), 16), dtype=torch.uint8, device=like.device)
+
+
+def _arg(t, dtype, shape, name, like=None):
+    """Check a tensor argument of the calls below: dtype, shape (None: any size
+    there), contiguous, on the GPU, and on like's device."""
+    _dev(t, dtype, name)
+    if t.dim() != len(shape) or any(w is not None and int(g) != int(w) for g, w in zip(t.shape, shape)):
+        raise ValueError(f"{name}: expected shape {tuple(shape)} (None: any), got {tuple(t.shape)}")
+    if like is not None and t.device != like.device:
+        raise ValueError(f"{name}: on {t.device}, the call's other tensors on {like.device}")
+    return t
+
+
+def _run(name, like, *args):
+    """Call the library on like's device, on that device's current stream."""
+    if like.device.index == torch.cuda.current_device():
+        _check(getattr(lib(), name)(*args, _stream()), name)
+    else:
+        with torch.cuda.device(like.device):
+            _check(getattr(lib(), name)(*args, _stream()), name)
 
 
 def pad32(n):
@@ -362,6 +397,63 @@ def mxfp8_quant_rows_T(x, group_row_off, group_off_pad, rows=None, row_map=None,
     return rc_, rs_, tc, ts
 
 
+def mxfp8_requant_mx4_sr_T(codes, sf, group_row_off, group_off_pad, seed=1, stream_id=0, max_pr=None,
+                           sf_layout=SF_ROWS):
+    """MXFP4 row-wise [R, C] -> MXFP8 SR transposed, group-major padded: (codes [C*P], sf [C*P/32])."""
+    _arg(codes, torch.uint8, (None, None), "codes")
+    R, C = codes.shape[0], 2 * codes.shape[1]
+    _arg(sf, torch.uint8, (R, C // 32), "sf", codes)
+    _arg(group_row_off, torch.int32, (None,), "group_row_off", codes)
+    G = group_row_off.numel() - 1
+    _arg(group_off_pad, torch.int32, (G + 1,), "group_off_pad", codes)
+    if max_pr is None:
+        max_pr = max_padded_rows(R, G)
+    oc = _empty((C * max_pr,), torch.uint8, codes)
+    os_ = _empty((C * max_pr // 32,), torch.uint8, codes)
+    _run("mxfp8_requant_mx4_sr_T", codes, _p(codes), _p(sf), R, C, _p(group_row_off), _p(group_off_pad), G, max_pr,
+         seed, stream_id, int(sf_layout), _p(oc), _p(os_))
+    return oc, os_
+
+
+# --------------------------------------------------------------------- MXFP4
+
+def mxfp4_quant(x, pre_op=PRE_NONE, out_map=None, copies=1, out=None):
+    """MXFP4 of x [R, C] (bf16 or float32) -> (codes [R, C/2] u8, sf [R, C/32] u8).
+    out_map [R*copies] int32: row r goes to the output rows out_map[r*copies + j]
+    (e.g. moe_route_topk's inv_perm, copies = k: the dispatch); the outputs then
+    have R*copies rows.  out: optional (codes, sf) tensors to write into; rows
+    that out_map does not name keep what they hold."""
+    dt = {torch.bfloat16: BF16, torch.float32: F32}.get(x.dtype)
+    if dt is None:
+        raise ValueError("mxfp4_quant: x must be bf16 or float32")
+    _arg(x, x.dtype, (None, None), "x")
+    R, C = x.shape
+    if out_map is not None:
+        _arg(out_map, torch.int32, (R * copies,), "out_map", x)
+    elif copies != 1:
+        raise ValueError("mxfp4_quant: copies needs out_map")
+    if out is None:
+        out = (_empty((R * copies, C // 2), torch.uint8, x), _empty((R * copies, C // 32), torch.uint8, x))
+    codes, sf = out
+    _arg(codes, torch.uint8, (None if out_map is not None else R, C // 2), "out codes", x)
+    _arg(sf, torch.uint8, (codes.shape[0], C // 32), "out sf", x)
+    _run("mxfp4_quant", x, _p(x), dt, R, C, _p(out_map), copies, codes.shape[0], int(pre_op), _p(codes), _p(sf))
+    return codes, sf
+
+
+def mxfp4_dequant(codes, sf, out_dtype=torch.float32):
+    """The values of MXFP4 codes [R, C/2], scales [R, C/32]: [R, C] float32 or bf16 (both exact)."""
+    dt = {torch.bfloat16: BF16, torch.float32: F32}.get(out_dtype)
+    if dt is None:
+        raise ValueError("mxfp4_dequant: out_dtype must be bf16 or float32")
+    _arg(codes, torch.uint8, (None, None), "codes")
+    R, C = codes.shape[0], 2 * codes.shape[1]
+    _arg(sf, torch.uint8, (R, C // 32), "sf", codes)
+    out = _empty((R, C), out_dtype, codes)
+    _run("mxfp4_dequant", codes, _p(codes), _p(sf), R, C, _p(out), dt)
+    return out
+
+
 # ------------------------------------------------------------------- routing
 
 def moe_route_topk(logits, k, bias=None):
@@ -498,6 +590,24 @@ def moe_grouped_gemm_bwd(dy_codes, dy_sf, wT_codes, wT_sf, dyT_codes, dyT_sf, xT
     return dx, dw
 
 
+def moe_grouped_gemm_mx4(a_codes, a_sf, b_codes, b_sf, expert_off, out_dtype=torch.bfloat16):
+    """MXFP4 A [M, K] x MXFP4 B [E, N, K] grouped by expert_off -> C [M, N] (bf16 or float32)."""
+    cd = {torch.float32: F32, torch.bfloat16: BF16}.get(out_dtype)
+    if cd is None:
+        raise ValueError("moe_grouped_gemm_mx4: out_dtype must be bf16 or float32")
+    _arg(a_codes, torch.uint8, (None, None), "a_codes")
+    M, Kh = a_codes.shape
+    _arg(a_sf, torch.uint8, (M, Kh // 16), "a_sf", a_codes)
+    _arg(b_codes, torch.uint8, (None, None, Kh), "b_codes", a_codes)
+    E, N, _ = b_codes.shape
+    _arg(b_sf, torch.uint8, (E, N, Kh // 16), "b_sf", a_codes)
+    _arg(expert_off, torch.int32, (E + 1,), "expert_off", a_codes)
+    c = _empty((M, N), out_dtype, a_codes)
+    _run("moe_grouped_gemm_mx4", a_codes, _p(a_codes), _p(a_sf), _p(b_codes), _p(b_sf), _p(expert_off), E, M, N,
+         2 * Kh, _p(c), cd)
+    return c
+
+
 # ----------------------------------------------------------- combine / misc
 
 def moe_combine(yp, gates, inv_perm):
@@ -610,6 +720,87 @@ def moe_router_wgrad(x, dlogits, perm, expert_off, k):
     rc = lib().moe_router_wgrad(_p(x), _p(dlogits), _p(perm), _p(expert_off), T, E, k, d, _p(dw), _p(ws), ws.numel(),
                                 _stream())
     _check(rc, "moe_router_wgrad")
+    return dw
+
+
+def _mask_u8(mask, T, like):
+    if mask is None:
+        return None
+    if mask.dtype == torch.bool:
+        mask = mask.view(torch.uint8)
+    return _arg(mask, torch.uint8, (T,), "token_mask", like)
+
+
+def moe_balance_loss(logits, topk_idx, bias=None, token_mask=None, seg_off=None):
+    """Balance loss of the router per token segment (see moe4.h) -> dict(loss [S]
+    float32, counts [S, E] int32, tokens [S] int32, probs [S, E] float32).
+    token_mask [T] bool or uint8: False for padding; seg_off [S + 1] int32 token
+    offsets (None: one segment)."""
+    _arg(logits, torch.float32, (None, None), "logits")
+    T, E = logits.shape
+    _arg(topk_idx, torch.int32, (T, None), "topk_idx", logits)
+    k = topk_idx.shape[1]
+    if bias is not None:
+        _arg(bias, torch.float32, (E,), "bias", logits)
+    mask = _mask_u8(token_mask, T, logits)
+    S = 1
+    if seg_off is not None:
+        _arg(seg_off, torch.int32, (None,), "seg_off", logits)
+        S = seg_off.numel() - 1
+    r = dict(loss=_empty((max(S, 0),), torch.float32, logits), counts=_empty((max(S, 0), E), torch.int32, logits),
+             tokens=_empty((max(S, 0),), torch.int32, logits), probs=_empty((max(S, 0), E), torch.float32, logits))
+    ws = _ws(lib().moe_balance_loss_ws_bytes(T, E, S), logits)
+    _run("moe_balance_loss", logits, _p(logits), _p(bias), _p(topk_idx), _p(mask), _p(seg_off), S, T, E, k,
+         _p(r["loss"]), _p(r["counts"]), _p(r["tokens"]), _p(r["probs"]), _p(ws), ws.numel())
+    return r
+
+
+def moe_balance_loss_backward(dloss, logits, counts, tokens, k, bias=None, token_mask=None, seg_off=None,
+                              dlogits=None, out=None):
+    """dlogits [T, E] float32 of sum_s dloss[s] * loss[s] (counts and tokens as
+    moe_balance_loss returned them), added to ``dlogits`` if given; ``out`` (which
+    may be ``dlogits``) receives it, else a new tensor."""
+    _arg(logits, torch.float32, (None, None), "logits")
+    T, E = logits.shape
+    _arg(counts, torch.int32, (None, E), "counts", logits)
+    S = counts.shape[0]
+    _arg(dloss, torch.float32, (S,), "dloss", logits)
+    _arg(tokens, torch.int32, (S,), "tokens", logits)
+    if bias is not None:
+        _arg(bias, torch.float32, (E,), "bias", logits)
+    mask = _mask_u8(token_mask, T, logits)
+    if seg_off is not None:
+        _arg(seg_off, torch.int32, (S + 1,), "seg_off", logits)
+    if dlogits is not None:
+        _arg(dlogits, torch.float32, (T, E), "dlogits", logits)
+    out = _empty((T, E), torch.float32, logits) if out is None else _arg(out, torch.float32, (T, E), "out", logits)
+    _run("moe_balance_loss_backward", logits, _p(dloss), _p(logits), _p(bias), _p(counts), _p(tokens), _p(mask),
+         _p(seg_off), S, T, E, k, _p(dlogits), _p(out))
+    return out
+
+
+def moe_unpermute_sum_router_dense(dxp, inv_perm, T, k, dlogits, w):
+    """dx [T, d] bf16: the un-permuting sum of dxp plus dlogits . w over all experts."""
+    _arg(dxp, torch.float32, (T * k, None), "dxp")
+    d = dxp.shape[1]
+    _arg(w, torch.bfloat16, (None, d), "w", dxp)
+    E = w.shape[0]
+    _arg(dlogits, torch.float32, (T, E), "dlogits", dxp)
+    _arg(inv_perm, torch.int32, (T * k,), "inv_perm", dxp)
+    dx = _empty((T, d), torch.bfloat16, dxp)
+    _run("moe_unpermute_sum_router_dense", dxp, _p(dxp), _p(inv_perm), T, k, d, _p(dlogits), E, _p(w), _p(dx))
+    return dx
+
+
+def moe_router_wgrad_dense(x, dlogits):
+    """dW_r [E, d] float32 = dlogits^T . x over all tokens and experts."""
+    _arg(x, torch.bfloat16, (None, None), "x")
+    T, d = x.shape
+    _arg(dlogits, torch.float32, (T, None), "dlogits", x)
+    E = dlogits.shape[1]
+    dw = _empty((E, d), torch.float32, x)
+    ws = _ws(lib().moe_router_wgrad_dense_ws_bytes(T, E, d), x)
+    _run("moe_router_wgrad_dense", x, _p(x), _p(dlogits), T, E, d, _p(dw), _p(ws), ws.numel())
     return dw
 
 

@@ -32,6 +32,9 @@ uint32_t take_dev_err_nvfp4();
 uint32_t take_dev_err_route();
 uint32_t take_dev_err_combine_q();
 uint32_t take_dev_err_router();
+uint32_t take_dev_err_mxfp4();
+uint32_t take_dev_err_balance();
+uint32_t take_dev_err_router_dense();
 // Test hook (moe4_debug_force_wait_timeout): bounded waits between
 // workgroups wait for a count that never arrives, with a tiny spin limit, so
 // that every wait gives up and reports MOE4_DEVERR_WAIT; kernels still exit.
@@ -111,6 +114,16 @@ __device__ inline uint32_t f32_to_bf16_bits(float f) {
 // non-NaN bytes to the values of the field-by-field definition (exponent
 // field e, mantissa m: (1 + m/8) 2^(e-7), subnormal m 2^-9), one instruction.
 __device__ inline float e4m3_to_f32(uint32_t b) { return __builtin_amdgcn_cvt_f32_fp8((int)b, 0); }
+
+// q * 2**e of the 8 E2M1 codes of word w (nibble i = value i), exact in
+// float32's range.
+__device__ inline void mx4_decode8(uint32_t w, int e, float (&v)[8]) {
+  const f32x2 d0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 0), d1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 1);
+  const f32x2 d2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 2), d3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(w, 1.0f, 3);
+  const float q[8] = {d0[0], d0[1], d1[0], d1[1], d2[0], d2[1], d3[0], d3[1]};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = __builtin_amdgcn_ldexpf(q[i], e);
+}
 
 // Mantissa factor 1.m of a positive normal float (its value over 2**floor(log2)).
 __device__ inline float mant_factor(float s) {

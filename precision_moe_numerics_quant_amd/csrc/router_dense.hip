@@ -1,0 +1,346 @@
+// The router's backward for a dense logit gradient (gfx950): a balance loss
+// puts a gradient on every expert's logit, so the products that only visit
+// each token's k selected experts (router.hip) do not cover it.
+//
+//   k_router_dx_dense  dx[t] = bf16(sum_j dXp[row(t, j)] + sum_e dz[t, e] W_r[e]):
+//                      the un-permuting sum with the GEMM dz . W_r under it,
+//                      128 x 128 tiles (T x d), the sum added in the epilogue.
+//   k_router_dw_dense  dW_r [E, d] = dz^T . x, 128 x 128 tiles (E x d), the
+//                      tokens split over workgroups whose partial tiles
+//                      k_router_dw_join adds in order.
+//
+// dz is float32 and the other operand bf16.  A float32 is exactly the sum of
+// three bf16 numbers (its 24 significand bits cut 8 + 8 + 8), so three bf16
+// MFMAs per fragment (v_mfma_f32_32x32x16_bf16) give exact products with
+// float32 accumulation: nothing of dz is rounded, at three bf16 MFMAs where a
+// float32 MFMA would take eight times as long as one.
+//
+// Both contractions run along a dimension that is not contiguous in memory
+// (W_r's rows; dz's and x's tokens): a thread loads 8 consecutive k of one or
+// two columns (whole cache lines across the wave) and the bytes are put into
+// fragment order on the way to LDS, [k / 8][row][8 k]: a fragment read is then
+// 16 consecutive bytes per lane, without bank conflicts.
+#include "gemm_common.h"
+#include "moe4_internal.h"
+
+namespace moe4 {
+
+namespace rd {
+constexpr int TM = 128, TN = 128, BK = 32, NT = 256;
+constexpr int KC = BK / 8;                  // 8-deep k chunks of a slab
+constexpr int PART_B = KC * TM * 16;        // bytes of one bf16 operand slab
+constexpr int STAGE = 4 * PART_B;           // three parts of dz, one of the other operand
+constexpr int MAXK = 16;
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+}  // namespace rd
+
+// 8 float32 values -> their three bf16 parts (the high 8 significand bits,
+// the next 8, the last 8; each subtraction is exact), 8 bf16 each.
+__device__ inline void split3(const float (&v)[8], u32x4 (&o)[3]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t h[2], m[2], lo[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const float a = v[2 * i + j];
+      h[j] = __float_as_uint(a) & 0xFFFF0000u;
+      const float r = a - __uint_as_float(h[j]);
+      m[j] = __float_as_uint(r) & 0xFFFF0000u;
+      lo[j] = __float_as_uint(r - __uint_as_float(m[j]));
+    }
+    o[0][i] = (h[0] >> 16) | h[1];
+    o[1][i] = (m[0] >> 16) | m[1];
+    o[2][i] = (lo[0] >> 16) | (lo[1] & 0xFFFF0000u);
+  }
+}
+
+// 8 dwords of two bf16 columns each (row i in w[i]) -> the 8 k of each column.
+__device__ inline void columns2(const uint32_t (&w)[8], u32x4& c0, u32x4& c1) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    c0[i] = (w[2 * i] & 0xFFFFu) | (w[2 * i + 1] << 16);
+    c1[i] = (w[2 * i] >> 16) | (w[2 * i + 1] & 0xFFFF0000u);
+  }
+}
+
+// One slab: wave (wm, wn) owns 64 x 64 of the tile, 2 x 2 MFMA blocks.
+__device__ inline void rd_compute(const uint8_t* st, int wm, int wn, f32x16 (&acc)[2][2]) {
+  using namespace rd;
+  const int l = threadIdx.x & 63, li = l & 31, g = l >> 5;
+#pragma unroll
+  for (int kk = 0; kk < BK / 16; ++kk) {
+    const int c = 2 * kk + g;  // lane half g holds k = 16 kk + 8 g .. + 7
+    bf16x8 a[3][2], b[2];
+#pragma unroll
+    for (int p = 0; p < 3; ++p)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        a[p][i] = *reinterpret_cast<const bf16x8*>(st + p * PART_B + (c * TM + wm + 32 * i + li) * 16);
+#pragma unroll
+    for (int j = 0; j < 2; ++j) b[j] = *reinterpret_cast<const bf16x8*>(st + 3 * PART_B + (c * TN + wn + 32 * j + li) * 16);
+#pragma unroll
+    for (int p = 2; p >= 0; --p)  // the smallest parts first
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[p][i], b[j], acc[i][j], 0, 0, 0);
+  }
+}
+
+// idx clamped to [0, n); a clamp is reported
+__device__ inline int64_t clamp_row(int64_t i, int64_t n, uint32_t* err) {
+  if (i < 0 || i >= n) {
+    atomicOr(err, MOE4_DEVERR_INDEX);
+    return i < 0 ? 0 : n - 1;
+  }
+  return i;
+}
+
+static __device__ uint32_t g_dev_err;
+uint32_t take_dev_err_router_dense() { return take_device_word(&g_dev_err); }
+
+__global__ void __launch_bounds__(rd::NT, 2)
+    k_router_dx_dense(const float* __restrict__ dxp, const int32_t* __restrict__ inv, int64_t T, int k, int64_t d,
+                      const float* __restrict__ dz, int E, const uint16_t* __restrict__ w, int64_t n_nt, int64_t n_all,
+                      uint16_t* __restrict__ dx) {
+  using namespace rd;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[2 * STAGE];  // two stages; then the float32 tile (64 KB both)
+  static_assert(2 * STAGE >= TM * TN * 4, "the epilogue's tile");
+  const int64_t tile = xcd_tile(blockIdx.x, n_all);
+  if (tile >= n_all) return;
+  const int64_t t0 = (tile / n_nt) * TM, c0 = (tile % n_nt) * TN;
+  const int tid = threadIdx.x, l = tid & 63, wv = tid >> 6;
+  const int wm = (wv >> 1) * 64, wn = (wv & 1) * 64;
+  // dz: units (row tid / 4 + 64 j, chunk tid % 4); W_r: unit (chunk tid / 64, columns 2 l, 2 l + 1)
+  const int ach = tid & 3, ar = tid >> 2;
+  const int64_t bc = c0 + 2 * l;
+  const bool vec = (E & 3) == 0;
+  float av[2][8];
+  uint32_t bw[8];
+  auto load = [&](int k0) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int64_t t = t0 + ar + 64 * j;
+      const int kb = k0 + 8 * ach;
+      const float* p = dz + t * E + kb;
+      if (t < T && vec && kb + 8 <= E) {
+        const f32x4 x0 = reinterpret_cast<const f32x4*>(p)[0], x1 = reinterpret_cast<const f32x4*>(p)[1];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          av[j][i] = x0[i];
+          av[j][4 + i] = x1[i];
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) av[j][i] = t < T && kb + i < E ? p[i] : 0.0f;
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int e = k0 + 8 * wv + i;
+      bw[i] = e < E && bc < d ? *reinterpret_cast<const uint32_t*>(w + (int64_t)e * d + bc) : 0u;
+    }
+  };
+  auto store = [&](uint8_t* st) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      u32x4 o[3];
+      split3(av[j], o);
+#pragma unroll
+      for (int p = 0; p < 3; ++p) *reinterpret_cast<u32x4*>(st + p * PART_B + (ach * TM + ar + 64 * j) * 16) = o[p];
+    }
+    u32x4 b0, b1;
+    columns2(bw, b0, b1);
+    *reinterpret_cast<u32x4*>(st + 3 * PART_B + (wv * TN + 2 * l) * 16) = b0;
+    *reinterpret_cast<u32x4*>(st + 3 * PART_B + (wv * TN + 2 * l + 1) * 16) = b1;
+  };
+  f32x16 acc[2][2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) acc[i][j] = f32x16{};
+  const int nk = (E + BK - 1) / BK;
+  load(0);
+  store(lds);
+  __syncthreads();
+  for (int s = 0; s < nk; ++s) {
+    if (s + 1 < nk) load((s + 1) * BK);  // in flight during this slab's MFMAs
+    rd_compute(lds + (s & 1) * STAGE, wm, wn, acc);
+    if (s + 1 < nk) store(lds + ((s + 1) & 1) * STAGE);
+    __syncthreads();
+  }
+  // the tile through LDS, so that a thread adds whole 16-byte pieces of rows
+  float* tl = reinterpret_cast<float*>(lds);
+  const int li = l & 31, g = l >> 5;
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int v = 0; v < 16; ++v)
+        tl[(wm + 32 * i + (v >> 2) * 8 + 4 * g + (v & 3)) * TN + wn + 32 * j + li] = acc[i][j][v];
+  __syncthreads();
+  const int64_t col = c0 + 4 * (tid & 31);
+  if (col >= d) return;
+  for (int r = tid >> 5; r < TM; r += NT / 32) {
+    const int64_t t = t0 + r;
+    if (t >= T) break;
+    f32x4 v[MAXK];
+#pragma unroll
+    for (int j = 0; j < MAXK; ++j)
+      if (j < k) v[j] = *reinterpret_cast<const f32x4*>(dxp + clamp_row(inv[t * k + j], T * k, &g_dev_err) * d + col);
+    f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int j = 0; j < MAXK; ++j)
+      if (j < k) s = s + v[j];
+    s = s + *reinterpret_cast<const f32x4*>(tl + r * TN + 4 * (tid & 31));
+    *reinterpret_cast<u32x2*>(dx + t * d + col) = u32x2{f32_to_bf16_bits(s[0]) | (f32_to_bf16_bits(s[1]) << 16),
+                                                        f32_to_bf16_bits(s[2]) | (f32_to_bf16_bits(s[3]) << 16)};
+  }
+}
+
+// Workgroup (tile, token share z): out + z * E * d gets the share's partial
+// products (out is dW itself when there is one share).
+__global__ void __launch_bounds__(rd::NT, 2)
+    k_router_dw_dense(const uint16_t* __restrict__ x, const float* __restrict__ dz, int64_t T, int E, int64_t d,
+                      int64_t n_nt, int64_t share, float* __restrict__ out) {
+  using namespace rd;
+  __shared__ __attribute__((aligned(16))) uint8_t lds[2 * STAGE];
+  const int64_t e0 = (blockIdx.x / n_nt) * TM, c0 = (blockIdx.x % n_nt) * TN;
+  const int64_t ta = (int64_t)blockIdx.y * share, tb = ta + share < T ? ta + share : T;
+  const int tid = threadIdx.x, l = tid & 63, wv = tid >> 6;
+  const int wm = (wv >> 1) * 64, wn = (wv & 1) * 64;
+  // dz: units (chunk wv, expert l + 64 j); x: unit (chunk wv, columns 2 l, 2 l + 1)
+  const int64_t bc = c0 + 2 * l;
+  float av[2][8];
+  uint32_t bw[8];
+  auto load = [&](int64_t k0) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int64_t t = k0 + 8 * wv + i;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int64_t e = e0 + l + 64 * j;
+        av[j][i] = t < tb && e < E ? dz[t * E + e] : 0.0f;
+      }
+      bw[i] = t < tb && bc < d ? *reinterpret_cast<const uint32_t*>(x + t * d + bc) : 0u;
+    }
+  };
+  auto store = [&](uint8_t* st) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      u32x4 o[3];
+      split3(av[j], o);
+#pragma unroll
+      for (int p = 0; p < 3; ++p) *reinterpret_cast<u32x4*>(st + p * PART_B + (wv * TM + l + 64 * j) * 16) = o[p];
+    }
+    u32x4 b0, b1;
+    columns2(bw, b0, b1);
+    *reinterpret_cast<u32x4*>(st + 3 * PART_B + (wv * TN + 2 * l) * 16) = b0;
+    *reinterpret_cast<u32x4*>(st + 3 * PART_B + (wv * TN + 2 * l + 1) * 16) = b1;
+  };
+  f32x16 acc[2][2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) acc[i][j] = f32x16{};
+  const int nk = tb > ta ? (int)((tb - ta + BK - 1) / BK) : 0;
+  if (nk > 0) {
+    load(ta);
+    store(lds);
+  }
+  __syncthreads();
+  for (int s = 0; s < nk; ++s) {
+    if (s + 1 < nk) load(ta + (int64_t)(s + 1) * BK);
+    rd_compute(lds + (s & 1) * STAGE, wm, wn, acc);
+    if (s + 1 < nk) store(lds + ((s + 1) & 1) * STAGE);
+    __syncthreads();
+  }
+  const int li = l & 31, g = l >> 5;
+  float* o = out + (int64_t)blockIdx.y * E * d;
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const int64_t col = c0 + wn + 32 * j + li;
+      if (col >= d) continue;
+#pragma unroll
+      for (int v = 0; v < 16; ++v) {
+        const int64_t e = e0 + wm + 32 * i + (v >> 2) * 8 + 4 * g + (v & 3);
+        if (e < E) o[e * d + col] = acc[i][j][v];
+      }
+    }
+}
+
+// dw = the partial products of the n shares, added in order (n4 = E d / 4).
+__global__ void __launch_bounds__(256) k_router_dw_join(const f32x4* __restrict__ part, int n, int64_t n4,
+                                                        f32x4* __restrict__ dw) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= n4) return;
+  f32x4 s = part[i];
+  for (int z = 1; z < n; ++z) s = s + part[z * n4 + i];
+  dw[i] = s;
+}
+
+// Token shares of the weight gradient: enough workgroups for two per CU
+// (rd::NT threads and 64 KB of LDS each), at least 8 slabs each.
+inline int dw_shares(int64_t T, int E, int64_t d) {
+  const int64_t tiles = ((E + rd::TM - 1) / rd::TM) * ((d + rd::TN - 1) / rd::TN);
+  int64_t n = 512 / tiles;
+  const int64_t most = T / (8 * rd::BK);
+  if (n > most) n = most;
+  return (int)(n < 1 ? 1 : n);
+}
+
+}  // namespace moe4
+
+using namespace moe4;
+
+extern "C" int moe_unpermute_sum_router_dense(const float* dxp, const int32_t* inv_perm, int64_t T, int32_t k, int64_t d,
+                                              const float* dlogits, int32_t E, const uint16_t* w, uint16_t* dx,
+                                              void* stream) {
+  MOE4_REQUIRE(T >= 0 && E >= 1 && k >= 1 && k <= rd::MAXK && d > 0 && d % 4 == 0, MOE4_EINVAL,
+               "moe_unpermute_sum_router_dense: need 1 <= k <= 16, E >= 1 and d % 4 == 0");
+  MOE4_REQUIRE(T * (int64_t)k < ((int64_t)1 << 31), MOE4_EINVAL, "moe_unpermute_sum_router_dense: T * k must be below 2^31");
+  MOE4_REQUIRE(T == 0 || (dxp && inv_perm && dlogits && w && dx), MOE4_EINVAL, "moe_unpermute_sum_router_dense: NULL pointer");
+  MOE4_REQUIRE(aligned16(dxp) && aligned16(dlogits) && aligned16(w) && aligned16(dx), MOE4_EALIGN,
+               "moe_unpermute_sum_router_dense: dxp, dlogits, w and dx must be 16-byte aligned");
+  if (T == 0) return MOE4_OK;
+  const int64_t n_nt = (d + rd::TN - 1) / rd::TN, n_all = n_nt * ((T + rd::TM - 1) / rd::TM);
+  MOE4_REQUIRE(n_all < ((int64_t)1 << 30), MOE4_EINVAL, "moe_unpermute_sum_router_dense: too large");
+  hipLaunchKernelGGL(k_router_dx_dense, dim3((unsigned)xcd_grid(n_all)), dim3(rd::NT), 0, as_stream(stream), dxp, inv_perm,
+                     T, k, d, dlogits, E, w, n_nt, n_all, dx);
+  return check_launch("moe_unpermute_sum_router_dense");
+}
+
+extern "C" size_t moe_router_wgrad_dense_ws_bytes(int64_t T, int32_t E, int64_t d) {
+  if (T < 0 || E < 1 || d < 1) return 0;
+  const int n = dw_shares(T, E, d);
+  return n > 1 ? (size_t)n * (size_t)E * (size_t)d * 4 : 0;
+}
+
+extern "C" int moe_router_wgrad_dense(const uint16_t* x, const float* dlogits, int64_t T, int32_t E, int64_t d, float* dw,
+                                      void* ws, size_t ws_bytes, void* stream) {
+  MOE4_REQUIRE(T >= 0 && E >= 1 && d > 0 && d % 4 == 0, MOE4_EINVAL, "moe_router_wgrad_dense: need T >= 0, E >= 1 and d % 4 == 0");
+  MOE4_REQUIRE(dw && (T == 0 || (x && dlogits)), MOE4_EINVAL, "moe_router_wgrad_dense: NULL pointer");
+  MOE4_REQUIRE(aligned16(x) && aligned16(dlogits) && aligned16(dw), MOE4_EALIGN,
+               "moe_router_wgrad_dense: x, dlogits and dw must be 16-byte aligned");
+  const int64_t n_nt = (d + rd::TN - 1) / rd::TN, tiles = n_nt * ((E + rd::TM - 1) / rd::TM);
+  MOE4_REQUIRE(tiles < ((int64_t)1 << 31), MOE4_EINVAL, "moe_router_wgrad_dense: too large");
+  const int n = dw_shares(T, E, d);
+  const size_t need = moe_router_wgrad_dense_ws_bytes(T, E, d);
+  MOE4_REQUIRE(need == 0 || (ws && ws_bytes >= need), MOE4_EWORKSPACE,
+               "moe_router_wgrad_dense: workspace of moe_router_wgrad_dense_ws_bytes() bytes required");
+  MOE4_REQUIRE(need == 0 || aligned16(ws), MOE4_EALIGN, "moe_router_wgrad_dense: ws must be 16-byte aligned");
+  const int64_t share = ((T + n - 1) / n + rd::BK - 1) / rd::BK * rd::BK;
+  const hipStream_t s = as_stream(stream);
+  float* out = n > 1 ? static_cast<float*>(ws) : dw;
+  hipLaunchKernelGGL(k_router_dw_dense, dim3((unsigned)tiles, (unsigned)n), dim3(rd::NT), 0, s, x, dlogits, T, E, d, n_nt,
+                     share, out);
+  if (n > 1) {
+    const int64_t n4 = (int64_t)E * d / 4;
+    hipLaunchKernelGGL(k_router_dw_join, dim3((unsigned)((n4 + 255) / 256)), dim3(256), 0, s,
+                       reinterpret_cast<const f32x4*>(ws), n, n4, reinterpret_cast<f32x4*>(dw));
+  }
+  return check_launch("moe_router_wgrad_dense");
+}

@@ -24,11 +24,12 @@ router logits.
 import torch
 
 from . import (NVFP4_4OVER6, PRE_SILU, PRE_SILU_AMAX, SF_BLOCKS, SF_ROWS, Moe4Unsupported, max_padded_rows,
-               moe_combine, moe_combine_hmx8, moe_dgates, moe_gather_rows, moe_grouped_gemm_bwd_dgrad,
+               moe_balance_loss, moe_balance_loss_backward, moe_combine, moe_combine_hmx8, moe_dgates, moe_gather_rows, moe_grouped_gemm_bwd_dgrad,
                moe_grouped_gemm_bwd_wgrad, moe_grouped_gemm_fwd, moe_grouped_gemm_fwd_hmx8,
-               moe_grouped_gemm_fwd_silu_amax, moe_grouped_gemm_mx,
+               moe_grouped_gemm_fwd_silu_amax, moe_grouped_gemm_mx, moe_grouped_gemm_mx4,
                moe_hmx8_quant, moe_route_backward, moe_route_topk, moe_router_logits, moe_router_wgrad,
-               moe_unpermute_sum, moe_unpermute_sum_router, mxfp8_quant, mxfp8_quant_requant_T, mxfp8_quant_rows_T,
+               moe_router_wgrad_dense, moe_unpermute_sum, moe_unpermute_sum_router, moe_unpermute_sum_router_dense,
+               mxfp4_quant, mxfp8_quant, mxfp8_quant_requant_T, mxfp8_quant_rows_T, mxfp8_requant_mx4_sr_T,
                mxfp8_requant_mx_sr_T, mxfp8_requant_sr_T, nvfp4_quant_46, nvfp4_quant_requant_T)
 
 ROLE_X, ROLE_H, ROLE_WUP, ROLE_WDOWN = 0, 1, 2, 3
@@ -49,6 +50,15 @@ def _side_stream(device):
 def _tick(timer, name):
     if timer is not None:
         timer(name)
+
+
+def _balance(fw, k, bias, token_mask, seg_off, timer):
+    """The router's balance loss of a forward's logits and routing, kept in
+    fw["balance"] (moe_balance_loss's dict) for the caller and the backward."""
+    fw["balance"] = moe_balance_loss(fw["logits"], fw["route"]["idx"], bias, token_mask, seg_off)
+    fw["balance_in"] = dict(bias=bias, token_mask=token_mask, seg_off=seg_off)
+    _tick(timer, "F2b balance loss")
+    return fw
 
 
 def quantize_weights(w_up, w_down, timer=None, seed=1, layer=0):
@@ -72,7 +82,7 @@ def quantize_weights(w_up, w_down, timer=None, seed=1, layer=0):
 
 
 def forward(x, w_up, w_down, logits, k, bias=None, wq=None, timer=None, seed=1, layer=0, combine_payload=False,
-            router_w=None):
+            router_w=None, balance=False, token_mask=None, seg_off=None):
     """x [T, d] bf16, w_up [E, F, d] / w_down [E, d, F] fp32, logits [T, E] fp32.
     (seed, layer): the SR key of the weights' backward copies made here.
     combine_payload: send the expert outputs to the combine as the 8.25-bit
@@ -81,7 +91,10 @@ def forward(x, w_up, w_down, logits, k, bias=None, wq=None, timer=None, seed=1, 
     backward treats that quantisation as the identity.
     router_w: [E, d] bf16 router weights; when given, the logits are made here
     by the BF16 router GEMM (logits may be None) and the backward adds the
-    router's input gradient to dx and returns its weight gradient."""
+    router's input gradient to dx and returns its weight gradient.
+    balance: also the router's balance loss per token segment (moe_balance_loss
+    with token_mask and seg_off) as fw["balance"]; the backward's dbalance is
+    its gradient."""
     T, d = x.shape
     E, F, _ = w_up.shape
     if wq is None:
@@ -147,15 +160,19 @@ def forward(x, w_up, w_down, logits, k, bias=None, wq=None, timer=None, seed=1, 
         _tick(timer, "F8 down GEMM (NVFP4)")
         y = moe_combine(Yp, r["gates"], r["inv_perm"])
         _tick(timer, "F9 combine")
-    return dict(y=y, route=r, xq=xq, xq_perm=xq_perm, U=U, hq=hq, Yp=Yp, wq=wq, dims=(T, d, F, E, k),
-                payload=payload, x=x, router_w=router_w, logits=logits)
+    fw = dict(y=y, route=r, xq=xq, xq_perm=xq_perm, U=U, hq=hq, Yp=Yp, wq=wq, dims=(T, d, F, E, k),
+              payload=payload, x=x, router_w=router_w, logits=logits)
+    return _balance(fw, k, bias, token_mask, seg_off, timer) if balance else fw
 
 
-def backward(fw, dy, seed=1, layer=0, timer=None, skip_empty_dw=False):
+def backward(fw, dy, seed=1, layer=0, timer=None, skip_empty_dw=False, dbalance=None):
     """dy [T, d] bf16 -> dict(dx [T, d] bf16, dW_up [E, F, d] fp32, dW_down [E, d, F] fp32, dg, dlogits, ...).
     skip_empty_dw: the weight gradients of experts that received no token are
     left unwritten (their gradient is zero; dW[e] holds a value iff
-    route off[e + 1] > off[e]) instead of being filled with zeros."""
+    route off[e + 1] > off[e]) instead of being filled with zeros.
+    dbalance: [S] float32 gradient of the balance losses of a forward made with
+    balance=True (e.g. the loss coefficient); their gradient joins dlogits, and
+    with the router its input and weight gradients then cover all experts."""
     T, d, F, E, k = fw["dims"]
     r = fw["route"]
     mpr = max_padded_rows(T * k, E)
@@ -168,7 +185,7 @@ def backward(fw, dy, seed=1, layer=0, timer=None, skip_empty_dw=False):
             return wq[name], None
         return mxfp8_requant_sr_T(*w, goff, goff, True, seed, sid(role), max_pr=rows), True
     hq, xp = fw["hq"], fw["xq_perm"]
-    return _backward_chain(fw, dy, timer, skip_empty_dw, dict(
+    return _backward_chain(fw, dy, timer, skip_empty_dw, dbalance, dict(
         wdT=lambda: wreq("wdT", wq["wd"], wq["off_d"], ROLE_WDOWN, E * d),
         hT=lambda: (mxfp8_requant_sr_T(*hq, r["off"], r["off_pad"], True, seed, sid(ROLE_H), max_pr=mpr,
                                        sf_layout=SF_BLOCKS), True),
@@ -177,7 +194,7 @@ def backward(fw, dy, seed=1, layer=0, timer=None, skip_empty_dw=False):
                                        max_pr=mpr, sf_layout=SF_BLOCKS), True)))
 
 
-def _backward_chain(fw, dy, timer, skip_empty_dw, req):
+def _backward_chain(fw, dy, timer, skip_empty_dw, dbalance, req):
     """The backward calls in order; req[name]() gives the transposed MXFP8
     operand 'wdT', 'hT', 'wuT' or 'xT' and whether a library call made it
     (for the timer).
@@ -199,6 +216,16 @@ def _backward_chain(fw, dy, timer, skip_empty_dw, req):
     mpr = max_padded_rows(A, E)
     g_flat = r["gates"].view(-1)
     rw = fw.get("router_w")
+    bal = fw.get("balance")
+    if dbalance is not None and bal is None:
+        raise ValueError("dbalance needs a forward made with balance=True")
+
+    def router_backward(dg):
+        dl = moe_route_backward(dg, r["gates"], r["idx"], E)
+        if dbalance is not None:
+            moe_balance_loss_backward(dbalance, fw["logits"], bal["counts"], bal["tokens"], k, dlogits=dl, out=dl,
+                                      **fw["balance_in"])
+        return dl
     side = None
     if timer is None and dy.is_cuda and A * d >= SIDE_STREAM_MIN_ELEMS:
         main = torch.cuda.current_stream(dy.device)
@@ -206,7 +233,7 @@ def _backward_chain(fw, dy, timer, skip_empty_dw, req):
         side.wait_stream(main)
         with torch.cuda.stream(side):
             dg = moe_dgates(dy, fw["Yp"], r["inv_perm"], k)
-            dlogits = moe_route_backward(dg, r["gates"], r["idx"], E)
+            dlogits = router_backward(dg)
 
     def get(name, label):
         out, called = req[name]()
@@ -250,9 +277,15 @@ def _backward_chain(fw, dy, timer, skip_empty_dw, req):
             _tick(timer, "B11 un-permute sum")
         dg = moe_dgates(dy, fw["Yp"], r["inv_perm"], k)
         _tick(timer, "B12 gate gradient")
-        dlogits = moe_route_backward(dg, r["gates"], r["idx"], E)
+        dlogits = router_backward(dg)
         _tick(timer, "B13 router backward")
-    if rw is not None:
+    if rw is not None and dbalance is not None:
+        # every expert's logit has a gradient: the dense forms
+        dx = moe_unpermute_sum_router_dense(dXp, r["inv_perm"], T, k, dlogits, rw)
+        _tick(timer, "B11 un-permute sum (+ router input gradient, dense)")
+        dW_router = moe_router_wgrad_dense(fw["x"], dlogits)
+        _tick(timer, "B14 router weight gradient (dense)")
+    elif rw is not None:
         # the router's input gradient joins the un-permuting sum; then its weight gradient
         dx = moe_unpermute_sum_router(dXp, r["inv_perm"], T, k, dlogits, r["idx"], rw)
         _tick(timer, "B11 un-permute sum (+ router input gradient)")
@@ -288,7 +321,8 @@ def quantize_weights_mx(w_up, w_down, timer=None, seed=1, layer=0):
                 shape=(E, F, d))
 
 
-def forward_mx(x, w_up, w_down, logits, k, bias=None, wq=None, timer=None, seed=1, layer=0):
+def forward_mx(x, w_up, w_down, logits, k, bias=None, wq=None, timer=None, seed=1, layer=0, balance=False,
+               token_mask=None, seg_off=None):
     T, d = x.shape
     E, F, _ = w_up.shape
     if wq is None:
@@ -310,10 +344,11 @@ def forward_mx(x, w_up, w_down, logits, k, bias=None, wq=None, timer=None, seed=
     _tick(timer, "F8 down GEMM (MXFP8)")
     y = moe_combine(Yp, r["gates"], r["inv_perm"])
     _tick(timer, "F9 combine")
-    return dict(y=y, route=r, xq_perm=xq_perm, U=U, hq=hq, Yp=Yp, wq=wq, dims=(T, d, F, E, k), mx=True)
+    fw = dict(y=y, route=r, xq_perm=xq_perm, U=U, hq=hq, Yp=Yp, wq=wq, dims=(T, d, F, E, k), mx=True, logits=logits)
+    return _balance(fw, k, bias, token_mask, seg_off, timer) if balance else fw
 
 
-def backward_mx(fw, dy, seed=1, layer=0, timer=None, skip_empty_dw=False):
+def backward_mx(fw, dy, seed=1, layer=0, timer=None, skip_empty_dw=False, dbalance=None):
     """The backward of forward_mx: the requantisations read MXFP8 operands."""
     T, d, F, E, k = fw["dims"]
     r = fw["route"]
@@ -332,7 +367,90 @@ def backward_mx(fw, dy, seed=1, layer=0, timer=None, skip_empty_dw=False):
         if pre:
             return wq[name], None
         return req(q, goff, goff, role, SF_ROWS, rows)
-    return _backward_chain(fw, dy, timer, skip_empty_dw, dict(
+    return _backward_chain(fw, dy, timer, skip_empty_dw, dbalance, dict(
+        wdT=lambda: wreq("wdT", wq["wd"], wq["off_d"], ROLE_WDOWN, E * d),
+        hT=lambda: req(fw["hq"], r["off"], r["off_pad"], ROLE_H, SF_BLOCKS, mpr),
+        wuT=lambda: wreq("wuT", wq["wu"], wq["off_f"], ROLE_WUP, E * F),
+        xT=lambda: req(fw["xq_perm"], r["off"], r["off_pad"], ROLE_X, SF_BLOCKS, mpr)))
+
+
+# ------------------------------------------------ MXFP4-forward variant
+#
+# The forward in MXFP4, the 4-bit format whose scales the block-scaled MFMA
+# applies itself: x is quantised once and written to its routed rows, the
+# weights and H = silu(U) along the forward contraction (no tensor scale); U
+# is stored in bf16.  The backward is the same chain with the transposed SR
+# requantisations reading the MXFP4 forward operands.
+
+def quantize_weights_mx4(w_up, w_down, timer=None, seed=1, layer=0, backward=True):
+    """MXFP4 of the fp32 masters and, with ``backward``, the backward's
+    transposed MXFP8 SR copies (SR stream 16*layer + role, as backward_mx4
+    would requantise them); a serving program leaves those out."""
+    E, F, d = w_up.shape
+    dev = w_up.device
+    off_f = torch.arange(E + 1, dtype=torch.int32, device=dev) * F
+    off_d = torch.arange(E + 1, dtype=torch.int32, device=dev) * d
+    _tick(timer, None)
+    wu = mxfp4_quant(w_up.view(E * F, d))
+    wd = mxfp4_quant(w_down.view(E * d, F))
+    _tick(timer, "F1 weight quant (MXFP4)")
+    wq = dict(wu=wu, wd=wd, off_f=off_f, off_d=off_d, shape=(E, F, d))
+    if backward:
+        wq["wuT"] = mxfp8_requant_mx4_sr_T(*wu, off_f, off_f, seed, 16 * layer + ROLE_WUP, max_pr=E * F)
+        wq["wdT"] = mxfp8_requant_mx4_sr_T(*wd, off_d, off_d, seed, 16 * layer + ROLE_WDOWN, max_pr=E * d)
+        wq["sr"] = (seed, layer)
+        _tick(timer, "F1 weight requant SR-T (MXFP4)")
+    return wq
+
+
+def forward_mx4(x, w_up, w_down, logits, k, bias=None, wq=None, timer=None, seed=1, layer=0, router_w=None,
+                balance=False, token_mask=None, seg_off=None):
+    """As forward, in MXFP4.  With wq (quantize_weights_mx4) the masters are not
+    read and may be None."""
+    T, d = x.shape
+    if wq is None:
+        wq = quantize_weights_mx4(w_up, w_down, timer, seed, layer)
+    E, F, _ = wq["shape"]
+    _tick(timer, None)
+    if router_w is not None:
+        logits = moe_router_logits(x, router_w)
+        _tick(timer, "F0 router GEMM (BF16)")
+    r = moe_route_topk(logits, k, bias)
+    _tick(timer, "F2-F3 route + permutation")
+    xq_perm = mxfp4_quant(x, out_map=r["inv_perm"], copies=k)
+    _tick(timer, "F4-F5 X quant + dispatch (MXFP4)")
+    wu_c, wu_s = wq["wu"]
+    wd_c, wd_s = wq["wd"]
+    U = moe_grouped_gemm_mx4(*xq_perm, wu_c.view(E, F, d // 2), wu_s.view(E, F, d // 32), r["off"], torch.bfloat16)
+    _tick(timer, "F6 up GEMM (MXFP4)")
+    hq = mxfp4_quant(U, PRE_SILU)
+    _tick(timer, "F7 SiLU + H quant (MXFP4)")
+    Yp = moe_grouped_gemm_mx4(*hq, wd_c.view(E, d, F // 2), wd_s.view(E, d, F // 32), r["off"], torch.float32)
+    _tick(timer, "F8 down GEMM (MXFP4)")
+    y = moe_combine(Yp, r["gates"], r["inv_perm"])
+    _tick(timer, "F9 combine")
+    fw = dict(y=y, route=r, xq_perm=xq_perm, U=U, hq=hq, Yp=Yp, wq=wq, dims=(T, d, F, E, k), x=x, router_w=router_w,
+              logits=logits)
+    return _balance(fw, k, bias, token_mask, seg_off, timer) if balance else fw
+
+
+def backward_mx4(fw, dy, seed=1, layer=0, timer=None, skip_empty_dw=False, dbalance=None):
+    """The backward of forward_mx4: the requantisations read MXFP4 operands."""
+    T, d, F, E, k = fw["dims"]
+    r = fw["route"]
+    mpr = max_padded_rows(T * k, E)
+    wq = fw["wq"]
+    pre = wq.get("sr") == (seed, layer)  # the weights were requantised with their forward quantisation
+
+    def req(q, goff, goff_pad, role, layout, max_pr):
+        return mxfp8_requant_mx4_sr_T(q[0], q[1], goff, goff_pad, seed, 16 * layer + role, max_pr=max_pr,
+                                      sf_layout=layout), True
+
+    def wreq(name, q, goff, role, rows):
+        if pre:
+            return wq[name], None
+        return req(q, goff, goff, role, SF_ROWS, rows)
+    return _backward_chain(fw, dy, timer, skip_empty_dw, dbalance, dict(
         wdT=lambda: wreq("wdT", wq["wd"], wq["off_d"], ROLE_WDOWN, E * d),
         hT=lambda: req(fw["hq"], r["off"], r["off_pad"], ROLE_H, SF_BLOCKS, mpr),
         wuT=lambda: wreq("wuT", wq["wu"], wq["off_f"], ROLE_WUP, E * F),
