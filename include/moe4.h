@@ -528,7 +528,8 @@ int moe_grouped_gemm_bwd(const uint8_t* dy_codes, const uint8_t* dy_sf,         
  * of an MXFP4 layer (fourweekmba.com page, the hardware table's 4-bit rate).
  * A scale byte of 255 makes the results it enters NaN.  Rows of C outside
  * [expert_off[0], expert_off[E]) are not written.  K % 32 == 0, N % 32 == 0;
- * each expert's B below 2 GiB; a_codes, b_codes and c 16-byte aligned.
+ * M_total < 2^31, N and K < 2^22, each expert's B below 2 GiB; a_codes,
+ * b_codes and c 16-byte aligned (the scales may have any alignment).
  */
 int moe_grouped_gemm_mx4(const uint8_t* a_codes, const uint8_t* a_sf, const uint8_t* b_codes, const uint8_t* b_sf,
                          const int32_t* expert_off, int32_t E, int64_t M_total, int64_t N, int64_t K,

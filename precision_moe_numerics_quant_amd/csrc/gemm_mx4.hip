@@ -63,6 +63,329 @@ __global__ void __launch_bounds__(m4s::NT)
     *reinterpret_cast<f32x4*>(static_cast<float*>(c) + row * N + col) = acc;
 }
 
+// ---------------------------------------------------------------- many rows
+// Persistent and warp-specialised, the structure of this library's other
+// grouped GEMMs: four producer waves only issue direct-to-LDS loads of a
+// 256-value K slab (128 code bytes and 8 scale bytes of each row) into a ring
+// of stages, four consumer waves only read LDS, run the MFMAs
+// (v_mfma_scale_f32_32x32x64_f8f6f4) and store; one barrier per slab.  128 x
+// TN tiles: consumers of 64 x TN / 2.
+//
+// Every load goes through a buffer descriptor that covers exactly the tile's
+// rows, so rows past the expert's last, past N, and K chunks past K (their
+// lanes' offsets are set out of range) arrive as zeros and no shape needs a
+// kernel of its own.  ALIGNED (K % 128 == 0, 4-byte aligned scale pointers):
+// a row's 8 scale bytes of a slab are two dwords; otherwise they lie in three
+// aligned dwords, and the consumer cuts its row's bytes out of them.
+namespace m4w {
+constexpr int TM = 128, NCW = 4, NT = 64 * (NCW + 4);
+constexpr int BK = 256, ROW_B = BK / 2;  // K values and code bytes of a row and slab
+typedef __attribute__((address_space(3))) void* lds_ptr;
+// 16-byte chunk c of a row sits at chunk c ^ ((row >> 1) & 7) (the 16 lanes of
+// a fragment read hit 16 distinct bank groups); applied through the global
+// address that each lane loads
+__device__ inline int swz(int row, int c) { return c ^ ((row >> 1) & 7); }
+// s_waitcnt immediates (vmcnt: bits 3:0 and 15:14; expcnt 6:4; lgkmcnt 11:8)
+constexpr int wait_vm(int n) { return (n & 15) | ((n >> 4) << 14) | (7 << 4) | (15 << 8); }
+constexpr int WAIT_LGKM0 = 15 | (3 << 14) | (7 << 4);
+constexpr int NT_STORE = 2;                // buffer-store cache policy: nontemporal
+constexpr uint32_t OOB = 0x80000000u;      // past every descriptor: loads return 0
+template <int TN, bool ALIGNED>
+struct Cfg {
+  static constexpr int ND = ALIGNED ? 2 : 3;             // scale dwords per row and slab
+  static constexpr int CODE_A = TM * ROW_B, CODE_B = TN * ROW_B;
+  static constexpr int GRPS = (TM + TN) / 64;            // 64-row scale groups (A's first)
+  static constexpr int UNITS = GRPS * ND;                // their loads: [group][dword][64 rows]
+  static constexpr int STAGE = CODE_A + CODE_B + UNITS * 256;
+  static constexpr int S = TN == 128 ? 4 : 3;
+  static constexpr int QB = TN / 32;                     // B's 8-row code loads per producer
+  static constexpr int NU = (UNITS + 3) / 4;             // scale loads per producer
+  static constexpr int I = 4 + QB + NU;                  // all of them: what the waits count
+  static_assert(S * STAGE + 16 <= 160 * 1024, "LDS");
+};
+}  // namespace m4w
+
+template <bool OUT_BF16, int TN, bool ALIGNED>
+__global__ void __launch_bounds__(m4w::NT, 1)
+    k_gemm_mx4_ws(const uint8_t* __restrict__ a_codes, const uint8_t* __restrict__ a_sf,
+                  const uint8_t* __restrict__ b_codes, const uint8_t* __restrict__ b_sf,
+                  const int32_t* __restrict__ off, int E, int64_t M_total, int64_t N, int64_t K, DgSplit sp,
+                  void* __restrict__ c) {
+  using namespace m4w;
+  using C = Cfg<TN, ALIGNED>;
+  constexpr int S = C::S, STAGE = C::STAGE, I = C::I, ND = C::ND;
+  __shared__ __attribute__((aligned(16))) uint8_t ring[S * STAGE];
+  __shared__ uint32_t s_nmt;
+  const int tid = threadIdx.x, l = tid & 63;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
+  // total m-tiles (before any load into LDS is in flight)
+  if (w == 0) {
+    uint32_t n = 0;
+    for (int e = l; e < E; e += 64) {
+      const int32_t m = off[e + 1] - off[e];
+      n += m > 0 ? (uint32_t)((m + TM - 1) / TM) : 0u;
+    }
+#pragma unroll
+    for (int o = 32; o >= 1; o >>= 1) n += __shfl_xor(n, o, 64);
+    if (l == 0) s_nmt = n;
+  }
+  __syncthreads();
+  const uint32_t n_nt = (uint32_t)((N + TN - 1) / TN), n_mt = s_nmt;
+  const uint32_t KH = (uint32_t)(K / 2), KS = (uint32_t)(K / 32), nk = (KS + 7) / 8;
+  // this workgroup's tiles: q = q0, q0 + stride, ... of its XCD (see DgSplit)
+  const uint32_t xcd = blockIdx.x % 8, stride = (gridDim.x - xcd + 7) / 8, q0 = blockIdx.x / 8;
+  const uint32_t sm = (8 / sp.xb) * sp.pm, q_end = (n_mt + sm - 1) / sm * (sp.pm * sp.pn);
+
+  if (w >= NCW) {
+    // ---- producer pw: 8-row code loads 4 pw .. of A and QB pw .. of B, scale units NU pw ..
+    const int pw = w - NCW;
+    __amdgpu_buffer_rsrc_t rac = make_rsrc(a_codes, 0), ras = rac, rbc = rac, rbs = rac;
+    uint32_t ax = 0, bx = 0;       // the scale descriptors' bytes ahead of the tile's first
+    MtCursor<TM> cur;
+    uint32_t pt = q0, ps = 0;
+    bool more = false;
+    auto seek = [&]() {
+      uint32_t mi = 0, nt = 0;
+      while (pt < q_end && !sp.tile(xcd, pt, n_mt, n_nt, mi, nt)) pt += stride;
+      more = pt < q_end && cur.seek(off, E, mi);
+      if (!more) return;
+      const int e = cur.e;
+      const int64_t row0 = (int64_t)ld_const(off, e) + (int64_t)(mi - cur.first) * TM, n0 = (int64_t)nt * TN;
+      const int64_t end = (int64_t)ld_const(off, e + 1) < M_total ? (int64_t)ld_const(off, e + 1) : M_total;
+      int64_t ra = end - row0 < TM ? end - row0 : TM;
+      const int64_t rb = N - n0 < TN ? N - n0 : TN, rowb = (int64_t)e * N + n0;
+      if (row0 < 0 || ra < 0) ra = 0;  // (offsets outside [0, M]: nothing is read)
+      rac = make_rsrc(a_codes + row0 * KH, (uint64_t)ra * KH);
+      rbc = make_rsrc(b_codes + rowb * KH, (uint64_t)rb * KH);
+      const uint8_t* as = a_sf + row0 * KS;
+      const uint8_t* bs = b_sf + rowb * KS;
+      if (!ALIGNED) {  // (whole dwords that hold a byte of the rows: never past their page)
+        ax = (uint32_t)reinterpret_cast<uintptr_t>(as) & 3u;
+        bx = (uint32_t)reinterpret_cast<uintptr_t>(bs) & 3u;
+      }
+      ras = make_rsrc(as - ax, ra ? ((uint64_t)ra * KS + ax + 3) / 4 * 4 : 0);
+      rbs = make_rsrc(bs - bx, ((uint64_t)rb * KS + bx + 3) / 4 * 4);
+      ps = 0;
+    };
+    seek();
+    auto issue = [&](int st) {
+      uint8_t* base = ring + st * STAGE;
+      const uint32_t kb = ps * (uint32_t)ROW_B, left = KS - 8 * ps;  // chunks of the row from this slab on
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int r = 32 * pw + 8 * q + (l >> 3);
+        const uint32_t ch = (uint32_t)swz(r, l & 7);
+        const uint32_t o = ch < left ? (uint32_t)r * KH + 16u * ch + kb : OOB;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rac, (lds_ptr)(base + (4 * pw + q) * 1024), 16, o, 0, 0, 0);
+      }
+#pragma unroll
+      for (int q = 0; q < C::QB; ++q) {
+        const int r = (TN / 4) * pw + 8 * q + (l >> 3);
+        const uint32_t ch = (uint32_t)swz(r, l & 7);
+        const uint32_t o = ch < left ? (uint32_t)r * KH + 16u * ch + kb : OOB;
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rbc, (lds_ptr)(base + C::CODE_A + (C::QB * pw + q) * 1024), 16, o, 0, 0, 0);
+      }
+#pragma unroll
+      for (int k = 0; k < C::NU; ++k) {
+        int u = C::NU * pw + k;
+        u = u < C::UNITS ? u : C::UNITS - 1;  // (the last unit again: every producer issues I loads)
+        const int grp = u / ND, d = u - grp * ND;
+        uint8_t* sb = base + C::CODE_A + C::CODE_B + u * 256;
+        const bool opa = grp < TM / 64;
+        const uint32_t r = (uint32_t)(opa ? 64 * grp : 64 * grp - TM) + l;
+        const uint32_t o = (((opa ? ax : bx) + r * KS + 8 * ps) & ~3u) + 4 * d;
+        if (opa) __builtin_amdgcn_raw_ptr_buffer_load_lds(ras, (lds_ptr)sb, 4, o, 0, 0, 0);
+        else __builtin_amdgcn_raw_ptr_buffer_load_lds(rbs, (lds_ptr)sb, 4, o, 0, 0, 0);
+      }
+      if (++ps == nk) {
+        pt += stride;
+        seek();
+      }
+    };
+    uint32_t n_iss = 0;
+    for (int st = 0; st < S - 1 && more; ++st) {
+      issue(st);
+      ++n_iss;
+    }
+    for (uint32_t gs = 0; gs < n_iss; ++gs) {
+      // slab gs landed (later slabs may still be in flight), then the barrier
+      const uint32_t rem = n_iss - 1 - gs;
+      __builtin_amdgcn_sched_barrier(0);
+      if (rem >= 2) __builtin_amdgcn_s_waitcnt(wait_vm(2 * I));
+      else if (rem == 1) __builtin_amdgcn_s_waitcnt(wait_vm(I));
+      else __builtin_amdgcn_s_waitcnt(wait_vm(0));
+      __builtin_amdgcn_s_barrier();
+      __builtin_amdgcn_sched_barrier(0);
+      asm volatile("" ::: "memory");
+      if (more) {
+        issue((int)((gs + S - 1) % S));
+        ++n_iss;
+      }
+    }
+    return;
+  }
+  // ---- consumers: wave w owns the 64 x (TN / 2) block (w / 2, w % 2)
+  constexpr int MI = 2, NJ = TN / 64;
+  const int g = (l >> 5) & 1, li = l & 31;
+  const int wm = (w >> 1) * 64, wn = (w & 1) * (TN / 2);
+  f32x16 acc[MI][NJ];
+#pragma unroll
+  for (int i = 0; i < MI; ++i)
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) acc[i][j] = f32x16{};
+  uint32_t sha[MI], shb[NJ];  // !ALIGNED: the rows' first scale byte in its dword
+  // one slab: four 64-value k steps; lane half g supplies K block 2 ks + g and
+  // its scale, byte 2 (ks % 2) of the row's scale dword ks / 2 shifted by g
+  // bytes.  left: scale blocks from this slab on (fewer than 8: the rest 0)
+  auto compute = [&](const uint8_t* base, uint32_t left) {
+    const uint8_t* la = base;
+    const uint8_t* lb = base + C::CODE_A;
+    const uint8_t* sc = base + C::CODE_A + C::CODE_B;
+    auto scales = [&](int r, uint32_t sh, uint32_t (&y)[2]) {  // r: row of A, or TM + row of B
+      const uint8_t* p = sc + (r >> 6) * (ND * 256) + (r & 63) * 4;
+      uint32_t d0 = *reinterpret_cast<const uint32_t*>(p), d1 = *reinterpret_cast<const uint32_t*>(p + 256);
+      if (!ALIGNED) {
+        const uint32_t d2 = *reinterpret_cast<const uint32_t*>(p + (ND - 1) * 256);
+        d0 = __builtin_amdgcn_alignbyte(d1, d0, sh);
+        d1 = __builtin_amdgcn_alignbyte(d2, d1, sh);
+      }
+      if (left < 8) {  // (uniform; a slab that ends inside the row's last blocks)
+        d0 &= left >= 4 ? ~0u : (1u << (8 * left)) - 1u;
+        d1 &= left > 4 ? (1u << (8 * (left - 4))) - 1u : 0u;
+      }
+      y[0] = d0 >> (8 * g);
+      y[1] = d1 >> (8 * g);
+    };
+    uint32_t ya[MI][2], yb[NJ][2];
+#pragma unroll
+    for (int i = 0; i < MI; ++i) scales(wm + 32 * i + li, sha[i], ya[i]);
+#pragma unroll
+    for (int j = 0; j < NJ; ++j) scales(TM + wn + 32 * j + li, shb[j], yb[j]);
+#pragma unroll
+    for (int ks = 0; ks < 4; ++ks) {
+      i32x4 fa[MI], fb[NJ];
+#pragma unroll
+      for (int i = 0; i < MI; ++i) {
+        const int r = wm + 32 * i + li;
+        fa[i] = *reinterpret_cast<const i32x4*>(la + r * ROW_B + 16 * swz(r, 2 * ks + g));
+      }
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) {
+        const int r = wn + 32 * j + li;
+        fb[j] = *reinterpret_cast<const i32x4*>(lb + r * ROW_B + 16 * swz(r, 2 * ks + g));
+      }
+#pragma unroll
+      for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+          const i32x8 xa = __builtin_shufflevector(fa[i], fa[i], 0, 1, 2, 3, -1, -1, -1, -1);
+          const i32x8 xb = __builtin_shufflevector(fb[j], fb[j], 0, 1, 2, 3, -1, -1, -1, -1);
+          // (the byte selector is an immediate)
+          if (ks & 1)
+            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(xa, xb, acc[i][j], FP4, FP4, 2, (int)ya[i][ks >> 1], 2,
+                                                                        (int)yb[j][ks >> 1]);
+          else
+            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(xa, xb, acc[i][j], FP4, FP4, 0, (int)ya[i][ks >> 1], 0,
+                                                                        (int)yb[j][ks >> 1]);
+        }
+    }
+  };
+  constexpr int ESZ = OUT_BF16 ? 2 : 4;
+  const uint32_t ld = (uint32_t)N * ESZ;  // output row pitch in bytes
+  const uint32_t lane_off = (uint32_t)(g * 4) * ld + (uint32_t)li * ESZ;
+  MtCursor<TM> cur;
+  uint32_t gs = 0;
+  for (uint32_t q = q0; q < q_end; q += stride) {
+    uint32_t mi, nt;
+    if (!sp.tile(xcd, q, n_mt, n_nt, mi, nt)) continue;
+    if (!cur.seek(off, E, mi)) break;
+    const int e = cur.e;
+    const int64_t row0 = (int64_t)ld_const(off, e) + (int64_t)(mi - cur.first) * TM, n0 = (int64_t)nt * TN;
+    const int64_t row_end = (int64_t)ld_const(off, e + 1) < M_total ? (int64_t)ld_const(off, e + 1) : M_total;
+    // waves whose rows or columns all lie past the tile's last skip their MFMAs
+    const bool active = row0 >= 0 && row0 + wm < row_end && n0 + wn < N;
+    if (!ALIGNED) {
+#pragma unroll
+      for (int i = 0; i < MI; ++i)
+        sha[i] = (uint32_t)(reinterpret_cast<uintptr_t>(a_sf) + (uint64_t)(row0 + wm + 32 * i + li) * KS) & 3u;
+#pragma unroll
+      for (int j = 0; j < NJ; ++j)
+        shb[j] = (uint32_t)(reinterpret_cast<uintptr_t>(b_sf) + (uint64_t)((int64_t)e * N + n0 + wn + 32 * j + li) * KS) & 3u;
+    }
+    for (uint32_t s = 0; s < nk; ++s, ++gs) {
+      __builtin_amdgcn_sched_barrier(0);
+      __builtin_amdgcn_s_waitcnt(WAIT_LGKM0);
+      __builtin_amdgcn_s_barrier();
+      __builtin_amdgcn_sched_barrier(0);
+      asm volatile("" ::: "memory");
+      if (active) compute(ring + (gs % S) * STAGE, KS - 8 * s);
+    }
+    // epilogue: each value straight from the accumulators; the descriptor
+    // covers the tile's rows up to the expert's last, so stores of rows past
+    // it are dropped
+    if (active) {
+      const int64_t nrows = row_end - row0 < TM ? row_end - row0 : TM;
+      const __amdgpu_buffer_rsrc_t rC = make_rsrc(static_cast<uint8_t*>(c) + row0 * (int64_t)ld, (uint64_t)nrows * ld);
+#pragma unroll
+      for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int j = 0; j < NJ; ++j) {
+          if (n0 + wn + 32 * j >= N) continue;  // (uniform; N % 32 == 0)
+          const uint32_t fo = (uint32_t)(wm + i * 32) * ld + (uint32_t)(n0 + wn + j * 32) * ESZ;
+#pragma unroll
+          for (int v = 0; v < 16; ++v) {
+            const uint32_t so = fo + (uint32_t)((v >> 2) * 8 + (v & 3)) * ld;
+            if (OUT_BF16)
+              __builtin_amdgcn_raw_buffer_store_b16((unsigned short)f32_to_bf16_bits(acc[i][j][v]), rC, lane_off, so, NT_STORE);
+            else
+              __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(acc[i][j][v]), rC, lane_off, so, NT_STORE);
+          }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+      for (int j = 0; j < NJ; ++j) acc[i][j] = f32x16{};
+  }
+}
+
+static int cu_count() {
+  static int n[64] = {0};
+  int dev = 0;
+  if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return 256;
+  if (n[dev] == 0) {
+    int v = 0;
+    if (hipDeviceGetAttribute(&v, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || v <= 0) v = 256;
+    n[dev] = v;
+  }
+  return n[dev];
+}
+
+template <bool OUT_BF16>
+static void launch_mx4(const uint8_t* ac, const uint8_t* as, const uint8_t* bc, const uint8_t* bs, const int32_t* off, int E,
+                       int64_t M, int64_t N, int64_t K, void* c, hipStream_t s) {
+  if (M <= 32 * (int64_t)E) {
+    const int n_nt = (int)((N + 63) / 64);
+    const int64_t m_tiles = (M + m4s::TR - 1) / m4s::TR + E;
+    hipLaunchKernelGGL(k_gemm_mx4_rows<OUT_BF16>, dim3((unsigned)(m_tiles * n_nt)), dim3(m4s::NT), 0, s, ac, as, bc, bs, off, E,
+                       M, N, K, n_nt, c);
+    return;
+  }
+  const dim3 grid((unsigned)(cu_count() < 8 ? 8 : cu_count()));
+  const bool al = K % 128 == 0 && aligned4(as) && aligned4(bs);
+#define MOE4_MX4(TN, AL)                                                                                                       \
+  hipLaunchKernelGGL((k_gemm_mx4_ws<OUT_BF16, TN, AL>), grid, dim3(m4w::NT), 0, s, ac, as, bc, bs, off, E, M, N, K,             \
+                     dg_split((N + TN - 1) / TN, m4w::TM, TN), c)
+  if (N % 256 == 0 || N > 512) {
+    if (al) MOE4_MX4(256, true);
+    else MOE4_MX4(256, false);
+  } else {
+    if (al) MOE4_MX4(128, true);
+    else MOE4_MX4(128, false);
+  }
+#undef MOE4_MX4
+}
+
 }  // namespace moe4
 
 using namespace moe4;
@@ -73,22 +396,18 @@ extern "C" int moe_grouped_gemm_mx4(const uint8_t* a_codes, const uint8_t* a_sf,
   MOE4_REQUIRE(c_dtype == MOE4_F32 || c_dtype == MOE4_BF16, MOE4_EINVAL, "moe_grouped_gemm_mx4: c_dtype must be F32 or BF16");
   MOE4_REQUIRE(E >= 1 && M_total >= 0 && N > 0 && K > 0 && K % 32 == 0 && N % 32 == 0, MOE4_EINVAL,
                "moe_grouped_gemm_mx4: need K % 32 == 0 and N % 32 == 0");
-  MOE4_REQUIRE(M_total < ((int64_t)1 << 31) && N * K < ((int64_t)1 << 32), MOE4_EINVAL,
-               "moe_grouped_gemm_mx4: M must be below 2^31 and each expert's B below 2 GiB");
+  MOE4_REQUIRE(M_total < ((int64_t)1 << 31) && N < ((int64_t)1 << 22) && K < ((int64_t)1 << 22) && N * K < ((int64_t)1 << 32),
+               MOE4_EINVAL, "moe_grouped_gemm_mx4: M must be below 2^31, N and K below 2^22, each expert's B below 2 GiB");
   MOE4_REQUIRE(expert_off && (M_total == 0 || (a_codes && a_sf && b_codes && b_sf && c)), MOE4_EINVAL,
                "moe_grouped_gemm_mx4: NULL pointer");
   MOE4_REQUIRE(aligned16(a_codes) && aligned16(b_codes) && aligned16(c), MOE4_EALIGN,
                "moe_grouped_gemm_mx4: a_codes, b_codes and c must be 16-byte aligned");
   if (M_total == 0) return MOE4_OK;
-  const int64_t m_tiles = (M_total + m4s::TR - 1) / m4s::TR + E;
-  const int n_nt = (int)((N + 63) / 64);
-  MOE4_REQUIRE(m_tiles * n_nt < ((int64_t)1 << 31), MOE4_EINVAL, "moe_grouped_gemm_mx4: too large");
-  const dim3 grid((unsigned)(m_tiles * n_nt));
+  MOE4_REQUIRE(((M_total + m4s::TR - 1) / m4s::TR + E) * ((N + 63) / 64) < ((int64_t)1 << 31), MOE4_EINVAL,
+               "moe_grouped_gemm_mx4: too large");
   if (c_dtype == MOE4_BF16)
-    hipLaunchKernelGGL(k_gemm_mx4_rows<true>, grid, dim3(m4s::NT), 0, as_stream(stream), a_codes, a_sf, b_codes, b_sf,
-                       expert_off, E, M_total, N, K, n_nt, c);
+    launch_mx4<true>(a_codes, a_sf, b_codes, b_sf, expert_off, E, M_total, N, K, c, as_stream(stream));
   else
-    hipLaunchKernelGGL(k_gemm_mx4_rows<false>, grid, dim3(m4s::NT), 0, as_stream(stream), a_codes, a_sf, b_codes, b_sf,
-                       expert_off, E, M_total, N, K, n_nt, c);
+    launch_mx4<false>(a_codes, a_sf, b_codes, b_sf, expert_off, E, M_total, N, K, c, as_stream(stream));
   return check_launch("moe_grouped_gemm_mx4");
 }

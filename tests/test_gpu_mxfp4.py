@@ -197,6 +197,24 @@ def test_gemm(M_list, N, K, dt):
     _gemm_check(got, og.grouped_nt(A, B, off), og.abs_bound_nt(A, B, off), K, dt == "bf16")
 
 
+@pytest.mark.parametrize("shift_a,shift_b", [(1, 0), (0, 3), (2, 1)])
+@pytest.mark.parametrize("M_list,N,K", [([150, 3, 77], 160, 512), ([2, 1], 64, 512), ([90, 40], 96, 544)])
+def test_gemm_scales_at_any_alignment(M_list, N, K, shift_a, shift_b):
+    """Scale tensors that start at any byte (a view into a larger buffer)."""
+    off, qa, qb = _operands(M_list, N, K, 5)
+    E = len(M_list)
+
+    def at(s, n):
+        buf = torch.empty(s.size + 16, dtype=torch.uint8, device="cuda")
+        v = buf[n:n + s.size].view(s.shape)
+        v.copy_(torch.from_numpy(s))
+        return v
+    want = _product(off, qa, qb, N, K, torch.float32)
+    got = m4.moe_grouped_gemm_mx4(cuda_u8(qa[0]), at(qa[1], shift_a), cuda_u8(qb[0]).view(E, N, K // 2),
+                                  at(qb[1], shift_b).view(E, N, K // 32), cuda_i32(off), torch.float32)
+    assert torch.equal(got, want)
+
+
 @pytest.mark.parametrize("M_list,N,K", [([50, 0, 90], 64, 128), ([300, 200], 256, 512), ([7, 0, 20, 3], 128, 96)])
 def test_gemm_exact_small_integers(M_list, N, K):
     """Small values under scales near one: every partial sum is exact in float32."""
