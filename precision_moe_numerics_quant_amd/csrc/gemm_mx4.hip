@@ -9,58 +9,173 @@ namespace moe4 {
 
 constexpr int FP4 = 4;  // the MFMA's operand format code of E2M1
 
+// Raw buffer loads.  An offset of OOB is past every descriptor: 0 comes back.
+constexpr uint32_t OOB = 0x80000000u;
+
+// Descriptor of the whole dwords that hold `bytes` bytes from p on (never
+// past the page that holds the last of them); ax: bytes ahead of p in it.
+__device__ inline __amdgpu_buffer_rsrc_t dword_rsrc(const uint8_t* p, uint64_t bytes, uint32_t& ax) {
+  ax = (uint32_t)__builtin_amdgcn_readfirstlane((int)((uint32_t)reinterpret_cast<uintptr_t>(p) & 3u));
+  return make_rsrc(p - ax, bytes ? (bytes + ax + 3) / 4 * 4 : 0);
+}
+
+// ----------------------------------------------------------------- few rows
+// With a handful of rows per expert the cost is streaming each active
+// expert's weights once.  The weights take the MFMA's M side
+// (v_mfma_scale_f32_16x16x128_f8f6f4), the expert's rows its N side, 16 at a
+// time.  A workgroup takes 16 WB weight rows of one expert and up to 16 PASSES
+// of its rows; its four waves split K (so that one token's eight experts
+// still fill the chip) and join their sums through LDS in wave order.  A wave
+// requests all the weights of its K share at once (NS steps of 128, the
+// smallest of 2, 3, 4, 6 and 8 that holds it: up to K = 4096), keeps them in registers for all its passes, and only the rows'
+// codes, from L2, are read per pass.  No LDS for the operands.
 namespace m4s {
-constexpr int NT = 256, TR = 16;  // rows of A per workgroup
-constexpr int KB = 128;           // K per MFMA
+constexpr int NT = 256, NWV = NT / 64, WB = 2, WROWS = 16 * WB;
+constexpr int KB = 128;           // K per step: lane (li, q) holds k = 128 s + 32 q .. of row li
+constexpr int PASSES = 4, TR = 16 * PASSES;
 }  // namespace m4s
 
-// A wave takes 16 rows of B[e] (the MFMA's M side) and 16 rows of A (its N
-// side); lane (li, q) holds the 32 values k = 128 s + 32 q .. of row li.
-template <bool OUT_BF16>
+// The expert and the tile in it of item idx, the experts holding count(rows)
+// items each, in order; false past the last.  Lane l counts the experts
+// [l P, (l + 1) P), so all the offsets are in flight at once.
+template <typename Count>
+__device__ inline bool nth_item(const int32_t* __restrict__ off, int E, int64_t idx, Count count, int& e_out, int64_t& i_out) {
+  const int l = threadIdx.x & 63, P = (E + 63) / 64;
+  const int e0 = l * P, e1 = e0 + P < E ? e0 + P : E;
+  int64_t mine = 0;
+  for (int e = e0; e < e1; ++e) mine += count(off[e + 1] - off[e]);
+  int64_t inc = mine;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int64_t y = __shfl_up(inc, o, 64);
+    if (l >= o) inc += y;
+  }
+  int64_t rest = idx - (inc - mine);  // the item's number among this lane's
+  const unsigned long long hit = __ballot(rest >= 0 && rest < mine);
+  if (hit == 0) return false;
+  int e = e0;
+  if (rest >= 0 && rest < mine) {
+    for (int64_t n; rest >= (n = count(off[e + 1] - off[e])); ++e) rest -= n;
+  }
+  const int src = __ffsll((long long)hit) - 1;
+  e_out = __builtin_amdgcn_readfirstlane(__shfl(e, src, 64));
+  i_out = __builtin_amdgcn_readfirstlane(__shfl((int)rest, src, 64));
+  return true;
+}
+
+// Grid: n_nt weight-row blocks x (slots for the experts' first TR rows, then
+// slots for the rest).  first: the number of those slots: E (slot = expert) or,
+// with fewer rows than experts, M_total (slot = number among the experts with
+// rows).  ALIGNED: K % 128 == 0 and 4-byte aligned scales, so that a row's
+// scales of a step are one dword.
+template <bool OUT_BF16, bool ALIGNED, int NS>
 __global__ void __launch_bounds__(m4s::NT)
     k_gemm_mx4_rows(const uint8_t* __restrict__ a_codes, const uint8_t* __restrict__ a_sf,
                     const uint8_t* __restrict__ b_codes, const uint8_t* __restrict__ b_sf,
-                    const int32_t* __restrict__ off, int E, int64_t M_total, int64_t N, int64_t K, int n_nt,
-                    void* __restrict__ c) {
+                    const int32_t* __restrict__ off, int E, int64_t M_total, int64_t N, int64_t K, uint32_t n_nt,
+                    int64_t first, void* __restrict__ c) {
   using namespace m4s;
-  int e;
-  int64_t mt;
-  if (!find_m_tile(off, E, TR, blockIdx.x / n_nt, e, mt)) return;
-  const int l = threadIdx.x & 63, li = l & 15, qg = l >> 4;
-  const int64_t n0 = ((int64_t)(blockIdx.x % n_nt) * (NT / 64) + (threadIdx.x >> 6)) * 16;
-  if (n0 >= N) return;
-  const int64_t r0 = (int64_t)off[e] + mt * TR;
-  const int64_t r1 = (int64_t)off[e + 1] < M_total ? (int64_t)off[e + 1] : M_total;
-  if (r0 < 0 || r0 >= r1) return;
-  const int64_t ra = r0 + li < r1 ? r0 + li : r1 - 1;  // (rows past the expert are never stored)
-  const int64_t KS = K / 32;
-  const uint8_t* ac = a_codes + ra * (K / 2);
-  const uint8_t* as = a_sf + ra * KS;
-  const uint8_t* bc = b_codes + ((int64_t)e * N + n0 + li) * (K / 2);
-  const uint8_t* bs = b_sf + ((int64_t)e * N + n0 + li) * KS;
-  f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
-  for (int64_t s = 0; s * KB < K; ++s) {
-    const int64_t kb = 4 * s + qg;  // this lane's block
-    u32x4 wa = {0u, 0u, 0u, 0u}, wb = wa;
-    int ya = 0, yb = 0;
-    if (kb < KS) {
-      wa = *reinterpret_cast<const u32x4*>(ac + 16 * kb);
-      wb = *reinterpret_cast<const u32x4*>(bc + 16 * kb);
-      ya = as[kb];
-      yb = bs[kb];
-    }
-    const i32x8 fb = {(int)wb[0], (int)wb[1], (int)wb[2], (int)wb[3], 0, 0, 0, 0};
-    const i32x8 fa = {(int)wa[0], (int)wa[1], (int)wa[2], (int)wa[3], 0, 0, 0, 0};
-    acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fb, fa, acc, FP4, FP4, 0, yb, 0, ya);
+  __shared__ f32x4 red[NWV][WB][64];
+  const int64_t slot = blockIdx.x / n_nt;
+  int e = (int)slot;
+  int64_t mt = 0;
+  if (slot >= first) {
+    if (!nth_item(off, E, slot - first, [](int m) { return (int64_t)(m > TR ? (m - 1) / TR : 0); }, e, mt)) return;
+    ++mt;
+  } else if (first < E) {
+    if (!nth_item(off, E, slot, [](int m) { return (int64_t)(m > 0); }, e, mt)) return;
   }
-  const int64_t row = r0 + li, col = n0 + 4 * qg;
-  if (row >= r1) return;
-  if (OUT_BF16)
-    *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(c) + row * N + col) =
-        u32x2{f32_to_bf16_bits(acc[0]) | (f32_to_bf16_bits(acc[1]) << 16),
-              f32_to_bf16_bits(acc[2]) | (f32_to_bf16_bits(acc[3]) << 16)};
-  else
-    *reinterpret_cast<f32x4*>(static_cast<float*>(c) + row * N + col) = acc;
+  const int64_t n0 = (int64_t)(blockIdx.x % n_nt) * WROWS;
+  const int64_t r0 = (int64_t)off[e] + mt * TR;
+  const int64_t re = (int64_t)off[e + 1] < M_total ? (int64_t)off[e + 1] : M_total;
+  const int64_t r1 = re < r0 + TR ? re : r0 + TR;
+  if (r0 < 0 || r0 >= r1) return;
+  const int l = threadIdx.x & 63, li = l & 15, qg = l >> 4;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t KH = (uint32_t)(K / 2), KS = (uint32_t)(K / 32), nst = (KS + 3) / 4;
+  const uint32_t spw = (nst + NWV - 1) / NWV;                       // steps per wave
+  const uint32_t s0 = spw * w, s1 = s0 + spw < nst ? s0 + spw : nst;
+  const int64_t rowb = (int64_t)e * N + n0, nb = N - n0 < WROWS ? N - n0 : WROWS;
+  const __amdgpu_buffer_rsrc_t rbc = make_rsrc(b_codes + rowb * KH, (uint64_t)nb * KH);
+  const __amdgpu_buffer_rsrc_t rac = make_rsrc(a_codes + r0 * KH, (uint64_t)(r1 - r0) * KH);
+  uint32_t ax, bx;
+  const __amdgpu_buffer_rsrc_t rbs = dword_rsrc(b_sf + rowb * KS, (uint64_t)nb * KS, bx);
+  const __amdgpu_buffer_rsrc_t ras = dword_rsrc(a_sf + r0 * KS, (uint64_t)(r1 - r0) * KS, ax);
+  // row r's codes of step s, and its scales: the step's dword (ALIGNED) or
+  // this lane's byte.  Steps past the wave's share and chunks past K count as
+  // zeros, codes and scale.
+  auto codes = [&](const __amdgpu_buffer_rsrc_t& rs, uint32_t r, uint32_t s) {
+    const uint32_t kb = 4 * s + qg;
+    return __builtin_bit_cast(i32x4, __builtin_amdgcn_raw_buffer_load_b128(rs, s < s1 && kb < KS ? r * KH + 16 * kb : OOB, 0, 0));
+  };
+  // ALIGNED: the dwords of NS steps in one load (they may reach past the
+  // wave's share or the row: step_scale drops those)
+  constexpr int NY = ALIGNED ? (NS + 3) / 4 * 4 : NS;
+  auto scales = [&](const __amdgpu_buffer_rsrc_t& rs, uint32_t x, uint32_t r, uint32_t s, uint32_t (&y)[NY]) {
+    if (ALIGNED) {
+#pragma unroll
+      for (int i = 0; i < NY; i += 4) {
+        const u32x4 v = __builtin_amdgcn_raw_buffer_load_b128(rs, r * KS + 4 * (s + i), 0, 0);
+        y[i] = v[0]; y[i + 1] = v[1]; y[i + 2] = v[2]; y[i + 3] = v[3];
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < NS; ++i) {
+        const uint32_t kb = 4 * (s + i) + qg;
+        y[i] = __builtin_amdgcn_raw_buffer_load_b8(rs, s + i < s1 && kb < KS ? x + r * KS + kb : OOB, 0, 0);
+      }
+    }
+  };
+  // (shifted where it is used: at the load it would wait for it)
+  auto step_scale = [&](uint32_t y, uint32_t s) { return ALIGNED ? (int)(s < s1 ? y >> (8 * qg) : 0u) : (int)y; };
+  i32x4 wq[NS][WB];
+  uint32_t wy[WB][NY];
+  auto weights = [&](uint32_t sb) {
+#pragma unroll
+    for (int b = 0; b < WB; ++b) {
+      scales(rbs, bx, 16 * b + li, sb, wy[b]);
+#pragma unroll
+      for (int s = 0; s < NS; ++s) wq[s][b] = codes(rbc, 16 * b + li, sb + s);
+    }
+  };
+  const bool held = spw <= NS;  // one batch of steps: the weights stay for all passes
+  if (held) weights(s0);
+  for (uint32_t p = 0; r0 + 16 * p < r1; ++p) {
+    f32x4 acc[WB];
+#pragma unroll
+    for (int b = 0; b < WB; ++b) acc[b] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (uint32_t sb = s0; sb < s1; sb += NS) {
+      if (!held) weights(sb);
+      i32x4 xq[NS];
+      uint32_t xy[NY];
+      scales(ras, ax, 16 * p + li, sb, xy);
+#pragma unroll
+      for (int s = 0; s < NS; ++s) xq[s] = codes(rac, 16 * p + li, sb + s);
+#pragma unroll
+      for (int s = 0; s < NS; ++s)
+#pragma unroll
+        for (int b = 0; b < WB; ++b)
+          acc[b] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+              __builtin_shufflevector(wq[s][b], wq[s][b], 0, 1, 2, 3, -1, -1, -1, -1),
+              __builtin_shufflevector(xq[s], xq[s], 0, 1, 2, 3, -1, -1, -1, -1), acc[b], FP4, FP4, 0,
+              step_scale(wy[b][s], sb + s), 0, step_scale(xy[s], sb + s));
+    }
+    if (p) __syncthreads();  // (the last pass's sums have been read)
+#pragma unroll
+    for (int b = 0; b < WB; ++b) red[w][b][l] = acc[b];
+    __syncthreads();
+    // wave b joins block b: lane (li, q) holds row li of the pass and weight
+    // rows n0 + 16 b + 4 q .. + 3, four consecutive output columns
+    const int64_t row = r0 + 16 * p + li, col = n0 + 16 * w + 4 * qg;
+    if (w < WB && row < r1 && col < N) {
+      const f32x4 v = ((red[0][w][l] + red[1][w][l]) + red[2][w][l]) + red[3][w][l];
+      if (OUT_BF16)
+        *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(c) + row * N + col) =
+            u32x2{f32_to_bf16_bits(v[0]) | (f32_to_bf16_bits(v[1]) << 16), f32_to_bf16_bits(v[2]) | (f32_to_bf16_bits(v[3]) << 16)};
+      else
+        *reinterpret_cast<f32x4*>(static_cast<float*>(c) + row * N + col) = v;
+    }
+  }
 }
 
 // ---------------------------------------------------------------- many rows
@@ -89,7 +204,6 @@ __device__ inline int swz(int row, int c) { return c ^ ((row >> 1) & 7); }
 constexpr int wait_vm(int n) { return (n & 15) | ((n >> 4) << 14) | (7 << 4) | (15 << 8); }
 constexpr int WAIT_LGKM0 = 15 | (3 << 14) | (7 << 4);
 constexpr int NT_STORE = 2;                // buffer-store cache policy: nontemporal
-constexpr uint32_t OOB = 0x80000000u;      // past every descriptor: loads return 0
 template <int TN, bool ALIGNED>
 struct Cfg {
   static constexpr int ND = ALIGNED ? 2 : 3;             // scale dwords per row and slab
@@ -364,15 +478,29 @@ static int cu_count() {
 template <bool OUT_BF16>
 static void launch_mx4(const uint8_t* ac, const uint8_t* as, const uint8_t* bc, const uint8_t* bs, const int32_t* off, int E,
                        int64_t M, int64_t N, int64_t K, void* c, hipStream_t s) {
+  const bool al = K % 128 == 0 && aligned4(as) && aligned4(bs);
   if (M <= 32 * (int64_t)E) {
-    const int n_nt = (int)((N + 63) / 64);
-    const int64_t m_tiles = (M + m4s::TR - 1) / m4s::TR + E;
-    hipLaunchKernelGGL(k_gemm_mx4_rows<OUT_BF16>, dim3((unsigned)(m_tiles * n_nt)), dim3(m4s::NT), 0, s, ac, as, bc, bs, off, E,
-                       M, N, K, n_nt, c);
+    const int64_t n_nt = (N + m4s::WROWS - 1) / m4s::WROWS, first = M < E ? M : E, slots = first + M / m4s::TR;
+    const dim3 grid((unsigned)(n_nt * slots));
+    const int64_t spw = ((K + m4s::KB - 1) / m4s::KB + m4s::NWV - 1) / m4s::NWV;
+#define MOE4_MX4S(AL, NS)                                                                                                      \
+  hipLaunchKernelGGL((k_gemm_mx4_rows<OUT_BF16, AL, NS>), grid, dim3(m4s::NT), 0, s, ac, as, bc, bs, off, E, M, N, K,           \
+                     (uint32_t)n_nt, first, c)
+#define MOE4_MX4S_AL(NS)            \
+  do {                              \
+    if (al) MOE4_MX4S(true, NS);    \
+    else MOE4_MX4S(false, NS);      \
+  } while (0)
+    if (spw <= 2) MOE4_MX4S_AL(2);
+    else if (spw == 3) MOE4_MX4S_AL(3);
+    else if (spw == 4) MOE4_MX4S_AL(4);
+    else if (spw <= 6) MOE4_MX4S_AL(6);
+    else MOE4_MX4S_AL(8);
+#undef MOE4_MX4S_AL
+#undef MOE4_MX4S
     return;
   }
   const dim3 grid((unsigned)(cu_count() < 8 ? 8 : cu_count()));
-  const bool al = K % 128 == 0 && aligned4(as) && aligned4(bs);
 #define MOE4_MX4(TN, AL)                                                                                                       \
   hipLaunchKernelGGL((k_gemm_mx4_ws<OUT_BF16, TN, AL>), grid, dim3(m4w::NT), 0, s, ac, as, bc, bs, off, E, M, N, K,             \
                      dg_split((N + TN - 1) / TN, m4w::TM, TN), c)
@@ -403,7 +531,7 @@ extern "C" int moe_grouped_gemm_mx4(const uint8_t* a_codes, const uint8_t* a_sf,
   MOE4_REQUIRE(aligned16(a_codes) && aligned16(b_codes) && aligned16(c), MOE4_EALIGN,
                "moe_grouped_gemm_mx4: a_codes, b_codes and c must be 16-byte aligned");
   if (M_total == 0) return MOE4_OK;
-  MOE4_REQUIRE(((M_total + m4s::TR - 1) / m4s::TR + E) * ((N + 63) / 64) < ((int64_t)1 << 31), MOE4_EINVAL,
+  MOE4_REQUIRE((M_total / m4s::TR + E) * ((N + m4s::WROWS - 1) / m4s::WROWS) < ((int64_t)1 << 31), MOE4_EINVAL,
                "moe_grouped_gemm_mx4: too large");
   if (c_dtype == MOE4_BF16)
     launch_mx4<true>(a_codes, a_sf, b_codes, b_sf, expert_off, E, M_total, N, K, c, as_stream(stream));
