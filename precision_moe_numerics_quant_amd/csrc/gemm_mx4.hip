@@ -189,9 +189,15 @@ __global__ void __launch_bounds__(m4s::NT)
 // Every load goes through a buffer descriptor that covers exactly the tile's
 // rows, so rows past the expert's last, past N, and K chunks past K (their
 // lanes' offsets are set out of range) arrive as zeros and no shape needs a
-// kernel of its own.  ALIGNED (K % 128 == 0, 4-byte aligned scale pointers):
-// a row's 8 scale bytes of a slab are two dwords; otherwise they lie in three
-// aligned dwords, and the consumer cuts its row's bytes out of them.
+// kernel of its own.
+//
+// Scales: a wave's load of 64 rows' scales touches 64 cache lines whatever it
+// takes from each, as long as four of its whole-row code loads, so the fewest
+// such loads win.  PAIR (K % 512 == 0, 16-byte aligned scales): one 16-byte
+// load per row brings two slabs' scales, into a ring of their own.  Otherwise
+// a 16-byte load per row and slab, from the dword that holds the first of its 8
+// scale bytes, and the consumer cuts them out (TN = 128 only: 256 columns with
+// a slab's scales in every stage do not fit the LDS).
 namespace m4w {
 constexpr int TM = 128, NCW = 4, NT = 64 * (NCW + 4);
 constexpr int BK = 256, ROW_B = BK / 2;  // K values and code bytes of a row and slab
@@ -200,35 +206,43 @@ typedef __attribute__((address_space(3))) void* lds_ptr;
 // a fragment read hit 16 distinct bank groups); applied through the global
 // address that each lane loads
 __device__ inline int swz(int row, int c) { return c ^ ((row >> 1) & 7); }
+// 16 bytes at each lane's offset into lane-consecutive LDS from p on
+__device__ __forceinline__ void load_lds(const __amdgpu_buffer_rsrc_t& rs, uint8_t* p, uint32_t off) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr)p, 16, off, 0, 0, 0);
+}
 // s_waitcnt immediates (vmcnt: bits 3:0 and 15:14; expcnt 6:4; lgkmcnt 11:8)
 constexpr int wait_vm(int n) { return (n & 15) | ((n >> 4) << 14) | (7 << 4) | (15 << 8); }
 constexpr int WAIT_LGKM0 = 15 | (3 << 14) | (7 << 4);
 constexpr int NT_STORE = 2;                // buffer-store cache policy: nontemporal
-template <int TN, bool ALIGNED>
+template <int TN, bool PAIR>
 struct Cfg {
-  static constexpr int ND = ALIGNED ? 2 : 3;             // scale dwords per row and slab
   static constexpr int CODE_A = TM * ROW_B, CODE_B = TN * ROW_B;
-  static constexpr int GRPS = (TM + TN) / 64;            // 64-row scale groups (A's first)
-  static constexpr int UNITS = GRPS * ND;                // their loads: [group][dword][64 rows]
-  static constexpr int STAGE = CODE_A + CODE_B + UNITS * 256;
+  static constexpr int GRPS = (TM + TN) / 64;            // 64-row scale groups (A's first), a load each
+  static constexpr int SCL = GRPS * 64 * 16;
+  static constexpr int STAGE = CODE_A + CODE_B + (PAIR ? 0 : SCL);
   static constexpr int S = TN == 128 ? 4 : 3;
-  static constexpr int QB = TN / 32;                     // B's 8-row code loads per producer
-  static constexpr int NU = (UNITS + 3) / 4;             // scale loads per producer
-  static constexpr int I = 4 + QB + NU;                  // all of them: what the waits count
-  static_assert(S * STAGE + 16 <= 160 * 1024, "LDS");
+  // PAIR: the scales of slabs 2 p and 2 p + 1 in buffer p % NP.  Slab j is
+  // requested after the barrier of slab j - S + 1, when slab j - S has been
+  // read: pair p + NP (slab 2 p + 2 NP) must come after slab 2 p + 1.
+  static constexpr int NP = PAIR ? (S + 2) / 2 : 0;
+  static_assert(!PAIR || 2 * NP - S >= 1, "pair ring");
+  static constexpr int RING = S * STAGE + NP * SCL;
+  static constexpr int IC = 4 + TN / 32;                 // code loads per producer and slab
+  static constexpr int NU = (GRPS + 3) / 4;              // scale loads per producer (PAIR: on even slabs)
+  static_assert(RING + 16 <= 160 * 1024, "LDS");
 };
 }  // namespace m4w
 
-template <bool OUT_BF16, int TN, bool ALIGNED>
+template <bool OUT_BF16, int TN, bool PAIR>
 __global__ void __launch_bounds__(m4w::NT, 1)
     k_gemm_mx4_ws(const uint8_t* __restrict__ a_codes, const uint8_t* __restrict__ a_sf,
                   const uint8_t* __restrict__ b_codes, const uint8_t* __restrict__ b_sf,
                   const int32_t* __restrict__ off, int E, int64_t M_total, int64_t N, int64_t K, DgSplit sp,
                   void* __restrict__ c) {
   using namespace m4w;
-  using C = Cfg<TN, ALIGNED>;
-  constexpr int S = C::S, STAGE = C::STAGE, I = C::I, ND = C::ND;
-  __shared__ __attribute__((aligned(16))) uint8_t ring[S * STAGE];
+  using C = Cfg<TN, PAIR>;
+  constexpr int S = C::S, STAGE = C::STAGE, QB = TN / 32;
+  __shared__ __attribute__((aligned(16))) uint8_t ring[C::RING];
   __shared__ uint32_t s_nmt;
   const int tid = threadIdx.x, l = tid & 63;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -251,7 +265,7 @@ __global__ void __launch_bounds__(m4w::NT, 1)
   const uint32_t sm = (8 / sp.xb) * sp.pm, q_end = (n_mt + sm - 1) / sm * (sp.pm * sp.pn);
 
   if (w >= NCW) {
-    // ---- producer pw: 8-row code loads 4 pw .. of A and QB pw .. of B, scale units NU pw ..
+    // ---- producer pw: 8-row code loads 4 pw .. of A and QB pw .. of B, scale groups NU pw ..
     const int pw = w - NCW;
     __amdgpu_buffer_rsrc_t rac = make_rsrc(a_codes, 0), ras = rac, rbc = rac, rbs = rac;
     uint32_t ax = 0, bx = 0;       // the scale descriptors' bytes ahead of the tile's first
@@ -273,43 +287,41 @@ __global__ void __launch_bounds__(m4w::NT, 1)
       rbc = make_rsrc(b_codes + rowb * KH, (uint64_t)rb * KH);
       const uint8_t* as = a_sf + row0 * KS;
       const uint8_t* bs = b_sf + rowb * KS;
-      if (!ALIGNED) {  // (whole dwords that hold a byte of the rows: never past their page)
-        ax = (uint32_t)reinterpret_cast<uintptr_t>(as) & 3u;
-        bx = (uint32_t)reinterpret_cast<uintptr_t>(bs) & 3u;
-      }
-      ras = make_rsrc(as - ax, ra ? ((uint64_t)ra * KS + ax + 3) / 4 * 4 : 0);
-      rbs = make_rsrc(bs - bx, ((uint64_t)rb * KS + bx + 3) / 4 * 4);
+      ras = dword_rsrc(as, (uint64_t)ra * KS, ax);
+      rbs = dword_rsrc(bs, (uint64_t)rb * KS, bx);
       ps = 0;
     };
     seek();
-    auto issue = [&](int st) {
-      uint8_t* base = ring + st * STAGE;
+    auto issue = [&](uint32_t j) {  // slab j of this workgroup
+      uint8_t* base = ring + (j % S) * STAGE;
       const uint32_t kb = ps * (uint32_t)ROW_B, left = KS - 8 * ps;  // chunks of the row from this slab on
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const int r = 32 * pw + 8 * q + (l >> 3);
         const uint32_t ch = (uint32_t)swz(r, l & 7);
         const uint32_t o = ch < left ? (uint32_t)r * KH + 16u * ch + kb : OOB;
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rac, (lds_ptr)(base + (4 * pw + q) * 1024), 16, o, 0, 0, 0);
+        load_lds(rac, base + (4 * pw + q) * 1024, o);
       }
 #pragma unroll
-      for (int q = 0; q < C::QB; ++q) {
+      for (int q = 0; q < QB; ++q) {
         const int r = (TN / 4) * pw + 8 * q + (l >> 3);
         const uint32_t ch = (uint32_t)swz(r, l & 7);
         const uint32_t o = ch < left ? (uint32_t)r * KH + 16u * ch + kb : OOB;
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rbc, (lds_ptr)(base + C::CODE_A + (C::QB * pw + q) * 1024), 16, o, 0, 0, 0);
+        load_lds(rbc, base + C::CODE_A + (QB * pw + q) * 1024, o);
       }
+      if (!PAIR || (ps & 1) == 0) {
+        uint8_t* sl = PAIR ? ring + S * STAGE + ((j >> 1) % (PAIR ? C::NP : 1)) * C::SCL : base + C::CODE_A + C::CODE_B;
 #pragma unroll
-      for (int k = 0; k < C::NU; ++k) {
-        int u = C::NU * pw + k;
-        u = u < C::UNITS ? u : C::UNITS - 1;  // (the last unit again: every producer issues I loads)
-        const int grp = u / ND, d = u - grp * ND;
-        uint8_t* sb = base + C::CODE_A + C::CODE_B + u * 256;
-        const bool opa = grp < TM / 64;
-        const uint32_t r = (uint32_t)(opa ? 64 * grp : 64 * grp - TM) + l;
-        const uint32_t o = (((opa ? ax : bx) + r * KS + 8 * ps) & ~3u) + 4 * d;
-        if (opa) __builtin_amdgcn_raw_ptr_buffer_load_lds(ras, (lds_ptr)sb, 4, o, 0, 0, 0);
-        else __builtin_amdgcn_raw_ptr_buffer_load_lds(rbs, (lds_ptr)sb, 4, o, 0, 0, 0);
+        for (int k = 0; k < C::NU; ++k) {
+          int grp = C::NU * pw + k;
+          grp = grp < C::GRPS ? grp : C::GRPS - 1;  // (the last group again: every producer issues as many loads)
+          uint8_t* sb = sl + grp * 1024;
+          const bool opa = grp < TM / 64;
+          const uint32_t r = (uint32_t)(opa ? 64 * grp : 64 * grp - TM) + l;
+          const uint32_t o = ((opa ? ax : bx) + r * KS + 8 * ps) & ~3u;
+          if (opa) load_lds(ras, sb, o);
+          else load_lds(rbs, sb, o);
+        }
       }
       if (++ps == nk) {
         pt += stride;
@@ -317,24 +329,20 @@ __global__ void __launch_bounds__(m4w::NT, 1)
       }
     };
     uint32_t n_iss = 0;
-    for (int st = 0; st < S - 1 && more; ++st) {
-      issue(st);
-      ++n_iss;
-    }
+    for (int st = 0; st < S - 1 && more; ++st) issue(n_iss++);
     for (uint32_t gs = 0; gs < n_iss; ++gs) {
-      // slab gs landed (later slabs may still be in flight), then the barrier
+      // slab gs landed (the loads of the rem later ones may still be in
+      // flight: PAIR has a slab's scale loads on every second one), then the barrier
       const uint32_t rem = n_iss - 1 - gs;
       __builtin_amdgcn_sched_barrier(0);
-      if (rem >= 2) __builtin_amdgcn_s_waitcnt(wait_vm(2 * I));
-      else if (rem == 1) __builtin_amdgcn_s_waitcnt(wait_vm(I));
+      if (rem >= 2) __builtin_amdgcn_s_waitcnt(wait_vm(2 * C::IC + (PAIR ? 1 : 2) * C::NU));
+      else if (rem == 1 && PAIR && (gs & 1) == 0) __builtin_amdgcn_s_waitcnt(wait_vm(C::IC));
+      else if (rem == 1) __builtin_amdgcn_s_waitcnt(wait_vm(C::IC + C::NU));
       else __builtin_amdgcn_s_waitcnt(wait_vm(0));
       __builtin_amdgcn_s_barrier();
       __builtin_amdgcn_sched_barrier(0);
       asm volatile("" ::: "memory");
-      if (more) {
-        issue((int)((gs + S - 1) % S));
-        ++n_iss;
-      }
+      if (more) issue(n_iss++);
     }
     return;
   }
@@ -347,25 +355,29 @@ __global__ void __launch_bounds__(m4w::NT, 1)
   for (int i = 0; i < MI; ++i)
 #pragma unroll
     for (int j = 0; j < NJ; ++j) acc[i][j] = f32x16{};
-  uint32_t sha[MI], shb[NJ];  // !ALIGNED: the rows' first scale byte in its dword
+  uint32_t sha[MI], shb[NJ];  // !PAIR: the rows' first scale byte in its dword
   // one slab: four 64-value k steps; lane half g supplies K block 2 ks + g and
   // its scale, byte 2 (ks % 2) of the row's scale dword ks / 2 shifted by g
   // bytes.  left: scale blocks from this slab on (fewer than 8: the rest 0)
-  auto compute = [&](const uint8_t* base, uint32_t left) {
-    const uint8_t* la = base;
-    const uint8_t* lb = base + C::CODE_A;
-    const uint8_t* sc = base + C::CODE_A + C::CODE_B;
+  auto compute = [&](uint32_t j, uint32_t left) {
+    const uint8_t* la = ring + (j % S) * STAGE;
+    const uint8_t* lb = la + C::CODE_A;
+    const uint8_t* sc = PAIR ? ring + S * STAGE + ((j >> 1) % (PAIR ? C::NP : 1)) * C::SCL + 8 * (j & 1) : lb + C::CODE_B;
     auto scales = [&](int r, uint32_t sh, uint32_t (&y)[2]) {  // r: row of A, or TM + row of B
-      const uint8_t* p = sc + (r >> 6) * (ND * 256) + (r & 63) * 4;
-      uint32_t d0 = *reinterpret_cast<const uint32_t*>(p), d1 = *reinterpret_cast<const uint32_t*>(p + 256);
-      if (!ALIGNED) {
-        const uint32_t d2 = *reinterpret_cast<const uint32_t*>(p + (ND - 1) * 256);
-        d0 = __builtin_amdgcn_alignbyte(d1, d0, sh);
-        d1 = __builtin_amdgcn_alignbyte(d2, d1, sh);
-      }
-      if (left < 8) {  // (uniform; a slab that ends inside the row's last blocks)
-        d0 &= left >= 4 ? ~0u : (1u << (8 * left)) - 1u;
-        d1 &= left > 4 ? (1u << (8 * (left - 4))) - 1u : 0u;
+      const uint8_t* p = sc + r * 16;
+      uint32_t d0, d1;
+      if (PAIR) {
+        const u32x2 d = *reinterpret_cast<const u32x2*>(p);
+        d0 = d[0];
+        d1 = d[1];
+      } else {
+        const u32x4 q = *reinterpret_cast<const u32x4*>(p);
+        d0 = __builtin_amdgcn_alignbyte(q[1], q[0], sh);
+        d1 = __builtin_amdgcn_alignbyte(q[2], q[1], sh);
+        if (left < 8) {  // (uniform; a slab that ends inside the row's last blocks)
+          d0 &= left >= 4 ? ~0u : (1u << (8 * left)) - 1u;
+          d1 &= left > 4 ? (1u << (8 * (left - 4))) - 1u : 0u;
+        }
       }
       y[0] = d0 >> (8 * g);
       y[1] = d1 >> (8 * g);
@@ -418,7 +430,7 @@ __global__ void __launch_bounds__(m4w::NT, 1)
     const int64_t row_end = (int64_t)ld_const(off, e + 1) < M_total ? (int64_t)ld_const(off, e + 1) : M_total;
     // waves whose rows or columns all lie past the tile's last skip their MFMAs
     const bool active = row0 >= 0 && row0 + wm < row_end && n0 + wn < N;
-    if (!ALIGNED) {
+    if (!PAIR) {
 #pragma unroll
       for (int i = 0; i < MI; ++i)
         sha[i] = (uint32_t)(reinterpret_cast<uintptr_t>(a_sf) + (uint64_t)(row0 + wm + 32 * i + li) * KS) & 3u;
@@ -432,7 +444,7 @@ __global__ void __launch_bounds__(m4w::NT, 1)
       __builtin_amdgcn_s_barrier();
       __builtin_amdgcn_sched_barrier(0);
       asm volatile("" ::: "memory");
-      if (active) compute(ring + (gs % S) * STAGE, KS - 8 * s);
+      if (active) compute(gs, KS - 8 * s);
     }
     // epilogue: each value straight from the accumulators; the descriptor
     // covers the tile's rows up to the expert's last, so stores of rows past
@@ -501,16 +513,13 @@ static void launch_mx4(const uint8_t* ac, const uint8_t* as, const uint8_t* bc, 
     return;
   }
   const dim3 grid((unsigned)(cu_count() < 8 ? 8 : cu_count()));
+  const bool pair = K % 512 == 0 && aligned16(as) && aligned16(bs);
 #define MOE4_MX4(TN, AL)                                                                                                       \
   hipLaunchKernelGGL((k_gemm_mx4_ws<OUT_BF16, TN, AL>), grid, dim3(m4w::NT), 0, s, ac, as, bc, bs, off, E, M, N, K,             \
                      dg_split((N + TN - 1) / TN, m4w::TM, TN), c)
-  if (N % 256 == 0 || N > 512) {
-    if (al) MOE4_MX4(256, true);
-    else MOE4_MX4(256, false);
-  } else {
-    if (al) MOE4_MX4(128, true);
-    else MOE4_MX4(128, false);
-  }
+  if (!pair) MOE4_MX4(128, false);
+  else if (N % 256 == 0 || N > 512) MOE4_MX4(256, true);
+  else MOE4_MX4(128, true);
 #undef MOE4_MX4
 }
 
