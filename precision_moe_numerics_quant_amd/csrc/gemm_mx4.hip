@@ -210,6 +210,10 @@ __device__ inline int swz(int row, int c) { return c ^ ((row >> 1) & 7); }
 __device__ __forceinline__ void load_lds(const __amdgpu_buffer_rsrc_t& rs, uint8_t* p, uint32_t off) {
   __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr)p, 16, off, 0, 0, 0);
 }
+// Row R of B's tile in LDS is row n of the tile in memory: the MFMA columns of
+// two neighbouring 32-row blocks are even and odd rows of B, so that a lane's
+// two values of an output row are neighbours and 32 lanes store whole lines
+__device__ inline int bmap(int R) { return (R & ~63) + 2 * (R & 31) + ((R >> 5) & 1); }
 // s_waitcnt immediates (vmcnt: bits 3:0 and 15:14; expcnt 6:4; lgkmcnt 11:8)
 constexpr int wait_vm(int n) { return (n & 15) | ((n >> 4) << 14) | (7 << 4) | (15 << 8); }
 constexpr int WAIT_LGKM0 = 15 | (3 << 14) | (7 << 4);
@@ -306,7 +310,7 @@ __global__ void __launch_bounds__(m4w::NT, 1)
       for (int q = 0; q < QB; ++q) {
         const int r = (TN / 4) * pw + 8 * q + (l >> 3);
         const uint32_t ch = (uint32_t)swz(r, l & 7);
-        const uint32_t o = ch < left ? (uint32_t)r * KH + 16u * ch + kb : OOB;
+        const uint32_t o = ch < left ? (uint32_t)bmap(r) * KH + 16u * ch + kb : OOB;
         load_lds(rbc, base + C::CODE_A + (QB * pw + q) * 1024, o);
       }
       if (!PAIR || (ps & 1) == 0) {
@@ -317,7 +321,7 @@ __global__ void __launch_bounds__(m4w::NT, 1)
           grp = grp < C::GRPS ? grp : C::GRPS - 1;  // (the last group again: every producer issues as many loads)
           uint8_t* sb = sl + grp * 1024;
           const bool opa = grp < TM / 64;
-          const uint32_t r = (uint32_t)(opa ? 64 * grp : 64 * grp - TM) + l;
+          const uint32_t r = opa ? 64 * grp + l : bmap(64 * grp - TM + l);
           const uint32_t o = ((opa ? ax : bx) + r * KS + 8 * ps) & ~3u;
           if (opa) load_lds(ras, sb, o);
           else load_lds(rbs, sb, o);
@@ -418,7 +422,7 @@ __global__ void __launch_bounds__(m4w::NT, 1)
   };
   constexpr int ESZ = OUT_BF16 ? 2 : 4;
   const uint32_t ld = (uint32_t)N * ESZ;  // output row pitch in bytes
-  const uint32_t lane_off = (uint32_t)(g * 4) * ld + (uint32_t)li * ESZ;
+  const uint32_t lane_off = (uint32_t)(g * 4) * ld + (uint32_t)li * (2 * ESZ);
   MtCursor<TM> cur;
   uint32_t gs = 0;
   for (uint32_t q = q0; q < q_end; q += stride) {
@@ -436,7 +440,7 @@ __global__ void __launch_bounds__(m4w::NT, 1)
         sha[i] = (uint32_t)(reinterpret_cast<uintptr_t>(a_sf) + (uint64_t)(row0 + wm + 32 * i + li) * KS) & 3u;
 #pragma unroll
       for (int j = 0; j < NJ; ++j)
-        shb[j] = (uint32_t)(reinterpret_cast<uintptr_t>(b_sf) + (uint64_t)((int64_t)e * N + n0 + wn + 32 * j + li) * KS) & 3u;
+        shb[j] = (uint32_t)(reinterpret_cast<uintptr_t>(b_sf) + (uint64_t)((int64_t)e * N + n0 + bmap(wn + 32 * j + li)) * KS) & 3u;
     }
     for (uint32_t s = 0; s < nk; ++s, ++gs) {
       __builtin_amdgcn_sched_barrier(0);
@@ -446,25 +450,27 @@ __global__ void __launch_bounds__(m4w::NT, 1)
       asm volatile("" ::: "memory");
       if (active) compute(gs, KS - 8 * s);
     }
-    // epilogue: each value straight from the accumulators; the descriptor
-    // covers the tile's rows up to the expert's last, so stores of rows past
-    // it are dropped
+    // epilogue: straight from the accumulators, a whole 128- or 256-byte row
+    // segment from 32 lanes (bmap); the descriptor covers the tile's rows up to
+    // the expert's last, so stores of rows past it are dropped
     if (active) {
       const int64_t nrows = row_end - row0 < TM ? row_end - row0 : TM;
       const __amdgpu_buffer_rsrc_t rC = make_rsrc(static_cast<uint8_t*>(c) + row0 * (int64_t)ld, (uint64_t)nrows * ld);
 #pragma unroll
       for (int i = 0; i < MI; ++i)
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) {
-          if (n0 + wn + 32 * j >= N) continue;  // (uniform; N % 32 == 0)
-          const uint32_t fo = (uint32_t)(wm + i * 32) * ld + (uint32_t)(n0 + wn + j * 32) * ESZ;
+        for (int j = 0; j < NJ; j += 2) {  // columns n0 + wn + 32 j + 2 li, + 1
+          const int64_t c0 = n0 + wn + 32 * j;
+          if (c0 >= N) continue;  // (uniform)
+          const uint32_t vo = c0 + 2 * li < N ? lane_off : OOB;  // (N % 32 == 0: half a column group may be past N)
+          const uint32_t fo = (uint32_t)(wm + i * 32) * ld + (uint32_t)c0 * ESZ;
 #pragma unroll
           for (int v = 0; v < 16; ++v) {
             const uint32_t so = fo + (uint32_t)((v >> 2) * 8 + (v & 3)) * ld;
+            const float v0 = acc[i][j][v], v1 = acc[i][j + 1][v];
             if (OUT_BF16)
-              __builtin_amdgcn_raw_buffer_store_b16((unsigned short)f32_to_bf16_bits(acc[i][j][v]), rC, lane_off, so, NT_STORE);
+              __builtin_amdgcn_raw_buffer_store_b32(f32_to_bf16_bits(v0) | (f32_to_bf16_bits(v1) << 16), rC, vo, so, NT_STORE);
             else
-              __builtin_amdgcn_raw_buffer_store_b32(__float_as_uint(acc[i][j][v]), rC, lane_off, so, NT_STORE);
+              __builtin_amdgcn_raw_buffer_store_b64(u32x2{__float_as_uint(v0), __float_as_uint(v1)}, rC, vo, so, NT_STORE);
           }
         }
     }
