@@ -2,6 +2,8 @@
 // e] . B[e]^T on the block-scaled FP4 MFMA, whose E8M0 scale per 32 values
 // along K is exactly MXFP4's.  Products of two E2M1 values and their power-of-
 // two scales are exact; the accumulation is float32.
+#include <type_traits>
+
 #include "gemm_common.h"
 #include "moe4_internal.h"
 
@@ -206,9 +208,9 @@ typedef __attribute__((address_space(3))) void* lds_ptr;
 // a fragment read hit 16 distinct bank groups); applied through the global
 // address that each lane loads
 __device__ inline int swz(int row, int c) { return c ^ ((row >> 1) & 7); }
-// 16 bytes at each lane's offset into lane-consecutive LDS from p on
-__device__ __forceinline__ void load_lds(const __amdgpu_buffer_rsrc_t& rs, uint8_t* p, uint32_t off) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr)p, 16, off, 0, 0, 0);
+// 16 bytes at each lane's offset + soff into lane-consecutive LDS from p on
+__device__ __forceinline__ void load_lds(const __amdgpu_buffer_rsrc_t& rs, uint8_t* p, uint32_t off, uint32_t soff) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr)p, 16, off, soff, 0, 0);
 }
 // Row R of B's tile in LDS is row n of the tile in memory: the MFMA columns of
 // two neighbouring 32-row blocks are even and odd rows of B, so that a lane's
@@ -296,35 +298,44 @@ __global__ void __launch_bounds__(m4w::NT, 1)
       ps = 0;
     };
     seek();
+    // each load's offset into its descriptor at K = 0: the same for every tile
+    // (the slab's offset goes in the scalar operand)
+    uint32_t aoff[4], boff[8], soff[2];
+    uint32_t chunk[2];  // the logical chunk of this lane in rows 0-7 and 8-15 of every 16
+#pragma unroll
+    for (int q = 0; q < 2; ++q) chunk[q] = (uint32_t)swz(8 * q + (l >> 3), l & 7);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) aoff[q] = (uint32_t)(32 * pw + 8 * q + (l >> 3)) * KH + 16u * chunk[q & 1];
+#pragma unroll
+    for (int q = 0; q < QB; ++q) boff[q] = (uint32_t)bmap((TN / 4) * pw + 8 * q + (l >> 3)) * KH + 16u * chunk[q & 1];
+    auto sgrp = [&](int k) {  // scale group k of this wave (the last one again: every producer issues as many loads)
+      const int grp = C::NU * pw + k;
+      return grp < C::GRPS ? grp : C::GRPS - 1;
+    };
+#pragma unroll
+    for (int k = 0; k < C::NU; ++k) {
+      const int grp = sgrp(k);
+      soff[k] = (uint32_t)(grp < TM / 64 ? 64 * grp + l : bmap(64 * grp - TM + l)) * KS;
+    }
     auto issue = [&](uint32_t j) {  // slab j of this workgroup
       uint8_t* base = ring + (j % S) * STAGE;
       const uint32_t kb = ps * (uint32_t)ROW_B, left = KS - 8 * ps;  // chunks of the row from this slab on
+      // (PAIR: whole slabs only)
+      auto at = [&](uint32_t o, int q) { return PAIR || chunk[q & 1] < left ? o : OOB; };
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int r = 32 * pw + 8 * q + (l >> 3);
-        const uint32_t ch = (uint32_t)swz(r, l & 7);
-        const uint32_t o = ch < left ? (uint32_t)r * KH + 16u * ch + kb : OOB;
-        load_lds(rac, base + (4 * pw + q) * 1024, o);
-      }
+      for (int q = 0; q < 4; ++q) load_lds(rac, base + (4 * pw + q) * 1024, at(aoff[q], q), kb);
 #pragma unroll
-      for (int q = 0; q < QB; ++q) {
-        const int r = (TN / 4) * pw + 8 * q + (l >> 3);
-        const uint32_t ch = (uint32_t)swz(r, l & 7);
-        const uint32_t o = ch < left ? (uint32_t)bmap(r) * KH + 16u * ch + kb : OOB;
-        load_lds(rbc, base + C::CODE_A + (QB * pw + q) * 1024, o);
-      }
+      for (int q = 0; q < QB; ++q) load_lds(rbc, base + C::CODE_A + (QB * pw + q) * 1024, at(boff[q], q), kb);
       if (!PAIR || (ps & 1) == 0) {
         uint8_t* sl = PAIR ? ring + S * STAGE + ((j >> 1) % (PAIR ? C::NP : 1)) * C::SCL : base + C::CODE_A + C::CODE_B;
 #pragma unroll
         for (int k = 0; k < C::NU; ++k) {
-          int grp = C::NU * pw + k;
-          grp = grp < C::GRPS ? grp : C::GRPS - 1;  // (the last group again: every producer issues as many loads)
+          const int grp = sgrp(k);
           uint8_t* sb = sl + grp * 1024;
           const bool opa = grp < TM / 64;
-          const uint32_t r = opa ? 64 * grp + l : bmap(64 * grp - TM + l);
-          const uint32_t o = ((opa ? ax : bx) + r * KS + 8 * ps) & ~3u;
-          if (opa) load_lds(ras, sb, o);
-          else load_lds(rbs, sb, o);
+          const uint32_t o = PAIR ? soff[k] : ((opa ? ax : bx) + soff[k]) & ~3u;  // (8 ps is whole dwords)
+          if (opa) load_lds(ras, sb, o, 8 * ps);
+          else load_lds(rbs, sb, o, 8 * ps);
         }
       }
       if (++ps == nk) {
@@ -348,6 +359,7 @@ __global__ void __launch_bounds__(m4w::NT, 1)
       asm volatile("" ::: "memory");
       if (more) issue(n_iss++);
     }
+    __builtin_amdgcn_s_barrier();  // (the consumers' barrier after their last slab)
     return;
   }
   // ---- consumers: wave w owns the 64 x (TN / 2) block (w / 2, w % 2)
@@ -360,24 +372,48 @@ __global__ void __launch_bounds__(m4w::NT, 1)
 #pragma unroll
     for (int j = 0; j < NJ; ++j) acc[i][j] = f32x16{};
   uint32_t sha[MI], shb[NJ];  // !PAIR: the rows' first scale byte in its dword
-  // one slab: four 64-value k steps; lane half g supplies K block 2 ks + g and
+  // A slab is four 64-value k steps.  Lane half g supplies K block 2 ks + g and
   // its scale, byte 2 (ks % 2) of the row's scale dword ks / 2 shifted by g
-  // bytes.  left: scale blocks from this slab on (fewer than 8: the rest 0)
-  auto compute = [&](uint32_t j, uint32_t left) {
-    const uint8_t* la = ring + (j % S) * STAGE;
-    const uint8_t* lb = la + C::CODE_A;
-    const uint8_t* sc = PAIR ? ring + S * STAGE + ((j >> 1) % (PAIR ? C::NP : 1)) * C::SCL + 8 * (j & 1) : lb + C::CODE_B;
-    auto scales = [&](int r, uint32_t sh, uint32_t (&y)[2]) {  // r: row of A, or TM + row of B
-      const uint8_t* p = sc + r * 16;
-      uint32_t d0, d1;
-      if (PAIR) {
-        const u32x2 d = *reinterpret_cast<const u32x2*>(p);
-        d0 = d[0];
-        d1 = d[1];
-      } else {
-        const u32x4 q = *reinterpret_cast<const u32x4*>(p);
+  // bytes.  With one consumer wave per SIMD nothing else hides the LDS
+  // latency, so the next step's fragments are read before the MFMAs of this
+  // one, across slabs and tiles too: the last step of a slab runs after the next
+  // slab's barrier (its fragments are in registers by then).  After the last
+  // slab of all that barrier is an extra one and the reads are of no use.
+  i32x4 fa[2][MI], fb[2][NJ];      // the fragments of even and odd steps
+  uint32_t ya[MI][2], yb[NJ][2];   // the slab's scales
+  // chunk 2 ks + g of a row sits at chunk (g ^ swizzle) ^ 2 ks: one lane offset,
+  // its k steps by an XOR (kept opaque: as loop invariants they would fill the
+  // registers that the accumulators need)
+  uint32_t lx = (uint32_t)li * ROW_B + 16u * (uint32_t)swz(li, g);
+  auto frags = [&](uint32_t j, int ks) {
+    const uint8_t* st = ring + (j % S) * STAGE;
+    const uint32_t o = lx ^ (32u * ks);
+    const uint8_t* la = st + wm * ROW_B + o;
+    const uint8_t* lb = st + C::CODE_A + wn * ROW_B + o;
+#pragma unroll
+    for (int i = 0; i < MI; ++i) fa[ks & 1][i] = *reinterpret_cast<const i32x4*>(la + 32 * i * ROW_B);
+#pragma unroll
+    for (int n = 0; n < NJ; ++n) fb[ks & 1][n] = *reinterpret_cast<const i32x4*>(lb + 32 * n * ROW_B);
+  };
+  // the raw scales of slab j (row r of A, or TM + row of B), and from those
+  // ya, yb; left: scale blocks from the slab on (fewer than 8: the rest 0)
+  using Raw = typename std::conditional<PAIR, u32x2, u32x4>::type;
+  Raw ra[MI], rb[NJ];
+  auto scales = [&](uint32_t j) {
+    const uint8_t* sc = PAIR ? ring + S * STAGE + ((j >> 1) % (PAIR ? C::NP : 1)) * C::SCL + 8 * (j & 1)
+                             : ring + (j % S) * STAGE + C::CODE_A + C::CODE_B;
+    auto get = [&](int r) { return *reinterpret_cast<const Raw*>(sc + r * 16); };
+#pragma unroll
+    for (int i = 0; i < MI; ++i) ra[i] = get(wm + 32 * i + li);
+#pragma unroll
+    for (int n = 0; n < NJ; ++n) rb[n] = get(TM + wn + 32 * n + li);
+  };
+  auto set_scales = [&](uint32_t left) {
+    auto put = [&](const Raw& q, uint32_t sh, uint32_t (&y)[2]) {
+      uint32_t d0 = q[0], d1 = q[1];
+      if (!PAIR) {
         d0 = __builtin_amdgcn_alignbyte(q[1], q[0], sh);
-        d1 = __builtin_amdgcn_alignbyte(q[2], q[1], sh);
+        d1 = __builtin_amdgcn_alignbyte(q[PAIR ? 1 : 2], q[1], sh);
         if (left < 8) {  // (uniform; a slab that ends inside the row's last blocks)
           d0 &= left >= 4 ? ~0u : (1u << (8 * left)) - 1u;
           d1 &= left > 4 ? (1u << (8 * (left - 4))) - 1u : 0u;
@@ -386,45 +422,46 @@ __global__ void __launch_bounds__(m4w::NT, 1)
       y[0] = d0 >> (8 * g);
       y[1] = d1 >> (8 * g);
     };
-    uint32_t ya[MI][2], yb[NJ][2];
 #pragma unroll
-    for (int i = 0; i < MI; ++i) scales(wm + 32 * i + li, sha[i], ya[i]);
+    for (int i = 0; i < MI; ++i) put(ra[i], sha[i], ya[i]);
 #pragma unroll
-    for (int j = 0; j < NJ; ++j) scales(TM + wn + 32 * j + li, shb[j], yb[j]);
+    for (int n = 0; n < NJ; ++n) put(rb[n], shb[n], yb[n]);
+  };
+  auto mfmas = [&](int ks) {
 #pragma unroll
-    for (int ks = 0; ks < 4; ++ks) {
-      i32x4 fa[MI], fb[NJ];
+    for (int i = 0; i < MI; ++i)
 #pragma unroll
-      for (int i = 0; i < MI; ++i) {
-        const int r = wm + 32 * i + li;
-        fa[i] = *reinterpret_cast<const i32x4*>(la + r * ROW_B + 16 * swz(r, 2 * ks + g));
+      for (int n = 0; n < NJ; ++n) {
+        const i32x8 xa = __builtin_shufflevector(fa[ks & 1][i], fa[ks & 1][i], 0, 1, 2, 3, -1, -1, -1, -1);
+        const i32x8 xb = __builtin_shufflevector(fb[ks & 1][n], fb[ks & 1][n], 0, 1, 2, 3, -1, -1, -1, -1);
+        // (the byte selector is an immediate)
+        if (ks & 1)
+          acc[i][n] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(xa, xb, acc[i][n], FP4, FP4, 2, (int)ya[i][ks >> 1], 2,
+                                                                      (int)yb[n][ks >> 1]);
+        else
+          acc[i][n] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(xa, xb, acc[i][n], FP4, FP4, 0, (int)ya[i][ks >> 1], 0,
+                                                                      (int)yb[n][ks >> 1]);
       }
-#pragma unroll
-      for (int j = 0; j < NJ; ++j) {
-        const int r = wn + 32 * j + li;
-        fb[j] = *reinterpret_cast<const i32x4*>(lb + r * ROW_B + 16 * swz(r, 2 * ks + g));
-      }
-#pragma unroll
-      for (int i = 0; i < MI; ++i)
-#pragma unroll
-        for (int j = 0; j < NJ; ++j) {
-          const i32x8 xa = __builtin_shufflevector(fa[i], fa[i], 0, 1, 2, 3, -1, -1, -1, -1);
-          const i32x8 xb = __builtin_shufflevector(fb[j], fb[j], 0, 1, 2, 3, -1, -1, -1, -1);
-          // (the byte selector is an immediate)
-          if (ks & 1)
-            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(xa, xb, acc[i][j], FP4, FP4, 2, (int)ya[i][ks >> 1], 2,
-                                                                        (int)yb[j][ks >> 1]);
-          else
-            acc[i][j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(xa, xb, acc[i][j], FP4, FP4, 0, (int)ya[i][ks >> 1], 0,
-                                                                        (int)yb[j][ks >> 1]);
-        }
-    }
+  };
+  auto barrier = [&]() {  // this wave's reads of the slab before are done
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_waitcnt(WAIT_LGKM0);
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("" ::: "memory");
   };
   constexpr int ESZ = OUT_BF16 ? 2 : 4;
   const uint32_t ld = (uint32_t)N * ESZ;  // output row pitch in bytes
   const uint32_t lane_off = (uint32_t)(g * 4) * ld + (uint32_t)li * (2 * ESZ);
   MtCursor<TM> cur;
   uint32_t gs = 0;
+#pragma unroll
+  for (int i = 0; i < MI; ++i) sha[i] = 0;
+#pragma unroll
+  for (int n = 0; n < NJ; ++n) shb[n] = 0;
+  barrier();
+  scales(0);
+  frags(0, 0);
   for (uint32_t q = q0; q < q_end; q += stride) {
     uint32_t mi, nt;
     if (!sp.tile(xcd, q, n_mt, n_nt, mi, nt)) continue;
@@ -442,18 +479,34 @@ __global__ void __launch_bounds__(m4w::NT, 1)
       for (int j = 0; j < NJ; ++j)
         shb[j] = (uint32_t)(reinterpret_cast<uintptr_t>(b_sf) + (uint64_t)((int64_t)e * N + n0 + bmap(wn + 32 * j + li)) * KS) & 3u;
     }
-    for (uint32_t s = 0; s < nk; ++s, ++gs) {
+    if (!active) {
+      for (uint32_t s = 0; s < nk; ++s, ++gs) barrier();
+      scales(gs);
+      frags(gs, 0);
+      continue;
+    }
+    set_scales(KS);
+    for (uint32_t s = 0; s < nk; ++s, ++gs) {  // (one basic block: the MFMAs stay between their reads)
+      asm volatile("" : "+v"(lx));
+#pragma unroll
+      for (int ks = 0; ks < 3; ++ks) {
+        frags(gs, ks + 1);
+        __builtin_amdgcn_sched_barrier(0);
+        mfmas(ks);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      barrier();
+      scales(gs + 1);
+      frags(gs + 1, 0);
       __builtin_amdgcn_sched_barrier(0);
-      __builtin_amdgcn_s_waitcnt(WAIT_LGKM0);
-      __builtin_amdgcn_s_barrier();
+      mfmas(3);
       __builtin_amdgcn_sched_barrier(0);
-      asm volatile("" ::: "memory");
-      if (active) compute(gs, KS - 8 * s);
+      set_scales(KS - 8 * (s + 1));  // (after the tile's last slab: set again for the next tile)
     }
     // epilogue: straight from the accumulators, a whole 128- or 256-byte row
     // segment from 32 lanes (bmap); the descriptor covers the tile's rows up to
     // the expert's last, so stores of rows past it are dropped
-    if (active) {
+    {
       const int64_t nrows = row_end - row0 < TM ? row_end - row0 : TM;
       const __amdgpu_buffer_rsrc_t rC = make_rsrc(static_cast<uint8_t*>(c) + row0 * (int64_t)ld, (uint64_t)nrows * ld);
 #pragma unroll
