@@ -702,8 +702,9 @@ size_t moe_router_wgrad_ws_bytes(int64_t T, int32_t E, int32_t k, int64_t d);
  * loss [n_seg], counts [n_seg, E] int32, tokens [n_seg] int32 (n_s), probs
  * [n_seg, E].  Sums over tokens in float32 in a fixed order (deterministic).
  * Indices outside [0, E) are clamped and reported (MOE4_DEVERR_INDEX).
- * 1 <= k <= min(E, 16), E <= 1024.  ws: moe_balance_loss_ws_bytes(T, E, n_seg),
- * the caller's, overwritten.
+ * 1 <= k <= min(E, 16), E <= 1024, n_seg <= 65535.
+ * ws: moe_balance_loss_ws_bytes(T, E, n_seg), the caller's, overwritten; calls
+ * in flight at the same time need workspaces of their own.
  */
 int moe_balance_loss(const float* logits, const float* bias, const int32_t* topk_idx, const uint8_t* token_mask,
                      const int32_t* seg_off, int32_t n_seg, int64_t T, int32_t E, int32_t k, float* loss,

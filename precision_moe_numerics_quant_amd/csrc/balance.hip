@@ -26,45 +26,65 @@ uint32_t take_dev_err_balance() { return take_device_word(&g_dev_err); }
 
 namespace bl {
 constexpr int MAXE = 1024, MAXK = 16;
-constexpr int PER = MAXE / 64;          // logits per lane at the most
-constexpr int NW = 4, THREADS = 64 * NW;
-constexpr int CH = 64;                  // tokens per chunk
-constexpr int SUM_T = 1024;
+constexpr int NW = 16, THREADS = 64 * NW;  // k_balance_part: waves per chunk
+constexpr int CH = 64;                     // tokens per chunk
+constexpr int SUM_T = 512, SUM_Q = 16;     // k_balance_sum: threads, column quads per workgroup
+constexpr int BWD_W = 4;                   // k_balance_bwd: waves (tokens) per workgroup
 }  // namespace bl
 
+__device__ inline float sum_xor16(float v) {
+  const auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(p[0]) + __uint_as_float(p[1]);
+}
+__device__ inline float sum_xor32(float v) {
+  const auto p = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(p[0]) + __uint_as_float(p[1]);
+}
+// The sum over the wave, in every lane (a fixed order, without LDS).
 __device__ inline float wave_sum(float v) {
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) v = v + __shfl_xor(v, o, 64);
-  return v;
+  v = v + lane_xor1(v);
+  v = v + lane_xor2(v);
+  v = v + __uint_as_float(dpp_u<DPP_HALF_MIRROR>(__float_as_uint(v)));
+  v = v + lane_xor8(v);
+  v = sum_xor16(v);
+  return sum_xor32(v);
 }
 
-// Row r of z in registers (expert l + 64 i in register i), turned into its
-// softmax; the experts past E, and every expert of a row of -infinities, are 0.
-__device__ inline void softmax_row(const float* __restrict__ logits, const float* __restrict__ bias, int64_t t, int E,
-                                   float (&p)[bl::PER]) {
+// Row t of z (expert l + 64 i in register i; -infinity past E).
+template <int PER>
+__device__ inline void load_row(const float* __restrict__ logits, const float (&b)[PER], int64_t t, int E, float (&z)[PER]) {
   const int l = threadIdx.x & 63;
-  float m = -INFINITY;
 #pragma unroll
-  for (int i = 0; i < bl::PER; ++i) {
-    const int e = l + 64 * i;
-    p[i] = -INFINITY;
-    if (e < E) {
-      p[i] = logits[t * E + e];
-      if (bias) p[i] = p[i] + bias[e];
-    }
-    m = fmaxf(m, p[i]);
-  }
+  for (int i = 0; i < PER; ++i) z[i] = l + 64 * i < E ? logits[t * E + l + 64 * i] + b[i] : -INFINITY;
+}
+
+// The lane's biases (0 without one: z + 0 is z).
+template <int PER>
+__device__ inline void load_bias(const float* __restrict__ bias, int E, float (&b)[PER]) {
+  const int l = threadIdx.x & 63;
+#pragma unroll
+  for (int i = 0; i < PER; ++i) b[i] = bias && l + 64 * i < E ? bias[l + 64 * i] : 0.0f;
+}
+
+// z turned into its softmax (every expert of a row of -infinities is 0).
+// exp(d) = 2^(d log2 e): for d <= 0 the product's rounding is as large an error
+// as the difference's own, and the hardware's 2^x is good to one unit.
+template <int PER>
+__device__ inline void softmax_row(float (&z)[PER]) {
+  float m = z[0];
+#pragma unroll
+  for (int i = 1; i < PER; ++i) m = fmaxf(m, z[i]);
   m = wave_max(m);
   float s = 0.0f;
 #pragma unroll
-  for (int i = 0; i < bl::PER; ++i) {
-    p[i] = m == -INFINITY ? 0.0f : expf(p[i] - m);
-    s = s + p[i];
+  for (int i = 0; i < PER; ++i) {
+    z[i] = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((z[i] - m) * 1.44269504f);
+    s = s + z[i];
   }
   s = wave_sum(s);
   const float r = s > 0.0f ? 1.0f / s : s;  // (a NaN stays one)
 #pragma unroll
-  for (int i = 0; i < bl::PER; ++i) p[i] = p[i] * r;
+  for (int i = 0; i < PER; ++i) z[i] = z[i] * r;
 }
 
 // Segment bounds; without offsets one segment of all T tokens.
@@ -83,34 +103,47 @@ __device__ inline int seg_of(const int32_t* __restrict__ off, int n_seg, int64_t
   return lo;
 }
 
+// One workgroup per chunk of CH tokens, a token per wave at a time, the next
+// token's row in flight during this one's softmax.  Partial rows have Ep =
+// 4 ceil(E / 4) columns (the last ones 0), so that the join reads 16 bytes a
+// lane.
+template <int PER>
 __global__ void __launch_bounds__(bl::THREADS)
     k_balance_part(const float* __restrict__ logits, const float* __restrict__ bias, const int32_t* __restrict__ idx,
                    const uint8_t* __restrict__ mask, const int32_t* __restrict__ seg_off, int n_seg, int64_t T, int E,
-                   int k, float* __restrict__ psum, int32_t* __restrict__ pcnt, int32_t* __restrict__ ptok) {
+                   int Ep, int k, float* __restrict__ psum, int32_t* __restrict__ pcnt, int32_t* __restrict__ ptok,
+                   int32_t* __restrict__ arrived) {
   using namespace bl;
-  __shared__ float lp[NW][MAXE];
-  __shared__ int lc[MAXE];
+  __shared__ float lp[NW][64 * PER];
+  __shared__ int lc[64 * PER];
   __shared__ int lt[NW];
-  const int tid = threadIdx.x, l = tid & 63, w = tid >> 6;
+  const int tid = threadIdx.x, l = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int64_t c = blockIdx.x, t0 = c * CH, t1 = t0 + CH < T ? t0 + CH : T;
+  if (c == 0)
+    for (int s = tid; s < n_seg; s += THREADS) arrived[s] = 0;
+  float bv[PER];
+  load_bias<PER>(bias, E, bv);
   for (int s = seg_of(seg_off, n_seg, t0, T); s < n_seg; ++s) {
     const int64_t sa = seg_at(seg_off, s, T), sb = seg_at(seg_off, s + 1, T);
     if (sa >= t1) break;
     const int64_t a = sa > t0 ? sa : t0, b = sb < t1 ? sb : t1;
     if (b <= a) continue;  // (uniform over the workgroup)
-    for (int e = tid; e < E; e += THREADS) lc[e] = 0;
+    for (int e = tid; e < 64 * PER; e += THREADS) lc[e] = 0;
     __syncthreads();
-    float acc[PER];
+    float acc[PER], z[PER];
 #pragma unroll
     for (int i = 0; i < PER; ++i) acc[i] = 0.0f;
     int n = 0;
-    for (int64_t t = a + w; t < b; t += NW) {
-      if (mask && !mask[t]) continue;
+    auto live = [&](int64_t t) { return t < b && (!mask || mask[t]); };
+    int64_t t = a + w;
+    while (t < b && !live(t)) t += NW;
+    if (t < b) load_row<PER>(logits, bv, t, E, z);
+    while (t < b) {
+      int64_t u = t + NW;
+      while (u < b && !live(u)) u += NW;
+      float y[PER];
+      if (u < b) load_row<PER>(logits, bv, u, E, y);
       ++n;
-      float p[PER];
-      softmax_row(logits, bias, t, E, p);
-#pragma unroll
-      for (int i = 0; i < PER; ++i) acc[i] = acc[i] + p[i];
       if (l < k) {
         int e = idx[t * k + l];
         if (e < 0 || e >= E) {
@@ -119,134 +152,199 @@ __global__ void __launch_bounds__(bl::THREADS)
         }
         atomicAdd(&lc[e], 1);
       }
+      softmax_row<PER>(z);
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        acc[i] = acc[i] + z[i];
+        z[i] = y[i];
+      }
+      t = u;
     }
 #pragma unroll
-    for (int i = 0; i < PER; ++i)
-      if (l + 64 * i < E) lp[w][l + 64 * i] = acc[i];
+    for (int i = 0; i < PER; ++i) lp[w][l + 64 * i] = acc[i];
     if (l == 0) lt[w] = n;
     __syncthreads();
     const int64_t row = c + s;
-    for (int e = tid; e < E; e += THREADS) {
-      psum[row * E + e] = ((lp[0][e] + lp[1][e]) + lp[2][e]) + lp[3][e];
-      pcnt[row * E + e] = lc[e];
+    for (int e = tid; e < Ep; e += THREADS) {
+      float v = lp[0][e];
+#pragma unroll
+      for (int i = 1; i < NW; ++i) v = v + lp[i][e];
+      psum[row * Ep + e] = v;
+      pcnt[row * Ep + e] = lc[e];
     }
-    if (tid == 0) ptok[row] = lt[0] + lt[1] + lt[2] + lt[3];
+    if (tid == 0) {
+      int m = 0;
+      for (int i = 0; i < NW; ++i) m += lt[i];
+      ptok[row] = m;
+    }
     __syncthreads();
   }
 }
 
-// One workgroup per segment: its partial rows in order.
+// Workgroup (column block, segment): 64 columns of the segment's partial rows,
+// dealt to 32 shares of the workgroup (rows g, g + 32, ... of four columns a
+// lane, eight rows in flight), which are joined in order.  The column blocks'
+// parts of the loss are summed in order by the segment's last workgroup (its
+// arrival count starts at 0, set by k_balance_part).
 __global__ void __launch_bounds__(bl::SUM_T)
     k_balance_sum(const float* __restrict__ psum, const int32_t* __restrict__ pcnt, const int32_t* __restrict__ ptok,
-                  const int32_t* __restrict__ seg_off, int64_t T, int E, int k, float* __restrict__ loss,
-                  int32_t* __restrict__ counts, int32_t* __restrict__ tokens, float* __restrict__ probs) {
+                  const int32_t* __restrict__ seg_off, int64_t T, int E, int Ep, int k, float* __restrict__ loss,
+                  int32_t* __restrict__ counts, int32_t* __restrict__ tokens, float* __restrict__ probs,
+                  float* __restrict__ ploss, int32_t* __restrict__ arrived) {
   using namespace bl;
-  __shared__ float lf[SUM_T / 64];
-  __shared__ float lp[SUM_T];
-  __shared__ int lc[SUM_T];
+  constexpr int G = SUM_T / SUM_Q;
+  __shared__ f32x4 lp[SUM_T];
+  __shared__ i32x4 lc[SUM_T];
   __shared__ int ln;
   const int tid = threadIdx.x;
-  const int s = blockIdx.x;
+  const int s = blockIdx.y, nb = gridDim.x;
   const int64_t a = seg_at(seg_off, s, T), b = seg_at(seg_off, s + 1, T);
   const int64_t c0 = a / CH, c1 = b > a ? (b - 1) / CH + 1 : c0;
-  // the experts side by side, the partial rows dealt over the rest of the
-  // workgroup: G shares of rows g, g + G, ..., joined in order
-  const int EW = (E + 63) / 64 * 64, G = SUM_T / EW, g = tid / EW, e = tid % EW;
+  const int Q = Ep / 4, g = tid / SUM_Q, q = blockIdx.x * SUM_Q + tid % SUM_Q;
   if (tid == 0) ln = 0;
-  float ps = 0.0f;
-  int cn = 0;
-  if (g < G && e < E)
-    for (int64_t c = c0 + g; c < c1; c += G) {
-      ps = ps + psum[(c + s) * E + e];
-      cn += pcnt[(c + s) * E + e];
+  f32x4 ps = {0.0f, 0.0f, 0.0f, 0.0f};
+  i32x4 cn = {0, 0, 0, 0};
+  if (q < Q) {
+    constexpr int U = 8;
+    const f32x4* pp = reinterpret_cast<const f32x4*>(psum);
+    const i32x4* pc = reinterpret_cast<const i32x4*>(pcnt);
+    for (int64_t c = c0 + g; c < c1; c += U * G) {
+      f32x4 v[U];
+      i32x4 m[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int64_t r = c + (int64_t)u * G;
+        v[u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        m[u] = i32x4{0, 0, 0, 0};
+        if (r < c1) {
+          v[u] = pp[(r + s) * Q + q];
+          m[u] = pc[(r + s) * Q + q];
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        ps = ps + v[u];
+        cn = cn + m[u];
+      }
     }
+  }
+  int n = 0;
+  for (int64_t c = c0 + tid; c < c1; c += SUM_T) n += ptok[c + s];
   lp[tid] = ps;
   lc[tid] = cn;
   __syncthreads();
-  int n = 0;
-  for (int64_t c = c0 + tid; c < c1; c += SUM_T) n += ptok[c + s];
   if (n) atomicAdd(&ln, n);
-  if (g == 0 && e < E)
+  if (g == 0)
     for (int i = 1; i < G; ++i) {
-      ps = ps + lp[i * EW + e];
-      cn += lc[i * EW + e];
+      ps = ps + lp[i * SUM_Q + tid];
+      cn = cn + lc[i * SUM_Q + tid];
     }
   __syncthreads();
   n = ln;
-  const float mean = n > 0 ? ps / (float)n : 0.0f;
-  float v = 0.0f;
-  if (g == 0 && e < E) {
-    if (counts) counts[(int64_t)s * E + e] = cn;
-    if (probs) probs[(int64_t)s * E + e] = mean;
-    v = (float)cn * mean;
+  float f = 0.0f;
+  if (g == 0 && q < Q) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int e = 4 * q + i;
+      if (e < E) {
+        const float mean = n > 0 ? ps[i] / (float)n : 0.0f;
+        counts[(int64_t)s * E + e] = cn[i];
+        probs[(int64_t)s * E + e] = mean;
+        f = f + (float)cn[i] * mean;
+      }
+    }
   }
-  v = wave_sum(v);
-  if ((tid & 63) == 0) lf[tid >> 6] = v;
-  __syncthreads();
-  if (tid == 0) {
-    float f = 0.0f;
-    for (int i = 0; i < SUM_T / 64; ++i) f = f + lf[i];
-    loss[s] = n > 0 ? f * ((float)E / ((float)k * (float)n)) : 0.0f;
-    tokens[s] = n;
+  if (tid < 64) {  // (the first wave holds all of g = 0)
+    f = wave_sum(f);
+    if (tid == 0) {
+      __hip_atomic_store(ploss + (int64_t)s * nb + blockIdx.x, f, __ATOMIC_RELEASE, __HIP_MEMORY_SCOPE_AGENT);
+      const int before = __hip_atomic_fetch_add(arrived + s, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
+      if (before == nb - 1) {
+        f = 0.0f;
+        for (int i = 0; i < nb; ++i)
+          f = f + __hip_atomic_load(ploss + (int64_t)s * nb + i, __ATOMIC_ACQUIRE, __HIP_MEMORY_SCOPE_AGENT);
+        loss[s] = n > 0 ? f * ((float)E / ((float)k * (float)n)) : 0.0f;
+        tokens[s] = n;
+      }
+    }
   }
 }
 
 // One wave per token.
-__global__ void __launch_bounds__(bl::THREADS)
+template <int PER>
+__global__ void __launch_bounds__(64 * bl::BWD_W)
     k_balance_bwd(const float* __restrict__ dloss, const float* __restrict__ logits, const float* __restrict__ bias,
                   const int32_t* __restrict__ counts, const int32_t* __restrict__ tokens,
                   const uint8_t* __restrict__ mask, const int32_t* __restrict__ seg_off, int n_seg, int64_t T, int E,
                   int k, const float* base, float* out) {  // base may be out
   using namespace bl;
-  const int64_t t = (int64_t)blockIdx.x * NW + (threadIdx.x >> 6);
+  const int64_t t = (int64_t)blockIdx.x * BWD_W + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l = threadIdx.x & 63;
   if (t >= T) return;
+  float o[PER], z[PER];
+#pragma unroll
+  for (int i = 0; i < PER; ++i) o[i] = base && l + 64 * i < E ? base[t * E + l + 64 * i] : 0.0f;
   const int s = seg_of(seg_off, n_seg, t, T);
   const bool live = s < n_seg && t >= seg_at(seg_off, s, T) && (!mask || mask[t]) && tokens[s] > 0;
-  float p[PER];
-#pragma unroll
-  for (int i = 0; i < PER; ++i) p[i] = 0.0f;
   if (live) {
-    const int32_t* cs = counts + (int64_t)s * E;
+    float bv[PER], c[PER];
+    load_bias<PER>(bias, E, bv);
+    load_row<PER>(logits, bv, t, E, z);
     const float n = (float)tokens[s];
     // counts from their mean: the same gradient (sum_e p = 1), without the
     // cancellation of two large numbers when the router is nearly even
     const float cm = (float)k * n / (float)E;
     const float f = dloss[s] * ((float)E / ((float)k * n)) / n;
-    softmax_row(logits, bias, t, E, p);
+#pragma unroll
+    for (int i = 0; i < PER; ++i) c[i] = l + 64 * i < E ? (float)counts[(int64_t)s * E + l + 64 * i] - cm : 0.0f;
+    softmax_row<PER>(z);
     float d = 0.0f;
 #pragma unroll
-    for (int i = 0; i < PER; ++i)
-      if (l + 64 * i < E) d = d + p[i] * ((float)cs[l + 64 * i] - cm);
+    for (int i = 0; i < PER; ++i) d = d + z[i] * c[i];
     d = wave_sum(d);
 #pragma unroll
-    for (int i = 0; i < PER; ++i)
-      if (l + 64 * i < E) p[i] = f * p[i] * (((float)cs[l + 64 * i] - cm) - d);
+    for (int i = 0; i < PER; ++i) o[i] = o[i] + f * z[i] * (c[i] - d);
   }
 #pragma unroll
-  for (int i = 0; i < PER; ++i) {
-    const int e = l + 64 * i;
-    if (e < E) out[t * E + e] = base ? base[t * E + e] + p[i] : p[i];
-  }
+  for (int i = 0; i < PER; ++i)
+    if (l + 64 * i < E) out[t * E + l + 64 * i] = o[i];
 }
 
-// Workspace: partial rows (ceil(T / CH) + n_seg of them): E float32 sums, E
-// counts, one token count.
+// Workspace: partial rows (ceil(T / CH) + n_seg of them): Ep float32 sums, Ep
+// counts, one token count; per segment the column blocks' parts of the loss
+// and an arrival count.
 struct BlLayout {
-  int64_t rows, off_cnt, off_tok, bytes;
+  int64_t rows, off_cnt, off_tok, off_loss, off_arr, bytes;
 };
+inline int bl_ep(int E) { return (E + 3) / 4 * 4; }
+inline int bl_blocks(int E) { return (E + 4 * bl::SUM_Q - 1) / (4 * bl::SUM_Q); }
 inline BlLayout bl_layout(int64_t T, int E, int n_seg) {
+  auto up = [](int64_t n) { return (n + 255) / 256 * 256; };
   BlLayout L;
   L.rows = (T + bl::CH - 1) / bl::CH + n_seg;
-  L.off_cnt = (L.rows * E * 4 + 255) / 256 * 256;
+  L.off_cnt = up(L.rows * bl_ep(E) * 4);
   L.off_tok = 2 * L.off_cnt;
-  L.bytes = L.off_tok + L.rows * 4;
+  L.off_loss = L.off_tok + up(L.rows * 4);
+  L.off_arr = L.off_loss + up((int64_t)n_seg * bl_blocks(E) * 4);
+  L.bytes = L.off_arr + (int64_t)n_seg * 4;
   return L;
 }
 
 }  // namespace moe4
 
 using namespace moe4;
+
+// The kernel for E experts: PER logits per lane (registers and exponentials
+// past the last expert cost as much as real ones)
+#define MOE4_BL_PER(LAUNCH)      \
+  do {                           \
+    if (E <= 64) LAUNCH(1);      \
+    else if (E <= 128) LAUNCH(2); \
+    else if (E <= 256) LAUNCH(4); \
+    else if (E <= 384) LAUNCH(6); \
+    else if (E <= 512) LAUNCH(8); \
+    else LAUNCH(16);             \
+  } while (0)
 
 extern "C" size_t moe_balance_loss_ws_bytes(int64_t T, int32_t E, int32_t n_seg) {
   if (T < 0 || E < 1 || n_seg < 1) return 0;
@@ -260,7 +358,8 @@ extern "C" int moe_balance_loss(const float* logits, const float* bias, const in
   MOE4_REQUIRE(T >= 0 && E >= 1 && E <= bl::MAXE && k >= 1 && k <= bl::MAXK && k <= E, MOE4_EINVAL,
                "moe_balance_loss: need T >= 0, 1 <= k <= min(E, 16), E <= 1024");
   MOE4_REQUIRE(T * (int64_t)k < ((int64_t)1 << 31), MOE4_EINVAL, "moe_balance_loss: T * k must be below 2^31");
-  MOE4_REQUIRE(n_seg >= 1 && (seg_off || n_seg == 1), MOE4_EINVAL, "moe_balance_loss: n_seg >= 1, with seg_off unless it is 1");
+  MOE4_REQUIRE(n_seg >= 1 && n_seg <= 65535 && (seg_off || n_seg == 1), MOE4_EINVAL,
+               "moe_balance_loss: 1 <= n_seg <= 65535, with seg_off unless it is 1");
   MOE4_REQUIRE(loss && counts && tokens && probs && (T == 0 || (logits && topk_idx)), MOE4_EINVAL,
                "moe_balance_loss: NULL pointer");
   const BlLayout L = bl_layout(T, E, n_seg);
@@ -271,12 +370,17 @@ extern "C" int moe_balance_loss(const float* logits, const float* bias, const in
   float* psum = reinterpret_cast<float*>(base);
   int32_t* pcnt = reinterpret_cast<int32_t*>(base + L.off_cnt);
   int32_t* ptok = reinterpret_cast<int32_t*>(base + L.off_tok);
+  float* ploss = reinterpret_cast<float*>(base + L.off_loss);
+  int32_t* arrived = reinterpret_cast<int32_t*>(base + L.off_arr);
   const hipStream_t st = as_stream(stream);
-  if (T > 0)
-    hipLaunchKernelGGL(k_balance_part, dim3((unsigned)((T + bl::CH - 1) / bl::CH)), dim3(bl::THREADS), 0, st, logits, bias,
-                       topk_idx, token_mask, seg_off, n_seg, T, E, k, psum, pcnt, ptok);
-  hipLaunchKernelGGL(k_balance_sum, dim3((unsigned)n_seg), dim3(bl::SUM_T), 0, st, psum, pcnt, ptok, seg_off, T, E, k,
-                     loss, counts, tokens, probs);
+  const int Ep = bl_ep(E);
+#define MOE4_BL_PART(PER)                                                                                               \
+  hipLaunchKernelGGL((k_balance_part<PER>), dim3((unsigned)(T > 0 ? (T + bl::CH - 1) / bl::CH : 1)), dim3(bl::THREADS), 0, \
+                     st, logits, bias, topk_idx, token_mask, seg_off, n_seg, T, E, Ep, k, psum, pcnt, ptok, arrived)
+  MOE4_BL_PER(MOE4_BL_PART);
+#undef MOE4_BL_PART
+  hipLaunchKernelGGL(k_balance_sum, dim3((unsigned)bl_blocks(E), (unsigned)n_seg), dim3(bl::SUM_T), 0, st, psum, pcnt, ptok,
+                     seg_off, T, E, Ep, k, loss, counts, tokens, probs, ploss, arrived);
   return check_launch("moe_balance_loss");
 }
 
@@ -292,7 +396,11 @@ extern "C" int moe_balance_loss_backward(const float* dloss, const float* logits
   MOE4_REQUIRE(dloss && counts && tokens && (T == 0 || (logits && dlogits)), MOE4_EINVAL,
                "moe_balance_loss_backward: NULL pointer");
   if (T == 0) return MOE4_OK;
-  hipLaunchKernelGGL(k_balance_bwd, dim3((unsigned)((T + bl::NW - 1) / bl::NW)), dim3(bl::THREADS), 0, as_stream(stream),
-                     dloss, logits, bias, counts, tokens, token_mask, seg_off, n_seg, T, E, k, dlogits_in, dlogits);
+#define MOE4_BL_BWD(PER)                                                                                              \
+  hipLaunchKernelGGL((k_balance_bwd<PER>), dim3((unsigned)((T + bl::BWD_W - 1) / bl::BWD_W)), dim3(64 * bl::BWD_W), 0, \
+                     as_stream(stream), dloss, logits, bias, counts, tokens, token_mask, seg_off, n_seg, T, E, k,      \
+                     dlogits_in, dlogits)
+  MOE4_BL_PER(MOE4_BL_BWD);
+#undef MOE4_BL_BWD
   return check_launch("moe_balance_loss_backward");
 }

@@ -188,10 +188,10 @@ __global__ void __launch_bounds__(m4s::NT)
 // (v_mfma_scale_f32_32x32x64_f8f6f4) and store; one barrier per slab.  128 x
 // TN tiles: consumers of 64 x TN / 2.
 //
-// Every load goes through a buffer descriptor that covers exactly the tile's
-// rows, so rows past the expert's last, past N, and K chunks past K (their
-// lanes' offsets are set out of range) arrive as zeros and no shape needs a
-// kernel of its own.
+// Every load goes through a buffer descriptor that ends with the operand's
+// rows, so rows past M or N and K chunks past K (their lanes' offsets are set
+// out of range) arrive as zeros and no shape needs a kernel of its own; rows
+// past the expert's last are the next expert's, and their results not stored.
 //
 // Scales: a wave's load of 64 rows' scales touches 64 cache lines whatever it
 // takes from each, as long as four of its whole-row code loads, so the fewest
@@ -209,6 +209,7 @@ typedef __attribute__((address_space(3))) void* lds_ptr;
 // address that each lane loads
 __device__ inline int swz(int row, int c) { return c ^ ((row >> 1) & 7); }
 // 16 bytes at each lane's offset + soff into lane-consecutive LDS from p on
+// (the descriptor's range check sees the lane's offset alone)
 __device__ __forceinline__ void load_lds(const __amdgpu_buffer_rsrc_t& rs, uint8_t* p, uint32_t off, uint32_t soff) {
   __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr)p, 16, off, soff, 0, 0);
 }
@@ -284,11 +285,12 @@ __global__ void __launch_bounds__(m4w::NT, 1)
       more = pt < q_end && cur.seek(off, E, mi);
       if (!more) return;
       const int e = cur.e;
-      const int64_t row0 = (int64_t)ld_const(off, e) + (int64_t)(mi - cur.first) * TM, n0 = (int64_t)nt * TN;
+      int64_t row0 = (int64_t)ld_const(off, e) + (int64_t)(mi - cur.first) * TM;
+      const int64_t n0 = (int64_t)nt * TN;
       const int64_t end = (int64_t)ld_const(off, e + 1) < M_total ? (int64_t)ld_const(off, e + 1) : M_total;
-      int64_t ra = end - row0 < TM ? end - row0 : TM;
+      if (row0 < 0 || row0 >= end) row0 = 0;  // (offsets outside [0, M]: other rows are read, none stored)
+      const int64_t ra = M_total - row0 < TM ? M_total - row0 : TM;
       const int64_t rb = N - n0 < TN ? N - n0 : TN, rowb = (int64_t)e * N + n0;
-      if (row0 < 0 || ra < 0) ra = 0;  // (offsets outside [0, M]: nothing is read)
       rac = make_rsrc(a_codes + row0 * KH, (uint64_t)ra * KH);
       rbc = make_rsrc(b_codes + rowb * KH, (uint64_t)rb * KH);
       const uint8_t* as = a_sf + row0 * KS;
@@ -333,9 +335,11 @@ __global__ void __launch_bounds__(m4w::NT, 1)
           const int grp = sgrp(k);
           uint8_t* sb = sl + grp * 1024;
           const bool opa = grp < TM / 64;
-          const uint32_t o = PAIR ? soff[k] : ((opa ? ax : bx) + soff[k]) & ~3u;  // (8 ps is whole dwords)
-          if (opa) load_lds(ras, sb, o, 8 * ps);
-          else load_lds(rbs, sb, o, 8 * ps);
+          // (PAIR: inside the row.  Otherwise the 16 bytes may reach past the last
+          // row: all of the offset in the operand that the range check sees)
+          const uint32_t o = PAIR ? soff[k] : (((opa ? ax : bx) + soff[k]) & ~3u) + 8 * ps, so = PAIR ? 8 * ps : 0;
+          if (opa) load_lds(ras, sb, o, so);
+          else load_lds(rbs, sb, o, so);
         }
       }
       if (++ps == nk) {
