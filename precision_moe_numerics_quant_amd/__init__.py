@@ -175,20 +175,35 @@ def _arg(t, dtype, shape, name, like=None):
     """Check a tensor argument of the calls below: dtype, shape (None: any size
     there), contiguous, on the GPU, and on like's device."""
     _dev(t, dtype, name)
-    if t.dim() != len(shape) or any(w is not None and int(g) != int(w) for g, w in zip(t.shape, shape)):
-        raise ValueError(f"{name}: expected shape {tuple(shape)} (None: any), got {tuple(t.shape)}")
+    s = t.shape
+    if s != shape and (len(s) != len(shape) or any(w is not None and g != w for g, w in zip(s, shape))):
+        raise ValueError(f"{name}: expected shape {tuple(shape)} (None: any), got {tuple(s)}")
     if like is not None and t.device != like.device:
         raise ValueError(f"{name}: on {t.device}, the call's other tensors on {like.device}")
     return t
 
 
+def _raw_stream(index):
+    """hipStream_t of the current stream of device index."""
+    return torch.cuda.current_stream(index).cuda_stream
+
+
+# the same without making a Stream object (2 us of a call that takes 10)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _raw_stream)
+
+
 def _run(name, like, *args):
-    """Call the library on like's device, on that device's current stream."""
-    if like.device.index == torch.cuda.current_device():
-        _check(getattr(lib(), name)(*args, _stream()), name)
+    """Call the library on like's device, on that device's current stream
+    (tensors among the arguments as their pointers)."""
+    args = [a.data_ptr() if isinstance(a, torch.Tensor) else a for a in args]
+    i = like.device.index
+    if i == torch.cuda.current_device():
+        rc = getattr(lib(), name)(*args, _raw_stream(i))
     else:
-        with torch.cuda.device(like.device):
-            _check(getattr(lib(), name)(*args, _stream()), name)
+        with torch.cuda.device(i):
+            rc = getattr(lib(), name)(*args, _raw_stream(i))
+    if rc:
+        _check(rc, name)
 
 
 def pad32(n):
@@ -410,8 +425,8 @@ def mxfp8_requant_mx4_sr_T(codes, sf, group_row_off, group_off_pad, seed=1, stre
         max_pr = max_padded_rows(R, G)
     oc = _empty((C * max_pr,), torch.uint8, codes)
     os_ = _empty((C * max_pr // 32,), torch.uint8, codes)
-    _run("mxfp8_requant_mx4_sr_T", codes, _p(codes), _p(sf), R, C, _p(group_row_off), _p(group_off_pad), G, max_pr,
-         seed, stream_id, int(sf_layout), _p(oc), _p(os_))
+    _run("mxfp8_requant_mx4_sr_T", codes, codes, sf, R, C, group_row_off, group_off_pad, G, max_pr,
+         seed, stream_id, int(sf_layout), oc, os_)
     return oc, os_
 
 
@@ -437,7 +452,7 @@ def mxfp4_quant(x, pre_op=PRE_NONE, out_map=None, copies=1, out=None):
     codes, sf = out
     _arg(codes, torch.uint8, (None if out_map is not None else R, C // 2), "out codes", x)
     _arg(sf, torch.uint8, (codes.shape[0], C // 32), "out sf", x)
-    _run("mxfp4_quant", x, _p(x), dt, R, C, _p(out_map), copies, codes.shape[0], int(pre_op), _p(codes), _p(sf))
+    _run("mxfp4_quant", x, x, dt, R, C, out_map, copies, codes.shape[0], int(pre_op), codes, sf)
     return codes, sf
 
 
@@ -450,7 +465,7 @@ def mxfp4_dequant(codes, sf, out_dtype=torch.float32):
     R, C = codes.shape[0], 2 * codes.shape[1]
     _arg(sf, torch.uint8, (R, C // 32), "sf", codes)
     out = _empty((R, C), out_dtype, codes)
-    _run("mxfp4_dequant", codes, _p(codes), _p(sf), R, C, _p(out), dt)
+    _run("mxfp4_dequant", codes, codes, sf, R, C, out, dt)
     return out
 
 
@@ -603,8 +618,8 @@ def moe_grouped_gemm_mx4(a_codes, a_sf, b_codes, b_sf, expert_off, out_dtype=tor
     _arg(b_sf, torch.uint8, (E, N, Kh // 16), "b_sf", a_codes)
     _arg(expert_off, torch.int32, (E + 1,), "expert_off", a_codes)
     c = _empty((M, N), out_dtype, a_codes)
-    _run("moe_grouped_gemm_mx4", a_codes, _p(a_codes), _p(a_sf), _p(b_codes), _p(b_sf), _p(expert_off), E, M, N,
-         2 * Kh, _p(c), cd)
+    _run("moe_grouped_gemm_mx4", a_codes, a_codes, a_sf, b_codes, b_sf, expert_off, E, M, N,
+         2 * Kh, c, cd)
     return c
 
 
@@ -750,8 +765,8 @@ def moe_balance_loss(logits, topk_idx, bias=None, token_mask=None, seg_off=None)
     r = dict(loss=_empty((max(S, 0),), torch.float32, logits), counts=_empty((max(S, 0), E), torch.int32, logits),
              tokens=_empty((max(S, 0),), torch.int32, logits), probs=_empty((max(S, 0), E), torch.float32, logits))
     ws = _ws(lib().moe_balance_loss_ws_bytes(T, E, S), logits)
-    _run("moe_balance_loss", logits, _p(logits), _p(bias), _p(topk_idx), _p(mask), _p(seg_off), S, T, E, k,
-         _p(r["loss"]), _p(r["counts"]), _p(r["tokens"]), _p(r["probs"]), _p(ws), ws.numel())
+    _run("moe_balance_loss", logits, logits, bias, topk_idx, mask, seg_off, S, T, E, k,
+         r["loss"], r["counts"], r["tokens"], r["probs"], ws, ws.numel())
     return r
 
 
@@ -774,8 +789,8 @@ def moe_balance_loss_backward(dloss, logits, counts, tokens, k, bias=None, token
     if dlogits is not None:
         _arg(dlogits, torch.float32, (T, E), "dlogits", logits)
     out = _empty((T, E), torch.float32, logits) if out is None else _arg(out, torch.float32, (T, E), "out", logits)
-    _run("moe_balance_loss_backward", logits, _p(dloss), _p(logits), _p(bias), _p(counts), _p(tokens), _p(mask),
-         _p(seg_off), S, T, E, k, _p(dlogits), _p(out))
+    _run("moe_balance_loss_backward", logits, dloss, logits, bias, counts, tokens, mask,
+         seg_off, S, T, E, k, dlogits, out)
     return out
 
 
@@ -788,7 +803,7 @@ def moe_unpermute_sum_router_dense(dxp, inv_perm, T, k, dlogits, w):
     _arg(dlogits, torch.float32, (T, E), "dlogits", dxp)
     _arg(inv_perm, torch.int32, (T * k,), "inv_perm", dxp)
     dx = _empty((T, d), torch.bfloat16, dxp)
-    _run("moe_unpermute_sum_router_dense", dxp, _p(dxp), _p(inv_perm), T, k, d, _p(dlogits), E, _p(w), _p(dx))
+    _run("moe_unpermute_sum_router_dense", dxp, dxp, inv_perm, T, k, d, dlogits, E, w, dx)
     return dx
 
 
@@ -800,7 +815,7 @@ def moe_router_wgrad_dense(x, dlogits):
     E = dlogits.shape[1]
     dw = _empty((E, d), torch.float32, x)
     ws = _ws(lib().moe_router_wgrad_dense_ws_bytes(T, E, d), x)
-    _run("moe_router_wgrad_dense", x, _p(x), _p(dlogits), T, E, d, _p(dw), _p(ws), ws.numel())
+    _run("moe_router_wgrad_dense", x, x, dlogits, T, E, d, dw, ws, ws.numel())
     return dw
 
 

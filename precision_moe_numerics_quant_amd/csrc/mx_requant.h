@@ -17,6 +17,16 @@ __device__ inline int mx_exponent(float amax) {
   return e > 127 ? 127 : (e < -127 ? -127 : e);
 }
 
+// The group of row r (off[0 .. G] ascending).
+__device__ inline int find_group(const int32_t* off, int G, int64_t r) {
+  int lo = 0, hi = G - 1;
+  while (lo < hi) {
+    int mid = (lo + hi + 1) >> 1;
+    if ((int64_t)off[mid] <= r) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+
 // Workgroup: 4 waves over 4 consecutive MX blocks (128 padded rows) x 512
 // columns.  Lane l of wave w takes columns c0 + 8l .. c0 + 8l + 7 of block w:
 // one 32-bit code word (8 E2M1 codes) and one E4M3 scale byte per row, so the
@@ -58,6 +68,16 @@ __device__ inline uint32_t sr_fp8_into(uint32_t old, float v, uint32_t r, int se
     case 1: return __builtin_amdgcn_cvt_scalef32_sr_fp8_f32(old, v, r, 1.0f, 1);
     case 2: return __builtin_amdgcn_cvt_scalef32_sr_fp8_f32(old, v, r, 1.0f, 2);
     default: return __builtin_amdgcn_cvt_scalef32_sr_fp8_f32(old, v, r, 1.0f, 3);
+  }
+}
+
+// SR E4M3 of v / scale (a power of two) into byte sel of old.
+__device__ inline uint32_t sr_fp8_scaled(uint32_t old, float v, uint32_t r, float scale, int sel) {
+  switch (sel) {
+    case 0: return __builtin_amdgcn_cvt_scalef32_sr_fp8_f32(old, v, r, scale, 0);
+    case 1: return __builtin_amdgcn_cvt_scalef32_sr_fp8_f32(old, v, r, scale, 1);
+    case 2: return __builtin_amdgcn_cvt_scalef32_sr_fp8_f32(old, v, r, scale, 2);
+    default: return __builtin_amdgcn_cvt_scalef32_sr_fp8_f32(old, v, r, scale, 3);
   }
 }
 

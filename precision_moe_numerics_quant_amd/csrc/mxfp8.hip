@@ -27,15 +27,6 @@ constexpr int TC = 128;   // columns per tile
 constexpr int MXT = 256;  // threads
 constexpr int MX_T_CPW = 4;  // column tiles per workgroup of the transposed kernels that stage a table
 
-__device__ inline int find_group(const int32_t* off, int G, int64_t r) {
-  int lo = 0, hi = G - 1;
-  while (lo < hi) {
-    int mid = (lo + hi + 1) >> 1;
-    if ((int64_t)off[mid] <= r) lo = mid; else hi = mid - 1;
-  }
-  return lo;
-}
-
 // E4M3 byte of w (|w| <= 448): RNE, or SR with the 16-bit word r16.
 template <bool SR>
 __device__ inline uint32_t mx_round(float w, uint32_t r16) {
@@ -144,13 +135,9 @@ __device__ inline bool tile_coords(const int32_t* off, const int32_t* offp, int 
 }
 
 // ---------------------------------------------------------------- requant-T
-// The source format: NVFP4 (codes [R, C/2], E4M3 scales [R, C/16], tensor
-// scales), MXFP8 row-wise (codes [R, C], E8M0 scales [R, C/32], no tensor
-// scale: S = 1) or MXFP4 row-wise (codes [R, C/2], E8M0 scales [R, C/32],
-// S = 1; a row whose scale byte is 255, E8M0's NaN, gives its columns' blocks
-// that scale byte).
-enum { SRC_NV4 = 0, SRC_MX8 = 1, SRC_MX4 = 2 };
-template <int SRC>
+// MX: the source is MXFP8 row-wise (codes [R, C], E8M0 scales [R, C/32], no
+// tensor scale: S = 1) instead of NVFP4.
+template <bool MX>
 __global__ void __launch_bounds__(rq::THREADS) k_requant_T(const uint8_t* __restrict__ codes,
                                                            const uint8_t* __restrict__ sf,
                                                            const float* __restrict__ ts, int ts_per_group, int64_t C,
@@ -159,7 +146,6 @@ __global__ void __launch_bounds__(rq::THREADS) k_requant_T(const uint8_t* __rest
                                                            int64_t max_pr, int64_t n_ct, uint32_t base, int sfb,
                                                            uint8_t* __restrict__ out_c, uint8_t* __restrict__ out_s) {
   using namespace rq;
-  constexpr bool MX8 = SRC == SRC_MX8, MX = SRC != SRC_NV4;
   __shared__ __attribute__((aligned(16))) uint8_t lq[COLS * ROWS];
   __shared__ uint8_t lsf[COLS * WAVES];  // [column][block]
   __shared__ int64_t lblk[WAVES][3];     // block's code offset at column 0, P (0: no block), scale offset at column 0
@@ -194,39 +180,32 @@ __global__ void __launch_bounds__(rq::THREADS) k_requant_T(const uint8_t* __rest
     *reinterpret_cast<uint32_t*>(lq + col * ROWS + swz(col, 2 * w + (k >> 2)) * 16 + (k & 3) * 4) = v;
   };
   int ex[8];
-  bool nan = false;  // SRC_MX4: a row with the scale byte 255
 #pragma unroll
   for (int q = 0; q < 8; ++q) ex[q] = -127;
   if (nvalid > 0 && c < C) {
-    // code words (FP4: 8 E2M1 codes in one dword; MXFP8: 8 E4M3 bytes in
+    // code words (NVFP4: 8 E2M1 codes in one dword; MXFP8: 8 E4M3 bytes in
     // two); scale bytes packed 4 rows per register
-    uint32_t cw[32][MX8 ? 2 : 1], sbp[8];
-    const uint8_t* crow = MX8 ? codes + src0 * C + c : codes + src0 * (C / 2) + c / 2;
+    uint32_t cw[32][MX ? 2 : 1], sbp[8];
+    const uint8_t* crow = MX ? codes + src0 * C + c : codes + src0 * (C / 2) + c / 2;
     const uint8_t* srow = MX ? sf + src0 * (C / 32) + c / 32 : sf + src0 * (C / 16) + c / 16;
 #pragma unroll
     for (int k = 0; k < 8; ++k) sbp[k] = 0u;
 #pragma unroll
     for (int i = 0; i < 32; ++i) {  // rows past the group repeat its last row and are never used
       const int64_t ri = i < nvalid ? i : nvalid - 1;
-      if (MX8) {
+      if (MX) {
         const u32x2 wv = *reinterpret_cast<const u32x2*>(crow + ri * C);
         cw[i][0] = wv[0];
-        cw[i][MX8 ? 1 : 0] = wv[1];
+        cw[i][MX ? 1 : 0] = wv[1];
       } else {
         cw[i][0] = *reinterpret_cast<const uint32_t*>(crow + ri * (C / 2));
       }
       sbp[i >> 2] |= (uint32_t)srow[ri * (MX ? C / 32 : C / 16)] << (8 * (i & 3));
     }
-    if (SRC == SRC_MX4) {
-#pragma unroll
-      for (int i = 0; i < 32; ++i) nan |= ((sbp[i >> 2] >> (8 * (i & 3))) & 0xFFu) == 255u;
-    }
     const float S = MX ? 1.0f : ts[ts_per_group ? g : 0];
     auto deq = [&](int i, float (&q)[8]) {
       const uint32_t sb = (sbp[i >> 2] >> (8 * (i & 3))) & 0xFFu;
-      // (MXFP4 reaches 6 * 2**127, past float32: a quarter of the value here)
-      if (SRC == SRC_MX4) mx4_decode8(cw[i][0], (int)sb - 129, q);
-      else if (MX8) dequant8_mx(u32x2{cw[i][0], cw[i][MX8 ? 1 : 0]}, sb, q);
+      if (MX) dequant8_mx(u32x2{cw[i][0], cw[i][MX ? 1 : 0]}, sb, q);
       else dequant8(cw[i][0], sb, q);
     };
     // block amax of fl(fl(q*sc)*S) per column: fl(max |q*sc| * S), as
@@ -246,32 +225,17 @@ __global__ void __launch_bounds__(rq::THREADS) k_requant_T(const uint8_t* __rest
     float pc[8];
 #pragma unroll
     for (int q = 0; q < 8; ++q) {
-      if (SRC == SRC_MX4) ex[q] = am[q] < 1.0f ? mx_exponent(4.0f * am[q]) : mx_exponent(am[q]) + 2;
-      else ex[q] = mx_exponent(am[q] * S);
+      ex[q] = mx_exponent(am[q] * S);
       pc[q] = __builtin_amdgcn_ldexpf(1.0f, -ex[q]);
     }
     if (MX) {  // decode again below instead of keeping the 256 decoded values live
 #pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        asm volatile("" : "+v"(cw[i][0]));
-        if (MX8) asm volatile("" : "+v"(cw[i][MX8 ? 1 : 0]));
-      }
+      for (int i = 0; i < 32; ++i) asm volatile("" : "+v"(cw[i][0]), "+v"(cw[i][MX ? 1 : 0]));
     }
     const int64_t j0 = src0 * (C / 2) + c / 2;  // pair index of (row src0, column c)
     const uint32_t key0 = fmix32(base);
     const bool fast = j0 + 31 * (C / 2) + 3 < ((int64_t)1 << 32);
-    if (SRC == SRC_MX4) {  // q * 2**(sb - 127 - ex), one power of two per value
-      auto deqw = [&](int i, float (&q)[8]) {
-        mx4_decode8(cw[i][0], 0, q);
-        const int sb = (int)((sbp[i >> 2] >> (8 * (i & 3))) & 0xFFu) - 127;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) q[j] = __builtin_amdgcn_ldexpf(q[j], sb - ex[j]);
-      };
-      const float one[8] = {1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f};
-      if (fast && nvalid == 32) requant_block<true, true>(deqw, nvalid, 1.0f, one, j0, C / 2, base, key0, put);
-      else if (fast) requant_block<true, false>(deqw, nvalid, 1.0f, one, j0, C / 2, base, key0, put);
-      else requant_block<false, false>(deqw, nvalid, 1.0f, one, j0, C / 2, base, key0, put);
-    } else if (!MX && fast && nvalid == 32 && fold_scale_ok(S)) {  // one multiply by S * 2^-ex per value
+    if (!MX && fast && nvalid == 32 && fold_scale_ok(S)) {  // one multiply by S * 2^-ex per value
       float f[8];
 #pragma unroll
       for (int q = 0; q < 8; ++q) f[q] = ex[q] == -127 ? 0.0f : S * pc[q];
@@ -289,7 +253,7 @@ __global__ void __launch_bounds__(rq::THREADS) k_requant_T(const uint8_t* __rest
       for (int q = 0; q < 8; ++q) put(k, q, 0u);
   }
 #pragma unroll
-  for (int q = 0; q < 8; ++q) lsf[(LCOLS * l + q) * WAVES + w] = nan ? 255u : (uint8_t)(ex[q] + 127);
+  for (int q = 0; q < 8; ++q) lsf[(LCOLS * l + q) * WAVES + w] = (uint8_t)(ex[q] + 127);
   __syncthreads();
   rq_store_tile(lq, lsf, lblk, c0, C, sfb, out_c, out_s);
 }
@@ -297,7 +261,7 @@ __global__ void __launch_bounds__(rq::THREADS) k_requant_T(const uint8_t* __rest
 // ------------------------------------------ weights of the MXFP8 forward
 // Float32 weights [G * grows, C] -> the row-wise MXFP8 RNE copy (blocks of 32
 // along the row, the forward contraction: the bytes of k_mx_rows) and, from
-// those codes with the same steps as k_requant_T<SRC_MX8>, the transposed MXFP8
+// those codes with the same steps as k_requant_T<true>, the transposed MXFP8
 // SR copy (group-major, grows rows per group, row-major scales), in one read
 // of the weights.  MXFP8 has no tensor scale, so no tile waits for the rest
 // of its group.  Tile: 4 waves x (32 rows = one transposed MX block) x 512
@@ -761,7 +725,7 @@ extern "C" int mxfp8_requant_sr_T(const uint8_t* codes, const uint8_t* sf, const
   const int64_t n_ct = (cols + rq::COLS - 1) / rq::COLS, n_rt = (max_padded_rows + rq::ROWS - 1) / rq::ROWS;
   MOE4_REQUIRE(n_ct * n_rt < (int64_t)1 << 31, MOE4_EINVAL, "mxfp8_requant_sr_T: tensor too large");
   const uint32_t base = sr_base_key(seed, stream_id);
-  hipLaunchKernelGGL(k_requant_T<SRC_NV4>, dim3((unsigned)(n_ct * n_rt)), dim3(rq::THREADS), 0, as_stream(stream), codes, sf, ts,
+  hipLaunchKernelGGL(k_requant_T<false>, dim3((unsigned)(n_ct * n_rt)), dim3(rq::THREADS), 0, as_stream(stream), codes, sf, ts,
                      ts_per_group, cols, group_row_off, group_off_pad, n_groups, rows, max_padded_rows, n_ct, base,
                      (int)(sf_layout == MOE4_SF_BLOCKS), out_codes, out_sf);
   return check_launch("mxfp8_requant_sr_T");
@@ -782,31 +746,10 @@ extern "C" int mxfp8_requant_mx_sr_T(const uint8_t* codes, const uint8_t* sf, in
   if (max_padded_rows == 0) return MOE4_OK;
   const int64_t n_ct = (cols + rq::COLS - 1) / rq::COLS, n_rt = (max_padded_rows + rq::ROWS - 1) / rq::ROWS;
   MOE4_REQUIRE(n_ct * n_rt < (int64_t)1 << 31, MOE4_EINVAL, "mxfp8_requant_mx_sr_T: tensor too large");
-  hipLaunchKernelGGL(k_requant_T<SRC_MX8>, dim3((unsigned)(n_ct * n_rt)), dim3(rq::THREADS), 0, as_stream(stream), codes,
+  hipLaunchKernelGGL(k_requant_T<true>, dim3((unsigned)(n_ct * n_rt)), dim3(rq::THREADS), 0, as_stream(stream), codes,
                      sf, nullptr, 0, cols, group_row_off, group_off_pad, n_groups, rows, max_padded_rows, n_ct,
                      sr_base_key(seed, stream_id), (int)(sf_layout == MOE4_SF_BLOCKS), out_codes, out_sf);
   return check_launch("mxfp8_requant_mx_sr_T");
-}
-
-extern "C" int mxfp8_requant_mx4_sr_T(const uint8_t* codes, const uint8_t* sf, int64_t rows, int64_t cols,
-                                     const int32_t* group_row_off, const int32_t* group_off_pad, int32_t n_groups,
-                                     int64_t max_padded_rows, uint64_t seed, uint32_t stream_id, int sf_layout,
-                                     uint8_t* out_codes, uint8_t* out_sf, void* stream) {
-  MOE4_REQUIRE(rows >= 0 && cols > 0 && cols % 32 == 0, MOE4_EINVAL, "mxfp8_requant_mx4_sr_T: cols must be a positive multiple of 32");
-  MOE4_REQUIRE(n_groups >= 1 && group_row_off && group_off_pad, MOE4_EINVAL, "mxfp8_requant_mx4_sr_T: group offsets required");
-  MOE4_REQUIRE(max_padded_rows >= 0 && max_padded_rows % 32 == 0, MOE4_EINVAL,
-               "mxfp8_requant_mx4_sr_T: max_padded_rows must be a multiple of 32");
-  MOE4_REQUIRE(sf_layout == MOE4_SF_ROWS || sf_layout == MOE4_SF_BLOCKS, MOE4_EINVAL,
-               "mxfp8_requant_mx4_sr_T: sf_layout must be MOE4_SF_ROWS or MOE4_SF_BLOCKS");
-  if (max_padded_rows == 0) return MOE4_OK;
-  MOE4_REQUIRE((rows == 0 || (codes && sf)) && out_codes && out_sf, MOE4_EINVAL, "mxfp8_requant_mx4_sr_T: NULL pointer");
-  MOE4_REQUIRE(aligned16(codes) && aligned16(out_codes), MOE4_EALIGN, "mxfp8_requant_mx4_sr_T: misaligned pointer");
-  const int64_t n_ct = (cols + rq::COLS - 1) / rq::COLS, n_rt = (max_padded_rows + rq::ROWS - 1) / rq::ROWS;
-  MOE4_REQUIRE(n_ct * n_rt < (int64_t)1 << 31, MOE4_EINVAL, "mxfp8_requant_mx4_sr_T: tensor too large");
-  hipLaunchKernelGGL(k_requant_T<SRC_MX4>, dim3((unsigned)(n_ct * n_rt)), dim3(rq::THREADS), 0, as_stream(stream), codes,
-                     sf, nullptr, 0, cols, group_row_off, group_off_pad, n_groups, rows, max_padded_rows, n_ct,
-                     sr_base_key(seed, stream_id), (int)(sf_layout == MOE4_SF_BLOCKS), out_codes, out_sf);
-  return check_launch("mxfp8_requant_mx4_sr_T");
 }
 
 extern "C" int mxfp8_quant_requant_T(const float* x, int64_t rows, int64_t cols, int32_t n_groups, uint64_t seed,
