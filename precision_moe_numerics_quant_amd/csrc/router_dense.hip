@@ -63,6 +63,14 @@ __device__ inline void columns2(const uint32_t (&w)[8], u32x4& c0, u32x4& c1) {
   }
 }
 
+// A thread's share of one slab in registers: 8 k of two rows or columns of dz
+// and of two columns of the other operand.  The kernels keep two of them, so
+// that a slab's loads have two slabs' MFMAs to land in.
+struct RdRegs {
+  float a[2][8];
+  uint32_t b[8];
+};
+
 // One slab: wave (wm, wn) owns 64 x 64 of the tile, 2 x 2 MFMA blocks.
 __device__ inline void rd_compute(const uint8_t* st, int wm, int wn, f32x16 (&acc)[2][2]) {
   using namespace rd;
@@ -105,52 +113,57 @@ __global__ void __launch_bounds__(rd::NT, 2)
                       uint16_t* __restrict__ dx) {
   using namespace rd;
   __shared__ __attribute__((aligned(16))) uint8_t lds[2 * STAGE];  // two stages; then the float32 tile (64 KB both)
+  __shared__ int32_t rows[TM * MAXK];                              // dXp's rows of the tile's tokens
   static_assert(2 * STAGE >= TM * TN * 4, "the epilogue's tile");
   const int64_t tile = xcd_tile(blockIdx.x, n_all);
   if (tile >= n_all) return;
   const int64_t t0 = (tile / n_nt) * TM, c0 = (tile % n_nt) * TN;
-  const int tid = threadIdx.x, l = tid & 63, wv = tid >> 6;
+  const int tid = threadIdx.x, l = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = (wv >> 1) * 64, wn = (wv & 1) * 64;
+  for (int i = tid; i < TM * k; i += NT)  // (tokens past T: any row)
+    rows[i] = t0 * k + i < T * k ? (int32_t)clamp_row(inv[t0 * k + i], T * k, &g_dev_err) : 0;
   // dz: units (row tid / 4 + 64 j, chunk tid % 4); W_r: unit (chunk tid / 64, columns 2 l, 2 l + 1)
   const int ach = tid & 3, ar = tid >> 2;
   const int64_t bc = c0 + 2 * l;
-  const bool vec = (E & 3) == 0;
-  float av[2][8];
-  uint32_t bw[8];
-  auto load = [&](int k0) {
+  // (a descriptor that ends with the tile's rows, and one per row of W_r: rows
+  // past T or E and columns past d come as zeros)
+  const __amdgpu_buffer_rsrc_t rz = make_rsrc(dz + t0 * E, (uint64_t)(T - t0 < TM ? T - t0 : TM) * E * 4);
+  const uint32_t zo = (uint32_t)ar * E * 4 + 32u * ach, z64 = 64u * (uint32_t)E * 4;
+  const uint32_t wo = (uint32_t)bc * 2;
+  auto load = [&](RdRegs& q, int k0) {
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      const int64_t t = t0 + ar + 64 * j;
-      const int kb = k0 + 8 * ach;
-      const float* p = dz + t * E + kb;
-      if (t < T && vec && kb + 8 <= E) {
-        const f32x4 x0 = reinterpret_cast<const f32x4*>(p)[0], x1 = reinterpret_cast<const f32x4*>(p)[1];
+      const uint32_t o = zo + j * z64 + (uint32_t)k0 * 4;
+      const u32x4 x0 = __builtin_amdgcn_raw_buffer_load_b128(rz, o, 0, 0), x1 = __builtin_amdgcn_raw_buffer_load_b128(rz, o + 16, 0, 0);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          av[j][i] = x0[i];
-          av[j][4 + i] = x1[i];
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) av[j][i] = t < T && kb + i < E ? p[i] : 0.0f;
+      for (int i = 0; i < 4; ++i) {
+        q.a[j][i] = __uint_as_float(x0[i]);
+        q.a[j][4 + i] = __uint_as_float(x1[i]);
       }
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int e = k0 + 8 * wv + i;
-      bw[i] = e < E && bc < d ? *reinterpret_cast<const uint32_t*>(w + (int64_t)e * d + bc) : 0u;
+      q.b[i] = __builtin_amdgcn_raw_buffer_load_b32(make_rsrc(w + (int64_t)(e < E ? e : 0) * d, e < E ? (uint64_t)d * 2 : 0), wo, 0, 0);
     }
   };
-  auto store = [&](uint8_t* st) {
+  // (k0: the slab's first expert; past E the row's values are the next row's)
+  auto store = [&](RdRegs& q, uint8_t* st, int k0) {
+    if (k0 + BK > E) {  // (uniform)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) q.a[j][i] = k0 + 8 * ach + i < E ? q.a[j][i] : 0.0f;
+    }
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       u32x4 o[3];
-      split3(av[j], o);
+      split3(q.a[j], o);
 #pragma unroll
       for (int p = 0; p < 3; ++p) *reinterpret_cast<u32x4*>(st + p * PART_B + (ach * TM + ar + 64 * j) * 16) = o[p];
     }
     u32x4 b0, b1;
-    columns2(bw, b0, b1);
+    columns2(q.b, b0, b1);
     *reinterpret_cast<u32x4*>(st + 3 * PART_B + (wv * TN + 2 * l) * 16) = b0;
     *reinterpret_cast<u32x4*>(st + 3 * PART_B + (wv * TN + 2 * l + 1) * 16) = b1;
   };
@@ -160,13 +173,20 @@ __global__ void __launch_bounds__(rd::NT, 2)
 #pragma unroll
     for (int j = 0; j < 2; ++j) acc[i][j] = f32x16{};
   const int nk = (E + BK - 1) / BK;
-  load(0);
-  store(lds);
+  RdRegs q0, q1;
+  load(q0, 0);
+  load(q1, BK);
+  store(q0, lds, 0);
   __syncthreads();
-  for (int s = 0; s < nk; ++s) {
-    if (s + 1 < nk) load((s + 1) * BK);  // in flight during this slab's MFMAs
-    rd_compute(lds + (s & 1) * STAGE, wm, wn, acc);
-    if (s + 1 < nk) store(lds + ((s + 1) & 1) * STAGE);
+  for (int s = 0; s < nk; s += 2) {  // (slabs past the last are zeros)
+    load(q0, (s + 2) * BK);
+    rd_compute(lds, wm, wn, acc);
+    store(q1, lds + STAGE, (s + 1) * BK);
+    __syncthreads();
+    if (s + 1 >= nk) break;
+    load(q1, (s + 3) * BK);
+    rd_compute(lds + STAGE, wm, wn, acc);
+    store(q0, lds, (s + 2) * BK);
     __syncthreads();
   }
   // the tile through LDS, so that a thread adds whole 16-byte pieces of rows
@@ -182,20 +202,33 @@ __global__ void __launch_bounds__(rd::NT, 2)
   __syncthreads();
   const int64_t col = c0 + 4 * (tid & 31);
   if (col >= d) return;
-  for (int r = tid >> 5; r < TM; r += NT / 32) {
-    const int64_t t = t0 + r;
-    if (t >= T) break;
-    f32x4 v[MAXK];
+  // ROWS tokens x JS slots of row loads in flight per lane
+  constexpr int ROWS = 4, JS = 8;
+  for (int r0 = tid >> 5; r0 < TM && t0 + r0 < T; r0 += ROWS * (NT / 32)) {
+    f32x4 sum[ROWS];
 #pragma unroll
-    for (int j = 0; j < MAXK; ++j)
-      if (j < k) v[j] = *reinterpret_cast<const f32x4*>(dxp + clamp_row(inv[t * k + j], T * k, &g_dev_err) * d + col);
-    f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int i = 0; i < ROWS; ++i) sum[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    for (int j0 = 0; j0 < k; j0 += JS) {
+      f32x4 v[ROWS][JS];
 #pragma unroll
-    for (int j = 0; j < MAXK; ++j)
-      if (j < k) s = s + v[j];
-    s = s + *reinterpret_cast<const f32x4*>(tl + r * TN + 4 * (tid & 31));
-    *reinterpret_cast<u32x2*>(dx + t * d + col) = u32x2{f32_to_bf16_bits(s[0]) | (f32_to_bf16_bits(s[1]) << 16),
-                                                        f32_to_bf16_bits(s[2]) | (f32_to_bf16_bits(s[3]) << 16)};
+      for (int i = 0; i < ROWS; ++i)
+#pragma unroll
+        for (int j = 0; j < JS; ++j)
+          if (j0 + j < k) v[i][j] = *reinterpret_cast<const f32x4*>(dxp + (int64_t)rows[(r0 + i * (NT / 32)) * k + j0 + j] * d + col);
+#pragma unroll
+      for (int i = 0; i < ROWS; ++i)
+#pragma unroll
+        for (int j = 0; j < JS; ++j)
+          if (j0 + j < k) sum[i] = sum[i] + v[i][j];
+    }
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+      const int r = r0 + i * (NT / 32);
+      if (t0 + r >= T) break;
+      const f32x4 s = sum[i] + *reinterpret_cast<const f32x4*>(tl + r * TN + 4 * (tid & 31));
+      *reinterpret_cast<u32x2*>(dx + (t0 + r) * d + col) = u32x2{f32_to_bf16_bits(s[0]) | (f32_to_bf16_bits(s[1]) << 16),
+                                                               f32_to_bf16_bits(s[2]) | (f32_to_bf16_bits(s[3]) << 16)};
+    }
   }
 }
 
@@ -208,34 +241,32 @@ __global__ void __launch_bounds__(rd::NT, 2)
   __shared__ __attribute__((aligned(16))) uint8_t lds[2 * STAGE];
   const int64_t e0 = (blockIdx.x / n_nt) * TM, c0 = (blockIdx.x % n_nt) * TN;
   const int64_t ta = (int64_t)blockIdx.y * share, tb = ta + share < T ? ta + share : T;
-  const int tid = threadIdx.x, l = tid & 63, wv = tid >> 6;
+  const int tid = threadIdx.x, l = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = (wv >> 1) * 64, wn = (wv & 1) * 64;
   // dz: units (chunk wv, expert l + 64 j); x: unit (chunk wv, columns 2 l, 2 l + 1)
   const int64_t bc = c0 + 2 * l;
-  float av[2][8];
-  uint32_t bw[8];
-  auto load = [&](int64_t k0) {
+  const uint32_t zo = (uint32_t)(e0 + l) * 4, xo = (uint32_t)bc * 2;
+  auto load = [&](RdRegs& q, int64_t k0) {  // a descriptor per row: tokens past the share, experts past E, columns past d are 0
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const int64_t t = k0 + 8 * wv + i;
+      const int64_t t = k0 + 8 * wv + i, tr = t < tb ? t : 0;
+      const __amdgpu_buffer_rsrc_t rz = make_rsrc(dz + tr * E, t < tb ? (uint64_t)E * 4 : 0);
+      const __amdgpu_buffer_rsrc_t rx = make_rsrc(x + tr * d, t < tb ? (uint64_t)d * 2 : 0);
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int64_t e = e0 + l + 64 * j;
-        av[j][i] = t < tb && e < E ? dz[t * E + e] : 0.0f;
-      }
-      bw[i] = t < tb && bc < d ? *reinterpret_cast<const uint32_t*>(x + t * d + bc) : 0u;
+      for (int j = 0; j < 2; ++j) q.a[j][i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rz, zo + 256 * j, 0, 0));
+      q.b[i] = __builtin_amdgcn_raw_buffer_load_b32(rx, xo, 0, 0);
     }
   };
-  auto store = [&](uint8_t* st) {
+  auto store = [&](const RdRegs& q, uint8_t* st) {
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
       u32x4 o[3];
-      split3(av[j], o);
+      split3(q.a[j], o);
 #pragma unroll
       for (int p = 0; p < 3; ++p) *reinterpret_cast<u32x4*>(st + p * PART_B + (wv * TM + l + 64 * j) * 16) = o[p];
     }
     u32x4 b0, b1;
-    columns2(bw, b0, b1);
+    columns2(q.b, b0, b1);
     *reinterpret_cast<u32x4*>(st + 3 * PART_B + (wv * TN + 2 * l) * 16) = b0;
     *reinterpret_cast<u32x4*>(st + 3 * PART_B + (wv * TN + 2 * l + 1) * 16) = b1;
   };
@@ -245,15 +276,20 @@ __global__ void __launch_bounds__(rd::NT, 2)
 #pragma unroll
     for (int j = 0; j < 2; ++j) acc[i][j] = f32x16{};
   const int nk = tb > ta ? (int)((tb - ta + BK - 1) / BK) : 0;
-  if (nk > 0) {
-    load(ta);
-    store(lds);
-  }
+  RdRegs q0, q1;
+  load(q0, ta);
+  load(q1, ta + BK);
+  store(q0, lds);
   __syncthreads();
-  for (int s = 0; s < nk; ++s) {
-    if (s + 1 < nk) load(ta + (int64_t)(s + 1) * BK);
-    rd_compute(lds + (s & 1) * STAGE, wm, wn, acc);
-    if (s + 1 < nk) store(lds + ((s + 1) & 1) * STAGE);
+  for (int s = 0; s < nk; s += 2) {  // (slabs past the last load zeros)
+    load(q0, ta + (int64_t)(s + 2) * BK);
+    rd_compute(lds, wm, wn, acc);
+    store(q1, lds + STAGE);
+    __syncthreads();
+    if (s + 1 >= nk) break;
+    load(q1, ta + (int64_t)(s + 3) * BK);
+    rd_compute(lds + STAGE, wm, wn, acc);
+    store(q0, lds);
     __syncthreads();
   }
   const int li = l & 31, g = l >> 5;
