@@ -64,8 +64,7 @@ __device__ inline void columns2(const uint32_t (&w)[8], u32x4& c0, u32x4& c1) {
 }
 
 // A thread's share of one slab in registers: 8 k of two rows or columns of dz
-// and of two columns of the other operand.  The kernels keep two of them, so
-// that a slab's loads have two slabs' MFMAs to land in.
+// and of two columns of the other operand.
 struct RdRegs {
   float a[2][8];
   uint32_t b[8];
@@ -107,14 +106,14 @@ __device__ inline int64_t clamp_row(int64_t i, int64_t n, uint32_t* err) {
 static __device__ uint32_t g_dev_err;
 uint32_t take_dev_err_router_dense() { return take_device_word(&g_dev_err); }
 
-__global__ void __launch_bounds__(rd::NT, 2)
+__global__ void __launch_bounds__(rd::NT, 4)
     k_router_dx_dense(const float* __restrict__ dxp, const int32_t* __restrict__ inv, int64_t T, int k, int64_t d,
                       const float* __restrict__ dz, int E, const uint16_t* __restrict__ w, int64_t n_nt, int64_t n_all,
                       uint16_t* __restrict__ dx) {
   using namespace rd;
-  __shared__ __attribute__((aligned(16))) uint8_t lds[2 * STAGE];  // two stages; then the float32 tile (64 KB both)
+  __shared__ __attribute__((aligned(16))) uint8_t lds[STAGE];  // a slab; then half the float32 tile (32 KB both)
   __shared__ int32_t rows[TM * MAXK];                              // dXp's rows of the tile's tokens
-  static_assert(2 * STAGE >= TM * TN * 4, "the epilogue's tile");
+  static_assert(STAGE >= TM * TN * 2, "the epilogue's half tile");
   const int64_t tile = xcd_tile(blockIdx.x, n_all);
   if (tile >= n_all) return;
   const int64_t t0 = (tile / n_nt) * TM, c0 = (tile % n_nt) * TN;
@@ -173,72 +172,60 @@ __global__ void __launch_bounds__(rd::NT, 2)
 #pragma unroll
     for (int j = 0; j < 2; ++j) acc[i][j] = f32x16{};
   const int nk = (E + BK - 1) / BK;
-  RdRegs q0, q1;
-  load(q0, 0);
-  load(q1, BK);
-  store(q0, lds, 0);
-  __syncthreads();
-  for (int s = 0; s < nk; s += 2) {  // (slabs past the last are zeros)
-    load(q0, (s + 2) * BK);
-    rd_compute(lds, wm, wn, acc);
-    store(q1, lds + STAGE, (s + 1) * BK);
+  RdRegs q;
+  load(q, 0);
+  for (int s = 0; s < nk; ++s) {
+    store(q, lds, s * BK);
     __syncthreads();
-    if (s + 1 >= nk) break;
-    load(q1, (s + 3) * BK);
-    rd_compute(lds + STAGE, wm, wn, acc);
-    store(q0, lds, (s + 2) * BK);
+    if (s + 1 < nk) load(q, (s + 1) * BK);  // in flight during this slab's MFMAs
+    rd_compute(lds, wm, wn, acc);
     __syncthreads();
   }
-  // the tile through LDS, so that a thread adds whole 16-byte pieces of rows
+  // the tile through LDS, 64 rows at a time, so that a thread adds whole
+  // 16-byte pieces of rows
   float* tl = reinterpret_cast<float*>(lds);
   const int li = l & 31, g = l >> 5;
-#pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int j = 0; j < 2; ++j)
-#pragma unroll
-      for (int v = 0; v < 16; ++v)
-        tl[(wm + 32 * i + (v >> 2) * 8 + 4 * g + (v & 3)) * TN + wn + 32 * j + li] = acc[i][j][v];
-  __syncthreads();
   const int64_t col = c0 + 4 * (tid & 31);
-  if (col >= d) return;
-  // ROWS tokens x JS slots of row loads in flight per lane
-  constexpr int ROWS = 4, JS = 8;
-  for (int r0 = tid >> 5; r0 < TM && t0 + r0 < T; r0 += ROWS * (NT / 32)) {
-    f32x4 sum[ROWS];
 #pragma unroll
-    for (int i = 0; i < ROWS; ++i) sum[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    for (int j0 = 0; j0 < k; j0 += JS) {
-      f32x4 v[ROWS][JS];
+  for (int h = 0; h < 2; ++h) {
+    if (wm == 64 * h) {
 #pragma unroll
-      for (int i = 0; i < ROWS; ++i)
+      for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int j = 0; j < JS; ++j)
-          if (j0 + j < k) v[i][j] = *reinterpret_cast<const f32x4*>(dxp + (int64_t)rows[(r0 + i * (NT / 32)) * k + j0 + j] * d + col);
+        for (int j = 0; j < 2; ++j)
 #pragma unroll
-      for (int i = 0; i < ROWS; ++i)
-#pragma unroll
-        for (int j = 0; j < JS; ++j)
-          if (j0 + j < k) sum[i] = sum[i] + v[i][j];
+          for (int v = 0; v < 16; ++v) tl[(32 * i + (v >> 2) * 8 + 4 * g + (v & 3)) * TN + wn + 32 * j + li] = acc[i][j][v];
     }
+    __syncthreads();
+    constexpr int JS = 8;  // row loads in flight per lane (with more, fewer workgroups fit: slower)
+    if (col < d)
+      for (int r = tid >> 5; r < 64 && t0 + 64 * h + r < T; r += NT / 32) {
+        const int32_t* rw = rows + (64 * h + r) * k;
+        f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (int j0 = 0; j0 < k; j0 += JS) {
+          f32x4 v[JS];
 #pragma unroll
-    for (int i = 0; i < ROWS; ++i) {
-      const int r = r0 + i * (NT / 32);
-      if (t0 + r >= T) break;
-      const f32x4 s = sum[i] + *reinterpret_cast<const f32x4*>(tl + r * TN + 4 * (tid & 31));
-      *reinterpret_cast<u32x2*>(dx + (t0 + r) * d + col) = u32x2{f32_to_bf16_bits(s[0]) | (f32_to_bf16_bits(s[1]) << 16),
-                                                               f32_to_bf16_bits(s[2]) | (f32_to_bf16_bits(s[3]) << 16)};
-    }
+          for (int j = 0; j < JS; ++j)
+            if (j0 + j < k) v[j] = *reinterpret_cast<const f32x4*>(dxp + (int64_t)rw[j0 + j] * d + col);
+#pragma unroll
+          for (int j = 0; j < JS; ++j)
+            if (j0 + j < k) s = s + v[j];
+        }
+        s = s + *reinterpret_cast<const f32x4*>(tl + r * TN + 4 * (tid & 31));
+        *reinterpret_cast<u32x2*>(dx + (t0 + 64 * h + r) * d + col) = u32x2{f32_to_bf16_bits(s[0]) | (f32_to_bf16_bits(s[1]) << 16),
+                                                                          f32_to_bf16_bits(s[2]) | (f32_to_bf16_bits(s[3]) << 16)};
+      }
+    __syncthreads();
   }
 }
 
 // Workgroup (tile, token share z): out + z * E * d gets the share's partial
 // products (out is dW itself when there is one share).
-__global__ void __launch_bounds__(rd::NT, 2)
+__global__ void __launch_bounds__(rd::NT, 4)
     k_router_dw_dense(const uint16_t* __restrict__ x, const float* __restrict__ dz, int64_t T, int E, int64_t d,
                       int64_t n_nt, int64_t share, float* __restrict__ out) {
   using namespace rd;
-  __shared__ __attribute__((aligned(16))) uint8_t lds[2 * STAGE];
+  __shared__ __attribute__((aligned(16))) uint8_t lds[STAGE];
   const int64_t e0 = (blockIdx.x / n_nt) * TM, c0 = (blockIdx.x % n_nt) * TN;
   const int64_t ta = (int64_t)blockIdx.y * share, tb = ta + share < T ? ta + share : T;
   const int tid = threadIdx.x, l = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -276,20 +263,13 @@ __global__ void __launch_bounds__(rd::NT, 2)
 #pragma unroll
     for (int j = 0; j < 2; ++j) acc[i][j] = f32x16{};
   const int nk = tb > ta ? (int)((tb - ta + BK - 1) / BK) : 0;
-  RdRegs q0, q1;
-  load(q0, ta);
-  load(q1, ta + BK);
-  store(q0, lds);
-  __syncthreads();
-  for (int s = 0; s < nk; s += 2) {  // (slabs past the last load zeros)
-    load(q0, ta + (int64_t)(s + 2) * BK);
-    rd_compute(lds, wm, wn, acc);
-    store(q1, lds + STAGE);
+  RdRegs q;
+  load(q, ta);
+  for (int s = 0; s < nk; ++s) {
+    store(q, lds);
     __syncthreads();
-    if (s + 1 >= nk) break;
-    load(q1, ta + (int64_t)(s + 3) * BK);
-    rd_compute(lds + STAGE, wm, wn, acc);
-    store(q0, lds);
+    if (s + 1 < nk) load(q, ta + (int64_t)(s + 1) * BK);  // in flight during this slab's MFMAs
+    rd_compute(lds, wm, wn, acc);
     __syncthreads();
   }
   const int li = l & 31, g = l >> 5;
@@ -318,11 +298,11 @@ __global__ void __launch_bounds__(256) k_router_dw_join(const f32x4* __restrict_
   dw[i] = s;
 }
 
-// Token shares of the weight gradient: enough workgroups for two per CU
-// (rd::NT threads and 64 KB of LDS each), at least 8 slabs each.
+// Token shares of the weight gradient: enough workgroups for four per CU, at
+// least 8 slabs each.
 inline int dw_shares(int64_t T, int E, int64_t d) {
   const int64_t tiles = ((E + rd::TM - 1) / rd::TM) * ((d + rd::TN - 1) / rd::TN);
-  int64_t n = 512 / tiles;
+  int64_t n = 1024 / tiles;
   const int64_t most = T / (8 * rd::BK);
   if (n > most) n = most;
   return (int)(n < 1 ? 1 : n);
