@@ -37,6 +37,14 @@ constexpr int KB = 128;           // K per step: lane (li, q) holds k = 128 s + 
 constexpr int PASSES = 4, TR = 16 * PASSES;
 }  // namespace m4s
 
+// lo | hi << 16 rounded to nearest even, by the converter (one instruction
+// where integer arithmetic takes eight)
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{lo, hi}), bf16x2));
+}
+
 // The expert and the tile in it of item idx, the experts holding count(rows)
 // items each, in order; false past the last.  Lane l counts the experts
 // [l P, (l + 1) P), so all the offsets are in flight at once.
@@ -173,7 +181,7 @@ __global__ void __launch_bounds__(m4s::NT)
       const f32x4 v = ((red[0][w][l] + red[1][w][l]) + red[2][w][l]) + red[3][w][l];
       if (OUT_BF16)
         *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(c) + row * N + col) =
-            u32x2{f32_to_bf16_bits(v[0]) | (f32_to_bf16_bits(v[1]) << 16), f32_to_bf16_bits(v[2]) | (f32_to_bf16_bits(v[3]) << 16)};
+            u32x2{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])};
       else
         *reinterpret_cast<f32x4*>(static_cast<float*>(c) + row * N + col) = v;
     }
@@ -209,7 +217,6 @@ typedef __attribute__((address_space(3))) void* lds_ptr;
 // address that each lane loads
 __device__ inline int swz(int row, int c) { return c ^ ((row >> 1) & 7); }
 // 16 bytes at each lane's offset + soff into lane-consecutive LDS from p on
-// (the descriptor's range check sees the lane's offset alone)
 __device__ __forceinline__ void load_lds(const __amdgpu_buffer_rsrc_t& rs, uint8_t* p, uint32_t off, uint32_t soff) {
   __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (lds_ptr)p, 16, off, soff, 0, 0);
 }
@@ -525,7 +532,7 @@ __global__ void __launch_bounds__(m4w::NT, 1)
             const uint32_t so = fo + (uint32_t)((v >> 2) * 8 + (v & 3)) * ld;
             const float v0 = acc[i][j][v], v1 = acc[i][j + 1][v];
             if (OUT_BF16)
-              __builtin_amdgcn_raw_buffer_store_b32(f32_to_bf16_bits(v0) | (f32_to_bf16_bits(v1) << 16), rC, vo, so, NT_STORE);
+              __builtin_amdgcn_raw_buffer_store_b32(bf16_pair(v0, v1), rC, vo, so, NT_STORE);
             else
               __builtin_amdgcn_raw_buffer_store_b64(u32x2{__float_as_uint(v0), __float_as_uint(v1)}, rC, vo, so, NT_STORE);
           }
@@ -554,12 +561,21 @@ template <bool OUT_BF16>
 static void launch_mx4(const uint8_t* ac, const uint8_t* as, const uint8_t* bc, const uint8_t* bs, const int32_t* off, int E,
                        int64_t M, int64_t N, int64_t K, void* c, hipStream_t s) {
   const bool al = K % 128 == 0 && aligned4(as) && aligned4(bs);
-  if (M <= 32 * (int64_t)E) {
+  const dim3 grid((unsigned)(cu_count() < 8 ? 8 : cu_count()));
+  // Few rows: up to 4 per expert on average, or up to 32 where the tiled kernel
+  // would not have a tile for every CU.  N = 1536, K = 4096, few-rows against
+  // tiled kernel, even routing | one power-law routing (1.1), in us:
+  //   384 experts, rows per expert 4: 242 - 286 | 88 - 76;  8: 254 - 284 | 130 - 83;
+  //   11: 261 - 285 | 163 - 86;  16: 301 - 285 | 210 - 110;  32: 405 - 293 | 363 - 162
+  //   (a popular expert's weights are read again for every 32 rows);
+  //   8 experts, rows per expert 8, 16, 32: 12 - 19, 12 - 19, 14 - 20
+  const int64_t tiles = ((M < E ? M : E) + M / m4w::TM) * ((N + 255) / 256);
+  if (M <= 4 * (int64_t)E || (M <= 32 * (int64_t)E && tiles < grid.x)) {
     const int64_t n_nt = (N + m4s::WROWS - 1) / m4s::WROWS, first = M < E ? M : E, slots = first + M / m4s::TR;
-    const dim3 grid((unsigned)(n_nt * slots));
+    const dim3 rgrid((unsigned)(n_nt * slots));
     const int64_t spw = ((K + m4s::KB - 1) / m4s::KB + m4s::NWV - 1) / m4s::NWV;
 #define MOE4_MX4S(AL, NS)                                                                                                      \
-  hipLaunchKernelGGL((k_gemm_mx4_rows<OUT_BF16, AL, NS>), grid, dim3(m4s::NT), 0, s, ac, as, bc, bs, off, E, M, N, K,           \
+  hipLaunchKernelGGL((k_gemm_mx4_rows<OUT_BF16, AL, NS>), rgrid, dim3(m4s::NT), 0, s, ac, as, bc, bs, off, E, M, N, K,           \
                      (uint32_t)n_nt, first, c)
 #define MOE4_MX4S_AL(NS)            \
   do {                              \
@@ -575,7 +591,6 @@ static void launch_mx4(const uint8_t* ac, const uint8_t* as, const uint8_t* bc, 
 #undef MOE4_MX4S
     return;
   }
-  const dim3 grid((unsigned)(cu_count() < 8 ? 8 : cu_count()));
   const bool pair = K % 512 == 0 && aligned16(as) && aligned16(bs);
 #define MOE4_MX4(TN, AL)                                                                                                       \
   hipLaunchKernelGGL((k_gemm_mx4_ws<OUT_BF16, TN, AL>), grid, dim3(m4w::NT), 0, s, ac, as, bc, bs, off, E, M, N, K,             \

@@ -197,6 +197,17 @@ def test_gemm(M_list, N, K, dt):
     _gemm_check(got, og.grouped_nt(A, B, off), og.abs_bound_nt(A, B, off), K, dt == "bf16")
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("N,K", [(288, 512), (288, 160), (544, 512)])
+def test_gemm_many_experts_of_few_rows(N, K, dt):
+    """Between the few-rows kernel's four rows per expert and a tile's 128: most experts end inside a tile."""
+    M_list = [(7 * i) % 23 if i % 3 else 0 for i in range(159)] + [301]
+    off, qa, qb = _operands(M_list, N, K, N + K)
+    got = _product(off, qa, qb, N, K, torch.bfloat16 if dt == "bf16" else torch.float32).float().cpu().numpy().astype(np.float64)
+    A, B = mxfp4.dequant(*qa), mxfp4.dequant(*qb).reshape(len(M_list), N, K)
+    _gemm_check(got, og.grouped_nt(A, B, off), og.abs_bound_nt(A, B, off), K, dt == "bf16")
+
+
 @pytest.mark.parametrize("shift_a,shift_b", [(1, 0), (0, 3), (2, 1)])
 @pytest.mark.parametrize("M_list,N,K", [([150, 3, 77], 160, 512), ([2, 1], 64, 512), ([90, 40], 96, 544)])
 def test_gemm_scales_at_any_alignment(M_list, N, K, shift_a, shift_b):
