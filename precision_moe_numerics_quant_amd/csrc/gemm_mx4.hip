@@ -196,10 +196,10 @@ __global__ void __launch_bounds__(m4s::NT)
 // (v_mfma_scale_f32_32x32x64_f8f6f4) and store; one barrier per slab.  128 x
 // TN tiles: consumers of 64 x TN / 2.
 //
-// Every load goes through a buffer descriptor that ends with the operand's
-// rows, so rows past M or N and K chunks past K (their lanes' offsets are set
-// out of range) arrive as zeros and no shape needs a kernel of its own; rows
-// past the expert's last are the next expert's, and their results not stored.
+// Every load goes through a buffer descriptor that ends with the expert's
+// rows, so rows past its last or N and K chunks past K (their lanes' offsets are
+// set out of range) arrive as zeros, cost no traffic and no shape needs a kernel
+// of its own.
 //
 // Scales: a wave's load of 64 rows' scales touches 64 cache lines whatever it
 // takes from each, as long as four of its whole-row code loads, so the fewest
@@ -295,8 +295,11 @@ __global__ void __launch_bounds__(m4w::NT, 1)
       int64_t row0 = (int64_t)ld_const(off, e) + (int64_t)(mi - cur.first) * TM;
       const int64_t n0 = (int64_t)nt * TN;
       const int64_t end = (int64_t)ld_const(off, e + 1) < M_total ? (int64_t)ld_const(off, e + 1) : M_total;
-      if (row0 < 0 || row0 >= end) row0 = 0;  // (offsets outside [0, M]: other rows are read, none stored)
-      const int64_t ra = M_total - row0 < TM ? M_total - row0 : TM;
+      int64_t ra = end - row0 < TM ? end - row0 : TM;
+      if (row0 < 0 || ra <= 0) {  // (offsets outside [0, M]: a row is read, none stored)
+        row0 = 0;
+        ra = 1;
+      }
       const int64_t rb = N - n0 < TN ? N - n0 : TN, rowb = (int64_t)e * N + n0;
       rac = make_rsrc(a_codes + row0 * KH, (uint64_t)ra * KH);
       rbc = make_rsrc(b_codes + rowb * KH, (uint64_t)rb * KH);
