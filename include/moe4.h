@@ -74,7 +74,7 @@ extern "C" {
 #define MOE4_DEVERR_WAIT 1u   /* a bounded wait between workgroups gave up: that
                                  call's results are wrong                       */
 #define MOE4_DEVERR_INDEX 2u  /* a routed row index outside its range was
-                                 clamped (gather, combine, un-permute, dgates,  \
+                                 clamped (gather, combine, un-permute, dgates,
                                  balance counts) or dropped (mxfp4_quant)       */
 
 #define MOE4_BF16 0
@@ -693,7 +693,8 @@ size_t moe_router_wgrad_ws_bytes(int64_t T, int32_t E, int32_t k, int64_t d);
  *   loss[s]      = E / (k * n_s) * sum_e counts[s, e] * probs[s, e]
  * (1 for an even router).  A segment without unmasked tokens has loss, probs
  * and counts 0.  A row of z that is -infinity throughout has probabilities 0;
- * -infinity elsewhere is a probability of 0.
+ * -infinity elsewhere is a probability of 0; a NaN or +infinity makes the row's
+ * probabilities NaN.
  * token_mask [T] uint8 or NULL: 0 = a padding token, whose logits and topk_idx
  *          are not read.
  * seg_off  NULL (n_seg = 1: one segment of all T tokens) or [n_seg + 1]
@@ -732,8 +733,8 @@ int moe_balance_loss_backward(const float* dloss, const float* logits, const flo
  * with float32 sums (the k rows in slot order; the products exact, from three
  * bf16 parts of each dlogits value, accumulated in float32 by the MFMA).
  * dxp [T*k, d] float32, dlogits [T, E] float32, w [E, d] bf16, dx [T, d] bf16,
- * all 16-byte aligned.  1 <= k <= 16, d % 4 == 0.  Out-of-range rows are
- * clamped and reported (MOE4_DEVERR_INDEX).
+ * all 16-byte aligned.  1 <= k <= 16, E < 2^20, d < 2^28, d % 4 == 0.
+ * Out-of-range rows are clamped and reported (MOE4_DEVERR_INDEX).
  */
 int moe_unpermute_sum_router_dense(const float* dxp, const int32_t* inv_perm, int64_t T, int32_t k, int64_t d,
                                    const float* dlogits, int32_t E, const uint16_t* w, uint16_t* dx, void* stream);
@@ -743,7 +744,8 @@ int moe_unpermute_sum_router_dense(const float* dxp, const int32_t* inv_perm, in
  * dlogits[t, e] * x[t, c]: the router's weight gradient for a dense logit
  * gradient.  Exact products as above, float32 accumulation, tokens cut into
  * shares whose sums are added in order (deterministic).  x [T, d] bf16,
- * dlogits [T, E], dw: 16-byte aligned; d % 4 == 0; zeros for T = 0.
+ * dlogits [T, E], dw: 16-byte aligned; E < 2^20, d < 2^28, d % 4 == 0; zeros
+ * for T = 0.
  * ws: moe_router_wgrad_dense_ws_bytes(T, E, d) bytes (0 for few tokens, then
  * ws may be NULL), the caller's, overwritten.
  */

@@ -37,14 +37,6 @@ constexpr int KB = 128;           // K per step: lane (li, q) holds k = 128 s + 
 constexpr int PASSES = 4, TR = 16 * PASSES;
 }  // namespace m4s
 
-// lo | hi << 16 rounded to nearest even, by the converter (one instruction
-// where integer arithmetic takes eight)
-__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
-  typedef float f32x2 __attribute__((ext_vector_type(2)));
-  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{lo, hi}), bf16x2));
-}
-
 // The expert and the tile in it of item idx, the experts holding count(rows)
 // items each, in order; false past the last.  Lane l counts the experts
 // [l P, (l + 1) P), so all the offsets are in flight at once.

@@ -109,6 +109,14 @@ __device__ inline uint32_t f32_to_bf16_bits(float f) {
   return (u + 0x7FFFu + ((u >> 16) & 1u)) >> 16;
 }
 
+// lo | hi << 16 rounded to nearest even, by the converter (one instruction
+// where integer arithmetic takes eight)
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2{lo, hi}), bf16x2));
+}
+
 // Exact float32 value of an E4M3FN byte b < 256 (NaN codes never occur here):
 // gfx950's FP8 converter decodes the OCP E4M3 format, and decodes all 254
 // non-NaN bytes to the values of the field-by-field definition (exponent

@@ -31,6 +31,7 @@ constexpr int KC = BK / 8;                  // 8-deep k chunks of a slab
 constexpr int PART_B = KC * TM * 16;        // bytes of one bf16 operand slab
 constexpr int STAGE = 4 * PART_B;           // three parts of dz, one of the other operand
 constexpr int MAXK = 16;
+constexpr int64_t MAXE = (1 << 20) - 1, MAXD = (1 << 28) - 1;  // (128 rows of dz and a row of W_r: 31-bit byte ranges)
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 }  // namespace rd
 
@@ -212,8 +213,7 @@ __global__ void __launch_bounds__(rd::NT, 4)
             if (j0 + j < k) s = s + v[j];
         }
         s = s + *reinterpret_cast<const f32x4*>(tl + r * TN + 4 * (tid & 31));
-        *reinterpret_cast<u32x2*>(dx + (t0 + 64 * h + r) * d + col) = u32x2{f32_to_bf16_bits(s[0]) | (f32_to_bf16_bits(s[1]) << 16),
-                                                                          f32_to_bf16_bits(s[2]) | (f32_to_bf16_bits(s[3]) << 16)};
+        *reinterpret_cast<u32x2*>(dx + (t0 + 64 * h + r) * d + col) = u32x2{bf16_pair(s[0], s[1]), bf16_pair(s[2], s[3])};
       }
     __syncthreads();
   }
@@ -315,8 +315,8 @@ using namespace moe4;
 extern "C" int moe_unpermute_sum_router_dense(const float* dxp, const int32_t* inv_perm, int64_t T, int32_t k, int64_t d,
                                               const float* dlogits, int32_t E, const uint16_t* w, uint16_t* dx,
                                               void* stream) {
-  MOE4_REQUIRE(T >= 0 && E >= 1 && k >= 1 && k <= rd::MAXK && d > 0 && d % 4 == 0, MOE4_EINVAL,
-               "moe_unpermute_sum_router_dense: need 1 <= k <= 16, E >= 1 and d % 4 == 0");
+  MOE4_REQUIRE(T >= 0 && E >= 1 && E <= rd::MAXE && k >= 1 && k <= rd::MAXK && d > 0 && d <= rd::MAXD && d % 4 == 0, MOE4_EINVAL,
+               "moe_unpermute_sum_router_dense: need 1 <= k <= 16, 1 <= E < 2^20, 0 < d < 2^28 and d % 4 == 0");
   MOE4_REQUIRE(T * (int64_t)k < ((int64_t)1 << 31), MOE4_EINVAL, "moe_unpermute_sum_router_dense: T * k must be below 2^31");
   MOE4_REQUIRE(T == 0 || (dxp && inv_perm && dlogits && w && dx), MOE4_EINVAL, "moe_unpermute_sum_router_dense: NULL pointer");
   MOE4_REQUIRE(aligned16(dxp) && aligned16(dlogits) && aligned16(w) && aligned16(dx), MOE4_EALIGN,
@@ -337,7 +337,8 @@ extern "C" size_t moe_router_wgrad_dense_ws_bytes(int64_t T, int32_t E, int64_t 
 
 extern "C" int moe_router_wgrad_dense(const uint16_t* x, const float* dlogits, int64_t T, int32_t E, int64_t d, float* dw,
                                       void* ws, size_t ws_bytes, void* stream) {
-  MOE4_REQUIRE(T >= 0 && E >= 1 && d > 0 && d % 4 == 0, MOE4_EINVAL, "moe_router_wgrad_dense: need T >= 0, E >= 1 and d % 4 == 0");
+  MOE4_REQUIRE(T >= 0 && E >= 1 && E <= rd::MAXE && d > 0 && d <= rd::MAXD && d % 4 == 0, MOE4_EINVAL,
+               "moe_router_wgrad_dense: need T >= 0, 1 <= E < 2^20, 0 < d < 2^28 and d % 4 == 0");
   MOE4_REQUIRE(dw && (T == 0 || (x && dlogits)), MOE4_EINVAL, "moe_router_wgrad_dense: NULL pointer");
   MOE4_REQUIRE(aligned16(x) && aligned16(dlogits) && aligned16(dw), MOE4_EALIGN,
                "moe_router_wgrad_dense: x, dlogits and dw must be 16-byte aligned");

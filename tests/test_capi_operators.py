@@ -99,6 +99,14 @@ def test_router_wgrad_dense_refusals(kw, rc):
                 v(0)) == rc
 
 
+@pytest.mark.parametrize("kw", [dict(E=1 << 20), dict(d=1 << 28)])
+def test_router_dense_sizes_past_a_descriptor(kw):
+    a = dict(E=4, d=64)
+    a.update(kw)
+    assert call("moe_unpermute_sum_router_dense", P, P, i64(8), i32(2), i64(a["d"]), P, i32(a["E"]), P, P, v(0)) == EINVAL
+    assert call("moe_router_wgrad_dense", P, P, i64(8), i32(a["E"]), i64(a["d"]), P, P, size(1 << 40), v(0)) == EINVAL
+
+
 def test_workspace_queries():
     L = _lib()
     L.moe_balance_loss_ws_bytes.restype = L.moe_router_wgrad_dense_ws_bytes.restype = size

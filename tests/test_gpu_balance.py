@@ -198,6 +198,24 @@ def test_dense_router_split_is_exact():
     assert np.array_equal(dw, dz.T * np.float32(0.5))
 
 
+def test_dense_router_gradients_that_are_not_finite():
+    """A NaN (every mantissa bit set) and an infinity spoil their token's dx and their expert's dW, and nothing else."""
+    T, E, d, k = 130, 40, 64, 2
+    rng = np.random.default_rng(3)
+    dz = rng.standard_normal((T, E)).astype(np.float32)
+    dz.view(np.uint32)[3, 5] = 0x7FFFFFFF
+    dz[129, 39] = np.inf
+    w = fmt.f64_to_bf16(1 + rng.random((E, d)))
+    x = fmt.f64_to_bf16(1 + rng.random((T, d)))
+    dx = m4.moe_unpermute_sum_router_dense(cuda_f32(np.ones((T * k, d), np.float32)), cuda_i32(rng.permutation(T * k).astype(np.int32)),
+                                           T, k, cuda_f32(dz), bf16_from_bits(w)).float().cpu().numpy()
+    bad = np.isin(np.arange(T), [3, 129])
+    assert not np.isfinite(dx[bad]).any() and np.isfinite(dx[~bad]).all()
+    dw = to_np(m4.moe_router_wgrad_dense(bf16_from_bits(x), cuda_f32(dz)))
+    bad = np.isin(np.arange(E), [5, 39])
+    assert not np.isfinite(dw[bad]).any() and np.isfinite(dw[~bad]).all()
+
+
 def test_dense_router_empty_batch_and_bad_rows():
     w = torch.zeros((8, 64), dtype=torch.bfloat16, device="cuda")
     x = torch.zeros((0, 64), dtype=torch.bfloat16, device="cuda")
