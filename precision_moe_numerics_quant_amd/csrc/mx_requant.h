@@ -133,6 +133,19 @@ __device__ inline void requant_block(Deq deq, int nvalid, float S, const float (
   }
 }
 
+// The tile's scale bytes (see rq_store_tile).
+__device__ inline void rq_store_scales(const uint8_t* lsf, const int64_t (&lblk)[rq::WAVES][3], int64_t c0, int64_t C,
+                                       int sfb, uint8_t* __restrict__ out_s) {
+  using namespace rq;
+#pragma unroll
+  for (int it = 0; it < COLS * WAVES / THREADS; ++it) {
+    const int idx = it * THREADS + threadIdx.x;
+    const int col = sfb ? idx % COLS : idx >> 2, b = sfb ? idx / COLS : idx & 3;
+    const int64_t Pb = lblk[b][1], gc = c0 + col;
+    if (Pb != 0 && gc < C) out_s[lblk[b][2] + (sfb ? gc : gc * (Pb / 32))] = lsf[col * WAVES + b];
+  }
+}
+
 // Store a workgroup's staged tile: lq [column][128 rows] (16-byte chunks
 // swizzled by column) leaves as each column's 128-byte runs of the 4 blocks;
 // lsf [column][block] as scale bytes, row-major (column stride P/32) or, with
@@ -152,13 +165,7 @@ __device__ inline void rq_store_tile(const uint8_t* lq, const uint8_t* lsf, cons
       *reinterpret_cast<u32x4*>(out_c + lblk[b][0] + gc * Pb + (chunk & 1) * 16) =
           *reinterpret_cast<const u32x4*>(lq + col * ROWS + swz(col, chunk) * 16);
   }
-#pragma unroll
-  for (int it = 0; it < COLS * WAVES / THREADS; ++it) {
-    const int idx = it * THREADS + tid;
-    const int col = sfb ? idx % COLS : idx >> 2, b = sfb ? idx / COLS : idx & 3;
-    const int64_t Pb = lblk[b][1], gc = c0 + col;
-    if (Pb != 0 && gc < C) out_s[lblk[b][2] + (sfb ? gc : gc * (Pb / 32))] = lsf[col * WAVES + b];
-  }
+  rq_store_scales(lsf, lblk, c0, C, sfb, out_s);
 }
 
 }  // namespace moe4

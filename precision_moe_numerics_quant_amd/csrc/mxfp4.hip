@@ -222,6 +222,12 @@ __global__ void __launch_bounds__(m4q::THREADS) k_mx4_dequant(const uint32_t* __
 // A wave's 32 x 16 scale bytes come as eight loads of 64 bytes and are turned
 // through LDS into each lane's 32 (32 byte loads a lane before: 150 -> 124 us at
 // 131072 x 1536).
+//
+// The codes leave in two halves of the lane's columns, so that a wave needs 8 KB
+// of LDS and three waves fit a SIMD (two with all columns at once: 125 -> 115 us
+// at 131072 x 1536, 280 -> 252 at 131072 x 4096); each half hashes its rows' keys
+// again.  The VALU bounds it (about 11 instructions a value), not the 1.56 bytes
+// a value (61 us at 131072 x 1536).
 namespace rq4 {
 // any byte of w zero
 __device__ inline uint32_t zero_byte(uint32_t w) { return (w - 0x01010101u) & ~w & 0x80808080u; }
@@ -234,14 +240,14 @@ __device__ inline bool odd_scales(uint32_t w) {
 }
 }  // namespace rq4
 
-__global__ void __launch_bounds__(rq::THREADS) k_requant_mx4_T(const uint8_t* __restrict__ codes,
+__global__ void __launch_bounds__(rq::THREADS, 3) k_requant_mx4_T(const uint8_t* __restrict__ codes,
                                                                const uint8_t* __restrict__ sf, int64_t C,
                                                                const int32_t* __restrict__ off,
                                                                const int32_t* __restrict__ offp, int G, int64_t R,
                                                                int64_t max_pr, int64_t n_ct, uint32_t base, int sfb,
                                                                uint8_t* __restrict__ out_c, uint8_t* __restrict__ out_s) {
   using namespace rq;
-  __shared__ __attribute__((aligned(16))) uint8_t lq[COLS * ROWS];
+  __shared__ __attribute__((aligned(16))) uint8_t lq[COLS / 2 * ROWS];  // half of each lane's columns
   __shared__ __attribute__((aligned(16))) uint8_t lsc[WAVES][16][32];  // [wave][source block][row]
   __shared__ uint8_t lsf[COLS * WAVES];  // [column][block]
   __shared__ int64_t lblk[WAVES][3];     // block's code offset at column 0, P (0: no block), scale offset at column 0
@@ -288,10 +294,10 @@ __global__ void __launch_bounds__(rq::THREADS) k_requant_mx4_T(const uint8_t* __
     for (int i = 0; i < 8; ++i) lsc[w][l & 15][4 * i + (l >> 4)] = (uint8_t)s[i];
   }
   __syncthreads();
-  // row group k (rows 4k..4k+3 of block w) of column col: dword k % 4 of
-  // 16-byte chunk 2w + k / 4 of the column's LDS run
+  // row group k (rows 4k..4k+3 of block w) of the lane's column 4 h + q: dword
+  // k % 4 of 16-byte chunk 2w + k / 4 of LDS run 4 l + q
   auto put = [&](int k, int q, uint32_t v) {
-    const int col = LCOLS * l + q;
+    const int col = LCOLS / 2 * l + q;
     *reinterpret_cast<uint32_t*>(lq + col * ROWS + swz(col, 2 * w + (k >> 2)) * 16 + (k & 3) * 4) = v;
   };
   int ex[8];
@@ -308,82 +314,109 @@ __global__ void __launch_bounds__(rq::THREADS) k_requant_mx4_T(const uint8_t* __
   const int64_t j0 = src0 * (C / 2) + c / 2;  // pair index of (row src0, column c)
   const uint32_t key0 = fmix32(base);
   const bool fast = src0 * (C / 2) + 32 * (C / 2) < ((int64_t)1 << 32);
-  if (fast && !__any(odd)) {
-    auto scale = [&](int i) { return __uint_as_float(((sbp[i >> 2] >> (8 * (i & 3))) & 0xFFu) << 23); };  // 2**(byte - 127)
+  const bool plain = fast && !__any(odd);  // (uniform over the wave)
+  auto scale = [&](int i) { return __uint_as_float(((sbp[i >> 2] >> (8 * (i & 3))) & 0xFFu) << 23); };  // 2**(byte - 127)
+  auto byte = [&](int i) { return (int)((sbp[i >> 2] >> (8 * (i & 3))) & 0xFFu); };
+  float sc[8];  // the result blocks' scales (any for an all-zero one)
+  {
     float am[8];
 #pragma unroll
     for (int q = 0; q < 8; ++q) am[q] = 0.0f;
+    if (plain) {
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      const float s = scale(i);
-      const f32x2 d0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(cw[i], s, 0), d1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(cw[i], s, 1);
-      const f32x2 d2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(cw[i], s, 2), d3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(cw[i], s, 3);
-      const float v[8] = {d0[0], d0[1], d1[0], d1[1], d2[0], d2[1], d3[0], d3[1]};
-#pragma unroll
-      for (int q = 0; q < 8; ++q) am[q] = fmaxf(am[q], fabsf(v[q]));
-    }
-    float sc[8];  // the result blocks' scales (any for an all-zero one)
-#pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      ex[q] = mx_exponent(am[q]);
-      sc[q] = ex[q] == -127 ? 1.0f : __uint_as_float((uint32_t)(ex[q] + 127) << 23);
-    }
-    // (decoded again below instead of keeping the 256 values live)
-#pragma unroll
-    for (int i = 0; i < 32; ++i) asm volatile("" : "+v"(cw[i]));
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      uint32_t od[8];
-#pragma unroll
-      for (int q = 0; q < 8; ++q) od[q] = 0u;
-#pragma unroll
-      for (int ii = 0; ii < 4; ++ii) {
-        const int i = 4 * k + ii;
+      for (int i = 0; i < 32; ++i) {
         const float s = scale(i);
-        const f32x2 d[4] = {__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(cw[i], s, 0), __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(cw[i], s, 1),
-                            __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(cw[i], s, 2), __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(cw[i], s, 3)};
-        const Fmix32x4 hw((uint32_t)j0 + (uint32_t)i * (uint32_t)(C / 2), key0);
+        const f32x2 d0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(cw[i], s, 0), d1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(cw[i], s, 1);
+        const f32x2 d2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(cw[i], s, 2), d3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(cw[i], s, 3);
+        const float v[8] = {d0[0], d0[1], d1[0], d1[1], d2[0], d2[1], d3[0], d3[1]};
 #pragma unroll
-        for (int p = 0; p < 4; ++p) {
-          const uint32_t word = hw.word(p);
-          od[2 * p] = sr_fp8_scaled(od[2 * p], d[p][0], word << 16, sc[2 * p], ii);
-          od[2 * p + 1] = sr_fp8_scaled(od[2 * p + 1], d[p][1], word & 0xFFFF0000u, sc[2 * p + 1], ii);
-        }
+        for (int q = 0; q < 8; ++q) am[q] = fmaxf(am[q], fabsf(v[q]));
       }
 #pragma unroll
-      for (int q = 0; q < 8; ++q) put(k, q, od[q]);
-    }
-  } else {
+      for (int q = 0; q < 8; ++q) ex[q] = mx_exponent(am[q]);
+    } else {
 #pragma unroll
-    for (int k = 0; k < 8; ++k) nan |= rq4::zero_byte(~sbp[k]) != 0u;  // a byte of 255
-    // a quarter of each value (MXFP4 reaches 6 * 2**127, past float32)
-    auto byte = [&](int i) { return (int)((sbp[i >> 2] >> (8 * (i & 3))) & 0xFFu); };
-    float am[8];
+      for (int k = 0; k < 8; ++k) nan |= rq4::zero_byte(~sbp[k]) != 0u;  // a byte of 255
+      // a quarter of each value (MXFP4 reaches 6 * 2**127, past float32)
 #pragma unroll
-    for (int q = 0; q < 8; ++q) am[q] = 0.0f;
+      for (int i = 0; i < 32; ++i) {
+        float v[8];
+        mx4_decode8(cw[i], byte(i) - 129, v);
 #pragma unroll
-    for (int i = 0; i < 32; ++i) {
-      float v[8];
-      mx4_decode8(cw[i], byte(i) - 129, v);
+        for (int q = 0; q < 8; ++q) am[q] = fmaxf(am[q], fabsf(v[q]));
+      }
 #pragma unroll
-      for (int q = 0; q < 8; ++q) am[q] = fmaxf(am[q], fabsf(v[q]));
+      for (int q = 0; q < 8; ++q) ex[q] = am[q] < 1.0f ? mx_exponent(4.0f * am[q]) : mx_exponent(am[q]) + 2;
     }
 #pragma unroll
-    for (int q = 0; q < 8; ++q) ex[q] = am[q] < 1.0f ? mx_exponent(4.0f * am[q]) : mx_exponent(am[q]) + 2;
+    for (int q = 0; q < 8; ++q) sc[q] = ex[q] == -127 ? 1.0f : __uint_as_float((uint32_t)(ex[q] + 127) << 23);
+  }
+#pragma unroll 1
+  for (int h = 0; h < 2; ++h) {  // columns 4 h .. 4 h + 3 of the lane
+    // (decoded and hashed again, instead of keeping 256 values live)
+    int64_t jh = j0;
+    asm volatile("" : "+v"(jh));
 #pragma unroll
     for (int i = 0; i < 32; ++i) asm volatile("" : "+v"(cw[i]));
-    auto deqw = [&](int i, float (&q)[8]) {  // q * 2**(sb - 127 - ex)
-      mx4_decode8(cw[i], 0, q);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) q[j] = __builtin_amdgcn_ldexpf(q[j], byte(i) - 127 - ex[j]);
-    };
-    const float one[8] = {1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f};
-    requant_block<false, true>(deqw, 32, 1.0f, one, j0, C / 2, base, key0, put);
+    for (int i = 0; i < 8; ++i) asm volatile("" : "+v"(sbp[i]));
+    if (plain) {
+      const uint32_t hm = 0u - (uint32_t)h;
+      float hs[4];
+#pragma unroll
+      for (int q = 0; q < 4; ++q) hs[q] = h ? sc[4 + q] : sc[q];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        uint32_t od[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) od[q] = 0u;
+#pragma unroll
+        for (int ii = 0; ii < 4; ++ii) {
+          const int i = 4 * k + ii;
+          const uint32_t cv = cw[i] >> (16 * h);
+          const float s = scale(i);
+          const f32x2 d[2] = {__builtin_amdgcn_cvt_scalef32_pk_f32_fp4(cv, s, 0), __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(cv, s, 1)};
+          Fmix32x4 hw((uint32_t)jh + (uint32_t)i * (uint32_t)(C / 2), key0);
+          hw.m0 += hw.d2 & hm;  // (words 2 h and 2 h + 1)
+#pragma unroll
+          for (int p = 0; p < 2; ++p) {
+            const uint32_t word = hw.word(p);
+            od[2 * p] = sr_fp8_scaled(od[2 * p], d[p][0], word << 16, hs[2 * p], ii);
+            od[2 * p + 1] = sr_fp8_scaled(od[2 * p + 1], d[p][1], word & 0xFFFF0000u, hs[2 * p + 1], ii);
+          }
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) put(k, q, od[q]);
+      }
+    } else {  // (the other half's codes are dropped: this path is rare)
+      auto deqw = [&](int i, float (&q)[8]) {  // q * 2**(sb - 127 - ex)
+        mx4_decode8(cw[i], 0, q);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) q[j] = __builtin_amdgcn_ldexpf(q[j], byte(i) - 127 - ex[j]);
+      };
+      uint32_t lo[4];
+      const float one[8] = {1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f, 1.0f};
+      requant_block<false, true>(deqw, 32, 1.0f, one, jh, C / 2, base, key0, [&](int k, int q, uint32_t v) {
+        if (q < 4) lo[q] = v;
+        else put(k, q - 4, h ? v : lo[q & 3]);
+      });
+    }
+    // the half's codes as 128-byte column runs, 8 lanes per run
+    __syncthreads();
+#pragma unroll
+    for (int it = 0; it < COLS / 2 * 8 / THREADS; ++it) {
+      const int idx = it * THREADS + tid, col = idx >> 3, chunk = idx & 7, b = chunk >> 1;
+      const int64_t Pb = lblk[b][1], gc = c0 + (col >> 2) * LCOLS + 4 * h + (col & 3);
+      if (Pb != 0 && gc < C)
+        *reinterpret_cast<u32x4*>(out_c + lblk[b][0] + gc * Pb + (chunk & 1) * 16) =
+            *reinterpret_cast<const u32x4*>(lq + col * ROWS + swz(col, chunk) * 16);
+    }
+    __syncthreads();
   }
 #pragma unroll
   for (int q = 0; q < 8; ++q) lsf[(LCOLS * l + q) * WAVES + w] = nan ? 255u : (uint8_t)(ex[q] + 127);
   __syncthreads();
-  rq_store_tile(lq, lsf, lblk, c0, C, sfb, out_c, out_s);
+  rq_store_scales(lsf, lblk, c0, C, sfb, out_s);
 }
 
 }  // namespace moe4
