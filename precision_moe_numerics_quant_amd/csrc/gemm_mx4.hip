@@ -29,8 +29,12 @@ __device__ inline __amdgpu_buffer_rsrc_t dword_rsrc(const uint8_t* p, uint64_t b
 // of its rows; its four waves split K (so that one token's eight experts
 // still fill the chip) and join their sums through LDS in wave order.  A wave
 // requests all the weights of its K share at once (NS steps of 128, the
-// smallest of 2, 3, 4, 6 and 8 that holds it: up to K = 4096), keeps them in registers for all its passes, and only the rows'
-// codes, from L2, are read per pass.  No LDS for the operands.
+// smallest of 2, 3, 4, 6 and 8 that holds it: up to K = 4096; a smaller NS has
+// fewer registers and more waves), keeps them in registers for all its passes,
+// and only the rows' codes, from L2, are read per pass.  No LDS for the
+// operands.  HBM bounds it: 384 experts of 1536 x 4096 (1.28 GB) with 4 rows each
+// in 242 us (5.3 TB/s; reads alone reach 6.2 here), one token's eight experts in
+// 8 us, which is latency: a wave's loads, the join, the launch.
 namespace m4s {
 constexpr int NT = 256, NWV = NT / 64, WB = 2, WROWS = 16 * WB;
 constexpr int KB = 128;           // K per step: lane (li, q) holds k = 128 s + 32 q .. of row li
@@ -187,6 +191,15 @@ __global__ void __launch_bounds__(m4s::NT)
 // of stages, four consumer waves only read LDS, run the MFMAs
 // (v_mfma_scale_f32_32x32x64_f8f6f4) and store; one barrier per slab.  128 x
 // TN tiles: consumers of 64 x TN / 2.
+//
+// What bounds it, at 131072 rows of eight experts, N = 1536, K = 4096 (503 us,
+// 3.3 PFLOP/s): the MFMAs on random operands alone run at the card's power
+// limit, 298 us (5.5 PFLOP/s); with their LDS reads 380; the loads into LDS
+// alone 335; both together 443 (they share the LDS port and the power); the
+// stores of the results, in bursts of all CUs at once, the rest.  384 experts
+// under power-law routing, 17 % of the rows padding: 662 us.  256 x 256 tiles
+// move a third fewer bytes per MFMA but leave one wave per SIMD that loads and
+// multiplies: 1006 us.  Ordinary instead of nontemporal stores: 510 us.
 //
 // Every load goes through a buffer descriptor that ends with the expert's
 // rows, so rows past its last or N and K chunks past K (their lanes' offsets are
@@ -590,6 +603,10 @@ static void launch_mx4(const uint8_t* ac, const uint8_t* as, const uint8_t* bc, 
 #define MOE4_MX4(TN, AL)                                                                                                       \
   hipLaunchKernelGGL((k_gemm_mx4_ws<OUT_BF16, TN, AL>), grid, dim3(m4w::NT), 0, s, ac, as, bc, bs, off, E, M, N, K,             \
                      dg_split((N + TN - 1) / TN, m4w::TM, TN), c)
+  // 256 columns unless that pads the last tile of a few: us at 131072 rows, 32
+  // experts, K = 2048, TN 128 - 256: N = 128 40 - 47, 384 78 - 82, 512 100 - 92,
+  // 640 124 - 118, 1536 303 - 262.  Without pairs of scales (TN = 128) 334 at
+  // N = 1536.
   if (!pair) MOE4_MX4(128, false);
   else if (N % 256 == 0 || N > 512) MOE4_MX4(256, true);
   else MOE4_MX4(128, true);

@@ -20,6 +20,14 @@
 // two columns (whole cache lines across the wave) and the bytes are put into
 // fragment order on the way to LDS, [k / 8][row][8 k]: a fragment read is then
 // 16 consecutive bytes per lane, without bank conflicts.
+//
+// Measured at 16384 tokens, k = 8, d = 4096, 384 experts: dx 537 us, against 427
+// for the un-permuting sum alone (2.1 GB gathered at 5.2 TB/s, the bound) and 213
+// for the GEMM alone, which hides partly behind the other workgroups' gathers:
+// four per CU (one LDS stage, one register set; two stages and 2 per CU: 587).
+// dW 190 us, 113 at the bf16 MFMA rate of a large product: its operands cross
+// from token-major rows through registers into LDS, three parts of dz each.
+// 64-deep slabs or 256-wide tiles would cut the workgroups per CU again.
 #include "gemm_common.h"
 #include "moe4_internal.h"
 
