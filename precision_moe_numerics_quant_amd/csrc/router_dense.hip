@@ -4,7 +4,7 @@
 //
 //   k_router_dx_dense  dx[t] = bf16(sum_j dXp[row(t, j)] + sum_e dz[t, e] W_r[e]):
 //                      the un-permuting sum with the GEMM dz . W_r under it,
-//                      128 x 128 tiles (T x d), the sum added in the epilogue.
+//                      64 x 128 tiles (T x d), the sum added in the epilogue.
 //   k_router_dw_dense  dW_r [E, d] = dz^T . x, 128 x 128 tiles (E x d), the
 //                      tokens split over workgroups whose partial tiles
 //                      k_router_dw_join adds in order.
@@ -21,11 +21,11 @@
 // fragment order on the way to LDS, [k / 8][row][8 k]: a fragment read is then
 // 16 consecutive bytes per lane, without bank conflicts.
 //
-// Measured at 16384 tokens, k = 8, d = 4096, 384 experts: dx 537 us, against 427
+// Measured at 16384 tokens, k = 8, d = 4096, 384 experts: dx 525 us, against 427
 // for the un-permuting sum alone (2.1 GB gathered at 5.2 TB/s, the bound) and 213
 // for the GEMM alone, which hides partly behind the other workgroups' gathers:
-// four per CU (one LDS stage, one register set; two stages and 2 per CU: 587).
-// dW 190 us, 113 at the bf16 MFMA rate of a large product: its operands cross
+// six per CU (one LDS stage, one register set; 128-row tiles with two stages, 2 per
+// CU: 587).  dW 213 us and 11 for the join, 113 at the bf16 MFMA rate of a large product: its operands cross
 // from token-major rows through registers into LDS, three parts of dz each.
 // 64-deep slabs or 256-wide tiles would cut the workgroups per CU again.
 #include "gemm_common.h"
@@ -39,6 +39,7 @@ constexpr int KC = BK / 8;                  // 8-deep k chunks of a slab
 constexpr int PART_B = KC * TM * 16;        // bytes of one bf16 operand slab
 constexpr int STAGE = 4 * PART_B;           // three parts of dz, one of the other operand
 constexpr int MAXK = 16;
+constexpr int CUS = 256;
 constexpr int64_t MAXE = (1 << 20) - 1, MAXD = (1 << 28) - 1;  // (128 rows of dz and a row of W_r: 31-bit byte ranges)
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 }  // namespace rd
@@ -72,34 +73,37 @@ __device__ inline void columns2(const uint32_t (&w)[8], u32x4& c0, u32x4& c1) {
   }
 }
 
-// A thread's share of one slab in registers: 8 k of two rows or columns of dz
-// and of two columns of the other operand.
+// A thread's share of one slab in registers: 8 k of a row (dx) or two columns (dW)
+// of dz and of two columns of the other operand.
 struct RdRegs {
   float a[2][8];
   uint32_t b[8];
 };
 
-// One slab: wave (wm, wn) owns 64 x 64 of the tile, 2 x 2 MFMA blocks.
-__device__ inline void rd_compute(const uint8_t* st, int wm, int wn, f32x16 (&acc)[2][2]) {
+// One slab of a tile of ROWS rows: wave (wm, wn) owns 32 MI x 32 NJ of it, in
+// MFMA blocks of 32 x 32.
+template <int ROWS, int MI, int NJ>
+__device__ inline void rd_compute(const uint8_t* st, int wm, int wn, f32x16 (&acc)[MI][NJ]) {
   using namespace rd;
+  constexpr int PART_A = KC * ROWS * 16;
   const int l = threadIdx.x & 63, li = l & 31, g = l >> 5;
 #pragma unroll
   for (int kk = 0; kk < BK / 16; ++kk) {
     const int c = 2 * kk + g;  // lane half g holds k = 16 kk + 8 g .. + 7
-    bf16x8 a[3][2], b[2];
+    bf16x8 a[3][MI], b[NJ];
 #pragma unroll
     for (int p = 0; p < 3; ++p)
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-        a[p][i] = *reinterpret_cast<const bf16x8*>(st + p * PART_B + (c * TM + wm + 32 * i + li) * 16);
+      for (int i = 0; i < MI; ++i)
+        a[p][i] = *reinterpret_cast<const bf16x8*>(st + p * PART_A + (c * ROWS + wm + 32 * i + li) * 16);
 #pragma unroll
-    for (int j = 0; j < 2; ++j) b[j] = *reinterpret_cast<const bf16x8*>(st + 3 * PART_B + (c * TN + wn + 32 * j + li) * 16);
+    for (int j = 0; j < NJ; ++j) b[j] = *reinterpret_cast<const bf16x8*>(st + 3 * PART_A + (c * TN + wn + 32 * j + li) * 16);
 #pragma unroll
     for (int p = 2; p >= 0; --p)  // the smallest parts first
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
+      for (int i = 0; i < MI; ++i)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[p][i], b[j], acc[i][j], 0, 0, 0);
+        for (int j = 0; j < NJ; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[p][i], b[j], acc[i][j], 0, 0, 0);
   }
 }
 
@@ -115,39 +119,44 @@ __device__ inline int64_t clamp_row(int64_t i, int64_t n, uint32_t* err) {
 static __device__ uint32_t g_dev_err;
 uint32_t take_dev_err_router_dense() { return take_device_word(&g_dev_err); }
 
+// ROWS x 128 tiles: a tile's gathers follow one another, so many small tiles side
+// by side hide them best until W_r's slabs are read too often.  64 rows: 525 us at
+// 16384 tokens (128 rows 531, 32 rows 544; at k = 2, 8000 tokens 156, 150, 190).
+// 32 rows where 64 would leave CUs with one tile or none: 512 tokens 25 - 28, 333
+// tokens with 130 experts, k = 6, d = 520 10 us (128 rows: 27).
+template <int ROWS>
 __global__ void __launch_bounds__(rd::NT, 4)
     k_router_dx_dense(const float* __restrict__ dxp, const int32_t* __restrict__ inv, int64_t T, int k, int64_t d,
                       const float* __restrict__ dz, int E, const uint16_t* __restrict__ w, int64_t n_nt, int64_t n_all,
                       uint16_t* __restrict__ dx) {
   using namespace rd;
-  __shared__ __attribute__((aligned(16))) uint8_t lds[STAGE];  // a slab; then half the float32 tile (32 KB both)
-  __shared__ int32_t rows[TM * MAXK];                              // dXp's rows of the tile's tokens
-  static_assert(STAGE >= TM * TN * 2, "the epilogue's half tile");
+  constexpr int PART_A = KC * ROWS * 16, SLAB = 3 * PART_A + PART_B;
+  constexpr int MI = ROWS / 32;
+  constexpr int HROWS = 32;  // rows of the float32 tile in LDS at a time
+  __shared__ __attribute__((aligned(16))) uint8_t lds[SLAB > HROWS * TN * 4 ? SLAB : HROWS * TN * 4];
+  __shared__ int32_t rows[ROWS * MAXK];  // dXp's rows of the tile's tokens
   const int64_t tile = xcd_tile(blockIdx.x, n_all);
   if (tile >= n_all) return;
-  const int64_t t0 = (tile / n_nt) * TM, c0 = (tile % n_nt) * TN;
+  const int64_t t0 = (tile / n_nt) * ROWS, c0 = (tile % n_nt) * TN;
   const int tid = threadIdx.x, l = tid & 63, wv = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int wm = (wv >> 1) * 64, wn = (wv & 1) * 64;
-  for (int i = tid; i < TM * k; i += NT)  // (tokens past T: any row)
+  const int wn = 32 * wv;  // the wave's columns
+  for (int i = tid; i < ROWS * k; i += NT)  // (tokens past T: any row)
     rows[i] = t0 * k + i < T * k ? (int32_t)clamp_row(inv[t0 * k + i], T * k, &g_dev_err) : 0;
-  // dz: units (row tid / 4 + 64 j, chunk tid % 4); W_r: unit (chunk tid / 64, columns 2 l, 2 l + 1)
+  // dz: unit (row tid / 4, chunk tid % 4; 32 rows: the first half of the threads); W_r: unit (chunk tid / 64, columns 2 l, 2 l + 1)
   const int ach = tid & 3, ar = tid >> 2;
   const int64_t bc = c0 + 2 * l;
   // (a descriptor that ends with the tile's rows, and one per row of W_r: rows
   // past T or E and columns past d come as zeros)
-  const __amdgpu_buffer_rsrc_t rz = make_rsrc(dz + t0 * E, (uint64_t)(T - t0 < TM ? T - t0 : TM) * E * 4);
-  const uint32_t zo = (uint32_t)ar * E * 4 + 32u * ach, z64 = 64u * (uint32_t)E * 4;
+  const __amdgpu_buffer_rsrc_t rz = make_rsrc(dz + t0 * E, (uint64_t)(T - t0 < ROWS ? T - t0 : ROWS) * E * 4);
+  const uint32_t zo = (uint32_t)ar * E * 4 + 32u * ach;
   const uint32_t wo = (uint32_t)bc * 2;
   auto load = [&](RdRegs& q, int k0) {
+    const uint32_t o = zo + (uint32_t)k0 * 4;
+    const u32x4 x0 = __builtin_amdgcn_raw_buffer_load_b128(rz, o, 0, 0), x1 = __builtin_amdgcn_raw_buffer_load_b128(rz, o + 16, 0, 0);
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const uint32_t o = zo + j * z64 + (uint32_t)k0 * 4;
-      const u32x4 x0 = __builtin_amdgcn_raw_buffer_load_b128(rz, o, 0, 0), x1 = __builtin_amdgcn_raw_buffer_load_b128(rz, o + 16, 0, 0);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        q.a[j][i] = __uint_as_float(x0[i]);
-        q.a[j][4 + i] = __uint_as_float(x1[i]);
-      }
+    for (int i = 0; i < 4; ++i) {
+      q.a[0][i] = __uint_as_float(x0[i]);
+      q.a[0][4 + i] = __uint_as_float(x1[i]);
     }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -159,27 +168,22 @@ __global__ void __launch_bounds__(rd::NT, 4)
   auto store = [&](RdRegs& q, uint8_t* st, int k0) {
     if (k0 + BK > E) {  // (uniform)
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) q.a[j][i] = k0 + 8 * ach + i < E ? q.a[j][i] : 0.0f;
+      for (int i = 0; i < 8; ++i) q.a[0][i] = k0 + 8 * ach + i < E ? q.a[0][i] : 0.0f;
     }
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
+    if (ar < ROWS) {
       u32x4 o[3];
-      split3(q.a[j], o);
+      split3(q.a[0], o);
 #pragma unroll
-      for (int p = 0; p < 3; ++p) *reinterpret_cast<u32x4*>(st + p * PART_B + (ach * TM + ar + 64 * j) * 16) = o[p];
+      for (int p = 0; p < 3; ++p) *reinterpret_cast<u32x4*>(st + p * PART_A + (ach * ROWS + ar) * 16) = o[p];
     }
     u32x4 b0, b1;
     columns2(q.b, b0, b1);
-    *reinterpret_cast<u32x4*>(st + 3 * PART_B + (wv * TN + 2 * l) * 16) = b0;
-    *reinterpret_cast<u32x4*>(st + 3 * PART_B + (wv * TN + 2 * l + 1) * 16) = b1;
+    *reinterpret_cast<u32x4*>(st + 3 * PART_A + (wv * TN + 2 * l) * 16) = b0;
+    *reinterpret_cast<u32x4*>(st + 3 * PART_A + (wv * TN + 2 * l + 1) * 16) = b1;
   };
-  f32x16 acc[2][2];
+  f32x16 acc[MI][1];
 #pragma unroll
-  for (int i = 0; i < 2; ++i)
-#pragma unroll
-    for (int j = 0; j < 2; ++j) acc[i][j] = f32x16{};
+  for (int i = 0; i < MI; ++i) acc[i][0] = f32x16{};
   const int nk = (E + BK - 1) / BK;
   RdRegs q;
   load(q, 0);
@@ -187,29 +191,23 @@ __global__ void __launch_bounds__(rd::NT, 4)
     store(q, lds, s * BK);
     __syncthreads();
     if (s + 1 < nk) load(q, (s + 1) * BK);  // in flight during this slab's MFMAs
-    rd_compute(lds, wm, wn, acc);
+    rd_compute<ROWS>(lds, 0, wn, acc);
     __syncthreads();
   }
-  // the tile through LDS, 64 rows at a time, so that a thread adds whole
+  // the tile through LDS, HROWS rows at a time, so that a thread adds whole
   // 16-byte pieces of rows
   float* tl = reinterpret_cast<float*>(lds);
   const int li = l & 31, g = l >> 5;
   const int64_t col = c0 + 4 * (tid & 31);
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    if (wm == 64 * h) {
+  for (int h = 0; h < ROWS / HROWS; ++h) {
 #pragma unroll
-      for (int i = 0; i < 2; ++i)
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-          for (int v = 0; v < 16; ++v) tl[(32 * i + (v >> 2) * 8 + 4 * g + (v & 3)) * TN + wn + 32 * j + li] = acc[i][j][v];
-    }
+    for (int v = 0; v < 16; ++v) tl[((v >> 2) * 8 + 4 * g + (v & 3)) * TN + wn + li] = acc[h][0][v];
     __syncthreads();
     constexpr int JS = 8;  // row loads in flight per lane (with more, fewer workgroups fit: slower)
     if (col < d)
-      for (int r = tid >> 5; r < 64 && t0 + 64 * h + r < T; r += NT / 32) {
-        const int32_t* rw = rows + (64 * h + r) * k;
+      for (int r = tid >> 5; r < HROWS && t0 + HROWS * h + r < T; r += NT / 32) {
+        const int32_t* rw = rows + (HROWS * h + r) * k;
         f32x4 s = {0.0f, 0.0f, 0.0f, 0.0f};
         for (int j0 = 0; j0 < k; j0 += JS) {
           f32x4 v[JS];
@@ -221,7 +219,7 @@ __global__ void __launch_bounds__(rd::NT, 4)
             if (j0 + j < k) s = s + v[j];
         }
         s = s + *reinterpret_cast<const f32x4*>(tl + r * TN + 4 * (tid & 31));
-        *reinterpret_cast<u32x2*>(dx + (t0 + 64 * h + r) * d + col) = u32x2{bf16_pair(s[0], s[1]), bf16_pair(s[2], s[3])};
+        *reinterpret_cast<u32x2*>(dx + (t0 + HROWS * h + r) * d + col) = u32x2{bf16_pair(s[0], s[1]), bf16_pair(s[2], s[3])};
       }
     __syncthreads();
   }
@@ -277,7 +275,7 @@ __global__ void __launch_bounds__(rd::NT, 4)
     store(q, lds);
     __syncthreads();
     if (s + 1 < nk) load(q, ta + (int64_t)(s + 1) * BK);  // in flight during this slab's MFMAs
-    rd_compute(lds, wm, wn, acc);
+    rd_compute<TM>(lds, wm, wn, acc);
     __syncthreads();
   }
   const int li = l & 31, g = l >> 5;
@@ -307,12 +305,19 @@ __global__ void __launch_bounds__(256) k_router_dw_join(const f32x4* __restrict_
 }
 
 // Token shares of the weight gradient: enough workgroups for four per CU, at
-// least 8 slabs each.
+// least 8 slabs each; where that does not give every CU one, at least 2
+// slabs (333 tokens, 130 experts, d = 520: 20 us in one share, 9.5 + 3 in five
+// with the join).
 inline int dw_shares(int64_t T, int E, int64_t d) {
   const int64_t tiles = ((E + rd::TM - 1) / rd::TM) * ((d + rd::TN - 1) / rd::TN);
   int64_t n = 1024 / tiles;
   const int64_t most = T / (8 * rd::BK);
   if (n > most) n = most;
+  if (n < 1) n = 1;
+  if (n * tiles < rd::CUS) {
+    n = rd::CUS / tiles;
+    if (n > T / (2 * rd::BK)) n = T / (2 * rd::BK);
+  }
   return (int)(n < 1 ? 1 : n);
 }
 
@@ -330,10 +335,14 @@ extern "C" int moe_unpermute_sum_router_dense(const float* dxp, const int32_t* i
   MOE4_REQUIRE(aligned16(dxp) && aligned16(dlogits) && aligned16(w) && aligned16(dx), MOE4_EALIGN,
                "moe_unpermute_sum_router_dense: dxp, dlogits, w and dx must be 16-byte aligned");
   if (T == 0) return MOE4_OK;
-  const int64_t n_nt = (d + rd::TN - 1) / rd::TN, n_all = n_nt * ((T + rd::TM - 1) / rd::TM);
-  MOE4_REQUIRE(n_all < ((int64_t)1 << 30), MOE4_EINVAL, "moe_unpermute_sum_router_dense: too large");
-  hipLaunchKernelGGL(k_router_dx_dense, dim3((unsigned)xcd_grid(n_all)), dim3(rd::NT), 0, as_stream(stream), dxp, inv_perm,
-                     T, k, d, dlogits, E, w, n_nt, n_all, dx);
+  const int64_t n_nt = (d + rd::TN - 1) / rd::TN, n64 = n_nt * ((T + 63) / 64), n32 = n_nt * ((T + 31) / 32);
+  MOE4_REQUIRE(n64 < ((int64_t)1 << 30), MOE4_EINVAL, "moe_unpermute_sum_router_dense: too large");
+#define MOE4_RDX(ROWS, TILES)                                                                                        \
+  hipLaunchKernelGGL(k_router_dx_dense<ROWS>, dim3((unsigned)xcd_grid(TILES)), dim3(rd::NT), 0, as_stream(stream), dxp, \
+                     inv_perm, T, k, d, dlogits, E, w, n_nt, TILES, dx)
+  if (n64 < 2 * rd::CUS) MOE4_RDX(32, n32);
+  else MOE4_RDX(64, n64);
+#undef MOE4_RDX
   return check_launch("moe_unpermute_sum_router_dense");
 }
 

@@ -164,7 +164,7 @@ def test_balance_deterministic_in_place_and_replayed():
 # -------------------------------------------------------------- dense router
 
 @pytest.mark.parametrize("T,E,k,d", [(1, 2, 1, 4), (200, 8, 2, 256), (333, 130, 6, 520), (50, 20, 16, 68), (130, 384, 8, 1024), (2500, 33, 3, 132),
-                                     (129, 129, 1, 132)])
+                                     (129, 129, 1, 132), (4100, 70, 3, 1028)])
 def test_dense_router_backward(T, E, k, d):
     rng = np.random.default_rng(T + d)
     inv = rng.permutation(T * k).astype(np.int32)
