@@ -188,18 +188,19 @@ __global__ void __launch_bounds__(m4s::NT)
 // Persistent and warp-specialised, the structure of this library's other
 // grouped GEMMs: four producer waves only issue direct-to-LDS loads of a
 // 256-value K slab (128 code bytes and 8 scale bytes of each row) into a ring
-// of stages, four consumer waves only read LDS, run the MFMAs
+// of stages, TN / 32 consumer waves of 64 x 64 only read LDS, run the MFMAs
 // (v_mfma_scale_f32_32x32x64_f8f6f4) and store; one barrier per slab.  128 x
-// TN tiles: consumers of 64 x TN / 2.
+// TN tiles.  (Four consumers of 64 x 128 read a quarter less from LDS but leave
+// one per SIMD: 260 against 244 us at 4096 rows of 384 experts, N = 4096, K =
+// 1536, 686 against 680 at 131072 rows of them, N = 1536, K = 4096.)
 //
-// What bounds it, at 131072 rows of eight experts, N = 1536, K = 4096 (503 us,
-// 3.3 PFLOP/s): the MFMAs on random operands alone run at the card's power
-// limit, 298 us (5.5 PFLOP/s); with their LDS reads 380; the loads into LDS
-// alone 335; both together 443 (they share the LDS port and the power); the
-// stores of the results, in bursts of all CUs at once, the rest.  384 experts
-// under power-law routing, 17 % of the rows padding: 662 us.  256 x 256 tiles
-// move a third fewer bytes per MFMA but leave one wave per SIMD that loads and
-// multiplies: 1006 us.  Ordinary instead of nontemporal stores: 510 us.
+// What bounds it, at 131072 rows of eight experts, N = 1536, K = 4096 (502 us,
+// 3.3 PFLOP/s): power.  The MFMAs on random operands alone take 298 us (5.5
+// PFLOP/s at 1.4 GHz; on zeros they run at 2.4); with their LDS reads 380; the
+// loads into LDS alone 335; both together 443.  384 experts under power-law
+// routing: 674 us, the clock at 1.74 GHz, the MFMAs busy 36 % of it.  256 x 256
+// tiles move a third fewer bytes per MFMA but leave one wave per SIMD that
+// loads and multiplies: 1006 us.  Ordinary instead of nontemporal stores: 510.
 //
 // Every load goes through a buffer descriptor that ends with the expert's
 // rows, so rows past its last or N and K chunks past K (their lanes' offsets are
@@ -214,7 +215,7 @@ __global__ void __launch_bounds__(m4s::NT)
 // scale bytes, and the consumer cuts them out (TN = 128 only: 256 columns with
 // a slab's scales in every stage do not fit the LDS).
 namespace m4w {
-constexpr int TM = 128, NCW = 4, NT = 64 * (NCW + 4);
+constexpr int TM = 128;
 constexpr int BK = 256, ROW_B = BK / 2;  // K values and code bytes of a row and slab
 typedef __attribute__((address_space(3))) void* lds_ptr;
 // 16-byte chunk c of a row sits at chunk c ^ ((row >> 1) & 7) (the 16 lanes of
@@ -235,6 +236,7 @@ constexpr int WAIT_LGKM0 = 15 | (3 << 14) | (7 << 4);
 constexpr int NT_STORE = 2;                // buffer-store cache policy: nontemporal
 template <int TN, bool PAIR>
 struct Cfg {
+  static constexpr int NCW = TN / 32, NT = 64 * (NCW + 4);  // consumer waves of 64 x 64, threads
   static constexpr int CODE_A = TM * ROW_B, CODE_B = TN * ROW_B;
   static constexpr int GRPS = (TM + TN) / 64;            // 64-row scale groups (A's first), a load each
   static constexpr int SCL = GRPS * 64 * 16;
@@ -253,14 +255,14 @@ struct Cfg {
 }  // namespace m4w
 
 template <bool OUT_BF16, int TN, bool PAIR>
-__global__ void __launch_bounds__(m4w::NT, 1)
+__global__ void __launch_bounds__(64 * (TN / 32 + 4), 1)
     k_gemm_mx4_ws(const uint8_t* __restrict__ a_codes, const uint8_t* __restrict__ a_sf,
                   const uint8_t* __restrict__ b_codes, const uint8_t* __restrict__ b_sf,
                   const int32_t* __restrict__ off, int E, int64_t M_total, int64_t N, int64_t K, DgSplit sp,
                   void* __restrict__ c) {
   using namespace m4w;
   using C = Cfg<TN, PAIR>;
-  constexpr int S = C::S, STAGE = C::STAGE, QB = TN / 32;
+  constexpr int S = C::S, STAGE = C::STAGE, QB = TN / 32, NCW = C::NCW;
   __shared__ __attribute__((aligned(16))) uint8_t ring[C::RING];
   __shared__ uint32_t s_nmt;
   const int tid = threadIdx.x, l = tid & 63;
@@ -381,10 +383,10 @@ __global__ void __launch_bounds__(m4w::NT, 1)
     __builtin_amdgcn_s_barrier();  // (the consumers' barrier after their last slab)
     return;
   }
-  // ---- consumers: wave w owns the 64 x (TN / 2) block (w / 2, w % 2)
-  constexpr int MI = 2, NJ = TN / 64;
+  // ---- consumers: wave w owns the 64 x 64 block (w / CWN, w % CWN)
+  constexpr int MI = 2, NJ = 2, CWN = TN / 64;
   const int g = (l >> 5) & 1, li = l & 31;
-  const int wm = (w >> 1) * 64, wn = (w & 1) * (TN / 2);
+  const int wm = w / CWN * 64, wn = w % CWN * 64;
   f32x16 acc[MI][NJ];
 #pragma unroll
   for (int i = 0; i < MI; ++i)
@@ -393,7 +395,7 @@ __global__ void __launch_bounds__(m4w::NT, 1)
   uint32_t sha[MI], shb[NJ];  // !PAIR: the rows' first scale byte in its dword
   // A slab is four 64-value k steps.  Lane half g supplies K block 2 ks + g and
   // its scale, byte 2 (ks % 2) of the row's scale dword ks / 2 shifted by g
-  // bytes.  With one consumer wave per SIMD nothing else hides the LDS
+  // bytes.  With one or two consumer waves per SIMD little else hides the LDS
   // latency, so the next step's fragments are read before the MFMAs of this
   // one, across slabs and tiles too: the last step of a slab runs after the next
   // slab's barrier (its fragments are in registers by then).  After the last
@@ -472,8 +474,60 @@ __global__ void __launch_bounds__(m4w::NT, 1)
   constexpr int ESZ = OUT_BF16 ? 2 : 4;
   const uint32_t ld = (uint32_t)N * ESZ;  // output row pitch in bytes
   const uint32_t lane_off = (uint32_t)(g * 4) * ld + (uint32_t)li * (2 * ESZ);
+  // DEFER (bf16 results, two slabs or more to a tile): a tile's results wait in
+  // half its accumulators' registers and are stored between the MFMAs of the
+  // next tile's first two slabs, an eighth of them after each MFMA step (1 % at
+  // K = 4096, 512 columns and K = 2048 89 - 85 us, 128 columns 44 - 38)
+  constexpr bool DEFER = OUT_BF16 && PAIR;
+  uint32_t pk[DEFER ? MI : 1][16];
+  __amdgpu_buffer_rsrc_t prc = make_rsrc(c, 0);  // (of nothing: the stores go nowhere)
+  uint32_t pvo = OOB, pfo = 0;
+  auto put_pending = [&](int i, int v) {
+    __builtin_amdgcn_raw_buffer_store_b32(pk[DEFER ? i : 0][v], prc, pvo, pfo + (uint32_t)(32 * i + (v >> 2) * 8 + (v & 3)) * ld, NT_STORE);
+  };
+  auto flush = [&]() {
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) put_pending(i, v);
+    prc = make_rsrc(c, 0);
+  };
+  if (DEFER) {
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+      for (int v = 0; v < 16; ++v) pk[DEFER ? i : 0][v] = 0;
+  }
   MtCursor<TM> cur;
   uint32_t gs = 0;
+  // one slab of an active tile; pend: the half of the pending stores that goes with it (2: none)
+  auto slab = [&](uint32_t s, int pend) {
+    asm volatile("" : "+v"(lx));
+    auto stores = [&](int ks) {
+      if (DEFER && pend < 2) {
+#pragma unroll
+        for (int v = 0; v < 4; ++v) put_pending(pend, 4 * ks + v);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    };
+#pragma unroll
+    for (int ks = 0; ks < 3; ++ks) {
+      frags(gs, ks + 1);
+      __builtin_amdgcn_sched_barrier(0);
+      mfmas(ks);
+      __builtin_amdgcn_sched_barrier(0);
+      stores(ks);
+    }
+    barrier();
+    scales(gs + 1);
+    frags(gs + 1, 0);
+    __builtin_amdgcn_sched_barrier(0);
+    mfmas(3);
+    __builtin_amdgcn_sched_barrier(0);
+    stores(3);
+    set_scales(KS - 8 * (s + 1));  // (after the tile's last slab: set again for the next tile)
+    ++gs;
+  };
 #pragma unroll
   for (int i = 0; i < MI; ++i) sha[i] = 0;
 #pragma unroll
@@ -499,51 +553,47 @@ __global__ void __launch_bounds__(m4w::NT, 1)
         shb[j] = (uint32_t)(reinterpret_cast<uintptr_t>(b_sf) + (uint64_t)((int64_t)e * N + n0 + bmap(wn + 32 * j + li)) * KS) & 3u;
     }
     if (!active) {
+      if (DEFER) flush();
       for (uint32_t s = 0; s < nk; ++s, ++gs) barrier();
       scales(gs);
       frags(gs, 0);
       continue;
     }
     set_scales(KS);
-    for (uint32_t s = 0; s < nk; ++s, ++gs) {  // (one basic block: the MFMAs stay between their reads)
-      asm volatile("" : "+v"(lx));
-#pragma unroll
-      for (int ks = 0; ks < 3; ++ks) {
-        frags(gs, ks + 1);
-        __builtin_amdgcn_sched_barrier(0);
-        mfmas(ks);
-        __builtin_amdgcn_sched_barrier(0);
-      }
-      barrier();
-      scales(gs + 1);
-      frags(gs + 1, 0);
-      __builtin_amdgcn_sched_barrier(0);
-      mfmas(3);
-      __builtin_amdgcn_sched_barrier(0);
-      set_scales(KS - 8 * (s + 1));  // (after the tile's last slab: set again for the next tile)
+    uint32_t s = 0;
+    if (DEFER) {
+      slab(0, 0);
+      slab(1, 1);
+      prc = make_rsrc(c, 0);
+      s = 2;
     }
+    for (; s < nk; ++s) slab(s, 2);  // (one basic block: the MFMAs stay between their reads)
     // epilogue: straight from the accumulators, a whole 128- or 256-byte row
     // segment from 32 lanes (bmap); the descriptor covers the tile's rows up to
     // the expert's last, so stores of rows past it are dropped
-    {
-      const int64_t nrows = row_end - row0 < TM ? row_end - row0 : TM;
-      const __amdgpu_buffer_rsrc_t rC = make_rsrc(static_cast<uint8_t*>(c) + row0 * (int64_t)ld, (uint64_t)nrows * ld);
+    // (NJ = 2: columns c0 + 2 li and + 1 of the wave's 64, N % 32 == 0: half of
+    // them may be past N)
+    const int64_t nrows = row_end - row0 < TM ? row_end - row0 : TM, c0 = n0 + wn;
+    const __amdgpu_buffer_rsrc_t rC = make_rsrc(static_cast<uint8_t*>(c) + row0 * (int64_t)ld, (uint64_t)nrows * ld);
+    const uint32_t vo = c0 + 2 * li < N ? lane_off : OOB, fo = (uint32_t)wm * ld + (uint32_t)c0 * ESZ;
+    if (DEFER) {
 #pragma unroll
       for (int i = 0; i < MI; ++i)
-        for (int j = 0; j < NJ; j += 2) {  // columns n0 + wn + 32 j + 2 li, + 1
-          const int64_t c0 = n0 + wn + 32 * j;
-          if (c0 >= N) continue;  // (uniform)
-          const uint32_t vo = c0 + 2 * li < N ? lane_off : OOB;  // (N % 32 == 0: half a column group may be past N)
-          const uint32_t fo = (uint32_t)(wm + i * 32) * ld + (uint32_t)c0 * ESZ;
 #pragma unroll
-          for (int v = 0; v < 16; ++v) {
-            const uint32_t so = fo + (uint32_t)((v >> 2) * 8 + (v & 3)) * ld;
-            const float v0 = acc[i][j][v], v1 = acc[i][j + 1][v];
-            if (OUT_BF16)
-              __builtin_amdgcn_raw_buffer_store_b32(bf16_pair(v0, v1), rC, vo, so, NT_STORE);
-            else
-              __builtin_amdgcn_raw_buffer_store_b64(u32x2{__float_as_uint(v0), __float_as_uint(v1)}, rC, vo, so, NT_STORE);
-          }
+        for (int v = 0; v < 16; ++v) pk[DEFER ? i : 0][v] = bf16_pair(acc[i][0][v], acc[i][1][v]);
+      prc = rC;
+      pvo = vo;
+      pfo = fo;
+    } else {
+#pragma unroll
+      for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int v = 0; v < 16; ++v) {
+          const uint32_t so = fo + (uint32_t)(32 * i + (v >> 2) * 8 + (v & 3)) * ld;
+          if (OUT_BF16)
+            __builtin_amdgcn_raw_buffer_store_b32(bf16_pair(acc[i][0][v], acc[i][1][v]), rC, vo, so, NT_STORE);
+          else
+            __builtin_amdgcn_raw_buffer_store_b64(u32x2{__float_as_uint(acc[i][0][v]), __float_as_uint(acc[i][1][v])}, rC, vo, so, NT_STORE);
         }
     }
 #pragma unroll
@@ -551,6 +601,7 @@ __global__ void __launch_bounds__(m4w::NT, 1)
 #pragma unroll
       for (int j = 0; j < NJ; ++j) acc[i][j] = f32x16{};
   }
+  if (DEFER) flush();
 }
 
 static int cu_count() {
@@ -601,12 +652,12 @@ static void launch_mx4(const uint8_t* ac, const uint8_t* as, const uint8_t* bc, 
   }
   const bool pair = K % 512 == 0 && aligned16(as) && aligned16(bs);
 #define MOE4_MX4(TN, AL)                                                                                                       \
-  hipLaunchKernelGGL((k_gemm_mx4_ws<OUT_BF16, TN, AL>), grid, dim3(m4w::NT), 0, s, ac, as, bc, bs, off, E, M, N, K,             \
+  hipLaunchKernelGGL((k_gemm_mx4_ws<OUT_BF16, TN, AL>), grid, dim3(64 * (TN / 32 + 4)), 0, s, ac, as, bc, bs, off, E, M, N, K, \
                      dg_split((N + TN - 1) / TN, m4w::TM, TN), c)
   // 256 columns unless that pads the last tile of a few: us at 131072 rows, 32
-  // experts, K = 2048, TN 128 - 256: N = 128 40 - 47, 384 78 - 82, 512 100 - 92,
-  // 640 124 - 118, 1536 303 - 262.  Without pairs of scales (TN = 128) 334 at
-  // N = 1536.
+  // experts, K = 2048, TN 128 - 256 (before the results waited for the next tile):
+  // N = 128 40 - 47, 384 78 - 82, 512 100 - 92, 640 124 - 118, 1536 303 - 262.
+  // Without pairs of scales (TN = 128) 334 at N = 1536.
   if (!pair) MOE4_MX4(128, false);
   else if (N % 256 == 0 || N > 512) MOE4_MX4(256, true);
   else MOE4_MX4(128, true);
