@@ -21,11 +21,12 @@
 // fragment order on the way to LDS, [k / 8][row][8 k]: a fragment read is then
 // 16 consecutive bytes per lane, without bank conflicts.
 //
-// Measured at 16384 tokens, k = 8, d = 4096, 384 experts: dx 525 us, against 427
+// Measured at 16384 tokens, k = 8, d = 4096, 384 experts: dx 505 us, against 427
 // for the un-permuting sum alone (2.1 GB gathered at 5.2 TB/s, the bound) and 213
 // for the GEMM alone, which hides partly behind the other workgroups' gathers:
 // six per CU (one LDS stage, one register set; 128-row tiles with two stages, 2 per
-// CU: 587).  dW 213 us and 11 for the join, 113 at the bf16 MFMA rate of a large product: its operands cross
+// CU: 587).  dW 213 us and 11 for the join, 113 at the bf16 MFMA rate of a large
+// product (the MFMAs busy 41 % of a clock that power holds at 1.5 GHz): its operands cross
 // from token-major rows through registers into LDS, three parts of dz each.
 // 64-deep slabs or 256-wide tiles would cut the workgroups per CU again.
 #include "gemm_common.h"
@@ -204,6 +205,9 @@ __global__ void __launch_bounds__(rd::NT, 4)
 #pragma unroll
     for (int v = 0; v < 16; ++v) tl[((v >> 2) * 8 + 4 * g + (v & 3)) * TN + wn + li] = acc[h][0][v];
     __syncthreads();
+    // many tiles: the rows, read once, leave W_r in the L2 (nontemporal: 524 -> 505 us at
+    // 16384 tokens, 236 -> 212 at 8000 with 64 experts; 24.5 -> 26.4 for the 32-row tiles' batches,
+    // which the caches hold)
     constexpr int JS = 8;  // row loads in flight per lane (with more, fewer workgroups fit: slower)
     if (col < d)
       for (int r = tid >> 5; r < HROWS && t0 + HROWS * h + r < T; r += NT / 32) {
@@ -213,7 +217,10 @@ __global__ void __launch_bounds__(rd::NT, 4)
           f32x4 v[JS];
 #pragma unroll
           for (int j = 0; j < JS; ++j)
-            if (j0 + j < k) v[j] = *reinterpret_cast<const f32x4*>(dxp + (int64_t)rw[j0 + j] * d + col);
+            if (j0 + j < k) {
+              const f32x4* q = reinterpret_cast<const f32x4*>(dxp + (int64_t)rw[j0 + j] * d + col);
+              v[j] = ROWS == 64 ? __builtin_nontemporal_load(q) : *q;
+            }
 #pragma unroll
           for (int j = 0; j < JS; ++j)
             if (j0 + j < k) s = s + v[j];
