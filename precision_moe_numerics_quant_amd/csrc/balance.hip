@@ -12,9 +12,9 @@
 //
 // Every kernel reads the logits once, a row per wave: 25 MB at 16384 x 384, where
 // k_balance_part takes 15 us (5 for the bytes; the rest is the latency of four
-// rows in turn per wave and the exponentials), k_balance_sum 9 (a launch and
-// a dependent chain over 256 partial rows), k_balance_bwd 19 (75 MB with the
-// gradient it adds to: 4 TB/s).  The sums over tokens are made in a fixed order (no floating-point
+// rows in turn per wave and the exponentials), k_balance_sum 7.6 (a launch and
+// a dependent chain over 256 partial rows), k_balance_bwd 16.5 (75 MB with
+// the gradient it adds to: 4.6 TB/s).  The sums over tokens are made in a fixed order (no floating-point
 // atomics): workgroup c sums the tokens of chunk c, and flushes a partial row
 // at every segment boundary inside it.  The pair (c, s) takes partial row
 // c + s: chunk and segment both only grow along the tokens, so the rows are
@@ -281,13 +281,17 @@ __global__ void __launch_bounds__(bl::SUM_T)
   }
   if (tid < 64) {  // (the first wave holds all of g = 0)
     f = wave_sum(f);
-    if (tid == 0) {
-      __hip_atomic_store(ploss + (int64_t)s * nb + blockIdx.x, f, __ATOMIC_RELEASE, __HIP_MEMORY_SCOPE_AGENT);
-      const int before = __hip_atomic_fetch_add(arrived + s, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
-      if (before == nb - 1) {
-        f = 0.0f;
-        for (int i = 0; i < nb; ++i)
-          f = f + __hip_atomic_load(ploss + (int64_t)s * nb + i, __ATOMIC_ACQUIRE, __HIP_MEMORY_SCOPE_AGENT);
+    int before = 0;
+    if (tid == 0) {  // (the addition releases the store before it)
+      __hip_atomic_store(ploss + (int64_t)s * nb + blockIdx.x, f, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      before = __hip_atomic_fetch_add(arrived + s, 1, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    if (__builtin_amdgcn_readfirstlane(before) == nb - 1) {  // (nb <= 16: a part per lane)
+      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
+      const float part = tid < nb ? __hip_atomic_load(ploss + (int64_t)s * nb + tid, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) : 0.0f;
+      f = 0.0f;
+      for (int i = 0; i < nb; ++i) f = f + __shfl(part, i, 64);
+      if (tid == 0) {
         loss[s] = n > 0 ? f * ((float)E / ((float)k * (float)n)) : 0.0f;
         tokens[s] = n;
       }
@@ -306,22 +310,29 @@ __global__ void __launch_bounds__(64 * bl::BWD_W)
   const int64_t t = (int64_t)blockIdx.x * BWD_W + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l = threadIdx.x & 63;
   if (t >= T) return;
-  float o[PER], z[PER];
+  float o[PER], z[PER], bv[PER], c[PER];
+  const int s = seg_of(seg_off, n_seg, t, T);
+  const bool live = s < n_seg && t >= seg_at(seg_off, s, T) && (!mask || mask[t]);
+  int cnt[PER], ns = 0;
+  float dl = 0.0f;
+  if (live) {  // (every load in flight before the first is used)
+    load_bias<PER>(bias, E, bv);
+#pragma unroll
+    for (int i = 0; i < PER; ++i) cnt[i] = l + 64 * i < E ? counts[(int64_t)s * E + l + 64 * i] : 0;
+    ns = tokens[s];
+    dl = dloss[s];
+    load_row<PER>(logits, bv, t, E, z);
+  }
 #pragma unroll
   for (int i = 0; i < PER; ++i) o[i] = base && l + 64 * i < E ? base[t * E + l + 64 * i] : 0.0f;
-  const int s = seg_of(seg_off, n_seg, t, T);
-  const bool live = s < n_seg && t >= seg_at(seg_off, s, T) && (!mask || mask[t]) && tokens[s] > 0;
-  if (live) {
-    float bv[PER], c[PER];
-    load_bias<PER>(bias, E, bv);
-    load_row<PER>(logits, bv, t, E, z);
-    const float n = (float)tokens[s];
+  if (live && ns > 0) {
+    const float n = (float)ns;
     // counts from their mean: the same gradient (sum_e p = 1), without the
     // cancellation of two large numbers when the router is nearly even
     const float cm = (float)k * n / (float)E;
-    const float f = dloss[s] * ((float)E / ((float)k * n)) / n;
+    const float f = dl * ((float)E / ((float)k * n)) / n;
 #pragma unroll
-    for (int i = 0; i < PER; ++i) c[i] = l + 64 * i < E ? (float)counts[(int64_t)s * E + l + 64 * i] - cm : 0.0f;
+    for (int i = 0; i < PER; ++i) c[i] = l + 64 * i < E ? (float)cnt[i] - cm : 0.0f;
     softmax_row<PER>(z);
     float d = 0.0f;
 #pragma unroll
