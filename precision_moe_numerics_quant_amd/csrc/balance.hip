@@ -14,8 +14,8 @@
 // k_balance_part takes 15 us (5 for the bytes; the rest is the latency of four
 // rows in turn per wave and the exponentials), k_balance_sum 7.6 (a launch and
 // a dependent chain over 256 partial rows), k_balance_bwd 16.5 (75 MB with
-// the gradient it adds to: 4.6 TB/s).  The sums over tokens are made in a fixed order (no floating-point
-// atomics): workgroup c sums the tokens of chunk c, and flushes a partial row
+// the gradient it adds to: 4.6 TB/s).  The sums over tokens are made in a fixed
+// order (no floating-point atomics): workgroup c sums the tokens of chunk c, and flushes a partial row
 // at every segment boundary inside it.  The pair (c, s) takes partial row
 // c + s: chunk and segment both only grow along the tokens, so the rows are
 // distinct and no prefix sum over the segments is needed.
