@@ -15,7 +15,9 @@
 // share it, and four pieces a lane are then transposed within those four lanes,
 // so that each holds one block: 16 code bytes and a scale byte to store, a
 // quarter of the store instructions (which is what the dispatch, storing
-// every block `copies` times, spends its time on).
+// every block `copies` times, spends its time on).  16384 x 4096 bf16 to eight
+// rows each (0.44 GB): 73 us, 6.0 TB/s; 73728 x 4096 float32 (1.37 GB): 238 us,
+// 5.7 TB/s; 131072 x 4096 decoded to bf16 (1.38 GB, mostly written): 252 us.
 #include "act.h"
 #include "moe4_internal.h"
 #include "mx_requant.h"

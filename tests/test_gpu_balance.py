@@ -161,6 +161,35 @@ def test_balance_deterministic_in_place_and_replayed():
         torch.cuda.synchronize()
 
 
+def test_two_calls_at_once():
+    """Calls in flight on two streams (each with its own workspace) give the bits of calls made alone."""
+    rng = np.random.default_rng(21)
+    cases = []
+    for T, E, d in ((4000, 384, 516), (3000, 64, 260)):
+        z = cuda_f32(rng.standard_normal((T, E)).astype(np.float32))
+        idx = cuda_i32(rng.integers(0, E, (T, 4)).astype(np.int32))
+        off = cuda_i32(np.array([0, 7, 7, T // 2, T], np.int32))
+        x = torch.from_numpy(rng.standard_normal((T, d)).astype(np.float32)).cuda().bfloat16()
+
+        def step(z=z, idx=idx, off=off, x=x):
+            b = m4.moe_balance_loss(z, idx, seg_off=off)
+            dz = m4.moe_balance_loss_backward(torch.ones(4, device="cuda"), z, b["counts"], b["tokens"], 4, seg_off=off)
+            return [b["loss"], b["counts"], dz, m4.moe_router_wgrad_dense(x, dz)]
+        cases.append(step)
+    alone = [[v.cpu() for v in step()] for step in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    got = [[], []]
+    for _ in range(4):
+        for i, (step, s) in enumerate(zip(cases, streams)):
+            with torch.cuda.stream(s):
+                got[i].append(step())
+    torch.cuda.synchronize()
+    for want, runs in zip(alone, got):
+        for run in runs:
+            assert all(torch.equal(w, v.cpu()) for w, v in zip(want, run))
+
+
 # -------------------------------------------------------------- dense router
 
 @pytest.mark.parametrize("T,E,k,d", [(1, 2, 1, 4), (200, 8, 2, 256), (333, 130, 6, 520), (50, 20, 16, 68), (130, 384, 8, 1024), (2500, 33, 3, 132),
