@@ -70,7 +70,10 @@ __device__ inline void load_bias(const float* __restrict__ bias, int E, float (&
   for (int i = 0; i < PER; ++i) b[i] = bias && l + 64 * i < E ? bias[l + 64 * i] : 0.0f;
 }
 
-// z turned into its softmax (every expert of a row of -infinities is 0).
+// z turned into its softmax (every expert of a row of -infinities is 0).  The
+// maximum passes over NaNs, so the zero is each -infinity's own and not the
+// row's: a NaN beside -infinities (masked experts, the places past E) stays one
+// and makes the sum, and with it the row, NaN.
 // exp(d) = 2^(d log2 e): for d <= 0 the product's rounding is as large an error
 // as the difference's own, and the hardware's 2^x is good to one unit.
 template <int PER>
@@ -82,7 +85,7 @@ __device__ inline void softmax_row(float (&z)[PER]) {
   float s = 0.0f;
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
-    z[i] = m == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((z[i] - m) * 1.44269504f);
+    z[i] = z[i] == -INFINITY ? 0.0f : __builtin_amdgcn_exp2f((z[i] - m) * 1.44269504f);
     s = s + z[i];
   }
   s = wave_sum(s);

@@ -1,0 +1,59 @@
+"""Edges of the balance loss: logits that are not finite."""
+import numpy as np
+import pytest
+import torch
+
+from gpu_helpers import cuda_f32, cuda_i32, to_np
+from oracle import balance as ob
+
+pytestmark = pytest.mark.gpu
+
+if torch.cuda.is_available():
+    import precision_moe_numerics_quant_amd as m4
+
+U = 2.0 ** -24
+
+
+# -------------------------------------------------------------- balance loss
+
+@pytest.mark.parametrize("bias", [False, True])
+@pytest.mark.parametrize("E", [1, 2, 8, 9, 64, 130, 384, 1024])
+def test_balance_rows_that_are_not_finite(E, bias):
+    """A row with a NaN or +infinity anywhere, whatever else it holds, has NaN probabilities, loss and gradient; a row
+    of -infinities has zeros; every other row is as ever.  One segment per row, then one for all."""
+    rng = np.random.default_rng(E)
+    T, k, inf, nan = 14, 1, np.inf, np.nan
+    z = rng.standard_normal((T, E)).astype(np.float32)
+    b = rng.standard_normal(E).astype(np.float32) if bias else None
+    z[1] = nan
+    z[2], z[2, E // 2] = -inf, nan
+    z[3, E - 1] = nan
+    z[4, 0] = inf
+    z[5], z[5, E - 1] = -inf, inf
+    z[6] = inf
+    z[7] = -inf
+    z[8, :E - 1] = -inf                         # one finite value (E = 1: an ordinary row)
+    z[9], z[9, 0] = inf, -inf
+    z[10, 0], z[10, E - 1] = -inf, nan
+    idx = rng.integers(0, E, (T, k)).astype(np.int32)
+    for seg in (np.arange(T + 1), [0, T]):
+        kw = dict(bias=None if b is None else cuda_f32(b), seg_off=cuda_i32(seg))
+        r = m4.moe_balance_loss(cuda_f32(z), cuda_i32(idx), **kw)
+        with np.errstate(invalid="ignore"):
+            o = ob.balance_loss(z, idx, b, None, seg)
+            dl = rng.standard_normal(len(seg) - 1).astype(np.float32)
+            g = ob.balance_grad(dl, z, o["counts"], o["tokens"], k, b, None, seg)
+        assert np.array_equal(to_np(r["counts"]), o["counts"]) and np.array_equal(to_np(r["tokens"]), o["tokens"])
+        got = to_np(m4.moe_balance_loss_backward(cuda_f32(dl), cuda_f32(z), r["counts"], r["tokens"], k, **kw))
+        # the argument of the exponential rounds twice at its magnitude (below 16 here), the exponential by two units,
+        # the sum of E terms E / 64 + 6 times, a reciprocal and a product; then 14 terms and E products of the loss
+        tol = (2 * 16 + E / 64 + 6 + 8 + 16 + E + 6) * U
+        for name in ("probs", "loss"):
+            a, w = to_np(r[name]).astype(np.float64), o[name]
+            assert np.array_equal(np.isnan(a), np.isnan(w)), name
+            ok = ~np.isnan(w)
+            assert (np.abs(a - w)[ok] <= tol * np.abs(w)[ok]).all(), name
+        assert np.array_equal(np.isnan(got), np.isnan(g))
+        # two terms of at most dloss E / (k n^2) max(c) each with p's error
+        lim = 4 * tol * np.abs(dl).max() * E * max(1, o["counts"].max())
+        assert (np.abs(got - g)[~np.isnan(g)] <= lim).all()

@@ -89,3 +89,14 @@ def test_dense_router_backward_reduces_to_the_sparse_one(T, E, k, d):
     dense, _ = router.unpermute_sum_dense(dxp, P["inv_perm"], T, k, dl, w)
     sparse = fmt.bf16_to_f32(router.unpermute_sum_router(dxp, P["inv_perm"], T, k, dl, idx, w)).astype(np.float64)
     assert np.allclose(sparse, dense, rtol=2.0 ** -7, atol=1e-5)
+
+
+def test_rows_that_are_not_finite():
+    """A NaN or +infinity makes its row NaN whatever else is in it; -infinities are zeros, also where there is nothing else."""
+    inf, nan = np.inf, np.nan
+    z = np.float32([[nan, nan, nan], [-inf, nan, -inf], [0, 1, nan], [0, inf, -inf], [-inf] * 3, [-inf, 0, 0]])
+    with np.errstate(invalid="ignore"):
+        r = ob.balance_loss(z, np.zeros((6, 1), int), seg_off=range(7))
+        g = ob.balance_grad(np.ones(6), z, r["counts"], r["tokens"], 1, seg_off=range(7))
+    assert np.isnan(r["probs"][:4]).all() and np.isnan(r["loss"][:4]).all() and np.isnan(g[:4]).all()
+    assert r["probs"][4:].tolist() == [[0, 0, 0], [0, 0.5, 0.5]] and r["loss"][4:].tolist() == [0, 0] and not g[4:].any()
