@@ -96,7 +96,7 @@ def test_rows_that_are_not_finite():
     inf, nan = np.inf, np.nan
     z = np.float32([[nan, nan, nan], [-inf, nan, -inf], [0, 1, nan], [0, inf, -inf], [-inf] * 3, [-inf, 0, 0]])
     with np.errstate(invalid="ignore"):
-        r = ob.balance_loss(z, np.zeros((6, 1), int), seg_off=range(7))
-        g = ob.balance_grad(np.ones(6), z, r["counts"], r["tokens"], 1, seg_off=range(7))
+        r = balance.balance_loss(z, np.zeros((6, 1), int), seg_off=range(7))
+        g = balance.balance_grad(np.ones(6), z, r["counts"], r["tokens"], 1, seg_off=range(7))
     assert np.isnan(r["probs"][:4]).all() and np.isnan(r["loss"][:4]).all() and np.isnan(g[:4]).all()
     assert r["probs"][4:].tolist() == [[0, 0, 0], [0, 0.5, 0.5]] and r["loss"][4:].tolist() == [0, 0] and not g[4:].any()
