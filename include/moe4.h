@@ -703,7 +703,7 @@ size_t moe_router_wgrad_ws_bytes(int64_t T, int32_t E, int32_t k, int64_t d);
  * loss [n_seg], counts [n_seg, E] int32, tokens [n_seg] int32 (n_s), probs
  * [n_seg, E].  Sums over tokens in float32 in a fixed order (deterministic).
  * Indices outside [0, E) are clamped and reported (MOE4_DEVERR_INDEX).
- * 1 <= k <= min(E, 16), E <= 1024, n_seg <= 65535.
+ * 1 <= k <= min(E, 16), E <= 1024, n_seg <= 65535, T <= 2^28 - 64, T * k < 2^31.
  * ws: moe_balance_loss_ws_bytes(T, E, n_seg), the caller's, overwritten; calls
  * in flight at the same time need workspaces of their own.
  */
@@ -720,7 +720,7 @@ size_t moe_balance_loss_ws_bytes(int64_t T, int32_t E, int32_t n_seg);
  * for the unmasked tokens t of segment s; dlogits_in[t, e] for every other
  * token.  dlogits_in [T, E] (e.g. moe_route_backward's output) may be NULL
  * (zeros) and may be dlogits itself.  counts and tokens as moe_balance_loss
- * wrote them; the other arguments as there.
+ * wrote them; the other arguments as there (T <= 2^28 - 64).
  */
 int moe_balance_loss_backward(const float* dloss, const float* logits, const float* bias, const int32_t* counts,
                               const int32_t* tokens, const uint8_t* token_mask, const int32_t* seg_off, int32_t n_seg,

@@ -34,6 +34,9 @@ constexpr int CH_MIN = 16, CH_MAX = 64;    // tokens per chunk (bl_chunk)
 constexpr int CHUNKS = 256;                // chunks that fill the chip
 constexpr int SUM_T = 512, SUM_Q = 16;     // k_balance_sum: threads, column quads per workgroup
 constexpr int BWD_W = 4;                   // k_balance_bwd: waves (tokens) per workgroup
+constexpr int64_t BWD_X = 1 << 22;         // its workgroups along x (2^24 of them would be 2^32 threads)
+// tokens: k_balance_part's threads, 16 per token, stay below the 2^32 of a grid dimension
+constexpr int64_t MAXT = (1 << 28) - CH_MAX;
 }  // namespace bl
 
 __device__ inline float sum_xor16(float v) {
@@ -302,7 +305,7 @@ __global__ void __launch_bounds__(bl::SUM_T)
   }
 }
 
-// One wave per token.
+// One wave per token; past 2^24 tokens the workgroups go on along y.
 template <int PER>
 __global__ void __launch_bounds__(64 * bl::BWD_W)
     k_balance_bwd(const float* __restrict__ dloss, const float* __restrict__ logits, const float* __restrict__ bias,
@@ -310,7 +313,7 @@ __global__ void __launch_bounds__(64 * bl::BWD_W)
                   const uint8_t* __restrict__ mask, const int32_t* __restrict__ seg_off, int n_seg, int64_t T, int E,
                   int k, const float* base, float* out) {  // base may be out
   using namespace bl;
-  const int64_t t = (int64_t)blockIdx.x * BWD_W + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int64_t t = ((int64_t)blockIdx.y * BWD_X + blockIdx.x) * BWD_W + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int l = threadIdx.x & 63;
   if (t >= T) return;
   float o[PER], z[PER], bv[PER], c[PER];
@@ -396,7 +399,8 @@ extern "C" int moe_balance_loss(const float* logits, const float* bias, const in
                                 size_t ws_bytes, void* stream) {
   MOE4_REQUIRE(T >= 0 && E >= 1 && E <= bl::MAXE && k >= 1 && k <= bl::MAXK && k <= E, MOE4_EINVAL,
                "moe_balance_loss: need T >= 0, 1 <= k <= min(E, 16), E <= 1024");
-  MOE4_REQUIRE(T * (int64_t)k < ((int64_t)1 << 31), MOE4_EINVAL, "moe_balance_loss: T * k must be below 2^31");
+  MOE4_REQUIRE(T <= bl::MAXT && T * (int64_t)k < ((int64_t)1 << 31), MOE4_EINVAL,
+               "moe_balance_loss: T must be at most 2^28 - 64 and T * k below 2^31");
   MOE4_REQUIRE(n_seg >= 1 && n_seg <= 65535 && (seg_off || n_seg == 1), MOE4_EINVAL,
                "moe_balance_loss: 1 <= n_seg <= 65535, with seg_off unless it is 1");
   MOE4_REQUIRE(loss && counts && tokens && probs && (T == 0 || (logits && topk_idx)), MOE4_EINVAL,
@@ -431,14 +435,15 @@ extern "C" int moe_balance_loss_backward(const float* dloss, const float* logits
                "moe_balance_loss_backward: need T >= 0, 1 <= k <= min(E, 16), E <= 1024");
   MOE4_REQUIRE(n_seg >= 1 && (seg_off || n_seg == 1), MOE4_EINVAL,
                "moe_balance_loss_backward: n_seg >= 1, with seg_off unless it is 1");
-  MOE4_REQUIRE(T < ((int64_t)1 << 31), MOE4_EINVAL, "moe_balance_loss_backward: T must be below 2^31");
+  MOE4_REQUIRE(T <= bl::MAXT, MOE4_EINVAL, "moe_balance_loss_backward: T must be at most 2^28 - 64");
   MOE4_REQUIRE(dloss && counts && tokens && (T == 0 || (logits && dlogits)), MOE4_EINVAL,
                "moe_balance_loss_backward: NULL pointer");
   if (T == 0) return MOE4_OK;
-#define MOE4_BL_BWD(PER)                                                                                              \
-  hipLaunchKernelGGL((k_balance_bwd<PER>), dim3((unsigned)((T + bl::BWD_W - 1) / bl::BWD_W)), dim3(64 * bl::BWD_W), 0, \
-                     as_stream(stream), dloss, logits, bias, counts, tokens, token_mask, seg_off, n_seg, T, E, k,      \
-                     dlogits_in, dlogits)
+  const int64_t wg = (T + bl::BWD_W - 1) / bl::BWD_W, ny = (wg + bl::BWD_X - 1) / bl::BWD_X;
+  const dim3 grid((unsigned)(wg < bl::BWD_X ? wg : bl::BWD_X), (unsigned)ny);
+#define MOE4_BL_BWD(PER)                                                                                       \
+  hipLaunchKernelGGL((k_balance_bwd<PER>), grid, dim3(64 * bl::BWD_W), 0, as_stream(stream), dloss, logits, bias, \
+                     counts, tokens, token_mask, seg_off, n_seg, T, E, k, dlogits_in, dlogits)
   MOE4_BL_PER(MOE4_BL_BWD);
 #undef MOE4_BL_BWD
   return check_launch("moe_balance_loss_backward");

@@ -1,0 +1,27 @@
+"""Sizes whose launch would exceed the 2**32 threads that a grid dimension may
+have: refused on the host with a message, nothing launched (no GPU needed)."""
+import ctypes
+
+from test_capi_exports import _lib
+
+v = ctypes.c_void_p
+i64, i32, size = ctypes.c_int64, ctypes.c_int32, ctypes.c_size_t
+P, O = v(4096), v(0)         # an aligned address that no refused call touches
+BIG = size(1 << 62)
+
+
+def refused(name, *args):
+    L = _lib()
+    L.moe4_last_error.restype = ctypes.c_char_p
+    f = getattr(L, name)
+    f.restype = ctypes.c_int
+    assert f(*args) == -1
+    msg = L.moe4_last_error().decode()
+    assert name in msg
+    return msg
+
+
+def test_balance_loss_and_gradient():
+    for T in ((1 << 28) - 63, 1 << 28, (1 << 31) - 1):
+        assert "2^28" in refused("moe_balance_loss", P, O, P, O, O, i32(1), i64(T), i32(2), i32(1), P, P, P, P, P, BIG, O)
+        assert "2^28" in refused("moe_balance_loss_backward", P, P, O, P, P, O, O, i32(1), i64(T), i32(2), i32(1), O, P, O)

@@ -1,4 +1,4 @@
-"""Edges of the balance loss: logits that are not finite."""
+"""Edges of the balance loss: logits that are not finite, launch sizes."""
 import numpy as np
 import pytest
 import torch
@@ -57,3 +57,36 @@ def test_balance_rows_that_are_not_finite(E, bias):
         # two terms of at most dloss E / (k n^2) max(c) each with p's error
         lim = 4 * tol * np.abs(dl).max() * E * max(1, o["counts"].max())
         assert (np.abs(got - g)[~np.isnan(g)] <= lim).all()
+
+
+def test_balance_gradient_of_more_tokens_than_one_grid_row():
+    """2**26 + 5 tokens: more than 2**32 threads of one wave per token.  Rows repeat a pattern of 1024, whose results
+    are checked in float64; equal rows have equal bits wherever they are."""
+    P, T, E, k = 1024, (1 << 26) + 5, 2, 1
+    rng = np.random.default_rng(26)
+    zp = rng.standard_normal((P, E)).astype(np.float32)
+    ip = (zp[:, 1] > zp[:, 0]).astype(np.int32)[:, None]
+    rep = lambda a: torch.cat([a.repeat(T // P, 1), a[:T % P]])
+    z, idx = rep(cuda_f32(zp)), rep(cuda_i32(ip))
+    r = m4.moe_balance_loss(z, idx)
+    p = ob.softmax(zp)
+    full, rest = T // P, T % P
+    count = np.bincount(ip[:, 0], minlength=E) * full + np.bincount(ip[:rest, 0], minlength=E)
+    mean = (p.sum(0) * full + p[:rest].sum(0)) / T
+    assert np.array_equal(to_np(r["counts"])[0], count) and int(r["tokens"][0]) == T
+    # sums of positive terms: 4 tokens in turn per wave, 16 waves, 2**20 chunks in 32 shares, the shares; each softmax
+    # is good to 32 units here
+    tol = (4 + 16 + (1 << 15) + 1 + 32 + 32 + 8) * U
+    assert (np.abs(to_np(r["probs"])[0] - mean) <= tol * mean).all()
+    loss = E / (k * T) * (count * mean).sum()
+    assert abs(float(r["loss"][0]) - loss) <= (tol + 8 * U) * loss
+    dl = torch.full((1,), 1e6, device="cuda")
+    g = m4.moe_balance_loss_backward(dl, z, r["counts"], r["tokens"], k)
+    c = count.astype(np.float64)
+    want = 1e6 * E / (k * float(T) ** 2) * p * (c[None, :] - (p @ c)[:, None])
+    dev = np.abs(c - c.mean()).max()
+    lim = 1e6 * E / (k * float(T) ** 2) * p * 2 * dev * (3 * 32 + 16) * U
+    # (the counts' difference from their mean: an exact integer less a rounded k n / E, half a unit of 2**25)
+    lim = lim + 1e6 * E / (k * float(T) ** 2) * p * 4
+    assert (np.abs(to_np(g[:P]) - want) <= lim).all()
+    assert torch.equal(g[:full * P].view(full, P, E), g[:P].expand(full, P, E)) and torch.equal(g[full * P:], g[:rest])
