@@ -29,6 +29,9 @@
  *    its constant SiLU / SiLU' tables (data of the code object): no call
  *    fills anything at run time, so any call may be the first one on a device
  *    and may be made inside a stream capture.
+ *  - A call whose launch would need more threads than a grid dimension holds
+ *    (2^32 - 1) is refused as too large (mxfp4_*, mxfp8_requant_mx4_sr_T,
+ *    moe_grouped_gemm_mx4 and the router's dense calls) before it is enqueued.
  *  - Sizes are int64_t; offsets and indices are int32_t device arrays.
  *  - Pointers must be 16-byte aligned.
  *

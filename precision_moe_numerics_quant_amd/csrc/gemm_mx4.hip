@@ -615,23 +615,31 @@ static int cu_count() {
   }
   return n[dev];
 }
+// workgroups of the tiled kernel (every XCD has one at least)
+static int ws_grid() { return cu_count() < 8 ? 8 : cu_count(); }
+
+// Whether a product goes to the few-rows kernel: up to 4 rows per expert on
+// average, or up to 32 where the tiled kernel would not have a tile for every
+// CU.  N = 1536, K = 4096, few-rows against tiled kernel, even routing | one power-law routing (1.1), in us:
+//   384 experts, rows per expert 4: 242 - 286 | 88 - 76;  8: 254 - 284 | 130 - 83;
+//   11: 261 - 285 | 163 - 86;  16: 301 - 285 | 210 - 110;  32: 405 - 293 | 363 - 162
+//   (a popular expert's weights are read again for every 32 rows);
+//   8 experts, rows per expert 8, 16, 32: 12 - 19, 12 - 19, 14 - 20
+static bool few_rows(int E, int64_t M, int64_t N) {
+  const int64_t tiles = ((M < E ? M : E) + M / m4w::TM) * ((N + 255) / 256);
+  return M <= 4 * (int64_t)E || (M <= 32 * (int64_t)E && tiles < ws_grid());
+}
+// its workgroups: blocks of weight rows, and slots (see the kernel)
+static int64_t rows_nt(int64_t N) { return (N + m4s::WROWS - 1) / m4s::WROWS; }
+static int64_t rows_slots(int E, int64_t M) { return (M < E ? M : E) + M / m4s::TR; }
 
 template <bool OUT_BF16>
 static void launch_mx4(const uint8_t* ac, const uint8_t* as, const uint8_t* bc, const uint8_t* bs, const int32_t* off, int E,
                        int64_t M, int64_t N, int64_t K, void* c, hipStream_t s) {
   const bool al = K % 128 == 0 && aligned4(as) && aligned4(bs);
-  const dim3 grid((unsigned)(cu_count() < 8 ? 8 : cu_count()));
-  // Few rows: up to 4 per expert on average, or up to 32 where the tiled kernel
-  // would not have a tile for every CU.  N = 1536, K = 4096, few-rows against
-  // tiled kernel, even routing | one power-law routing (1.1), in us:
-  //   384 experts, rows per expert 4: 242 - 286 | 88 - 76;  8: 254 - 284 | 130 - 83;
-  //   11: 261 - 285 | 163 - 86;  16: 301 - 285 | 210 - 110;  32: 405 - 293 | 363 - 162
-  //   (a popular expert's weights are read again for every 32 rows);
-  //   8 experts, rows per expert 8, 16, 32: 12 - 19, 12 - 19, 14 - 20
-  const int64_t tiles = ((M < E ? M : E) + M / m4w::TM) * ((N + 255) / 256);
-  if (M <= 4 * (int64_t)E || (M <= 32 * (int64_t)E && tiles < grid.x)) {
-    const int64_t n_nt = (N + m4s::WROWS - 1) / m4s::WROWS, first = M < E ? M : E, slots = first + M / m4s::TR;
-    const dim3 rgrid((unsigned)(n_nt * slots));
+  if (few_rows(E, M, N)) {
+    const int64_t n_nt = rows_nt(N), first = M < E ? M : E;
+    const dim3 rgrid((unsigned)(n_nt * rows_slots(E, M)));
     const int64_t spw = ((K + m4s::KB - 1) / m4s::KB + m4s::NWV - 1) / m4s::NWV;
 #define MOE4_MX4S(AL, NS)                                                                                                      \
   hipLaunchKernelGGL((k_gemm_mx4_rows<OUT_BF16, AL, NS>), rgrid, dim3(m4s::NT), 0, s, ac, as, bc, bs, off, E, M, N, K,           \
@@ -650,6 +658,7 @@ static void launch_mx4(const uint8_t* ac, const uint8_t* as, const uint8_t* bc, 
 #undef MOE4_MX4S
     return;
   }
+  const dim3 grid((unsigned)ws_grid());
   const bool pair = K % 512 == 0 && aligned16(as) && aligned16(bs);
 #define MOE4_MX4(TN, AL)                                                                                                       \
   hipLaunchKernelGGL((k_gemm_mx4_ws<OUT_BF16, TN, AL>), grid, dim3(64 * (TN / 32 + 4)), 0, s, ac, as, bc, bs, off, E, M, N, K, \
@@ -681,8 +690,10 @@ extern "C" int moe_grouped_gemm_mx4(const uint8_t* a_codes, const uint8_t* a_sf,
   MOE4_REQUIRE(aligned16(a_codes) && aligned16(b_codes) && aligned16(c), MOE4_EALIGN,
                "moe_grouped_gemm_mx4: a_codes, b_codes and c must be 16-byte aligned");
   if (M_total == 0) return MOE4_OK;
-  MOE4_REQUIRE((M_total / m4s::TR + E) * ((N + m4s::WROWS - 1) / m4s::WROWS) < ((int64_t)1 << 31), MOE4_EINVAL,
-               "moe_grouped_gemm_mx4: too large");
+  // (the tiled kernel's grid is fixed; its tile counts are 32-bit)
+  MOE4_REQUIRE(few_rows(E, M_total, N) ? grid_fits(rows_nt(N) * rows_slots(E, M_total), m4s::NT)
+                                       : (M_total / m4s::TR + E) * rows_nt(N) < ((int64_t)1 << 31),
+               MOE4_EINVAL, "moe_grouped_gemm_mx4: too large");
   if (c_dtype == MOE4_BF16)
     launch_mx4<true>(a_codes, a_sf, b_codes, b_sf, expert_off, E, M_total, N, K, c, as_stream(stream));
   else

@@ -443,8 +443,8 @@ extern "C" int mxfp4_quant(const void* x, int dtype, int64_t rows, int64_t cols,
   const int64_t pieces = rows * (cols / 8), units = (pieces + m4q::UNIT - 1) / m4q::UNIT;
   const int threads = pre_op == MOE4_PRE_SILU ? m4q::THREADS_SILU : m4q::THREADS;
   int64_t wg = (units + threads / 64 - 1) / (threads / 64);
-  MOE4_REQUIRE(wg < ((int64_t)1 << 31), MOE4_EINVAL, "mxfp4_quant: tensor too large");
   if (pre_op == MOE4_PRE_SILU && wg > m4q::SILU_WG) wg = m4q::SILU_WG;
+  MOE4_REQUIRE(grid_fits(wg, threads), MOE4_EINVAL, "mxfp4_quant: tensor too large");
   const float* tab = nullptr;
   if (pre_op == MOE4_PRE_SILU) {
     const int rc = act_tables(&tab);
@@ -476,7 +476,7 @@ extern "C" int mxfp4_dequant(const uint8_t* codes, const uint8_t* sf, int64_t ro
   MOE4_REQUIRE(codes && sf && out, MOE4_EINVAL, "mxfp4_dequant: NULL pointer");
   MOE4_REQUIRE(aligned16(codes) && aligned16(out), MOE4_EALIGN, "mxfp4_dequant: codes and out must be 16-byte aligned");
   const int64_t pieces = rows * (cols / 8), wg = (pieces + m4q::THREADS - 1) / m4q::THREADS;
-  MOE4_REQUIRE(wg < ((int64_t)1 << 31), MOE4_EINVAL, "mxfp4_dequant: tensor too large");
+  MOE4_REQUIRE(grid_fits(wg, m4q::THREADS), MOE4_EINVAL, "mxfp4_dequant: tensor too large");
   const uint32_t* cw = reinterpret_cast<const uint32_t*>(codes);
   if (out_dtype == MOE4_F32)
     hipLaunchKernelGGL(k_mx4_dequant<MOE4_F32>, dim3((unsigned)wg), dim3(m4q::THREADS), 0, as_stream(stream), cw, sf, pieces, out);
@@ -499,7 +499,7 @@ extern "C" int mxfp8_requant_mx4_sr_T(const uint8_t* codes, const uint8_t* sf, i
   MOE4_REQUIRE((rows == 0 || (codes && sf)) && out_codes && out_sf, MOE4_EINVAL, "mxfp8_requant_mx4_sr_T: NULL pointer");
   MOE4_REQUIRE(aligned16(codes) && aligned16(out_codes), MOE4_EALIGN, "mxfp8_requant_mx4_sr_T: misaligned pointer");
   const int64_t n_ct = (cols + rq::COLS - 1) / rq::COLS, n_rt = (max_padded_rows + rq::ROWS - 1) / rq::ROWS;
-  MOE4_REQUIRE(n_ct * n_rt < (int64_t)1 << 31, MOE4_EINVAL, "mxfp8_requant_mx4_sr_T: tensor too large");
+  MOE4_REQUIRE(grid_fits(n_ct * n_rt, rq::THREADS), MOE4_EINVAL, "mxfp8_requant_mx4_sr_T: tensor too large");
   hipLaunchKernelGGL(k_requant_mx4_T, dim3((unsigned)(n_ct * n_rt)), dim3(rq::THREADS), 0, as_stream(stream), codes, sf,
                      cols, group_row_off, group_off_pad, n_groups, rows, max_padded_rows, n_ct,
                      sr_base_key(seed, stream_id), (int)(sf_layout == MOE4_SF_BLOCKS), out_codes, out_sf);

@@ -343,7 +343,7 @@ extern "C" int moe_unpermute_sum_router_dense(const float* dxp, const int32_t* i
                "moe_unpermute_sum_router_dense: dxp, dlogits, w and dx must be 16-byte aligned");
   if (T == 0) return MOE4_OK;
   const int64_t n_nt = (d + rd::TN - 1) / rd::TN, n64 = n_nt * ((T + 63) / 64), n32 = n_nt * ((T + 31) / 32);
-  MOE4_REQUIRE(n64 < ((int64_t)1 << 30), MOE4_EINVAL, "moe_unpermute_sum_router_dense: too large");
+  MOE4_REQUIRE(grid_fits(xcd_grid(n64), rd::NT), MOE4_EINVAL, "moe_unpermute_sum_router_dense: too large");
 #define MOE4_RDX(ROWS, TILES)                                                                                        \
   hipLaunchKernelGGL(k_router_dx_dense<ROWS>, dim3((unsigned)xcd_grid(TILES)), dim3(rd::NT), 0, as_stream(stream), dxp, \
                      inv_perm, T, k, d, dlogits, E, w, n_nt, TILES, dx)
@@ -367,7 +367,7 @@ extern "C" int moe_router_wgrad_dense(const uint16_t* x, const float* dlogits, i
   MOE4_REQUIRE(aligned16(x) && aligned16(dlogits) && aligned16(dw), MOE4_EALIGN,
                "moe_router_wgrad_dense: x, dlogits and dw must be 16-byte aligned");
   const int64_t n_nt = (d + rd::TN - 1) / rd::TN, tiles = n_nt * ((E + rd::TM - 1) / rd::TM);
-  MOE4_REQUIRE(tiles < ((int64_t)1 << 31), MOE4_EINVAL, "moe_router_wgrad_dense: too large");
+  MOE4_REQUIRE(grid_fits(tiles, rd::NT), MOE4_EINVAL, "moe_router_wgrad_dense: too large");
   const int n = dw_shares(T, E, d);
   const size_t need = moe_router_wgrad_dense_ws_bytes(T, E, d);
   MOE4_REQUIRE(need == 0 || (ws && ws_bytes >= need), MOE4_EWORKSPACE,
