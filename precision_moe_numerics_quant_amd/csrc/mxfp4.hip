@@ -437,8 +437,9 @@ extern "C" int mxfp4_quant(const void* x, int dtype, int64_t rows, int64_t cols,
                  "mxfp4_quant: out_map needs copies >= 1, out_rows >= 0 and rows * copies below 2^31");
   else
     MOE4_REQUIRE(copies == 1 && out_rows == rows, MOE4_EINVAL, "mxfp4_quant: without out_map, copies = 1 and out_rows = rows");
-  if (rows == 0 || out_rows == 0) return MOE4_OK;
-  MOE4_REQUIRE(x && codes && sf, MOE4_EINVAL, "mxfp4_quant: NULL pointer");
+  if (rows == 0) return MOE4_OK;
+  // (no output rows: nothing is written, but every entry of out_map is reported)
+  MOE4_REQUIRE(x && (out_rows == 0 || (codes && sf)), MOE4_EINVAL, "mxfp4_quant: NULL pointer");
   MOE4_REQUIRE(aligned16(x) && aligned16(codes), MOE4_EALIGN, "mxfp4_quant: x and codes must be 16-byte aligned");
   const int64_t pieces = rows * (cols / 8), units = (pieces + m4q::UNIT - 1) / m4q::UNIT;
   const int threads = pre_op == MOE4_PRE_SILU ? m4q::THREADS_SILU : m4q::THREADS;

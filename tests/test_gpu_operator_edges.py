@@ -1,4 +1,5 @@
-"""Edges of the balance loss: logits that are not finite, launch sizes."""
+"""Edges of the balance loss and MXFP4 quantisation: logits that are not finite,
+launch sizes, a dispatch to no rows."""
 import numpy as np
 import pytest
 import torch
@@ -90,3 +91,16 @@ def test_balance_gradient_of_more_tokens_than_one_grid_row():
     lim = lim + 1e6 * E / (k * float(T) ** 2) * p * 4
     assert (np.abs(to_np(g[:P]) - want) <= lim).all()
     assert torch.equal(g[:full * P].view(full, P, E), g[:P].expand(full, P, E)) and torch.equal(g[full * P:], g[:rest])
+
+
+# --------------------------------------------------------------------- MXFP4
+
+def test_quant_dispatch_without_output_rows_reports():
+    """No output rows at all: every entry is outside and reported."""
+    x = torch.ones((3, 64), dtype=torch.bfloat16, device="cuda")
+    out = (torch.empty((0, 32), dtype=torch.uint8, device="cuda"), torch.empty((0, 2), dtype=torch.uint8, device="cuda"))
+    m4.mxfp4_quant(x, out_map=cuda_i32([0, 1, 2]), out=out)
+    with pytest.raises(m4.Moe4DeviceError, match="clamped"):
+        m4.moe4_debug_check()
+    m4.mxfp4_quant(torch.empty((0, 64), dtype=torch.bfloat16, device="cuda"), out_map=cuda_i32([]), out=out)
+    m4.moe4_debug_check()
