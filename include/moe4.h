@@ -359,8 +359,9 @@ int mxfp8_requant_mx4_sr_T(const uint8_t* codes, const uint8_t* sf, int64_t rows
  *          codes to its routed rows (moe_route_topk's inv_perm), each token
  *          quantised once.  Output rows that no entry names are not written;
  *          entries outside [0, out_rows) are dropped and reported
- *          (MOE4_DEVERR_INDEX); rows named twice by different tokens hold
- *          either one's values, block by block.
+ *          (MOE4_DEVERR_INDEX).  A row should be named once: one that
+ *          different tokens name ends up with a mixture (a block's codes of
+ *          one beside the scale of another).
  * codes [out_rows, cols/2], sf [out_rows, cols/32]; cols % 32 == 0; x and
  * codes 16-byte aligned.
  */

@@ -436,8 +436,8 @@ def mxfp4_quant(x, pre_op=PRE_NONE, out_map=None, copies=1, out=None):
     """MXFP4 of x [R, C] (bf16 or float32) -> (codes [R, C/2] u8, sf [R, C/32] u8).
     out_map [R*copies] int32: row r goes to the output rows out_map[r*copies + j]
     (e.g. moe_route_topk's inv_perm, copies = k: the dispatch); the outputs then
-    have R*copies rows.  out: optional (codes, sf) tensors to write into; rows
-    that out_map does not name keep what they hold."""
+    have R*copies rows; name each row once.  out: optional (codes, sf) tensors to
+    write into; rows that out_map does not name keep what they hold."""
     dt = {torch.bfloat16: BF16, torch.float32: F32}.get(x.dtype)
     if dt is None:
         raise ValueError("mxfp4_quant: x must be bf16 or float32")
