@@ -738,6 +738,9 @@ int moe_balance_loss_backward(const float* dloss, const float* logits, const flo
  * bf16 parts of each dlogits value, accumulated in float32 by the MFMA).
  * dxp [T*k, d] float32, dlogits [T, E] float32, w [E, d] bf16, dx [T, d] bf16,
  * all 16-byte aligned.  1 <= k <= 16, E < 2^20, d < 2^28, d % 4 == 0.
+ * An infinite dlogits value counts as one: its results are infinite, or NaN
+ * where it meets a zero or an infinity of the other sign.  A product of a finite
+ * dlogits value and an infinite w may be NaN instead of infinite.
  * Out-of-range rows are clamped and reported (MOE4_DEVERR_INDEX).
  */
 int moe_unpermute_sum_router_dense(const float* dxp, const int32_t* inv_perm, int64_t T, int32_t k, int64_t d,

@@ -45,8 +45,11 @@ constexpr int64_t MAXE = (1 << 20) - 1, MAXD = (1 << 28) - 1;  // (128 rows of d
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 }  // namespace rd
 
+constexpr int CLASS_INF = 0x204;  // -infinity, +infinity
+
 // 8 float32 values -> their three bf16 parts (the high 8 significand bits,
-// the next 8, the last 8; each subtraction is exact), 8 bf16 each.
+// the next 8, the last 8; each subtraction is exact), 8 bf16 each.  An infinity
+// is all in the first part (less itself it would be a NaN).
 __device__ inline void split3(const float (&v)[8], u32x4 (&o)[3]) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -55,7 +58,7 @@ __device__ inline void split3(const float (&v)[8], u32x4 (&o)[3]) {
     for (int j = 0; j < 2; ++j) {
       const float a = v[2 * i + j];
       h[j] = __float_as_uint(a) & 0xFFFF0000u;
-      const float r = a - __uint_as_float(h[j]);
+      const float r = __builtin_amdgcn_classf(a, CLASS_INF) ? 0.0f : a - __uint_as_float(h[j]);
       m[j] = __float_as_uint(r) & 0xFFFF0000u;
       lo[j] = __float_as_uint(r - __uint_as_float(m[j]));
     }

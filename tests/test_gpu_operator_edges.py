@@ -1,11 +1,12 @@
-"""Edges of the balance loss and MXFP4 quantisation: logits that are not finite,
-launch sizes, a dispatch to no rows."""
+"""Edges of the balance loss, the dense router backward and MXFP4 quantisation:
+logits and gradients that are not finite, launch sizes, a dispatch to no rows."""
 import numpy as np
 import pytest
 import torch
 
-from gpu_helpers import cuda_f32, cuda_i32, to_np
+from gpu_helpers import bf16_from_bits, cuda_f32, cuda_i32, to_np
 from oracle import balance as ob
+from oracle import formats as fmt
 
 pytestmark = pytest.mark.gpu
 
@@ -91,6 +92,32 @@ def test_balance_gradient_of_more_tokens_than_one_grid_row():
     lim = lim + 1e6 * E / (k * float(T) ** 2) * p * 4
     assert (np.abs(to_np(g[:P]) - want) <= lim).all()
     assert torch.equal(g[:full * P].view(full, P, E), g[:P].expand(full, P, E)) and torch.equal(g[full * P:], g[:rest])
+
+
+# -------------------------------------------------------------- dense router
+
+def test_dense_router_infinite_gradients():
+    """An infinite dlogits value gives infinite results of the products' signs, two of opposite signs a NaN; a NaN of
+    any payload gives NaN."""
+    T, E, d, k = 130, 40, 64, 2
+    rng = np.random.default_rng(3)
+    dz = rng.standard_normal((T, E)).astype(np.float32)
+    dz[3, 5], dz[129, 39] = np.inf, -np.inf
+    dz[64, 7], dz[64, 8] = np.inf, -np.inf
+    dz.view(np.uint32)[70, 20], dz.view(np.uint32)[71, 21] = 0x7F800001, 0xFFFFFFFF
+    sign = np.where(rng.random(d) < 0.5, -1.0, 1.0)
+    w = fmt.f64_to_bf16((1 + rng.random((E, d))) * sign)
+    x = fmt.f64_to_bf16((1 + rng.random((T, d))) * sign)
+    dx = m4.moe_unpermute_sum_router_dense(cuda_f32(np.ones((T * k, d), np.float32)), cuda_i32(rng.permutation(T * k).astype(np.int32)),
+                                           T, k, cuda_f32(dz), bf16_from_bits(w)).float().cpu().numpy()
+    assert np.array_equal(dx[3], np.inf * sign) and np.array_equal(dx[129], -np.inf * sign)
+    assert np.isnan(dx[[64, 70, 71]]).all()
+    assert np.isfinite(dx[~np.isin(np.arange(T), [3, 64, 70, 71, 129])]).all()
+    dw = to_np(m4.moe_router_wgrad_dense(bf16_from_bits(x), cuda_f32(dz)))
+    for e, s in ((5, 1), (7, 1), (8, -1), (39, -1)):
+        assert np.array_equal(dw[e], s * np.inf * sign), e
+    assert np.isnan(dw[[20, 21]]).all()
+    assert np.isfinite(dw[~np.isin(np.arange(E), [5, 7, 8, 20, 21, 39])]).all()
 
 
 # --------------------------------------------------------------------- MXFP4
