@@ -78,7 +78,9 @@ extern "C" {
                                  call's results are wrong                       */
 #define MOE4_DEVERR_INDEX 2u  /* a routed row index outside its range was
                                  clamped (gather, combine, un-permute, dgates,
-                                 balance counts) or dropped (mxfp4_quant)       */
+                                 balance counts) or dropped (mxfp4_quant), or a
+                                 padded offset led out of the outputs
+                                 (mxfp8_requant_mx4_sr_T)                       */
 
 #define MOE4_BF16 0
 #define MOE4_F32 1
@@ -329,7 +331,9 @@ int mxfp8_quant_rows_T(const void* x, int dtype, int64_t rows, int64_t cols,
  * backward operands of an MXFP4 forward (lhc.media page, the paragraphs on
  * transposition and on requantising with stochastic rounding).  A source row
  * whose scale byte is 255 (NaN) gives each column block that meets it the
- * scale byte 255.
+ * scale byte 255.  group_off_pad: ascending multiples of 32 from 0 to at most
+ * max_padded_rows; blocks whose offsets are not are left unwritten and reported
+ * (MOE4_DEVERR_INDEX).
  */
 int mxfp8_requant_mx4_sr_T(const uint8_t* codes, const uint8_t* sf, int64_t rows, int64_t cols,
                            const int32_t* group_row_off, const int32_t* group_off_pad, int32_t n_groups,

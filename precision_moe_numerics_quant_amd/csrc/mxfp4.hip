@@ -257,11 +257,19 @@ __global__ void __launch_bounds__(rq::THREADS, 3) k_requant_mx4_T(const uint8_t*
   const int64_t c0 = (int64_t)(blockIdx.x % n_ct) * COLS;
   const int64_t pr = ((int64_t)(blockIdx.x / n_ct) * WAVES + w) * 32;
   const int64_t ptot = offp[G];
-  const bool present = pr < ptot && ptot <= max_pr;
   int64_t P = 0, pr_in_g = 0, src0 = 0, obase = 0, sbase = 0;
-  int nvalid = 0;
+  int nvalid = 0, g = 0;
+  // the block's group; offsets that would lead out of the outputs are reported
+  // and their blocks left alone
+  bool present = pr < ptot, bad = ptot > max_pr;
   if (present) {
-    const int g = find_group(offp, G, pr);
+    g = find_group(offp, G, pr);
+    const int64_t o0 = offp[g], o1 = offp[g + 1];
+    bad = bad || o0 < 0 || o0 > pr || o1 <= pr || o1 > max_pr || ((o0 | o1) & 31) != 0;
+  }
+  if (bad && l == 0) atomicOr(&g_dev_err, MOE4_DEVERR_INDEX);
+  present = present && !bad;
+  if (present) {
     pr_in_g = pr - offp[g];
     P = (int64_t)offp[g + 1] - offp[g];
     src0 = (int64_t)off[g] + pr_in_g;

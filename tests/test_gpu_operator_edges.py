@@ -1,5 +1,8 @@
-"""Edges of the balance loss, the dense router backward and MXFP4 quantisation:
-logits and gradients that are not finite, launch sizes, a dispatch to no rows."""
+"""Edges of the balance loss, the dense router backward, MXFP4 quantisation and
+its transposed requantisation: logits and gradients that are not finite, launch
+sizes, a dispatch to no rows, padded offsets outside the outputs."""
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -131,3 +134,22 @@ def test_quant_dispatch_without_output_rows_reports():
         m4.moe4_debug_check()
     m4.mxfp4_quant(torch.empty((0, 64), dtype=torch.bfloat16, device="cuda"), out_map=cuda_i32([]), out=out)
     m4.moe4_debug_check()
+
+
+@pytest.mark.parametrize("offp", [[0, 1 << 20, 64], [-64, 32, 64], [0, 96, 64], [0, 5, 64], [0, 32, 96], [0, 32, -32]])
+def test_requant_padded_offsets_outside(offp):
+    """Padded offsets that are not ascending multiples of 32 up to max_padded_rows: reported, and nothing written around
+    the outputs (offsets that end below zero leave no blocks at all)."""
+    C, mpr, guard = 544, 64, 1 << 16
+    q, s = torch.zeros((40, C // 2), dtype=torch.uint8, device="cuda"), torch.full((40, C // 32), 127, dtype=torch.uint8, device="cuda")
+    oc, os_ = (torch.full((2 * guard + n,), 0x5A, dtype=torch.uint8, device="cuda") for n in (C * mpr, C * mpr // 32))
+    ptr = lambda t: ctypes.c_void_p(t.data_ptr())
+    off, op = cuda_i32([0, 20, 40]), cuda_i32(offp)
+    rc = m4.lib().mxfp8_requant_mx4_sr_T(ptr(q), ptr(s), 40, C, ptr(off), ptr(op), 2, mpr, 1, 2, 0, ptr(oc[guard:]), ptr(os_[guard:]),
+                                         ctypes.c_void_p(torch.cuda.current_stream().cuda_stream))
+    assert rc == 0
+    if offp[-1] > 0:
+        with pytest.raises(m4.Moe4DeviceError, match="offset"):
+            m4.moe4_debug_check()
+    for t in (oc, os_):
+        assert (t[:guard] == 0x5A).all() and (t[-guard:] == 0x5A).all()
