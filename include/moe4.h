@@ -739,7 +739,9 @@ int moe_balance_loss_backward(const float* dloss, const float* logits, const flo
  * gradient that is not confined to the selected experts (a balance loss):
  *   dx[t, c] = bf16(sum_j dxp[inv_perm[t*k+j], c] + sum_e dlogits[t, e] * w[e, c])
  * with float32 sums (the k rows in slot order; the products exact, from three
- * bf16 parts of each dlogits value, accumulated in float32 by the MFMA).
+ * bf16 parts of each dlogits value, accumulated in float32 by the MFMA; a
+ * dlogits value below 2^-110 is cut by less than 2^-133, bf16's smallest
+ * subnormal).
  * dxp [T*k, d] float32, dlogits [T, E] float32, w [E, d] bf16, dx [T, d] bf16,
  * all 16-byte aligned.  1 <= k <= 16, E < 2^20, d < 2^28, d % 4 == 0.
  * An infinite dlogits value counts as one: its results are infinite, or NaN

@@ -9,11 +9,13 @@
 //                      tokens split over workgroups whose partial tiles
 //                      k_router_dw_join adds in order.
 //
-// dz is float32 and the other operand bf16.  A float32 is exactly the sum of
-// three bf16 numbers (its 24 significand bits cut 8 + 8 + 8), so three bf16
-// MFMAs per fragment (v_mfma_f32_32x32x16_bf16) give exact products with
-// float32 accumulation: nothing of dz is rounded, at three bf16 MFMAs where a
-// float32 MFMA would take eight times as long as one.
+// dz is float32 and the other operand bf16.  A float32 from 2^-110 on is exactly
+// the sum of three bf16 numbers (its 24 significand bits cut 8 + 8 + 8; the MFMA
+// keeps bf16's subnormals), so three bf16 MFMAs per fragment
+// (v_mfma_f32_32x32x16_bf16) give exact products with float32 accumulation:
+// nothing of dz is rounded, at three bf16 MFMAs where a float32 MFMA would take
+// eight times as long as one.  Below 2^-110 the last part ends at bf16's
+// smallest subnormal: dz is cut by less than 2^-133.
 //
 // Both contractions run along a dimension that is not contiguous in memory
 // (W_r's rows; dz's and x's tokens): a thread loads 8 consecutive k of one or

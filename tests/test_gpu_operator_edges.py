@@ -1,6 +1,6 @@
 """Edges of the balance loss, the dense router backward, MXFP4 quantisation and
-its transposed requantisation: logits and gradients that are not finite, launch
-sizes, a dispatch to no rows, padded offsets outside the outputs."""
+its transposed requantisation: logits and gradients that are not finite or tiny,
+launch sizes, a dispatch to no rows, padded offsets outside the outputs."""
 import ctypes
 
 import numpy as np
@@ -121,6 +121,19 @@ def test_dense_router_infinite_gradients():
         assert np.array_equal(dw[e], s * np.inf * sign), e
     assert np.isnan(dw[[20, 21]]).all()
     assert np.isfinite(dw[~np.isin(np.arange(E), [5, 7, 8, 20, 21, 39])]).all()
+
+
+def test_dense_router_split_of_small_gradients():
+    """One-hot x: dW is dz itself, exactly from 2**-110 on (the lowest significand bit is then bf16's smallest
+    subnormal, 2**-133); below, short of it by less than 2**-133."""
+    rng = np.random.default_rng(8)
+    eye = bf16_from_bits(fmt.f64_to_bf16(np.eye(64)))
+    m = rng.integers(1 << 23, 1 << 24, (64, 64)).astype(np.float64) * np.where(rng.random((64, 64)) < 0.5, -1, 1)
+    dz = (m * np.exp2(rng.integers(-133, -110, (64, 64)))).astype(np.float32)
+    assert np.array_equal(to_np(m4.moe_router_wgrad_dense(eye, cuda_f32(dz))), dz.T)
+    dz = (m * np.exp2(rng.integers(-149, -133, (64, 64)))).astype(np.float32)
+    got = to_np(m4.moe_router_wgrad_dense(eye, cuda_f32(dz))).astype(np.float64)
+    assert (np.abs(got - dz.T.astype(np.float64)) < 2.0 ** -133).all()
 
 
 # --------------------------------------------------------------------- MXFP4
