@@ -15,8 +15,9 @@ Zipf(1.1) expert bias; upstream gradient N(0, 1e-3); synthetic seeded inputs
 resident in HBM before the timed region.
 
 The same layer with an MXFP8 forward (the pages' higher-precision layers,
-and their full-MXFP8 baseline) is timed on the same inputs afterwards and
-reported under `mxfp8_forward_variant`.
+and their full-MXFP8 baseline) and with an MXFP4 forward is timed on the same
+inputs afterwards and reported under `mxfp8_forward_variant` and
+`mxfp4_forward_variant`.
 
 Printed: one JSON line.  `value` is the step's grouped-GEMM work (6 GEMMs,
 2*M*N*K each, padding excluded) divided by the whole step time; the
@@ -315,33 +316,34 @@ def gpu_run(steps, warmup, layer_only=False):
     payload = combine_payload_bench(fw, c)
     small = small_configs_bench(inp, fw["wq"])
     del fw, bw
-    # the MXFP8-forward variant of the same layer on the same inputs
-    def step_mx(t=None):
-        fw = layer.forward_mx(inp["x"], inp["w_up"], inp["w_down"], inp["logits"], k, inp["bias"], timer=t,
-                              seed=synth.SR_SEED)
-        layer.backward_mx(fw, inp["dy"], seed=synth.SR_SEED, timer=t, skip_empty_dw=True)
-    for _ in range(warmup):
-        step_mx()
-    torch.cuda.synchronize()
-    start.record()
-    for _ in range(steps):
-        step_mx()
-    end.record()
-    torch.cuda.synchronize()
-    ms_mx = start.elapsed_time(end) / steps
-    events.clear()
-    step_mx(timer)
-    torch.cuda.synchronize()
-    per_mx = {}
-    prev = None
-    for name, ev in events:
-        if prev is not None and name is not None:
-            per_mx[name] = round(prev.elapsed_time(ev), 4)
-        prev = ev
+    # the MXFP8- and MXFP4-forward variants of the same layer on the same inputs
+    def variant(forward, backward):
+        def step_v(t=None):
+            fw = forward(inp["x"], inp["w_up"], inp["w_down"], inp["logits"], k, inp["bias"], timer=t, seed=synth.SR_SEED)
+            backward(fw, inp["dy"], seed=synth.SR_SEED, timer=t, skip_empty_dw=True)
+        for _ in range(warmup):
+            step_v()
+        torch.cuda.synchronize()
+        start.record()
+        for _ in range(steps):
+            step_v()
+        end.record()
+        torch.cuda.synchronize()
+        ms = start.elapsed_time(end) / steps
+        events.clear()
+        step_v(timer)
+        torch.cuda.synchronize()
+        per_v, prev = {}, None
+        for name, ev in events:
+            if prev is not None and name is not None:
+                per_v[name] = round(prev.elapsed_time(ev), 4)
+            prev = ev
+        return ms, per_v
+    variants = variant(layer.forward_mx, layer.backward_mx), variant(layer.forward_mx4, layer.backward_mx4)
     # last, since its memory pool makes the caching allocator's later large
     # allocations slow: the step replayed from one HIP graph
     graph_run = graph_steps(step, steps, ref_outputs)
-    return (c, ms_step, wall, per, off, off_pad, (ms_mx, per_mx), payload, (small, router_r), zero_fill,
+    return (c, ms_step, wall, per, off, off_pad, variants, payload, (small, router_r), zero_fill,
             device_error, graph_run)
 
 
@@ -682,7 +684,7 @@ def main():
         print(f"bench.py runs on one GPU only: the library has no multi-GPU path (asked for --gpus {args.gpus}).",
               file=sys.stderr)
         sys.exit(2)
-    c, ms_step, wall, per, off, off_pad, mxv, payload, small, zero_fill, device_error, graph_run = gpu_run(args.steps, args.warmup,
+    c, ms_step, wall, per, off, off_pad, variants, payload, small, zero_fill, device_error, graph_run = gpu_run(args.steps, args.warmup,
                                                                                   args.layer_only)
     table = work_table(c, off, off_pad)
     peaks = {"hbm": PEAK_HBM, "f16": PEAK_F16, "fp8": PEAK_FP8}
@@ -770,19 +772,22 @@ def main():
                                "ms_per_step": None if graph_run["ms_per_step"] is None
                                else round(graph_run["ms_per_step"], 3)}
     if not args.layer_only:
-        ms_mx, per_mx = mxv
+        def variant(ms, per_v, fmt):
+            return {
+                "ms_per_step": round(ms, 3),
+                "value": round(step_gemm_flops / (ms * 1e-3) / 1e12, 2),
+                "fwd_gemm_tflops": {n: round(2.0 * c["T"] * c["k"] * c["d"] * c["F"] / (per_v[n] * 1e-3) / 1e12, 1)
+                                    for n in (f"F6 up GEMM ({fmt})", f"F8 down GEMM ({fmt})") if n in per_v},
+                "breakdown_ms": per_v,
+            }
         out.update({
             "wgrad_zero_fill": zero_fill,
             "quantizer_microbench": quantizer_microbench(),
             # the same layer with an MXFP8 forward (the pages' higher-precision
-            # layers, and their full-MXFP8 baseline): whole step, and per call (ms)
-            "mxfp8_forward_variant": {
-                "ms_per_step": round(ms_mx, 3),
-                "value": round(step_gemm_flops / (ms_mx * 1e-3) / 1e12, 2),
-                "fwd_gemm_tflops": {n: round(2.0 * c["T"] * c["k"] * c["d"] * c["F"] / (per_mx[n] * 1e-3) / 1e12, 1)
-                                    for n in ("F6 up GEMM (MXFP8)", "F8 down GEMM (MXFP8)") if n in per_mx},
-                "breakdown_ms": per_mx,
-            },
+            # layers, and their full-MXFP8 baseline) and with an MXFP4 forward:
+            # whole step, and per call (ms)
+            "mxfp8_forward_variant": variant(*variants[0], "MXFP8"),
+            "mxfp4_forward_variant": variant(*variants[1], "MXFP4"),
             # the combine fed by the 8.25-bit payload the pages send back between GPUs
             "combine_payload_8p25": payload,
             # the small workloads: weight streaming (RL-shaped forward) and launch latency (tiny layer)
