@@ -13,8 +13,8 @@
 // Every kernel reads the logits once, a row per wave: 25 MB at 16384 x 384, where
 // k_balance_part takes 15 us (5 for the bytes; the rest is the latency of four
 // rows in turn per wave and the exponentials), k_balance_sum 7.6 (a launch and
-// a dependent chain over 256 partial rows), k_balance_bwd 16.5 (75 MB with
-// the gradient it adds to: 4.6 TB/s).  The sums over tokens are made in a fixed
+// a dependent chain over 256 partial rows), k_balance_bwd 17 (75 MB with
+// the gradient it adds to: 4.4 TB/s).  The sums over tokens are made in a fixed
 // order (no floating-point atomics): workgroup c sums the tokens of chunk c, and flushes a partial row
 // at every segment boundary inside it.  The pair (c, s) takes partial row
 // c + s: chunk and segment both only grow along the tokens, so the rows are
@@ -31,7 +31,7 @@ namespace bl {
 constexpr int MAXE = 1024, MAXK = 16;
 constexpr int NW = 16, THREADS = 64 * NW;  // k_balance_part: waves per chunk
 constexpr int CH_MIN = 16, CH_MAX = 64;    // tokens per chunk (bl_chunk)
-constexpr int CHUNKS = 256;                // chunks that fill the chip
+constexpr int CHUNKS = 256;                // chunks that fill the chip (a constant: the workspace query names no device)
 constexpr int SUM_T = 512, SUM_Q = 16;     // k_balance_sum: threads, column quads per workgroup
 constexpr int BWD_W = 4;                   // k_balance_bwd: waves (tokens) per workgroup
 constexpr int64_t BWD_X = 1 << 22;         // its workgroups along x (2^24 of them would be 2^32 threads)
@@ -78,7 +78,8 @@ __device__ inline void load_bias(const float* __restrict__ bias, int E, float (&
 // row's: a NaN beside -infinities (masked experts, the places past E) stays one
 // and makes the sum, and with it the row, NaN.
 // exp(d) = 2^(d log2 e): for d <= 0 the product's rounding is as large an error
-// as the difference's own, and the hardware's 2^x is good to one unit.
+// as the difference's own, and the hardware's 2^x is good to one unit (results
+// below 2^-126 are zeros).
 template <int PER>
 __device__ inline void softmax_row(float (&z)[PER]) {
   float m = z[0];

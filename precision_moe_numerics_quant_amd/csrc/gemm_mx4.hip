@@ -192,15 +192,19 @@ __global__ void __launch_bounds__(m4s::NT)
 // (v_mfma_scale_f32_32x32x64_f8f6f4) and store; one barrier per slab.  128 x
 // TN tiles.  (Four consumers of 64 x 128 read a quarter less from LDS but leave
 // one per SIMD: 260 against 244 us at 4096 rows of 384 experts, N = 4096, K =
-// 1536, 686 against 680 at 131072 rows of them, N = 1536, K = 4096.)
+// 1536; before the stores were deferred 686 against 680 at 131072 rows of them,
+// N = 1536, K = 4096.)
 //
 // What bounds it, at 131072 rows of eight experts, N = 1536, K = 4096 (502 us,
-// 3.3 PFLOP/s): power.  The MFMAs on random operands alone take 298 us (5.5
-// PFLOP/s at 1.4 GHz; on zeros they run at 2.4); with their LDS reads 380; the
-// loads into LDS alone 335; both together 443.  384 experts under power-law
-// routing: 674 us, the clock at 1.74 GHz, the MFMAs busy 36 % of it.  256 x 256
-// tiles move a third fewer bytes per MFMA but leave one wave per SIMD that
-// loads and multiplies: 1006 us.  Ordinary instead of nontemporal stores: 510.
+// 3.3 PFLOP/s): no one unit.  Parts of the kernel timed alone, one run each: the
+// MFMAs on random operands 298 us (5.5 PFLOP/s at 1.4 GHz, where power holds the
+// clock; on zeros they run at 2.4), with their LDS reads 380, the loads into LDS
+// 335, loads and MFMAs 443.  384 experts under power-law routing: 593 us in a
+// loop, 655 under the profiler, there at 1.85 GHz with the MFMAs busy 35 % of
+// the cycles, the VALU 20 and the LDS 24.  256 x 256 tiles move a third fewer
+// bytes per MFMA but leave one wave per SIMD that loads and multiplies: 1006 us.
+// Ordinary instead of nontemporal stores: 510.  Float32 results (N = 4096, K =
+// 1536, 2.1 GB of them, stored between tiles): 847 us, 581 at the copy rate.
 //
 // Every load goes through a buffer descriptor that ends with the expert's
 // rows, so rows past its last or N and K chunks past K (their lanes' offsets are
@@ -623,7 +627,8 @@ static int ws_grid() { return cu_count() < 8 ? 8 : cu_count(); }
 // CU.  N = 1536, K = 4096, few-rows against tiled kernel, even routing | one power-law routing (1.1), in us:
 //   384 experts, rows per expert 4: 242 - 286 | 88 - 76;  8: 254 - 284 | 130 - 83;
 //   11: 261 - 285 | 163 - 86;  16: 301 - 285 | 210 - 110;  32: 405 - 293 | 363 - 162
-//   (a popular expert's weights are read again for every 32 rows);
+//   (a popular expert's weights are read again for every 64 rows, past K = 4096
+//   for every 16);
 //   8 experts, rows per expert 8, 16, 32: 12 - 19, 12 - 19, 14 - 20
 static bool few_rows(int E, int64_t M, int64_t N) {
   const int64_t tiles = ((M < E ? M : E) + M / m4w::TM) * ((N + 255) / 256);

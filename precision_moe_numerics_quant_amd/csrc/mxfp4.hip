@@ -18,6 +18,7 @@
 // every block `copies` times, spends its time on).  16384 x 4096 bf16 to eight
 // rows each (0.44 GB): 73 us, 6.0 TB/s; 73728 x 4096 float32 (1.37 GB): 238 us,
 // 5.7 TB/s; 131072 x 4096 decoded to bf16 (1.38 GB, mostly written): 252 us.
+// With SiLU the VALU takes over (busy 82 %): 131072 x 1536 bf16 (0.51 GB): 111 us.
 #include "act.h"
 #include "moe4_internal.h"
 #include "mx_requant.h"
@@ -228,15 +229,15 @@ __global__ void __launch_bounds__(m4q::THREADS) k_mx4_dequant(const uint32_t* __
 // The codes leave in two halves of the lane's columns, so that a wave needs 8 KB
 // of LDS and three waves fit a SIMD (two with all columns at once: 125 -> 115 us
 // at 131072 x 1536, 280 -> 252 at 131072 x 4096); each half hashes its rows' keys
-// again.  The VALU bounds it (about 11 instructions a value), not the 1.56 bytes
-// a value (61 us at 131072 x 1536).
+// again.  Its 13 VALU instructions a value keep the VALU busy for 67 % of the
+// cycles (112 us under the profiler); the 1.56 bytes a value would take 62.
 namespace rq4 {
 // any byte of w zero
 __device__ inline uint32_t zero_byte(uint32_t w) { return (w - 0x01010101u) & ~w & 0x80808080u; }
-// any byte below 20 or above 251 (20 = 16 + 4: a byte below it has high nibble
-// 0, or high nibble 1 and value 16 .. 19)
+// any byte below 20 or above 251
 __device__ inline bool odd_scales(uint32_t w) {
   const uint32_t big = zero_byte(~(w | 0x03030303u));                 // 252 .. 255
+  // below 20: bit 7 clear, and clear after adding 108 to the other seven
   const uint32_t small = ~((w & 0x7F7F7F7Fu) + 0x6C6C6C6Cu) & ~w & 0x80808080u;  // below 20
   return (big | small) != 0u;
 }
@@ -398,7 +399,10 @@ __global__ void __launch_bounds__(rq::THREADS, 3) k_requant_mx4_T(const uint8_t*
 #pragma unroll
         for (int q = 0; q < 4; ++q) put(k, q, od[q]);
       }
-    } else {  // (the other half's codes are dropped: this path is rare)
+    } else {
+      // (both halves are made and one is dropped.  A block of zeros has the scale
+      // byte 0, so a wave that meets one comes here: 131072 x 1536 by events 119 us
+      // without zero rows, 147 with one in a thousand, 182 in a hundred, 218 in ten)
       auto deqw = [&](int i, float (&q)[8]) {  // q * 2**(sb - 127 - ex)
         mx4_decode8(cw[i], 0, q);
 #pragma unroll

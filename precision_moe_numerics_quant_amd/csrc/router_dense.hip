@@ -23,13 +23,14 @@
 // fragment order on the way to LDS, [k / 8][row][8 k]: a fragment read is then
 // 16 consecutive bytes per lane, without bank conflicts.
 //
-// Measured at 16384 tokens, k = 8, d = 4096, 384 experts: dx 505 us, against 427
+// Measured at 16384 tokens, k = 8, d = 4096, 384 experts: dx 507 us, against 427
 // for the un-permuting sum alone (2.1 GB gathered at 5.2 TB/s, the bound) and 213
 // for the GEMM alone, which hides partly behind the other workgroups' gathers:
 // six per CU (one LDS stage, one register set; 128-row tiles with two stages, 2 per
-// CU: 587).  dW 213 us and 11 for the join, 113 at the bf16 MFMA rate of a large
-// product (the MFMAs busy 41 % of a clock that power holds at 1.5 GHz): its operands cross
-// from token-major rows through registers into LDS, three parts of dz each.
+// CU: 587).  dW 216 us (181 to 256 from launch to launch: power moves the clock
+// about 1.7 GHz) and 11 for the join, 113 at the bf16 MFMA rate of a large
+// product; the MFMAs and the VALU are busy 40 % of the cycles each: its operands
+// cross from token-major rows through registers into LDS, three parts of dz each.
 // 64-deep slabs or 256-wide tiles would cut the workgroups per CU again.
 #include "gemm_common.h"
 #include "moe4_internal.h"
@@ -42,7 +43,7 @@ constexpr int KC = BK / 8;                  // 8-deep k chunks of a slab
 constexpr int PART_B = KC * TM * 16;        // bytes of one bf16 operand slab
 constexpr int STAGE = 4 * PART_B;           // three parts of dz, one of the other operand
 constexpr int MAXK = 16;
-constexpr int CUS = 256;
+constexpr int CUS = 256;  // (MI355X; not asked of the device: the workspace query, which names none, uses it too)
 constexpr int64_t MAXE = (1 << 20) - 1, MAXD = (1 << 28) - 1;  // (128 rows of dz and a row of W_r: 31-bit byte ranges)
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 }  // namespace rd
