@@ -444,12 +444,12 @@ extern "C" int mxfp4_quant(const void* x, int dtype, int64_t rows, int64_t cols,
                "mxfp4_quant: cols must be a positive multiple of 32");
   MOE4_REQUIRE(pre_op == MOE4_PRE_NONE || (pre_op == MOE4_PRE_SILU && dtype == MOE4_BF16), MOE4_EINVAL,
                "mxfp4_quant: pre_op must be NONE, or SILU with bf16 x");
+  if (rows == 0) return MOE4_OK;  // (an empty map's pointer is NULL)
   if (out_map)
     MOE4_REQUIRE(copies >= 1 && out_rows >= 0 && rows * copies < ((int64_t)1 << 31), MOE4_EINVAL,
                  "mxfp4_quant: out_map needs copies >= 1, out_rows >= 0 and rows * copies below 2^31");
   else
     MOE4_REQUIRE(copies == 1 && out_rows == rows, MOE4_EINVAL, "mxfp4_quant: without out_map, copies = 1 and out_rows = rows");
-  if (rows == 0) return MOE4_OK;
   // (no output rows: nothing is written, but every entry of out_map is reported)
   MOE4_REQUIRE(x && (out_rows == 0 || (codes && sf)), MOE4_EINVAL, "mxfp4_quant: NULL pointer");
   MOE4_REQUIRE(aligned16(x) && aligned16(codes), MOE4_EALIGN, "mxfp4_quant: x and codes must be 16-byte aligned");

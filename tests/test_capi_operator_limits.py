@@ -29,6 +29,14 @@ def test_balance_loss_and_gradient():
         assert "2^28" in refused("moe_balance_loss_backward", P, P, O, P, P, O, O, i32(1), i64(T), i32(2), i32(1), O, P, O)
 
 
+@pytest.mark.parametrize("copies", [1, 8])
+def test_quant_of_no_rows_with_an_empty_map(copies):
+    """An empty map's pointer is NULL: nothing to do, whatever copies says."""
+    f = _lib().mxfp4_quant
+    f.restype = ctypes.c_int
+    assert f(O, 0, i64(0), i64(64), O, i32(copies), i64(0), 0, O, O, O) == 0
+
+
 @pytest.mark.parametrize("name,args", [
     ("mxfp4_quant", (P, 0, i64(1 << 32), i64(32), O, i32(1), i64(1 << 32), 0, P, P, O)),
     ("mxfp4_dequant", (P, P, i64(1 << 30), i64(32), P, 0, O)),

@@ -219,6 +219,18 @@ def test_quant_dispatch_of_many_copies_and_silu(copies, silu):
     assert_bytes_equal(to_np(got[1]), s[inv], "scales")
 
 
+def test_empty_batch():
+    """No rows: an empty dispatch, and the MXFP4 forward with its balance loss."""
+    x = torch.empty((0, 64), dtype=torch.bfloat16, device="cuda")
+    for silu in (m4.PRE_NONE, m4.PRE_SILU):
+        codes, sf = m4.mxfp4_quant(x, silu, out_map=cuda_i32([]), copies=8)
+        assert codes.shape == (0, 32) and sf.shape == (0, 2)
+    inp, c = synth.config_inputs(1, device="cpu"), synth.CONFIGS[1]
+    fw = layer.forward_mx4(inp["x"][:0].cuda(), inp["w_up"].cuda(), inp["w_down"].cuda(), inp["logits"][:0].cuda(), c["k"], balance=True)
+    assert fw["y"].shape == (0, c["d"]) and not fw["balance"]["loss"].any() and not fw["balance"]["tokens"].any()
+    m4.moe4_debug_check()
+
+
 def _requant_check(q, s, off, lay, what):
     offp = mx.padded_offsets(off)
     got = m4.mxfp8_requant_mx4_sr_T(cuda_u8(q), cuda_u8(s), cuda_i32(off), cuda_i32(offp), 7, 33, int(offp[-1]), lay)
