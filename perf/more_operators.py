@@ -130,7 +130,7 @@ def prepare(case, seed):
     M = T * k
     r = _routing(c, seed)
     s.update(off=r["off"], counts=r["counts"], map=r["perm"])
-    gates = r["gates"].reshape(-1)[r["perm"].long()].contiguous()
+    gates = r["gates"].reshape(-1)  # by assignment: row r of the product has the gate of assignment map[r]
     if op == "gated":
         K, F = c["K"], c["F"]
         s.update(x=_randn((T, K), _gen(seed, 2), 1.0, BF), w=_randn((E, 2, F, K), _gen(seed, 3), 0.02, BF),
@@ -191,6 +191,13 @@ def _rows(s, x, a, b, mapped):
     return x[s["map"][a:b].long() // s["case"]["k"]].float()
 
 
+def _scale(s, a, b, mapped):
+    """Their gates, as a column (1 without)."""
+    if s["scale"] is None:
+        return 1.0
+    return (s["scale"][s["map"][a:b].long()] if mapped else s["scale"][a:b])[:, None]
+
+
 def _gated(s):
     c = s["case"]
     M, F = c["T"] * c["k"], c["F"]
@@ -215,9 +222,8 @@ def _gated_dgrad(s):
         dh = _rows(s, s["dy"], a, b, True) @ s["w"][e].float()
         g, u = s["gu"][a:b, 0].float(), s["gu"][a:b, 1].float()
         f, df = _act(c["act"], g)
-        h = f * u
-        if c["scale"]:
-            dh, h = dh * s["scale"][a:b, None], h * s["scale"][a:b, None]
+        sc = _scale(s, a, b, True)
+        dh, h = dh * sc, f * u * sc
         dgu[a:b, 0], dgu[a:b, 1], hs[a:b] = dh * u * df, dh * f, h
     return dict(dgu=dgu, hs=hs)
 
@@ -243,12 +249,12 @@ def _dgrad(s):
     hs = torch.empty(out.shape, dtype=BF, device=DEV) if c["act"] != "none" else None
     for e, a, b in _experts(s):
         z = _rows(s, s["dy"], a, b, c["mapped"]) @ s["w"][e].float()
-        if c["scale"]:
-            z = z * s["scale"][a:b, None]
+        sc = _scale(s, a, b, c["mapped"])
+        z = z * sc
         if hs is not None:
             f, df = _act(c["act"], s["pre"][a:b].float())
             z = z * df
-            hs[a:b] = f * s["scale"][a:b, None] if c["scale"] else f
+            hs[a:b] = f * sc
         out[a:b] = z
     return dict(dx=out) if hs is None else dict(dx=out, hs=hs)
 
@@ -406,7 +412,7 @@ def _exact_product(s):
         F = c["F"]
         dgu, hs = new(M, 2, F), new(M, F)
         for e, a, b in spans:
-            w = s["scale"][a:b].double()[:, None] if c["scale"] else 1.0
+            w = s["scale"].double().index_select(0, s["map"][a:b])[:, None] if c["scale"] else 1.0
             dh = w * torch.mm(_exact_rows(s, s["dy"], a, b, True), s["w"][e].double())
             g, u = s["gu"][a:b].double().unbind(1)
             f, df = _d_sigmoid(c["act"], g)
@@ -426,7 +432,8 @@ def _exact_product(s):
     if op == "dgrad":
         out, hs = new(M, K), new(M, K) if c["act"] != "none" else None
         for e, a, b in spans:
-            w = s["scale"][a:b].double()[:, None] if c["scale"] else 1.0
+            rows = s["map"][a:b].long() if c["mapped"] else slice(a, b)
+            w = s["scale"].double()[rows][:, None] if c["scale"] else 1.0
             z = w * torch.mm(_exact_rows(s, s["dy"], a, b, c["mapped"]), s["w"][e].double())
             if hs is not None:
                 x = s["pre"][a:b].double()
