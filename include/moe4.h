@@ -31,7 +31,8 @@
  *    and may be made inside a stream capture.
  *  - A call whose launch would need more threads than a grid dimension holds
  *    (2^32 - 1) is refused as too large (mxfp4_*, mxfp8_requant_mx4_sr_T,
- *    moe_grouped_gemm_mx4 and the router's dense calls) before it is enqueued.
+ *    moe_grouped_gemm_mx4, the router's dense calls, the BF16 products and the
+ *    dropout calls) before it is enqueued.
  *  - Sizes are int64_t; offsets and indices are int32_t device arrays.
  *  - Pointers must be 16-byte aligned.
  *
@@ -765,6 +766,132 @@ int moe_unpermute_sum_router_dense(const float* dxp, const int32_t* inv_perm, in
 int moe_router_wgrad_dense(const uint16_t* x, const float* dlogits, int64_t T, int32_t E, int64_t d, float* dw,
                            void* ws, size_t ws_bytes, void* stream);
 size_t moe_router_wgrad_dense_ws_bytes(int64_t T, int32_t E, int64_t d);
+
+/* ---------------------------------------------------- the layer in BF16 */
+/*
+ * The expert layer without quantisation: BF16 operands and activations (some
+ * activations remain in BF16, and BF16 is what the 4-bit rates are measured
+ * against: lhc.media page, paragraph on the precisions that remain;
+ * fourweekmba.com page, the hardware table), for experts kept at full
+ * precision, for a shared expert that every token takes (E = 1), and to
+ * measure what the quantised forms change.  The experts' arithmetic beyond
+ * SiLU (gates, biases, dropout) is not on the pages; these are the usual forms.
+ *
+ * Common to the five products below:
+ *  - Rows are grouped by expert: the rows of expert e are expert_off[e] ..
+ *    expert_off[e+1] - 1 (ascending offsets within [0, M_total]).  Rows of the
+ *    outputs outside [expert_off[0], expert_off[E]) are not written, and rows of
+ *    the inputs there are not read.
+ *  - An operand may be gathered: with a map [M_total] row r of the product is
+ *    row map[r] / map_div of the operand (moe_route_topk's perm with map_div =
+ *    k: the dispatch, without a gathered copy).  Without a map (NULL) it has
+ *    M_total rows.  A map entry outside [0, rows * map_div) counts as a row of
+ *    zeros and is reported (MOE4_DEVERR_INDEX).  A row scale is indexed like the
+ *    rows: row_scale[map[r]] with a map (the gates [T, k] as they are; it then has
+ *    rows * map_div entries), row_scale[r] without.
+ *  - Exact products, float32 accumulation, one rounding of each result (of
+ *    bf16 outputs, and none of float32 ones).  act: MOE4_ACT_NONE, MOE4_ACT_SILU
+ *    (x sigmoid(x)) or MOE4_ACT_GELU (the tanh form, x sigmoid(2 sqrt(2/pi) (x +
+ *    0.044715 x^3))); act(-infinity) = -0.
+ *  - Every width is a multiple of 8 below 2^20, each expert's matrix below 1 GiB
+ *    (wgrad: its float32 gradient below 2 GiB), a mapped operand below 2 GiB,
+ *    M_total and the operands' rows below 2^31, E <= 4096.  Pointers 16-byte
+ *    aligned (maps and row scales 4-byte).  Deterministic.
+ */
+#define MOE4_ACT_NONE 0
+#define MOE4_ACT_SILU 1
+#define MOE4_ACT_GELU 2
+
+/*
+ * moe_grouped_gemm_bf16 - c[r] = act(a[r] . w[e]^T + bias[e]) + residual[r].
+ * a [a_rows, K] bf16 (gathered by row_map, map_div), w [E, N, K] bf16, bias
+ * [E, N] float32 or NULL, residual [M_total, N] of c's type or NULL (it may be
+ * c), c [M_total, N] float32 or bf16 (c_dtype).  pre [M_total, N] bf16 or NULL
+ * receives a . w^T + bias, which the gradients need where act is not NONE.
+ */
+int moe_grouped_gemm_bf16(const uint16_t* a, int64_t a_rows, const int32_t* row_map, int32_t map_div,
+                          const uint16_t* w, const float* bias, const int32_t* expert_off, int32_t E,
+                          int64_t M_total, int64_t N, int64_t K, int act, const void* residual, void* c,
+                          int c_dtype, uint16_t* pre, void* stream);
+
+/*
+ * moe_gated_gemm_bf16 - the gated block's input projections, activation and
+ * product in one pass: with g = a . w[e, 0]^T + bias[e, 0] and u = a .
+ * w[e, 1]^T + bias[e, 1], h = act(g) * u (from the unrounded g and u).
+ * w [E, 2, F, K] bf16, bias [E, 2, F] float32 or NULL, h [M_total, F] bf16; gu
+ * [M_total, 2, F] bf16 or NULL receives g and u for the backward.
+ */
+int moe_gated_gemm_bf16(const uint16_t* a, int64_t a_rows, const int32_t* row_map, int32_t map_div,
+                        const uint16_t* w, const float* bias, const int32_t* expert_off, int32_t E,
+                        int64_t M_total, int64_t F, int64_t K, int act, uint16_t* h, uint16_t* gu, void* stream);
+
+/*
+ * moe_grouped_gemm_bf16_dgrad - the input gradient of c = a . w^T, and through
+ * the activation that made a where there is one: with z = row_scale[r] *
+ * (dy[r] . w[e]),
+ *   dx[r] = z + add[r]                                 (act NONE, pre NULL)
+ *   dx[r] = z * act'(pre[r]) + add[r], hs[r] = row_scale[r] * act(pre[r])
+ * dy [dy_rows, N] bf16 (gathered by row_map, map_div), row_scale float32 or NULL
+ * (ones; e.g. the gates), w [E, N, K] bf16, pre [M_total, K] bf16, add [M_total,
+ * K] of dx's type or NULL (another branch's gradient; it may be dx), dx [M_total,
+ * K] float32 or bf16 (dx_dtype), hs [M_total, K] bf16 or NULL: the scaled rows
+ * that the weight gradient takes beside the unscaled dy.
+ */
+int moe_grouped_gemm_bf16_dgrad(const uint16_t* dy, int64_t dy_rows, const int32_t* row_map, int32_t map_div,
+                                const float* row_scale, const uint16_t* w, const int32_t* expert_off, int32_t E,
+                                int64_t M_total, int64_t N, int64_t K, int act, const uint16_t* pre,
+                                const void* add, void* dx, int dx_dtype, uint16_t* hs, void* stream);
+
+/*
+ * moe_gated_gemm_bf16_dgrad - the same through the gated block: with dh =
+ * row_scale[r] * (dy[r] . w[e]) and g, u = gu[r],
+ *   dgu[r, 0] = dh * u * act'(g), dgu[r, 1] = dh * act(g),
+ *   hs[r] = row_scale[r] * act(g) * u.
+ * w [E, N, F] bf16 (the output projection), gu and dgu [M_total, 2, F] bf16 (dgu
+ * may be gu), hs [M_total, F] bf16 or NULL.  dgu, as [M_total, 2F], and w's
+ * [E, 2F, K] view then go to moe_grouped_gemm_bf16_dgrad and _wgrad.
+ */
+int moe_gated_gemm_bf16_dgrad(const uint16_t* dy, int64_t dy_rows, const int32_t* row_map, int32_t map_div,
+                              const float* row_scale, const uint16_t* w, const int32_t* expert_off, int32_t E,
+                              int64_t M_total, int64_t N, int64_t F, int act, const uint16_t* gu, uint16_t* dgu,
+                              uint16_t* hs, void* stream);
+
+/*
+ * moe_grouped_gemm_bf16_wgrad - weight and bias gradients: over the rows r of
+ * expert e, dw[e] = beta dw[e] + sum dy[r]^T a[r] and, with db,
+ * db[e] = beta db[e] + sum db_scale[r] dy[r] (db_scale a row scale of dy, or NULL: ones).
+ * dy [dy_rows, N] and a [a_rows, K] bf16, each gathered if its map is given
+ * (map_div for both); dw [E, N, K], db [E, N] (or NULL) float32.  beta 0 or 1.
+ * Experts without rows: zeros, or with MOE4_WGRAD_SKIP_EMPTY in flags (or beta
+ * = 1) left as they are.
+ */
+int moe_grouped_gemm_bf16_wgrad(const uint16_t* dy, int64_t dy_rows, const int32_t* dy_map, const uint16_t* a,
+                                int64_t a_rows, const int32_t* a_map, int32_t map_div, const int32_t* expert_off,
+                                int32_t E, int64_t M_total, int64_t N, int64_t K, float* dw, float beta, int flags,
+                                const float* db_scale, float* db, void* stream);
+
+/*
+ * moe_combine_dropout - moe_combine, dropout and residual in one pass:
+ *   y[t, c] = bf16(residual[t, c] + keep(i) * (65536 / q) * acc), i = t * d + c,
+ * acc moe_combine's float32 sum, q = round((1 - p) 65536) (ties to even).  keep(i)
+ * is 1 iff the 16 random bits of element i, those of the stochastic rounding for
+ * (seed, stream_id, i), are below q: the mask is never stored.  A dropped value
+ * is 0 whatever acc holds; p = 1 drops all.  residual [T, d] bf16 or NULL (it
+ * may be y).  yp [T*k, d] float32, gates [T, k], inv_perm [T*k], y [T, d] bf16.
+ * 1 <= k <= 16, d % 4 == 0, T * k < 2^31, 0 <= p <= 1.  Rows outside [0, T*k) are
+ * clamped and reported (MOE4_DEVERR_INDEX).
+ */
+int moe_combine_dropout(const float* yp, const float* gates, const int32_t* inv_perm, int64_t T, int32_t k,
+                        int64_t d, double p, uint64_t seed, uint32_t stream_id, const uint16_t* residual,
+                        uint16_t* y, void* stream);
+
+/*
+ * moe_dropout_backward - dx = keep(i) * (65536 / q) * dy, the gradient of
+ * moe_combine_dropout in acc under the same p, seed and stream_id.  dy and dx
+ * [T, d] bf16 (dx may be dy), d % 4 == 0.
+ */
+int moe_dropout_backward(const uint16_t* dy, int64_t T, int64_t d, double p, uint64_t seed, uint32_t stream_id,
+                         uint16_t* dx, void* stream);
 
 /*
  * moe_silu_eval - correctly rounded float32 silu(u) and silu'(u) of bf16 u

@@ -34,6 +34,7 @@ gemm      float64 grouped GEMMs on exactly dequantised operands
 layer     the whole expert layer, forward and backward
 mxfp4     MXFP4 quantisation and its transposed requantisation to MXFP8
 balance   the router's balance loss and its gradient
+bf16      the expert layer in BF16: gated and plain products, dropout
 combine_q the combine-path quantiser (block Hadamard + 8-bit fixed-point MX)
 
 Parity pins: every function here is pinned in ``tests/test_oracle_*.py``

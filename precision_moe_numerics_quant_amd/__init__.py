@@ -21,6 +21,7 @@ PRE_NONE, PRE_SILU, PRE_SILU_AMAX = 0, 1, 2
 EUNSUPPORTED = -5
 EDEVICE = -6
 RNE, SR = 0, 1
+ACT_NONE, ACT_SILU, ACT_GELU = 0, 1, 2
 SF_ROWS, SF_BLOCKS = 0, 1   # group-major scale arrangement: [C][P_g/32] or [P_g/32][C]
 
 _c_void_p = ctypes.c_void_p
@@ -30,6 +31,7 @@ _int = ctypes.c_int
 _u64 = ctypes.c_uint64
 _u32 = ctypes.c_uint32
 _f32 = ctypes.c_float
+_f64 = ctypes.c_double
 _size = ctypes.c_size_t
 
 _SIGS = {
@@ -105,6 +107,19 @@ _SIGS = {
                                               _c_void_p, _c_void_p]),
     "moe_router_wgrad_dense": (_int, [_c_void_p, _c_void_p, _i64, _i32, _i64, _c_void_p, _c_void_p, _size, _c_void_p]),
     "moe_router_wgrad_dense_ws_bytes": (_size, [_i64, _i32, _i64]),
+    "moe_grouped_gemm_bf16": (_int, [_c_void_p, _i64, _c_void_p, _i32, _c_void_p, _c_void_p, _c_void_p, _i32, _i64, _i64,
+                                     _i64, _int, _c_void_p, _c_void_p, _int, _c_void_p, _c_void_p]),
+    "moe_gated_gemm_bf16": (_int, [_c_void_p, _i64, _c_void_p, _i32, _c_void_p, _c_void_p, _c_void_p, _i32, _i64, _i64,
+                                   _i64, _int, _c_void_p, _c_void_p, _c_void_p]),
+    "moe_grouped_gemm_bf16_dgrad": (_int, [_c_void_p, _i64, _c_void_p, _i32, _c_void_p, _c_void_p, _c_void_p, _i32, _i64,
+                                           _i64, _i64, _int, _c_void_p, _c_void_p, _c_void_p, _int, _c_void_p, _c_void_p]),
+    "moe_gated_gemm_bf16_dgrad": (_int, [_c_void_p, _i64, _c_void_p, _i32, _c_void_p, _c_void_p, _c_void_p, _i32, _i64,
+                                         _i64, _i64, _int, _c_void_p, _c_void_p, _c_void_p, _c_void_p]),
+    "moe_grouped_gemm_bf16_wgrad": (_int, [_c_void_p, _i64, _c_void_p, _c_void_p, _i64, _c_void_p, _i32, _c_void_p, _i32,
+                                           _i64, _i64, _i64, _c_void_p, _f32, _int, _c_void_p, _c_void_p, _c_void_p]),
+    "moe_combine_dropout": (_int, [_c_void_p, _c_void_p, _c_void_p, _i64, _i32, _i64, _f64, _u64, _u32, _c_void_p,
+                                   _c_void_p, _c_void_p]),
+    "moe_dropout_backward": (_int, [_c_void_p, _i64, _i64, _f64, _u64, _u32, _c_void_p, _c_void_p]),
     "moe_grouped_gemm_fwd_hmx8": (_int, [_c_void_p, _c_void_p, _c_void_p, _int, _c_void_p, _c_void_p, _c_void_p,
                                          _c_void_p, _i32, _i64, _i64, _i64, _c_void_p, _c_void_p, _c_void_p,
                                          _c_void_p]),
@@ -623,7 +638,168 @@ def moe_grouped_gemm_mx4(a_codes, a_sf, b_codes, b_sf, expert_off, out_dtype=tor
     return c
 
 
+# ------------------------------------------------------------------ BF16 GEMMs
+
+def _bf16_rows(x, row_map, map_div, name):
+    """The (gathered) bf16 operand's checks -> rows of the product."""
+    _arg(x, torch.bfloat16, (None, None), name)
+    if row_map is None:
+        if map_div != 1:
+            raise ValueError(f"{name}: map_div needs a map")
+        return x.shape[0]
+    _arg(row_map, torch.int32, (None,), f"{name}'s map", x)
+    return row_map.numel()
+
+
+def _row_scale(s, x, row_map, map_div, name):
+    """Check a row scale of x: one per row, or with a map one per entry it may hold."""
+    return s if s is None else _arg(s, torch.float32, (x.shape[0] * (1 if row_map is None else map_div),), name, x)
+
+
+def _out_dtype(dtype, name):
+    dt = {torch.float32: F32, torch.bfloat16: BF16}.get(dtype)
+    if dt is None:
+        raise ValueError(f"{name}: out_dtype must be bf16 or float32")
+    return dt
+
+
+def moe_grouped_gemm_bf16(a, w, expert_off, bias=None, act=ACT_NONE, residual=None, row_map=None, map_div=1,
+                          out_dtype=torch.bfloat16, save_pre=False, out=None):
+    """act(A . w[e]^T + bias[e]) + residual per expert -> (c [M, N], pre [M, N] bf16 or None).
+    a [R, K] bf16, w [E, N, K] bf16, bias [E, N] float32, residual [M, N] of
+    out_dtype; row_map [M] int32: row r of A is a[row_map[r] // map_div].  out: a
+    tensor for c (it may be the residual)."""
+    dt = _out_dtype(out_dtype, "moe_grouped_gemm_bf16")
+    M = _bf16_rows(a, row_map, map_div, "a")
+    K = a.shape[1]
+    _arg(w, torch.bfloat16, (None, None, K), "w", a)
+    E, N, _ = w.shape
+    _arg(expert_off, torch.int32, (E + 1,), "expert_off", a)
+    if bias is not None:
+        _arg(bias, torch.float32, (E, N), "bias", a)
+    if residual is not None:
+        _arg(residual, out_dtype, (M, N), "residual", a)
+    c = _empty((M, N), out_dtype, a) if out is None else _arg(out, out_dtype, (M, N), "out", a)
+    pre = _empty((M, N), torch.bfloat16, a) if save_pre else None
+    _run("moe_grouped_gemm_bf16", a, a, a.shape[0], row_map, map_div, w, bias, expert_off, E, M, N, K, int(act), residual,
+         c, dt, pre)
+    return c, pre
+
+
+def moe_gated_gemm_bf16(a, w, expert_off, bias=None, act=ACT_SILU, row_map=None, map_div=1, save=True):
+    """The gated block's first half: act(A . w[e, 0]^T + b) * (A . w[e, 1]^T + b') ->
+    (h [M, F] bf16, gu [M, 2, F] bf16 or None: the two products, for the backward).
+    a [R, K] bf16 (gathered as in moe_grouped_gemm_bf16), w [E, 2, F, K] bf16, bias [E, 2, F] float32."""
+    M = _bf16_rows(a, row_map, map_div, "a")
+    K = a.shape[1]
+    _arg(w, torch.bfloat16, (None, 2, None, K), "w", a)
+    E, _, F, _ = w.shape
+    _arg(expert_off, torch.int32, (E + 1,), "expert_off", a)
+    if bias is not None:
+        _arg(bias, torch.float32, (E, 2, F), "bias", a)
+    h = _empty((M, F), torch.bfloat16, a)
+    gu = _empty((M, 2, F), torch.bfloat16, a) if save else None
+    _run("moe_gated_gemm_bf16", a, a, a.shape[0], row_map, map_div, w, bias, expert_off, E, M, F, K, int(act), h, gu)
+    return h, gu
+
+
+def moe_grouped_gemm_bf16_dgrad(dy, w, expert_off, pre=None, act=ACT_NONE, row_scale=None, row_map=None, map_div=1,
+                                out_dtype=torch.bfloat16, add=None, out=None):
+    """Input gradient: z = row_scale * (dY . w[e]), with pre through the activation that made the
+    input -> (dx [M, K], hs [M, K] bf16 or None): z + add, or z * act'(pre) + add and row_scale *
+    act(pre).  add [M, K] of out_dtype; out: a tensor for dx (it may be add).
+    dy [R, N] bf16 (gathered as above), w [E, N, K] bf16, pre [M, K] bf16, row_scale float32:
+    [M] by row, or with a map [R * map_div] by the map's entry (the gates, flat)."""
+    dt = _out_dtype(out_dtype, "moe_grouped_gemm_bf16_dgrad")
+    M = _bf16_rows(dy, row_map, map_div, "dy")
+    N = dy.shape[1]
+    _arg(w, torch.bfloat16, (None, N, None), "w", dy)
+    E, _, K = w.shape
+    _arg(expert_off, torch.int32, (E + 1,), "expert_off", dy)
+    _row_scale(row_scale, dy, row_map, map_div, "row_scale")
+    if pre is not None:
+        _arg(pre, torch.bfloat16, (M, K), "pre", dy)
+    if add is not None:
+        _arg(add, out_dtype, (M, K), "add", dy)
+    dx = _empty((M, K), out_dtype, dy) if out is None else _arg(out, out_dtype, (M, K), "out", dy)
+    hs = _empty((M, K), torch.bfloat16, dy) if pre is not None else None
+    _run("moe_grouped_gemm_bf16_dgrad", dy, dy, dy.shape[0], row_map, map_div, row_scale, w, expert_off, E, M, N, K, int(act),
+         pre, add, dx, dt, hs)
+    return dx, hs
+
+
+def moe_gated_gemm_bf16_dgrad(dy, w, gu, expert_off, act=ACT_SILU, row_scale=None, row_map=None, map_div=1):
+    """Through the output projection and the gated block: dh = row_scale * (dY . w[e]) ->
+    (dgu [M, 2, F] bf16: dh u act'(g) and dh act(g), hs [M, F] bf16 = row_scale * act(g) * u).
+    dy [R, N] bf16 (gathered as above), w [E, N, F] bf16, gu [M, 2, F] bf16 as the forward kept it."""
+    M = _bf16_rows(dy, row_map, map_div, "dy")
+    N = dy.shape[1]
+    _arg(w, torch.bfloat16, (None, N, None), "w", dy)
+    E, _, F = w.shape
+    _arg(expert_off, torch.int32, (E + 1,), "expert_off", dy)
+    _arg(gu, torch.bfloat16, (M, 2, F), "gu", dy)
+    _row_scale(row_scale, dy, row_map, map_div, "row_scale")
+    dgu = _empty((M, 2, F), torch.bfloat16, dy)
+    hs = _empty((M, F), torch.bfloat16, dy)
+    _run("moe_gated_gemm_bf16_dgrad", dy, dy, dy.shape[0], row_map, map_div, row_scale, w, expert_off, E, M, N, F, int(act), gu,
+         dgu, hs)
+    return dgu, hs
+
+
+def moe_grouped_gemm_bf16_wgrad(dy, a, expert_off, dy_map=None, a_map=None, map_div=1, dw=None, beta=0.0, skip_empty=False,
+                                bias_grad=False, db_scale=None, db=None):
+    """dw[e] = beta dw[e] + sum over e's rows of dY^T . A -> (dw [E, N, K] float32, db [E, N]
+    float32 or None: beta db[e] + sum of db_scale * dY).  dy [R, N], a [R', K] bf16, each
+    gathered if its map is given; skip_empty as in moe_grouped_gemm_bwd_wgrad."""
+    if map_div != 1 and dy_map is None and a_map is None:
+        raise ValueError("moe_grouped_gemm_bf16_wgrad: map_div needs a map")
+    M = _bf16_rows(dy, dy_map, 1, "dy")
+    _arg(a, torch.bfloat16, (M if a_map is None else None, None), "a", dy)
+    if a_map is not None:
+        _arg(a_map, torch.int32, (M,), "a's map", dy)
+    N, K = dy.shape[1], a.shape[1]
+    _arg(expert_off, torch.int32, (None,), "expert_off", dy)
+    E = expert_off.numel() - 1
+    if beta and (dw is None or (bias_grad and db is None)):
+        raise ValueError("moe_grouped_gemm_bf16_wgrad: beta needs dw (and db) to add to")
+    dw = _empty((max(E, 0), N, K), torch.float32, dy) if dw is None else _arg(dw, torch.float32, (E, N, K), "dw", dy)
+    if db is not None:
+        _arg(db, torch.float32, (E, N), "db", dy)
+    elif bias_grad:
+        db = _empty((max(E, 0), N), torch.float32, dy)
+    _row_scale(db_scale, dy, dy_map, map_div, "db_scale")
+    _run("moe_grouped_gemm_bf16_wgrad", dy, dy, dy.shape[0], dy_map, a, a.shape[0], a_map, map_div, expert_off, E, M, N, K, dw,
+         float(beta), WGRAD_SKIP_EMPTY if skip_empty else 0, db_scale, db)
+    return dw, db
+
+
 # ----------------------------------------------------------- combine / misc
+
+def moe_combine_dropout(yp, gates, inv_perm, p, seed=1, stream_id=0, residual=None, out=None):
+    """y [T, d] bf16 = residual + dropout(sum_j gates[t, j] * yp[inv_perm[t*k+j]]): an element is kept
+    with probability 1 - p (to 2**-17) by the counter hash of (seed, stream_id, its index) and then
+    scaled by the inverse.  residual [T, d] bf16; out: a tensor for y (it may be the residual)."""
+    _arg(gates, torch.float32, (None, None), "gates")
+    T, k = gates.shape
+    _arg(yp, torch.float32, (T * k, None), "yp", gates)
+    d = yp.shape[1]
+    _arg(inv_perm, torch.int32, (T * k,), "inv_perm", gates)
+    if residual is not None:
+        _arg(residual, torch.bfloat16, (T, d), "residual", gates)
+    y = _empty((T, d), torch.bfloat16, gates) if out is None else _arg(out, torch.bfloat16, (T, d), "out", gates)
+    _run("moe_combine_dropout", gates, yp, gates, inv_perm, T, k, d, float(p), seed, stream_id, residual, y)
+    return y
+
+
+def moe_dropout_backward(dy, p, seed=1, stream_id=0, out=None):
+    """The gradient of moe_combine_dropout in the combined sum (the same p, seed and stream_id):
+    dy [T, d] bf16 where kept, scaled, else 0.  out: a tensor for it (it may be dy)."""
+    _arg(dy, torch.bfloat16, (None, None), "dy")
+    T, d = dy.shape
+    dx = _empty((T, d), torch.bfloat16, dy) if out is None else _arg(out, torch.bfloat16, (T, d), "out", dy)
+    _run("moe_dropout_backward", dy, dy, T, d, float(p), seed, stream_id, dx)
+    return dx
+
 
 def moe_combine(yp, gates, inv_perm):
     T, k = gates.shape

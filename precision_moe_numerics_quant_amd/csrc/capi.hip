@@ -79,7 +79,8 @@ extern "C" int moe4_debug_check(void* stream) {
   if (e == hipSuccess) e = hipGetLastError();
   if (e != hipSuccess) return fail(MOE4_EHIP, std::string("moe4_debug_check: ") + hipGetErrorString(e));
   const uint32_t bits = take_dev_err_nvfp4() | take_dev_err_route() | take_dev_err_combine_q() | take_dev_err_router() |
-                        take_dev_err_mxfp4() | take_dev_err_balance() | take_dev_err_router_dense();
+                        take_dev_err_mxfp4() | take_dev_err_balance() | take_dev_err_router_dense() |
+                        take_dev_err_gemm_bf16() | take_dev_err_gemm_bf16_wgrad() | take_dev_err_dropout();
   if (bits == 0) return MOE4_OK;
   std::string msg = "moe4_debug_check: device-side error";
   if (bits & MOE4_DEVERR_WAIT) msg += "; a bounded wait between workgroups gave up (that call's results are wrong)";

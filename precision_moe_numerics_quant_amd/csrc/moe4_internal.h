@@ -37,6 +37,9 @@ uint32_t take_dev_err_router();
 uint32_t take_dev_err_mxfp4();
 uint32_t take_dev_err_balance();
 uint32_t take_dev_err_router_dense();
+uint32_t take_dev_err_gemm_bf16();
+uint32_t take_dev_err_gemm_bf16_wgrad();
+uint32_t take_dev_err_dropout();
 // Test hook (moe4_debug_force_wait_timeout): bounded waits between
 // workgroups wait for a count that never arrives, with a tiny spin limit, so
 // that every wait gives up and reports MOE4_DEVERR_WAIT; kernels still exit.

@@ -23,8 +23,10 @@ router logits.
 """
 import torch
 
-from . import (NVFP4_4OVER6, PRE_SILU, PRE_SILU_AMAX, SF_BLOCKS, SF_ROWS, Moe4Unsupported, max_padded_rows,
-               moe_balance_loss, moe_balance_loss_backward, moe_combine, moe_combine_hmx8, moe_dgates, moe_gather_rows, moe_grouped_gemm_bwd_dgrad,
+from . import (ACT_SILU, NVFP4_4OVER6, PRE_SILU, PRE_SILU_AMAX, SF_BLOCKS, SF_ROWS, Moe4Unsupported, max_padded_rows,
+               moe_balance_loss, moe_balance_loss_backward, moe_combine, moe_combine_dropout, moe_combine_hmx8, moe_dgates,
+               moe_dropout_backward, moe_gated_gemm_bf16, moe_gated_gemm_bf16_dgrad, moe_gather_rows, moe_grouped_gemm_bf16,
+               moe_grouped_gemm_bf16_dgrad, moe_grouped_gemm_bf16_wgrad, moe_grouped_gemm_bwd_dgrad,
                moe_grouped_gemm_bwd_wgrad, moe_grouped_gemm_fwd, moe_grouped_gemm_fwd_hmx8,
                moe_grouped_gemm_fwd_silu_amax, moe_grouped_gemm_mx, moe_grouped_gemm_mx4,
                moe_hmx8_quant, moe_route_backward, moe_route_topk, moe_router_logits, moe_router_wgrad,
@@ -32,7 +34,7 @@ from . import (NVFP4_4OVER6, PRE_SILU, PRE_SILU_AMAX, SF_BLOCKS, SF_ROWS, Moe4Un
                mxfp4_quant, mxfp8_quant, mxfp8_quant_requant_T, mxfp8_quant_rows_T, mxfp8_requant_mx4_sr_T,
                mxfp8_requant_mx_sr_T, mxfp8_requant_sr_T, nvfp4_quant_46, nvfp4_quant_requant_T)
 
-ROLE_X, ROLE_H, ROLE_WUP, ROLE_WDOWN = 0, 1, 2, 3
+ROLE_X, ROLE_H, ROLE_WUP, ROLE_WDOWN, ROLE_DROPOUT = 0, 1, 2, 3, 4
 
 _SIDE = {}  # device index -> the backward's second stream (default priority)
 # smallest T * k * d whose untimed backward uses the second stream (below it
@@ -455,3 +457,126 @@ def backward_mx4(fw, dy, seed=1, layer=0, timer=None, skip_empty_dw=False, dbala
         hT=lambda: req(fw["hq"], r["off"], r["off_pad"], ROLE_H, SF_BLOCKS, mpr),
         wuT=lambda: wreq("wuT", wq["wu"], wq["off_f"], ROLE_WUP, E * F),
         xT=lambda: req(fw["xq_perm"], r["off"], r["off_pad"], ROLE_X, SF_BLOCKS, mpr)))
+
+
+# ------------------------------------------------ BF16 layer
+#
+# The layer without quantisation, gated or not, for the layers and experts kept
+# in BF16 and to measure the quantised forms against: x is gathered by the
+# products themselves, the activations leave them in bf16, Yp in float32 (what
+# the combine and the gate gradient take).  A shared expert is the same block
+# over all tokens with one expert; its output projection adds to y.
+
+def _up_bf16(x, w, off, bias, act, row_map, map_div, save):
+    """h and, with save, the pre-activations, of gated ([E, 2, F, d]) or plain ([E, F, d]) input projections."""
+    if w.dim() == 4:
+        return moe_gated_gemm_bf16(x, w, off, bias, act, row_map, map_div, save)
+    return moe_grouped_gemm_bf16(x, w, off, bias, act, row_map=row_map, map_div=map_div, save_pre=save)
+
+
+def _down_dgrad_bf16(dy, w, pre, off, act, row_scale, row_map, map_div):
+    """The pre-activations' gradient as [M, F] or [M, 2F], and the scaled activations."""
+    if pre.dim() == 3:
+        dpre, hs = moe_gated_gemm_bf16_dgrad(dy, w, pre, off, act, row_scale, row_map, map_div)
+        return dpre.view(pre.shape[0], -1), hs
+    return moe_grouped_gemm_bf16_dgrad(dy, w, off, pre, act, row_scale, row_map, map_div)
+
+
+def forward_bf16(x, w_up, w_down, logits, k, bias=None, b_up=None, b_down=None, act=ACT_SILU, shared=None, residual=None,
+                 dropout=0.0, timer=None, seed=1, layer=0, router_w=None, balance=False, token_mask=None, seg_off=None, save=True):
+    """x [T, d] bf16; w_up [E, F, d], or [E, 2, F, d] for gated experts
+    (act(gate) * up), w_down [E, d, F], all bf16; b_up and b_down their biases
+    (float32, without the last dimension) or None.
+    shared: dict(w_up, w_down, and optionally b_up, b_down) of a shared expert, each with E = 1.
+    y = residual + dropout(routed experts' output) + shared expert's output;
+    residual [T, d] bf16 or None, dropout the probability (random words of (seed,
+    stream 16 * layer + 4)).  save: keep what the backward needs.
+    The other arguments as in forward."""
+    T, d = x.shape
+    _tick(timer, None)
+    if router_w is not None:
+        logits = moe_router_logits(x, router_w)
+        _tick(timer, "F0 router GEMM (BF16)")
+    r = moe_route_topk(logits, k, bias)
+    _tick(timer, "F2-F3 route + permutation")
+    h, pre = _up_bf16(x, w_up, r["off"], b_up, act, r["perm"], k, save)
+    _tick(timer, "F6 up GEMM + activation (BF16)")
+    Yp, _ = moe_grouped_gemm_bf16(h, w_down, r["off"], b_down, out_dtype=torch.float32)
+    _tick(timer, "F8 down GEMM (BF16)")
+    if dropout or residual is not None:
+        y = moe_combine_dropout(Yp, r["gates"], r["inv_perm"], dropout, seed, 16 * layer + ROLE_DROPOUT, residual)
+        _tick(timer, "F9 combine + dropout + residual")
+    else:
+        y = moe_combine(Yp, r["gates"], r["inv_perm"])
+        _tick(timer, "F9 combine")
+    sh_pre = sh_off = None
+    if shared is not None:
+        sh_off = torch.arange(2, dtype=torch.int32, device=x.device) * T
+        sh, sh_pre = _up_bf16(x, shared["w_up"], sh_off, shared.get("b_up"), act, None, 1, save)
+        moe_grouped_gemm_bf16(sh, shared["w_down"], sh_off, shared.get("b_down"), residual=y, out=y)
+        _tick(timer, "F10 shared expert (BF16)")
+    fw = dict(y=y, route=r, pre=pre, Yp=Yp, dims=(T, d, w_down.shape[2], w_down.shape[0], k), x=x, w_up=w_up, w_down=w_down,
+              biases=(b_up is not None, b_down is not None), act=act, shared=shared, shared_pre=sh_pre, shared_off=sh_off,
+              residual=residual, dropout=(dropout, seed, 16 * layer + ROLE_DROPOUT), router_w=router_w, logits=logits)
+    return _balance(fw, k, bias, token_mask, seg_off, timer) if balance else fw
+
+
+def backward_bf16(fw, dy, timer=None, skip_empty_dw=False, dbalance=None):
+    """dy [T, d] bf16 -> dict(dx [T, d] bf16, dW_up, dW_down, db_up, db_down (float32;
+    None without a bias), dresidual, dg, dlogits, dW_router, and with a shared
+    expert shared=dict(dW_up, dW_down, db_up, db_down))."""
+    T, d, F, E, k = fw["dims"]
+    r, x, act = fw["route"], fw["x"], fw["act"]
+    has_bu, has_bd = fw["biases"]
+    p, seed, stream_id = fw["dropout"]
+    if fw["pre"] is None:
+        raise ValueError("backward_bf16 needs a forward made with save=True")
+    if dbalance is not None and fw.get("balance") is None:
+        raise ValueError("dbalance needs a forward made with balance=True")
+    g_flat = r["gates"].view(-1)
+    _tick(timer, None)
+    dyd = moe_dropout_backward(dy, p, seed, stream_id) if p else dy
+    if p:
+        _tick(timer, "B0 dropout gradient")
+    dpre, hs = _down_dgrad_bf16(dyd, fw["w_down"], fw["pre"], r["off"], act, g_flat, r["perm"], k)
+    _tick(timer, "B3 down dgrad + activation gradient (BF16)")
+    dW_down, db_down = moe_grouped_gemm_bf16_wgrad(dyd, hs, r["off"], dy_map=r["perm"], map_div=k, skip_empty=skip_empty_dw,
+                                                   bias_grad=has_bd, db_scale=g_flat if has_bd else None)
+    _tick(timer, "B5 down wgrad (BF16)")
+    w_up = fw["w_up"]
+    dXp, _ = moe_grouped_gemm_bf16_dgrad(dpre, w_up.view(E, -1, d), r["off"], out_dtype=torch.float32)
+    _tick(timer, "B8 up dgrad (BF16)")
+    dW_up, db_up = moe_grouped_gemm_bf16_wgrad(dpre, x, r["off"], a_map=r["perm"], map_div=k, skip_empty=skip_empty_dw,
+                                               bias_grad=has_bu)
+    _tick(timer, "B10 up wgrad (BF16)")
+    dg = moe_dgates(dyd, fw["Yp"], r["inv_perm"], k)
+    _tick(timer, "B12 gate gradient")
+    dlogits = moe_route_backward(dg, r["gates"], r["idx"], E)
+    if dbalance is not None:
+        moe_balance_loss_backward(dbalance, fw["logits"], fw["balance"]["counts"], fw["balance"]["tokens"], k, dlogits=dlogits,
+                                  out=dlogits, **fw["balance_in"])
+    _tick(timer, "B13 router backward")
+    rw, dW_router = fw["router_w"], None
+    if rw is None:
+        dx = moe_unpermute_sum(dXp, r["inv_perm"], T, k)
+    elif dbalance is not None:
+        dx = moe_unpermute_sum_router_dense(dXp, r["inv_perm"], T, k, dlogits, rw)
+        dW_router = moe_router_wgrad_dense(x, dlogits)
+    else:
+        dx = moe_unpermute_sum_router(dXp, r["inv_perm"], T, k, dlogits, r["idx"], rw)
+        dW_router = moe_router_wgrad(x, dlogits, r["perm"], r["off"], k)
+    _tick(timer, "B11 un-permute sum (+ router gradients)")
+    out = dict(dx=dx, dresidual=dy if fw["residual"] is not None else None, dg=dg, dlogits=dlogits, dW_up=dW_up.view(w_up.shape),
+               dW_down=dW_down, db_up=None if db_up is None else db_up.view(w_up.shape[:-1]), db_down=db_down, dW_router=dW_router,
+               dXp=dXp, dpre=dpre, hs=hs)
+    if fw["shared"] is not None:
+        s, off = fw["shared"], fw["shared_off"]
+        dpre, hs = _down_dgrad_bf16(dy, s["w_down"], fw["shared_pre"], off, act, None, None, 1)
+        dwd, dbd = moe_grouped_gemm_bf16_wgrad(dy, hs, off, bias_grad=s.get("b_down") is not None)
+        # its input gradient joins the routed one
+        moe_grouped_gemm_bf16_dgrad(dpre, s["w_up"].view(1, -1, d), off, add=dx, out=dx)
+        dwu, dbu = moe_grouped_gemm_bf16_wgrad(dpre, x, off, bias_grad=s.get("b_up") is not None)
+        out["shared"] = dict(dW_up=dwu.view(s["w_up"].shape), dW_down=dwd, db_up=None if dbu is None else dbu.view(s["w_up"].shape[:-1]),
+                             db_down=dbd)
+        _tick(timer, "B15 shared expert (BF16)")
+    return out
