@@ -62,171 +62,201 @@ __device__ inline float row_scale(const float* scale, const int32_t* map, int64_
 }
 
 // ------------------------------------------------------------- activations
-// act(x) = x t with t = sigmoid(p): p = x (SiLU), or GELU by its tanh form,
-// whose (1 + tanh(v)) / 2 is sigmoid(2 v); act'(x) = t + x t (1 - t) p'.
+// act(x) = x t with t = sigmoid(p), p = x (c1 + c3 x^2): SiLU has c1 = 1, c3 = 0;
+// GELU by its tanh form, whose (1 + tanh(v)) / 2 is sigmoid(2 v), c1 = 2 sqrt(2 / pi)
+// and c3 = 0.044715 c1.  act'(x) = t + x t (1 - t) p'.
 // EXACT (float32 results): exp and the division to within an ulp; otherwise
 // the hardware's exp2 and reciprocal, whose relative error (|p| 2^-24 and 1 ulp)
 // is far below the half step of 2^-9 that rounding to bf16 costs.
 // Infinities: act(-inf) = -0, act(inf) = inf, act' = 0 and 1 there.
+struct ActCoef {
+  float c1, c3;
+  __host__ __device__ ActCoef(int act) : c1(act == MOE4_ACT_GELU ? 1.5957691216f : 1.0f), c3(act == MOE4_ACT_GELU ? 1.5957691216f * 0.044715f : 0.0f) {}
+};
 template <bool EXACT>
 __device__ inline float sigmoid_of(float p) {
   if (EXACT) return 1.0f / (1.0f + expf(-p));
   return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(p * -1.44269504f));
 }
 template <bool EXACT>
-__device__ inline void act_of(int act, float x, float& f, float& df) {
-  constexpr float C = 1.5957691216f, B = 0.044715f;  // 2 sqrt(2 / pi)
-  if (act == MOE4_ACT_NONE) {
-    f = x;
-    df = 1.0f;
-    return;
-  }
-  float p = x, dp = 1.0f;
-  if (act == MOE4_ACT_GELU) {
-    const float x2 = x * x;
-    p = C * fmaf(B * x2, x, x);
-    dp = fmaf(3.0f * B * C, x2, C);
-  }
-  const float t = sigmoid_of<EXACT>(p), s = t * (1.0f - t);
+__device__ inline void act_of(const ActCoef& a, float x, float& f, float& df) {
+  const float x2 = fminf(x * x, 1e30f);   // (x^2 past the range, times c3 = 0)
+  const float t = sigmoid_of<EXACT>(x * fmaf(a.c3, x2, a.c1)), s = t * (1.0f - t);
   f = t == 0.0f ? -0.0f : x * t;
-  // (x s before dp: x^2 alone may exceed the range where s x dp does not)
-  df = s == 0.0f ? t : fmaf(x * s, dp, t);
+  // (x s before p': x^2 alone may exceed the range where s x p' does not)
+  df = s == 0.0f ? t : fmaf(x * s, fmaf(3.0f * a.c3, x2, a.c1), t);
 }
 
 // ---------------------------------------------------------------- epilogues
-// W consecutive values, W % 4 == 0
+// Buffer accesses of W consecutive values (4 or 8) at an element offset from
+// the descriptor's base; PAST as the offset reads zeros and stores nothing.
+constexpr uint32_t PAST = 0x20000000u;   // (times 4 or 2 bytes: past 2^30, the largest descriptor here, and no wrap)
 template <int W>
-__device__ inline void load_bf16(const uint16_t* p, float (&v)[W]) {
+__device__ inline void load_bf16(const __amdgpu_buffer_rsrc_t& rs, uint32_t o, float (&v)[W]) {
+  uint32_t q[W / 2];
+  if (W == 8) {
+    const auto x = __builtin_amdgcn_raw_buffer_load_b128(rs, o * 2, 0, 0);
+    q[0] = x[0]; q[1] = x[1]; q[W / 2 - 2] = x[2]; q[W / 2 - 1] = x[3];
+  } else {
+    const auto x = __builtin_amdgcn_raw_buffer_load_b64(rs, o * 2, 0, 0);
+    q[0] = x[0]; q[1] = x[1];
+  }
+#pragma unroll
+  for (int i = 0; i < W; ++i) v[i] = bf16_bits_to_f32((i & 1) ? q[i / 2] >> 16 : q[i / 2] & 0xFFFFu);
+}
+template <int W>
+__device__ inline void load_f32(const __amdgpu_buffer_rsrc_t& rs, uint32_t o, float (&v)[W]) {
 #pragma unroll
   for (int i = 0; i < W; i += 4) {
-    const u32x2 q = *reinterpret_cast<const u32x2*>(p + i);
-    v[i] = bf16_bits_to_f32(q[0] & 0xFFFFu);
-    v[i + 1] = bf16_bits_to_f32(q[0] >> 16);
-    v[i + 2] = bf16_bits_to_f32(q[1] & 0xFFFFu);
-    v[i + 3] = bf16_bits_to_f32(q[1] >> 16);
+    const auto x = __builtin_amdgcn_raw_buffer_load_b128(rs, (o + i) * 4, 0, 0);
+#pragma unroll
+    for (int n = 0; n < 4; ++n) v[i + n] = __uint_as_float(x[n]);
   }
 }
 template <int W>
-__device__ inline void load_f32(const float* p, float (&v)[W]) {
-#pragma unroll
-  for (int i = 0; i < W; i += 4) {
-    const f32x4 q = *reinterpret_cast<const f32x4*>(p + i);
-    v[i] = q[0]; v[i + 1] = q[1]; v[i + 2] = q[2]; v[i + 3] = q[3];
-  }
+__device__ inline void store_bf16(const __amdgpu_buffer_rsrc_t& rs, uint32_t o, const float (&v)[W]) {
+  if (W == 8)
+    __builtin_amdgcn_raw_buffer_store_b128(
+        u32x4{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]), bf16_pair(v[W - 4], v[W - 3]), bf16_pair(v[W - 2], v[W - 1])}, rs, o * 2, 0, 0);
+  else
+    __builtin_amdgcn_raw_buffer_store_b64(u32x2{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])}, rs, o * 2, 0, 0);
 }
 template <int W>
-__device__ inline void store_bf16(uint16_t* p, const float (&v)[W]) {
+__device__ inline void store_f32(const __amdgpu_buffer_rsrc_t& rs, uint32_t o, const float (&v)[W]) {
 #pragma unroll
-  for (int i = 0; i < W; i += 4) *reinterpret_cast<u32x2*>(p + i) = u32x2{bf16_pair(v[i], v[i + 1]), bf16_pair(v[i + 2], v[i + 3])};
-}
-template <int W>
-__device__ inline void store_f32(float* p, const float (&v)[W]) {
-#pragma unroll
-  for (int i = 0; i < W; i += 4) *reinterpret_cast<f32x4*>(p + i) = f32x4{v[i], v[i + 1], v[i + 2], v[i + 3]};
+  for (int i = 0; i < W; i += 4)
+    __builtin_amdgcn_raw_buffer_store_b128(u32x4{__float_as_uint(v[i]), __float_as_uint(v[i + 1]), __float_as_uint(v[i + 2]), __float_as_uint(v[i + 3])},
+                                           rs, (o + i) * 4, 0, 0);
 }
 
-// c = q + res, at element `at`
-template <bool OUT_BF16, int W>
-__device__ inline void add_store(const Bf16Args& p, int64_t at, float (&q)[W]) {
-  if (p.res) {
-    float v[W];
-    if (OUT_BF16) load_bf16<W>(static_cast<const uint16_t*>(p.res) + at, v);
-    else load_f32<W>(static_cast<const float*>(p.res) + at, v);
-#pragma unroll
-    for (int i = 0; i < W; ++i) q[i] = q[i] + v[i];
-  }
-  if (OUT_BF16) store_bf16<W>(static_cast<uint16_t*>(p.c) + at, q);
-  else store_f32<W>(static_cast<float*>(p.c) + at, q);
-}
+// A tile's epilogue: descriptors that start with its first row and end with its
+// last, so that rows past it are neither read nor stored.  Element (r, n) of
+// them is at offset r N + n (of gu and dgu: (2 r + half) N + n).
+template <int MODE, bool OUT_BF16>
+struct Bf16Epilogue {
+  static constexpr int CW = MODE == GDGRAD ? 2 : 1, XW = MODE == GATED ? 2 : 1, IW = MODE == GDGRAD ? 2 : 1;
+  static constexpr int CB = OUT_BF16 ? 2 : 4;
+  __amdgpu_buffer_rsrc_t c, aux, in, res, bias;
+  uint32_t N;
+  ActCoef act;
+  bool has_act, has_aux, has_in, has_res, has_bias;
 
-// The W results z (GATED: z and z1) of row r, columns n .. n + W - 1, of expert e.
-template <int MODE, bool OUT_BF16, int W>
-__device__ inline void bf16_epilogue(const Bf16Args& p, int e, int64_t r, int64_t n, const float (&z)[W], const float (&z1)[W]) {
-  const int64_t at = r * p.N + n;
-  float v[W], h[W];
-  if (MODE == FWD) {
-    float q[W];
-#pragma unroll
-    for (int i = 0; i < W; ++i) q[i] = z[i];
-    if (p.bias) {
-      load_f32<W>(p.bias + e * p.N + n, v);
+  __device__ Bf16Epilogue(const Bf16Args& p, int e, int64_t row0, int32_t rows) : act(p.act) {
+    N = (uint32_t)p.N;
+    has_act = p.act != MOE4_ACT_NONE;
+    has_aux = p.aux != nullptr;
+    has_in = p.in != nullptr;
+    has_res = p.res != nullptr;
+    has_bias = p.bias != nullptr;
+    const int64_t at = row0 * p.N, n = (int64_t)rows * p.N;
+    c = make_rsrc(static_cast<uint8_t*>(p.c) + at * CW * CB, (uint64_t)n * CW * CB);
+    aux = make_rsrc(p.aux + at * XW, has_aux ? (uint64_t)n * XW * 2 : 0);
+    in = make_rsrc(p.in + at * IW, has_in ? (uint64_t)n * IW * 2 : 0);
+    res = make_rsrc(static_cast<const uint8_t*>(p.res) + at * CB, has_res ? (uint64_t)n * CB : 0);
+    const int64_t nb = p.N * (MODE == GATED ? 2 : 1);
+    bias = make_rsrc(p.bias + e * nb, has_bias ? (uint64_t)nb * 4 : 0);
+  }
+  template <int W>
+  __device__ void add_store(uint32_t o, float (&q)[W]) const {
+    if (has_res) {
+      float v[W];
+      if (OUT_BF16) load_bf16<W>(res, o, v);
+      else load_f32<W>(res, o, v);
 #pragma unroll
       for (int i = 0; i < W; ++i) q[i] = q[i] + v[i];
     }
-    if (p.aux) store_bf16<W>(p.aux + at, q);
-    if (p.act != MOE4_ACT_NONE) {
+    if (OUT_BF16) store_bf16<W>(c, o, q);
+    else store_f32<W>(c, o, q);
+  }
+  // The W results z (GATED: z and z1) of row r of the tile, columns n .. n + W -
+  // 1 (n >= N: nothing happens); s: the row's scale.
+  template <int W>
+  __device__ void put(uint32_t r, uint32_t n, float s, const float (&z)[W], const float (&z1)[W]) const {
+    const bool ok = n < N;
+    const uint32_t o = ok ? r * N + n : PAST, o0 = ok ? 2 * r * N + n : PAST, o1 = ok ? o0 + N : PAST;
+    float v[W], h[W], q[W], d;
+    if (MODE == FWD) {
 #pragma unroll
-      for (int i = 0; i < W; ++i) {
-        float d;
-        act_of<!OUT_BF16>(p.act, q[i], h[i], d);
-        q[i] = h[i];
+      for (int i = 0; i < W; ++i) q[i] = z[i];
+      if (has_bias) {
+        load_f32<W>(bias, ok ? n : PAST, v);
+#pragma unroll
+        for (int i = 0; i < W; ++i) q[i] = q[i] + v[i];
       }
-    }
-    add_store<OUT_BF16, W>(p, at, q);
-  } else if (MODE == GATED) {
-    float g[W], u[W];
-#pragma unroll
-    for (int i = 0; i < W; ++i) {
-      g[i] = z[i];
-      u[i] = z1[i];
-    }
-    if (p.bias) {
-      load_f32<W>(p.bias + (int64_t)e * 2 * p.N + n, v);
-#pragma unroll
-      for (int i = 0; i < W; ++i) g[i] = g[i] + v[i];
-      load_f32<W>(p.bias + ((int64_t)e * 2 + 1) * p.N + n, v);
-#pragma unroll
-      for (int i = 0; i < W; ++i) u[i] = u[i] + v[i];
-    }
-    if (p.aux) {
-      store_bf16<W>(p.aux + 2 * r * p.N + n, g);
-      store_bf16<W>(p.aux + (2 * r + 1) * p.N + n, u);
-    }
-#pragma unroll
-    for (int i = 0; i < W; ++i) {
-      float d;
-      act_of<false>(p.act, g[i], h[i], d);
-      h[i] = h[i] * u[i];
-    }
-    store_bf16<W>(static_cast<uint16_t*>(p.c) + at, h);
-  } else {
-    const float s = row_scale(p.scale, p.map, r, p.a_rows * p.div);
-    float q[W];
-#pragma unroll
-    for (int i = 0; i < W; ++i) q[i] = s * z[i];
-    if (MODE == DGRAD) {
-      if (p.in) {
-        load_bf16<W>(p.in + at, v);
+      if (has_aux) store_bf16<W>(aux, o, q);
+      if (has_act) {
 #pragma unroll
         for (int i = 0; i < W; ++i) {
-          float d;
-          act_of<!OUT_BF16>(p.act, v[i], h[i], d);
-          q[i] = q[i] * d;
-          h[i] = s * h[i];
+          act_of<!OUT_BF16>(act, q[i], h[i], d);
+          q[i] = h[i];
         }
-        if (p.aux) store_bf16<W>(p.aux + at, h);
       }
-      add_store<OUT_BF16, W>(p, at, q);
-    } else {
+      add_store<W>(o, q);
+    } else if (MODE == GATED) {
       float u[W];
-      const uint16_t* gu = p.in + 2 * r * p.N + n;
-      load_bf16<W>(gu, v);
-      load_bf16<W>(gu + p.N, u);
 #pragma unroll
       for (int i = 0; i < W; ++i) {
-        float f, d;
-        act_of<false>(p.act, v[i], f, d);
-        h[i] = s * (f * u[i]);
-        v[i] = q[i] * u[i] * d;
-        u[i] = q[i] * f;
+        q[i] = z[i];
+        u[i] = z1[i];
       }
-      if (p.aux) store_bf16<W>(p.aux + at, h);
-      uint16_t* d = static_cast<uint16_t*>(p.c) + 2 * r * p.N + n;
-      store_bf16<W>(d, v);
-      store_bf16<W>(d + p.N, u);
+      if (has_bias) {
+        load_f32<W>(bias, ok ? n : PAST, v);
+#pragma unroll
+        for (int i = 0; i < W; ++i) q[i] = q[i] + v[i];
+        load_f32<W>(bias, ok ? n + N : PAST, v);
+#pragma unroll
+        for (int i = 0; i < W; ++i) u[i] = u[i] + v[i];
+      }
+      if (has_aux) {
+        store_bf16<W>(aux, o0, q);
+        store_bf16<W>(aux, o1, u);
+      }
+#pragma unroll
+      for (int i = 0; i < W; ++i) {
+        if (has_act) act_of<false>(act, q[i], h[i], d);
+        else h[i] = q[i];
+        h[i] = h[i] * u[i];
+      }
+      store_bf16<W>(c, o, h);
+    } else {
+#pragma unroll
+      for (int i = 0; i < W; ++i) q[i] = s * z[i];
+      if (MODE == DGRAD) {
+        if (has_in) {
+          load_bf16<W>(in, o, v);
+#pragma unroll
+          for (int i = 0; i < W; ++i) {
+            if (has_act) {
+              act_of<!OUT_BF16>(act, v[i], h[i], d);
+              q[i] = q[i] * d;
+            } else {
+              h[i] = v[i];
+            }
+            h[i] = s * h[i];
+          }
+          if (has_aux) store_bf16<W>(aux, o, h);
+        }
+        add_store<W>(o, q);
+      } else {
+        float u[W];
+        load_bf16<W>(in, o0, v);
+        load_bf16<W>(in, o1, u);
+#pragma unroll
+        for (int i = 0; i < W; ++i) {
+          float f = v[i];
+          d = 1.0f;
+          if (has_act) act_of<false>(act, v[i], f, d);
+          h[i] = s * (f * u[i]);
+          v[i] = q[i] * u[i] * d;
+          u[i] = q[i] * f;
+        }
+        if (has_aux) store_bf16<W>(aux, o, h);
+        store_bf16<W>(c, o0, v);
+        store_bf16<W>(c, o1, u);
+      }
     }
   }
-}
+};
 
 // The weight gradient: dw[e] = beta dw[e] + sum over e's rows r of dy[r]^T a[r],
 // db[e] = beta db[e] + sum of db_scale[r] dy[r]; each operand with a map or without.

@@ -1,0 +1,42 @@
+// The tiled core of the BF16 expert products (gfx950): the ring in LDS, the
+// fragment reads and the direct loads.
+#pragma once
+#include "bf16_gemm.h"
+
+namespace moe4 {
+namespace t16 {
+
+constexpr int NT = 256;                      // four waves, 2 x 2
+constexpr int TM = 256, TN = 256, BK = 32;   // tile, contraction step
+constexpr int S = 4;                         // stages of the ring
+constexpr int HALF = 256 * BK * 2, STAGE = 2 * HALF, RING = S * STAGE;
+constexpr int LOADS = 8;                     // direct loads of a wave and stage
+constexpr uint32_t OOB = 0x80000000u;        // past every descriptor: zeros arrive
+typedef __attribute__((address_space(3))) uint8_t* lds_u8;
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x8 __attribute__((ext_vector_type(8)));
+
+// s_waitcnt immediates (vmcnt: bits 3:0 and 15:14; expcnt 6:4; lgkmcnt 11:8)
+constexpr int wait_vm(int n) { return (n & 15) | ((n >> 4) << 14) | (7 << 4) | (15 << 8); }
+constexpr int WAIT_LGKM0 = 15 | (3 << 14) | (7 << 4);
+
+// Buffer descriptor of a wave-uniform range as four scalar registers.
+__device__ __forceinline__ u32x4 rsrc4(const void* p, uint64_t bytes) {
+  const uint64_t a = reinterpret_cast<uint64_t>(p);
+  const uint32_t n = bytes > 0x7FFFFFF0ull ? 0x7FFFFFF0u : (uint32_t)bytes;
+  return u32x4{(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)a),
+               (uint32_t)__builtin_amdgcn_readfirstlane((int)((uint32_t)(a >> 32) & 0xFFFFu)),
+               (uint32_t)__builtin_amdgcn_readfirstlane((int)n), 0x00020000u};
+}
+
+// 16 bytes at each lane's offset + soff into lane-consecutive LDS from `lds` on
+// (a byte address in LDS).  Inline assembly because the compiler, which does not
+// know that other stages are read meanwhile, would wait for every load in flight
+// before each LDS read; it has no output register, and its completion is waited
+// for by hand (wait_vm) before the barrier that hands the stage over.
+__device__ __forceinline__ void load_lds(const u32x4& rs, uint32_t lds, uint32_t off, uint32_t soff) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(lds), "v"(off), "s"(rs), "s"(soff) : "memory", "m0");
+}
+
+}  // namespace t16
+}  // namespace moe4
