@@ -795,7 +795,7 @@ size_t moe_router_wgrad_dense_ws_bytes(int64_t T, int32_t E, int64_t d);
  *    0.044715 x^3))); act(-infinity) = -0.
  *  - Every width is a multiple of 8 below 2^20, each expert's matrix below 1 GiB
  *    (wgrad: its float32 gradient below 2 GiB), a mapped operand below 2 GiB,
- *    M_total and the operands' rows below 2^31, E <= 4096.  Pointers 16-byte
+ *    M_total and the operands' rows below 2^31, E <= 2048.  Pointers 16-byte
  *    aligned (maps and row scales 4-byte).  Deterministic.
  */
 #define MOE4_ACT_NONE 0

@@ -6,11 +6,9 @@
 namespace moe4 {
 namespace t16 {
 
-constexpr int NT = 256;                      // four waves, 2 x 2
-constexpr int TM = 256, TN = 256, BK = 32;   // tile, contraction step
-constexpr int S = 4;                         // stages of the ring
-constexpr int HALF = 256 * BK * 2, STAGE = 2 * HALF, RING = S * STAGE;
-constexpr int LOADS = 8;                     // direct loads of a wave and stage
+constexpr int NT = 512;                      // eight waves of 64 x 128, 4 x 2
+constexpr int TM = 256, TN = 256, BK = 64;   // tile, contraction slab
+constexpr int HALF = 256 * BK * 2, STAGE = 2 * HALF, RING = 2 * STAGE;   // two slabs
 constexpr uint32_t OOB = 0x80000000u;        // past every descriptor: zeros arrive
 typedef __attribute__((address_space(3))) uint8_t* lds_u8;
 typedef short s16x4 __attribute__((ext_vector_type(4)));
@@ -34,8 +32,15 @@ __device__ __forceinline__ u32x4 rsrc4(const void* p, uint64_t bytes) {
 // know that other stages are read meanwhile, would wait for every load in flight
 // before each LDS read; it has no output register, and its completion is waited
 // for by hand (wait_vm) before the barrier that hands the stage over.
+// (M0 is not in the clobber list, which does not take it; nothing else in these
+// kernels uses it.)
 __device__ __forceinline__ void load_lds(const u32x4& rs, uint32_t lds, uint32_t off, uint32_t soff) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(lds), "v"(off), "s"(rs), "s"(soff) : "memory", "m0");
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(lds), "v"(off), "s"(rs), "s"(soff) : "memory");
+}
+
+// 4 bytes at each lane's offset into lane-consecutive LDS
+__device__ __forceinline__ void load_lds4(const u32x4& rs, uint32_t lds, uint32_t off) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(lds), "v"(off), "s"(rs) : "memory");
 }
 
 }  // namespace t16

@@ -14,39 +14,50 @@ template <int N>
 using Int = std::integral_constant<int, N>;
 
 namespace t16 {
-constexpr int MAX_E = 4096;
+constexpr int MAX_E = 2048;
 constexpr int GM = 4;            // m-tiles of a group (see tile order)
 }  // namespace t16
 
-// One m-tile: rows row0 .. row0 + rows - 1 of expert e, 64 mi rows of LDS.
-struct MTile {
+// A tile: rows row0 .. row0 + rows - 1 of expert e (mb
+// blocks of 16 for each of the four wave rows), n-tile nt.
+struct Tile {
   int e;
-  int32_t row0, rows, mi;
+  int32_t row0, rows, mb;
+  uint32_t nt;
 };
 
+// cap: log2 of a tile's most rows; gsz = GM n_nt, its magic as in udiv_magic
 template <int MODE, bool OUT_BF16>
-__global__ void __launch_bounds__(t16::NT, 1) k_bf16_tile(Bf16Args p, int cap, uint32_t n_nt) {
+__global__ void __launch_bounds__(t16::NT, 1) k_bf16_tile(Bf16Args p, int cap, uint32_t n_nt, uint32_t gsz, uint32_t gsz_magic) {
   using namespace t16;
   constexpr bool TR = MODE == DGRAD || MODE == GDGRAD;   // w's columns are the product's: read transposed
   constexpr int NW = MODE == GATED ? TN / 2 : TN;        // the tile's columns
   __shared__ __attribute__((aligned(16))) uint8_t ring[RING];
-  __shared__ uint32_t s_first[MAX_E + 1];
-  __shared__ uint32_t s_scan[4];
+  __shared__ int32_t s_off[MAX_E + 1];                   // the experts' first rows, clamped
+  __shared__ uint32_t s_first[MAX_E + 1];                // and first m-tiles
+  __shared__ int32_t s_map[8 * 64];                      // the next tile's map entries, 32 of each wave
+  __shared__ uint32_t s_scan[8];
   const int tid = threadIdx.x, l = tid & 63, li = l & 15, q = l >> 4;
-  const int w = __builtin_amdgcn_readfirstlane(tid >> 6), wm = w >> 1, wn = w & 1;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6), wm = w >> 1, wn = w & 1, grp = w >> 2;
   const uint32_t lds0 = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_u8)ring);
+  const uint32_t ldsm = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_u8)(uint8_t*)(s_map + 64 * w));
 
   // the experts' first m-tiles: thread t counts experts t P .. t P + P - 1
   const int E = p.E;
   const int32_t M = (int32_t)p.M;
-  auto tiles_of = [&](int32_t n) __attribute__((always_inline)) { return n > 0 ? ((uint32_t)n + (1u << cap) - 1) >> cap : 0u; };
-  auto rows_of = [&](int32_t r0, int32_t r1) __attribute__((always_inline)) { return (r1 < M ? r1 : M) - (r0 > 0 ? r0 : 0); };
+  for (int e = tid; e <= E; e += NT) {
+    const int32_t o = p.off[e];
+    s_off[e] = o < 0 ? 0 : (o < M ? o : M);
+  }
+  __syncthreads();
+  auto tiles_of = [&](int e) __attribute__((always_inline)) {
+    const int32_t n = s_off[e + 1] - s_off[e];
+    return n > 0 ? ((uint32_t)n + (1u << cap) - 1) >> cap : 0u;
+  };
   {
     const int P = (E + NT - 1) / NT;
     uint32_t mine = 0;
-    for (int e = tid * P; e < (tid + 1) * P && e < E; ++e) {
-      mine += tiles_of(rows_of(p.off[e], p.off[e + 1]));
-    }
+    for (int e = tid * P; e < (tid + 1) * P && e < E; ++e) mine += tiles_of(e);
     uint32_t inc = mine;
 #pragma unroll
     for (int o = 1; o < 64; o <<= 1) {
@@ -59,7 +70,7 @@ __global__ void __launch_bounds__(t16::NT, 1) k_bf16_tile(Bf16Args p, int cap, u
     for (int i = 0; i < w; ++i) run += s_scan[i];
     for (int e = tid * P; e < (tid + 1) * P && e < E; ++e) {
       s_first[e] = run;
-      run += tiles_of(rows_of(p.off[e], p.off[e + 1]));
+      run += tiles_of(e);
     }
     if (tid == NT - 1) s_first[E] = run;   // (threads past E hold the total too)
     __syncthreads();
@@ -70,120 +81,164 @@ __global__ void __launch_bounds__(t16::NT, 1) k_bf16_tile(Bf16Args p, int cap, u
   const uint32_t t_end = (xcd + 1) * per < total ? (xcd + 1) * per : total, t_begin = xcd * per + blockIdx.x / 8;
   if (t_begin >= t_end) return;
 
-  // tile t -> its m-tile and n-tile
-  auto locate = [&](uint32_t t, MTile& m, uint32_t& nt) __attribute__((always_inline)) {
-    const uint32_t gsz = GM * n_nt, g = t / gsz, r = t - g * gsz;
-    const uint32_t gm = n_mt - g * GM < GM ? n_mt - g * GM : GM;
-    nt = r / gm;
-    const uint32_t mi = g * GM + (r - nt * gm);
-    // the last expert e with s_first[e] <= mi (experts without tiles share their successor's)
-    int lo = 0;
-    for (int step = E <= 64 ? 1 : (E <= 64 * 64 ? 64 : 4096); step >= 1; step /= 64) {
-      const int at = lo + l * step;
-      const unsigned long long b = __ballot(at <= E && s_first[at <= E ? at : E] <= mi);
-      lo += (63 - __clzll((long long)b)) * step;
-    }
-    m.e = __builtin_amdgcn_readfirstlane(lo);
-    // (scalar loads: a vector load here would wait for the loads in flight)
-    const int32_t r0 = ld_const(p.off, m.e), n = rows_of(r0, ld_const(p.off, m.e + 1));
-    const uint32_t cnt = tiles_of(n), even = (((uint32_t)n + cnt - 1) / cnt + 63) / 64 * 64;   // rows of all tiles but the last
-    const int32_t at = (int32_t)((mi - __builtin_amdgcn_readfirstlane(s_first[m.e])) * even);
-    m.row0 = (r0 > 0 ? r0 : 0) + at;
-    m.rows = n - at < (int32_t)even ? (n > at ? n - at : 0) : (int32_t)even;
-    m.mi = (m.rows + 63) / 64;
+  // The lane number, kept from the optimiser: what a tile's start and end make
+  // of it would be hoisted out of the tile loop and fill the registers that the
+  // contraction needs.
+  auto lane = [&]() __attribute__((always_inline)) {
+    int x = l;
+    asm volatile("" : "+v"(x));
+    return x;
   };
 
-  const uint32_t K = (uint32_t)p.K, N = (uint32_t)p.N, KB = K * 2, nk0 = ((K + BK - 1) / BK + 1) / 2 * 2, nk = nk0 < S ? S : nk0;
+  // tile t of the order: groups of GM m-tiles, in a group the m-tiles fastest
+  auto locate = [&](uint32_t t, Tile& m) __attribute__((always_inline)) {
+    const uint32_t g = __builtin_amdgcn_readfirstlane(udiv_magic(t, gsz, gsz_magic)), r = t - g * gsz;
+    const uint32_t gm = n_mt - g * GM < GM ? n_mt - g * GM : GM;
+    m.nt = gm == 4 ? r / 4 : gm == 3 ? r / 3 : gm == 2 ? r / 2 : r;
+    const uint32_t mi = g * GM + (r - m.nt * gm);
+    // the last expert e with s_first[e] <= mi (experts without tiles share their successor's)
+    int lo = 0;
+    const int l = lane();
+    if (E > 64) lo = (63 - __clzll((long long)__ballot(64 * l <= E && s_first[64 * l <= E ? 64 * l : E] <= mi))) * 64;
+    const int at = lo + l;
+    m.e = __builtin_amdgcn_readfirstlane(lo + 63 - __clzll((long long)__ballot(at <= E && s_first[at <= E ? at : E] <= mi)));
+    const int32_t r0 = __builtin_amdgcn_readfirstlane(s_off[m.e]), r1 = __builtin_amdgcn_readfirstlane(s_off[m.e + 1]);
+    m.row0 = r0 + (int32_t)((mi - __builtin_amdgcn_readfirstlane(s_first[m.e])) << cap);
+    m.rows = r1 - m.row0 < (1 << cap) ? r1 - m.row0 : 1 << cap;
+    m.mb = (m.rows + 63) / 64;
+  };
+
+  const uint32_t K = (uint32_t)p.K, N = (uint32_t)p.N, KB = K * 2, nk = (K + BK - 1) / BK;
   const uint32_t ldb = TR ? N * 2 : KB;                     // bytes of a row of w
 
   // ------------------------------------------------------------- load stream
-  // (past the last tile it goes on with descriptors of nothing, so that every
-  // step issues as many loads)
+  // It runs a slab ahead; the tile after the one being loaded is located,
+  // and its map entries fetched, a tile ahead.  Past the last tile it goes on
+  // with descriptors of nothing, so that every slab has as many loads.
   uint32_t lt = t_begin, ls = 0;
+  Tile ahead;
   u32x4 ra, rb;
   uint32_t voa[4], vob[4];
-  const uint32_t ca = (l & 3) ^ ((l >> 4) & 3);             // A: the chunk that lands in slot l & 3 of row l >> 2
-  auto cb = [&](int t) __attribute__((always_inline)) { return TR ? ((uint32_t)(l & 31) ^ (4 * ((2 * t + (l >> 5)) & 3))) : ((uint32_t)(l & 3) ^ ((2 * t + (l >> 5)) & 3)); };
-  auto seek = [&]() __attribute__((always_inline)) {
+  // the chunk (16 bytes) that lands in this lane's slot: load t of A has rows 32 w
+  // + 8 t + l / 8, slot l % 8; so has B, or with TR k rows 8 w + 2 t + l / 32, slot l % 32
+  auto ca = [&](int t, int l) __attribute__((always_inline)) { return (uint32_t)(l & 7) ^ (4 * (t & 1) + (l >> 4)); };
+  auto cb = [&](int t, int l) __attribute__((always_inline)) {
+    return TR ? (uint32_t)(l & 31) ^ (4 * ((2 * t + (l >> 5)) & 3)) : (uint32_t)(l & 7) ^ (2 * (t & 3) + ((l >> 4) & 1));
+  };
+  auto prefetch = [&]() __attribute__((always_inline)) {
+    if (lt >= t_end) return;
+    locate(lt, ahead);
+    __builtin_amdgcn_s_waitcnt(WAIT_LGKM0);   // (the entries there have been read)
+    if (p.map) load_lds4(rsrc4(p.map + ahead.row0, (uint64_t)ahead.rows * 4), ldsm, 4 * (32 * w + l));
+  };
+  // the loads go on with tile `ahead` (its map entries have landed: they are
+  // older than a slab that has been waited for), which is returned
+  auto bind = [&]() __attribute__((always_inline)) {
+    const Tile m = ahead;
+    const int l = lane();
     ls = 0;
     if (lt >= t_end) {
       ra = rsrc4(p.a, 0);
       rb = ra;
-      return;
+      return m;
     }
-    MTile m;
-    uint32_t nt;
-    locate(lt, m, nt);
-    const int64_t n0 = (int64_t)nt * NW;
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
-      const int r = 64 * w + 16 * t + (l >> 2);
-      uint32_t o = OOB;
-      if (r < m.rows) {
-        const int64_t row = mapped_row(p.map, (int64_t)m.row0 + r, p.div, p.magic, p.a_rows, &g_dev_err);
-        if (row >= 0) o = (uint32_t)(p.map ? row : r) * KB + 16 * ca;
+      const int r = 32 * w + 8 * t + (l >> 3);
+      uint32_t row = (uint32_t)r;
+      bool ok = r < m.rows;
+      if (p.map && ok) {
+        const int32_t i = s_map[r + 32 * w];
+        row = udiv_magic((uint32_t)i, p.div, p.magic);
+        ok = i >= 0 && row < (uint32_t)p.a_rows;
+        if (!ok) atomicOr(&g_dev_err, MOE4_DEVERR_INDEX);
       }
-      voa[t] = o;
+      voa[t] = ok ? row * KB + 16 * ca(t, l) : OOB;
     }
     ra = rsrc4(p.map ? p.a : p.a + (int64_t)m.row0 * p.K, (uint64_t)(p.map ? p.a_rows : m.rows) * KB);
+    const uint32_t n0 = m.nt * NW;
     if (TR) {
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
-        const uint32_t k = 8 * w + 2 * t + (l >> 5), c = cb(t);
+        const uint32_t k = 8 * w + 2 * t + (l >> 5), c = cb(t, l);
         vob[t] = n0 + 8 * c < N ? k * ldb + 16 * c : OOB;
       }
       rb = rsrc4(p.w + (int64_t)m.e * p.K * p.N + n0, (uint64_t)(K * (uint64_t)N - n0) * 2);
     } else {
-      const int64_t row0 = MODE == GATED ? (int64_t)m.e * 2 * p.N : (int64_t)m.e * p.N;
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
-        const uint32_t R = 64 * w + 16 * t + (l >> 2);      // GATED: 64 gate and 64 up columns for each wave column
-        const uint32_t n = MODE == GATED ? (uint32_t)n0 + 64 * (R >> 7) + (R & 63) : (uint32_t)n0 + R;
+        const uint32_t R = 32 * w + 8 * t + (l >> 3);       // GATED: 64 gate and 64 up columns for each wave column
+        const uint32_t n = MODE == GATED ? n0 + 64 * (R >> 7) + (R & 63) : n0 + R;
         const uint32_t row = MODE == GATED ? ((R >> 6) & 1) * N + n : n;
-        vob[t] = n < N ? row * KB + 16 * cb(t) : OOB;
+        vob[t] = n < N ? row * KB + 16 * cb(t, l) : OOB;
       }
-      rb = rsrc4(p.w + row0 * p.K, (uint64_t)(MODE == GATED ? 2 : 1) * N * KB);
+      rb = rsrc4(p.w + (MODE == GATED ? 2 : 1) * (int64_t)m.e * p.N * p.K, (uint64_t)(MODE == GATED ? 2 : 1) * N * KB);
     }
+    if (K < BK) {
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        if (ca(t, l) >= K / 8) voa[t] = OOB;
+        if (!TR && cb(t, l) >= K / 8) vob[t] = OOB;
+      }
+    }
+    lt += stride;
+    prefetch();
+    return m;
   };
-  // this wave's loads of a stage, four of each operand
+  // this wave's loads of a slab, four of each operand.  (Their offsets stay in
+  // registers of their own: one that is written again for the next load waits
+  // until the load before has left for the memory pipeline, and the MFMAs behind
+  // it wait too.)
   auto load_a = [&](int t, uint32_t stage) __attribute__((always_inline)) {
-    load_lds(ra, lds0 + stage * STAGE + (4 * w + t) * 1024, 4 * ls + ca < K / 8 ? voa[t] : OOB, ls * (BK * 2));
+    load_lds(ra, lds0 + stage * STAGE + (4 * w + t) * 1024, voa[t], ls * (BK * 2));
   };
   auto load_b = [&](int t, uint32_t stage) __attribute__((always_inline)) {
-    const uint32_t dst = lds0 + stage * STAGE + HALF + (4 * w + t) * 1024;
-    // (TR: rows past K lie past the descriptor, so all of the offset in the operand that is checked)
-    if (TR) load_lds(rb, dst, vob[t] + ls * BK * ldb, 0);
-    else load_lds(rb, dst, 4 * ls + cb(t) < K / 8 ? vob[t] : OOB, ls * (BK * 2));
+    load_lds(rb, lds0 + stage * STAGE + HALF + (4 * w + t) * 1024, vob[t], TR ? 0 : ls * (BK * 2));
   };
+  // the next slab of the tile: B's k rows by the descriptor; before a last slab
+  // that ends inside it, the chunks past K drop out
+  auto advance = [&]() __attribute__((always_inline)) {
+    ++ls;
+    if (TR) {
+      const uint64_t base = ((uint64_t)rb[1] << 32 | rb[0]) + BK * ldb;
+      const uint32_t left = rb[2] > BK * ldb ? rb[2] - BK * ldb : 0;
+      rb = rsrc4(reinterpret_cast<const void*>(base), left);
+    }
+    if (8 * ls + 8 > K / 8 && 8 * ls < K / 8 + 8) {
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        if (8 * ls + ca(t, l) >= K / 8) voa[t] = OOB;
+        if (!TR && 8 * ls + cb(t, l) >= K / 8) vob[t] = OOB;
+      }
+    }
+  };
+
   // --------------------------------------------------------------- fragments
-  uint32_t lb[4];                                            // TR: the lane's offset for each pair of column blocks
-  uint32_t la = 0, lbn = 0;
+  uint32_t lb[4];    // the lane's offset for each pair of column blocks (!TR: for each half of the slab)
+  uint32_t la[2];    // A: for each half of the slab
   if (TR) {
     const int j = li >> 2, s = li & 3;
 #pragma unroll
     for (int pb = 0; pb < 4; ++pb) lb[pb] = HALF + (8 * q + j) * 512 + 16 * (16 * wn + 4 * (pb ^ j) + s);
   } else {
-    lbn = HALF + (128 * wn + 8 * (li >> 2) + (li & 3)) * 64 + 16 * (q ^ (li >> 2));
+#pragma unroll
+    for (int h = 0; h < 2; ++h) lb[h] = HALF + (128 * wn + 8 * (li >> 2) + (li & 3)) * 128 + 16 * ((4 * h + q) ^ (li >> 1));
   }
-  auto frag_a = [&](bf16x8& f, int i, uint32_t st) __attribute__((always_inline)) { f = *reinterpret_cast<const bf16x8*>(ring + st + la + 1024 * i); };
-  auto frag_b = [&](bf16x8& f, int i, uint32_t st) __attribute__((always_inline)) {
+  auto frag_a = [&](bf16x8& f, int i, int h, uint32_t st) __attribute__((always_inline)) {
+    f = *reinterpret_cast<const bf16x8*>(ring + st + la[h] + 2048 * i);
+  };
+  auto frag_b = [&](bf16x8& f, int i, int h, uint32_t st) __attribute__((always_inline)) {
     const int pb = i >> 1, b = i & 1;
     if (TR) {
       typedef __attribute__((address_space(3))) s16x4* lp;
-      const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)(lds_u8)(ring + st + lb[pb] + 8 * b));
-      const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)(lds_u8)(ring + st + lb[pb] + 8 * b + 2048));
+      const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)(lds_u8)(ring + st + lb[pb] + 16384 * h + 8 * b));
+      const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)(lds_u8)(ring + st + lb[pb] + 16384 * h + 8 * b + 2048));
       f = __builtin_bit_cast(bf16x8, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
     } else {
-      f = *reinterpret_cast<const bf16x8*>(ring + st + lbn + 2048 * pb + 256 * b);
+      f = *reinterpret_cast<const bf16x8*>(ring + st + lb[h] + 4096 * pb + 512 * b);
     }
   };
 
-  // waits until all of this wave's loads but those of the S - 2 latest stages
-  // have landed
-  auto landed = [&]() __attribute__((always_inline)) {
-    __builtin_amdgcn_sched_barrier(0);
-    __builtin_amdgcn_s_waitcnt(wait_vm((S - 2) * LOADS));
-  };
   auto barrier = [&]() __attribute__((always_inline)) {
     __builtin_amdgcn_sched_barrier(0);
     __builtin_amdgcn_s_waitcnt(WAIT_LGKM0);
@@ -192,81 +247,82 @@ __global__ void __launch_bounds__(t16::NT, 1) k_bf16_tile(Bf16Args p, int cap, u
     asm volatile("" ::: "memory");
   };
 
-  seek();
-  for (int s = 0; s < S; ++s) {
+  prefetch();
+  __builtin_amdgcn_s_waitcnt(wait_vm(0));
+  Tile cur = bind();
 #pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      load_a(t, s);
-      load_b(t, s);
-    }
-    ++ls;
+  for (int t = 0; t < 4; ++t) {
+    load_a(t, 0);
+    load_b(t, 0);
   }
+  advance();
+  __builtin_amdgcn_s_waitcnt(wait_vm(0));
+  barrier();
+  if (grp) barrier();
 
-  uint32_t gs = 0;   // stage counter of the compute stream
+  uint32_t gs = 0;       // the slab's place in the ring
   for (uint32_t ct = t_begin; ct < t_end; ct += stride) {
-    MTile m;
-    uint32_t nt;
-    locate(ct, m, nt);
-    auto run = [&](auto mb) __attribute__((always_inline)) {
-      constexpr int MB = decltype(mb)::value;
-      f32x4 acc[MB][8];
-      bf16x8 fa[2][MB], fb[2][8];
-      // One step: the MFMAs of set CUR, the loads into this step's stage (every
-      // wave has read it), the reads of the next stage into the other set.
-      auto step = [&](auto cur) __attribute__((always_inline)) {
-        constexpr int CUR = decltype(cur)::value;
-        landed();
-        barrier();
-        const uint32_t nst = ((gs + 1) % S) * STAGE, stg = gs % S;
+    const Tile m = cur;
+    const int mb = m.mb;
+    f32x4 acc[4][8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          if (i < MB) frag_a(fa[1 - CUR][i < MB ? i : 0], i, nst);
-          frag_b(fb[1 - CUR][i], i, nst);
-          if (i < 4) load_a(i, stg);
-          else load_b(i - 4, stg);
-          if (i < MB) {
+    for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int n = 0; n < 8; ++n)
-              acc[i < MB ? i : 0][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[CUR][n], fa[CUR][i < MB ? i : 0], acc[i < MB ? i : 0][n], 0, 0, 0);
-          }
-          __builtin_amdgcn_sched_barrier(0);
+      for (int n = 0; n < 8; ++n) acc[i][n] = f32x4{};
+    {
+      const int li = lane() & 15, q = lane() >> 4;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) la[h] = (16 * mb * wm + li) * 128 + 16 * ((4 * h + q) ^ (li >> 1));
+    }
+    bf16x8 fa[4], fb[8];
+    auto reads = [&](int h) __attribute__((always_inline)) {
+      const uint32_t st = gs * STAGE;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        frag_b(fb[i], i, h, st);
+        if (i < 4) frag_a(fa[i], i, h, st);
+      }
+    };
+    auto mfmas = [&]() __attribute__((always_inline)) {
+      __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (i < mb) {
+#pragma unroll
+          for (int n = 0; n < 8; ++n) acc[i][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[n], fa[i], acc[i][n], 0, 0, 0);
         }
-        ++ls;
-        gs = __builtin_amdgcn_readfirstlane(gs + 1);
-      };
+      }
+      __builtin_amdgcn_s_setprio(0);
+    };
+    for (uint32_t s = 0; s < nk; ++s) {
+      if (s == nk - 1) cur = bind();
+      reads(0);
 #pragma unroll
-      for (int i = 0; i < MB; ++i)
-#pragma unroll
-        for (int n = 0; n < 8; ++n) acc[i][n] = f32x4{};
-      la = (16 * MB * wm + li) * 64 + 16 * (q ^ (li >> 2));
-      __builtin_amdgcn_s_waitcnt(wait_vm((S - 1) * LOADS));
+      for (int t = 0; t < 4; ++t) {
+        load_a(t, 1 - gs);
+        load_b(t, 1 - gs);
+      }
+      advance();
       barrier();
-      {
-        const uint32_t st = (gs % S) * STAGE;
+      mfmas();
+      barrier();
+      reads(1);
+      if (grp) __builtin_amdgcn_s_waitcnt(wait_vm(0));
+      barrier();
+      mfmas();
+      if (!grp) __builtin_amdgcn_s_waitcnt(wait_vm(0));
+      barrier();
+      gs = 1 - gs;
+    }
+    const Bf16Epilogue<MODE, OUT_BF16> epi(p, m.e, m.row0, m.rows);
 #pragma unroll
-        for (int i = 0; i < MB; ++i) frag_a(fa[0][i], i, st);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) frag_b(fb[0][i], i, st);
-      }
-      // the loads are S steps ahead: from step nk - S on they are the next tile's.
-      // (The last step reads fragments of the next tile's first stage, of no use:
-      // its rows lie differently over the waves.)
-      for (uint32_t s = 0; s < nk; s += 2) {
-        if (s == nk - S) {
-          lt += stride;
-          seek();
-        }
-        step(Int<0>{});
-        step(Int<1>{});
-      }
-      const Bf16Epilogue<MODE, OUT_BF16> epi(p, m.e, m.row0, m.rows);
-#pragma unroll
-      for (int i = 0; i < MB; ++i) {
-        const int r = 16 * MB * wm + 16 * i + li;
+    for (int i = 0; i < 4; ++i) {
+      if (i < mb) {
+        const int li = lane() & 15, q = lane() >> 4, r = 16 * mb * wm + 16 * i + li;
         const float sc = (MODE == DGRAD || MODE == GDGRAD) && r < m.rows ? row_scale(p.scale, p.map, (int64_t)m.row0 + r, p.a_rows * p.div) : 1.0f;
 #pragma unroll
         for (int pb = 0; pb < (MODE == GATED ? 2 : 4); ++pb) {
-          const uint32_t n = nt * NW + (MODE == GATED ? 64 : 128) * wn + 32 * pb + 8 * q;
+          const uint32_t n = m.nt * NW + (MODE == GATED ? 64 : 128) * wn + 32 * pb + 8 * q;
           const f32x4 x = acc[i][2 * pb], y = acc[i][2 * pb + 1];
           const f32x4 x1 = acc[i][MODE == GATED ? 2 * pb + 4 : 0], y1 = acc[i][MODE == GATED ? 2 * pb + 5 : 0];
           const float z[8] = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
@@ -275,12 +331,9 @@ __global__ void __launch_bounds__(t16::NT, 1) k_bf16_tile(Bf16Args p, int cap, u
           __builtin_amdgcn_sched_barrier(0);
         }
       }
-    };
-    if (m.mi >= 4) run(Int<8>{});
-    else if (m.mi == 3) run(Int<6>{});
-    else if (m.mi == 2) run(Int<4>{});
-    else run(Int<2>{});
+    }
   }
+  if (!grp) barrier();
   __builtin_amdgcn_s_waitcnt(wait_vm(0));   // (no load into this workgroup's LDS outlives it)
 }
 
@@ -304,16 +357,17 @@ static int launch_bf16(const Bf16Args& p, void* stream, const char* name) {
   const int cus = cu_count() / 8 * 8 < 8 ? 8 : cu_count() / 8 * 8;
   int cap = 8;   // log2 of a tile's most rows
   while (cap > 6 && ((p.M >> cap) + (p.M < p.E ? p.M : p.E)) * nt < cus) --cap;
+  const uint32_t gsz = (uint32_t)(t16::GM * nt), magic = gsz <= 1 ? 0xFFFFFFFFu : (uint32_t)(((uint64_t)1 << 32) / gsz);
   MOE4_REQUIRE(((p.M >> cap) + p.E) * nt < ((int64_t)1 << 31), MOE4_EINVAL, std::string(name) + ": too large");
-  hipLaunchKernelGGL((k_bf16_tile<MODE, OUT_BF16>), dim3((unsigned)cus), dim3(NT), 0, as_stream(stream), p, cap, (uint32_t)nt);
+  hipLaunchKernelGGL((k_bf16_tile<MODE, OUT_BF16>), dim3((unsigned)cus), dim3(NT), 0, as_stream(stream), p, cap, (uint32_t)nt, gsz, magic);
   return check_launch(name);
 }
 
 // What the four calls check alike.  rows of a: M without a map.
 static int check_bf16(const Bf16Args& p, const char* name) {
   const std::string s(name);
-  MOE4_REQUIRE(p.E >= 1 && p.E <= 4096 && p.M >= 0 && p.N > 0 && p.K > 0 && p.N % 8 == 0 && p.K % 8 == 0, MOE4_EINVAL,
-               s + ": need 1 <= E <= 4096 and widths that are multiples of 8");
+  MOE4_REQUIRE(p.E >= 1 && p.E <= 2048 && p.M >= 0 && p.N > 0 && p.K > 0 && p.N % 8 == 0 && p.K % 8 == 0, MOE4_EINVAL,
+               s + ": need 1 <= E <= 2048 and widths that are multiples of 8");
   MOE4_REQUIRE(p.M < ((int64_t)1 << 31) && p.a_rows >= 0 && p.a_rows < ((int64_t)1 << 31) && p.N < ((int64_t)1 << 20) &&
                    p.K < ((int64_t)1 << 20) && p.N * p.K < ((int64_t)1 << 29),
                MOE4_EINVAL, s + ": rows must be below 2^31, widths below 2^20, each expert's matrix below 1 GiB");

@@ -90,8 +90,8 @@ extern "C" int moe_grouped_gemm_bf16_wgrad(const uint16_t* dy, int64_t dy_rows, 
                                            int64_t N, int64_t K, float* dw, float beta, int flags, const float* db_scale, float* db,
                                            void* stream) {
   const std::string s("moe_grouped_gemm_bf16_wgrad");
-  MOE4_REQUIRE(E >= 1 && E <= 4096 && M_total >= 0 && N > 0 && K > 0 && N % 8 == 0 && K % 8 == 0, MOE4_EINVAL,
-               s + ": need 1 <= E <= 4096 and widths that are multiples of 8");
+  MOE4_REQUIRE(E >= 1 && E <= 2048 && M_total >= 0 && N > 0 && K > 0 && N % 8 == 0 && K % 8 == 0, MOE4_EINVAL,
+               s + ": need 1 <= E <= 2048 and widths that are multiples of 8");
   MOE4_REQUIRE(M_total < ((int64_t)1 << 31) && dy_rows >= 0 && a_rows >= 0 && dy_rows < ((int64_t)1 << 31) && a_rows < ((int64_t)1 << 31) &&
                    N < ((int64_t)1 << 20) && K < ((int64_t)1 << 20) && N * K < ((int64_t)1 << 29),
                MOE4_EINVAL, s + ": rows must be below 2^31, widths below 2^20, each expert's matrix below 2 GiB");
