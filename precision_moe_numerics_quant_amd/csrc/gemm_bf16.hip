@@ -18,21 +18,21 @@ constexpr int MAX_E = 2048;
 constexpr int GM = 4;            // m-tiles of a group (see tile order)
 }  // namespace t16
 
-// A tile: rows row0 .. row0 + rows - 1 of expert e (mb
-// blocks of 16 for each of the four wave rows), n-tile nt.
+// A tile: rows row0 .. row0 + rows - 1 of expert e, n-tile nt.
 struct Tile {
   int e;
-  int32_t row0, rows, mb;
+  int32_t row0, rows;
   uint32_t nt;
 };
 
-// cap: log2 of a tile's most rows; gsz = GM n_nt, its magic as in udiv_magic
+// cap: log2 of a tile's most rows
 template <int MODE, bool OUT_BF16>
-__global__ void __launch_bounds__(t16::NT, 1) k_bf16_tile(Bf16Args p, int cap, uint32_t n_nt, uint32_t gsz, uint32_t gsz_magic) {
+__global__ void __launch_bounds__(t16::NT, 1) k_bf16_tile(Bf16Args p, int cap, uint32_t n_nt) {
   using namespace t16;
   constexpr bool TR = MODE == DGRAD || MODE == GDGRAD;   // w's columns are the product's: read transposed
   constexpr int NW = MODE == GATED ? TN / 2 : TN;        // the tile's columns
   __shared__ __attribute__((aligned(16))) uint8_t ring[RING];
+  __shared__ __attribute__((aligned(16))) Tile s_tile[NT];   // this workgroup's next tiles
   __shared__ int32_t s_off[MAX_E + 1];                   // the experts' first rows, clamped
   __shared__ uint32_t s_first[MAX_E + 1];                // and first m-tiles
   __shared__ int32_t s_map[8 * 64];                      // the next tile's map entries, 32 of each wave
@@ -75,11 +75,13 @@ __global__ void __launch_bounds__(t16::NT, 1) k_bf16_tile(Bf16Args p, int cap, u
     if (tid == NT - 1) s_first[E] = run;   // (threads past E hold the total too)
     __syncthreads();
   }
-  const uint32_t n_mt = __builtin_amdgcn_readfirstlane(s_first[E]), total = n_mt * n_nt;
-  // this workgroup's tiles: its XCD's share in order, every gridDim / 8-th of it
-  const uint32_t xcd = blockIdx.x % 8, stride = gridDim.x / 8, per = (total + 7) / 8;
-  const uint32_t t_end = (xcd + 1) * per < total ? (xcd + 1) * per : total, t_begin = xcd * per + blockIdx.x / 8;
-  if (t_begin >= t_end) return;
+  // Tile order: groups of GM m-tiles, in a group the m-tiles fastest, so that
+  // the 32 workgroups of an XCD work on GM row blocks and the column blocks of
+  // one or two experts at a time.  The XCDs take chunks of tiles in turn: whole
+  // groups where there are enough of them, else single tiles or a few.
+  const uint32_t n_mt = __builtin_amdgcn_readfirstlane(s_first[E]), total = n_mt * n_nt, gsz = GM * n_nt;
+  const uint32_t xcd = blockIdx.x % 8, stride = gridDim.x / 8;
+  const uint32_t chunk = total >= 16 * gsz ? gsz : (total + gridDim.x - 1) / gridDim.x;
 
   // The lane number, kept from the optimiser: what a tile's start and end make
   // of it would be hoisted out of the tile loop and fill the registers that the
@@ -90,33 +92,14 @@ __global__ void __launch_bounds__(t16::NT, 1) k_bf16_tile(Bf16Args p, int cap, u
     return x;
   };
 
-  // tile t of the order: groups of GM m-tiles, in a group the m-tiles fastest
-  auto locate = [&](uint32_t t, Tile& m) __attribute__((always_inline)) {
-    const uint32_t g = __builtin_amdgcn_readfirstlane(udiv_magic(t, gsz, gsz_magic)), r = t - g * gsz;
-    const uint32_t gm = n_mt - g * GM < GM ? n_mt - g * GM : GM;
-    m.nt = gm == 4 ? r / 4 : gm == 3 ? r / 3 : gm == 2 ? r / 2 : r;
-    const uint32_t mi = g * GM + (r - m.nt * gm);
-    // the last expert e with s_first[e] <= mi (experts without tiles share their successor's)
-    int lo = 0;
-    const int l = lane();
-    if (E > 64) lo = (63 - __clzll((long long)__ballot(64 * l <= E && s_first[64 * l <= E ? 64 * l : E] <= mi))) * 64;
-    const int at = lo + l;
-    m.e = __builtin_amdgcn_readfirstlane(lo + 63 - __clzll((long long)__ballot(at <= E && s_first[at <= E ? at : E] <= mi)));
-    const int32_t r0 = __builtin_amdgcn_readfirstlane(s_off[m.e]), r1 = __builtin_amdgcn_readfirstlane(s_off[m.e + 1]);
-    m.row0 = r0 + (int32_t)((mi - __builtin_amdgcn_readfirstlane(s_first[m.e])) << cap);
-    m.rows = r1 - m.row0 < (1 << cap) ? r1 - m.row0 : 1 << cap;
-    m.mb = (m.rows + 63) / 64;
-  };
-
   const uint32_t K = (uint32_t)p.K, N = (uint32_t)p.N, KB = K * 2, nk = (K + BK - 1) / BK;
   const uint32_t ldb = TR ? N * 2 : KB;                     // bytes of a row of w
 
   // ------------------------------------------------------------- load stream
-  // It runs a slab ahead; the tile after the one being loaded is located,
-  // and its map entries fetched, a tile ahead.  Past the last tile it goes on
-  // with descriptors of nothing, so that every slab has as many loads.
-  uint32_t lt = t_begin, ls = 0;
-  Tile ahead;
+  // It runs a slab ahead; the map entries of the tile after the one being
+  // loaded are fetched a tile ahead.  Past the last tile it goes on with
+  // descriptors of nothing, so that every slab has as many loads.
+  uint32_t ln = 0, n_my = 0, ls = 0;   // the next tile to load, this batch's tiles, slab
   u32x4 ra, rb;
   uint32_t voa[4], vob[4];
   // the chunk (16 bytes) that lands in this lane's slot: load t of A has rows 32 w
@@ -125,23 +108,28 @@ __global__ void __launch_bounds__(t16::NT, 1) k_bf16_tile(Bf16Args p, int cap, u
   auto cb = [&](int t, int l) __attribute__((always_inline)) {
     return TR ? (uint32_t)(l & 31) ^ (4 * ((2 * t + (l >> 5)) & 3)) : (uint32_t)(l & 7) ^ (2 * (t & 3) + ((l >> 4) & 1));
   };
-  auto prefetch = [&]() __attribute__((always_inline)) {
-    if (lt >= t_end) return;
-    locate(lt, ahead);
-    __builtin_amdgcn_s_waitcnt(WAIT_LGKM0);   // (the entries there have been read)
-    if (p.map) load_lds4(rsrc4(p.map + ahead.row0, (uint64_t)ahead.rows * 4), ldsm, 4 * (32 * w + l));
+  auto tile = [&](uint32_t i) __attribute__((always_inline)) {
+    const Tile x = s_tile[i];
+    return Tile{__builtin_amdgcn_readfirstlane(x.e), __builtin_amdgcn_readfirstlane(x.row0), __builtin_amdgcn_readfirstlane(x.rows),
+                (uint32_t)__builtin_amdgcn_readfirstlane((int)x.nt)};
   };
-  // the loads go on with tile `ahead` (its map entries have landed: they are
-  // older than a slab that has been waited for), which is returned
+  auto fetch_map = [&](uint32_t i) __attribute__((always_inline)) {
+    if (!p.map || i >= n_my) return;
+    const Tile x = tile(i);
+    __builtin_amdgcn_s_waitcnt(WAIT_LGKM0);   // (the entries there have been read)
+    load_lds4(rsrc4(p.map + x.row0, (uint64_t)x.rows * 4), ldsm, 4 * (32 * w + lane()));
+  };
+  // the loads go on with tile ln (its map entries have landed: they are older
+  // than a slab that has been waited for)
   auto bind = [&]() __attribute__((always_inline)) {
-    const Tile m = ahead;
-    const int l = lane();
     ls = 0;
-    if (lt >= t_end) {
+    if (ln >= n_my) {
       ra = rsrc4(p.a, 0);
       rb = ra;
-      return m;
+      return;
     }
+    const Tile m = tile(ln);
+    const int l = lane();
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
       const int r = 32 * w + 8 * t + (l >> 3);
@@ -181,9 +169,8 @@ __global__ void __launch_bounds__(t16::NT, 1) k_bf16_tile(Bf16Args p, int cap, u
         if (!TR && cb(t, l) >= K / 8) vob[t] = OOB;
       }
     }
-    lt += stride;
-    prefetch();
-    return m;
+    ++ln;
+    fetch_map(ln);
   };
   // this wave's loads of a slab, four of each operand.  (Their offsets stay in
   // registers of their own: one that is written again for the next load waits
@@ -204,7 +191,7 @@ __global__ void __launch_bounds__(t16::NT, 1) k_bf16_tile(Bf16Args p, int cap, u
       const uint32_t left = rb[2] > BK * ldb ? rb[2] - BK * ldb : 0;
       rb = rsrc4(reinterpret_cast<const void*>(base), left);
     }
-    if (8 * ls + 8 > K / 8 && 8 * ls < K / 8 + 8) {
+    if (8 * ls + 8 > K / 8 && 8 * ls < K / 8) {
 #pragma unroll
       for (int t = 0; t < 4; ++t) {
         if (8 * ls + ca(t, l) >= K / 8) voa[t] = OOB;
@@ -238,7 +225,6 @@ __global__ void __launch_bounds__(t16::NT, 1) k_bf16_tile(Bf16Args p, int cap, u
       f = *reinterpret_cast<const bf16x8*>(ring + st + lb[h] + 4096 * pb + 512 * b);
     }
   };
-
   auto barrier = [&]() __attribute__((always_inline)) {
     __builtin_amdgcn_sched_barrier(0);
     __builtin_amdgcn_s_waitcnt(WAIT_LGKM0);
@@ -247,94 +233,132 @@ __global__ void __launch_bounds__(t16::NT, 1) k_bf16_tile(Bf16Args p, int cap, u
     asm volatile("" ::: "memory");
   };
 
-  prefetch();
-  __builtin_amdgcn_s_waitcnt(wait_vm(0));
-  Tile cur = bind();
-#pragma unroll
-  for (int t = 0; t < 4; ++t) {
-    load_a(t, 0);
-    load_b(t, 0);
-  }
-  advance();
-  __builtin_amdgcn_s_waitcnt(wait_vm(0));
-  barrier();
-  if (grp) barrier();
-
-  uint32_t gs = 0;       // the slab's place in the ring
-  for (uint32_t ct = t_begin; ct < t_end; ct += stride) {
-    const Tile m = cur;
-    const int mb = m.mb;
-    f32x4 acc[4][8];
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int n = 0; n < 8; ++n) acc[i][n] = f32x4{};
+  // -------------------------------------------------------- batches of tiles
+  for (uint32_t j0 = 0;; j0 += NT) {
     {
-      const int li = lane() & 15, q = lane() >> 4;
-#pragma unroll
-      for (int h = 0; h < 2; ++h) la[h] = (16 * mb * wm + li) * 128 + 16 * ((4 * h + q) ^ (li >> 1));
-    }
-    bf16x8 fa[4], fb[8];
-    auto reads = [&](int h) __attribute__((always_inline)) {
-      const uint32_t st = gs * STAGE;
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        frag_b(fb[i], i, h, st);
-        if (i < 4) frag_a(fa[i], i, h, st);
+      const uint32_t J = (j0 + tid) * stride + blockIdx.x / 8, c = J / chunk, t = (c * 8 + xcd) * chunk + (J - c * chunk);
+      Tile x{0, 0, 0, 0};
+      if (t < total) {
+        const uint32_t g = t / gsz, r = t - g * gsz, gm = n_mt - g * GM < GM ? n_mt - g * GM : GM;
+        x.nt = r / gm;
+        const uint32_t mi = g * GM + (r - x.nt * gm);
+        // the last expert e with s_first[e] <= mi (experts without tiles share their successor's)
+        int lo = 0, hi = E;
+        while (hi - lo > 1) {
+          const int mid = (lo + hi) / 2;
+          if (s_first[mid] <= mi) lo = mid;
+          else hi = mid;
+        }
+        x.e = lo;
+        x.row0 = s_off[lo] + (int32_t)((mi - s_first[lo]) << cap);
+        const int32_t n = s_off[lo + 1] - x.row0;
+        x.rows = n < (1 << cap) ? n : 1 << cap;
       }
-    };
-    auto mfmas = [&]() __attribute__((always_inline)) {
-      __builtin_amdgcn_s_setprio(1);
+      s_tile[tid] = x;
+      n_my = __syncthreads_count(t < total);
+    }
+    if (n_my == 0) break;
+    ln = 0;
+    fetch_map(0);
+    __builtin_amdgcn_s_waitcnt(wait_vm(0));
+    bind();
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      load_a(t, 0);
+      load_b(t, 0);
+    }
+    advance();
+    __builtin_amdgcn_s_waitcnt(wait_vm(0));
+    barrier();
+    // The two groups of waves take turns: one runs the MFMAs of half a slab
+    // while the other reads its fragments of the next half and requests the
+    // slab after, a barrier between the turns.  Group 1 is a turn behind.
+    if (grp) barrier();
+    uint32_t gs = 0;       // the slab's place in the ring
+    for (uint32_t ct = 0; ct < n_my; ++ct) {
+      const Tile m = tile(ct);
+      const int mb = (m.rows + 63) / 64;   // blocks of 16 rows of a wave
+      f32x4 acc[4][8];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int n = 0; n < 8; ++n) acc[i][n] = f32x4{};
+      {
+        const int li = lane() & 15, q = lane() >> 4;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) la[h] = (16 * mb * wm + li) * 128 + 16 * ((4 * h + q) ^ (li >> 1));
+      }
+      bf16x8 fa[4], fb[8];
+      auto reads = [&](int h) __attribute__((always_inline)) {
+        const uint32_t st = gs * STAGE;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          frag_b(fb[i], i, h, st);
+          if (i < 4) frag_a(fa[i], i, h, st);
+        }
+      };
+      // the turn's barrier comes four MFMAs before its end: the other group's
+      // first ones then follow without a gap
+      auto mfmas = [&](bool bar) __attribute__((always_inline)) {
+        __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+        for (int i = 3; i >= 0; --i) {
+          if (i < mb) {
+#pragma unroll
+            for (int n = 0; n < (i ? 8 : 4); ++n) acc[i][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[n], fa[i], acc[i][n], 0, 0, 0);
+          }
+        }
+        if (bar) barrier();
+#pragma unroll
+        for (int n = 4; n < 8; ++n) acc[0][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[n], fa[0], acc[0][n], 0, 0, 0);
+        __builtin_amdgcn_s_setprio(0);
+      };
+      for (uint32_t s = 0; s < nk; ++s) {
+        // the next slab's loads must have landed before the end of group 1's
+        // second reading turn, which is group 0's second turn at the MFMAs
+        if (s == nk - 1) bind();
+        reads(0);
+#pragma unroll
+        for (int t = 0; t < 4; ++t) {
+          load_a(t, 1 - gs);
+          load_b(t, 1 - gs);
+        }
+        advance();
+        barrier();
+        mfmas(true);
+        reads(1);
+        if (grp) __builtin_amdgcn_s_waitcnt(wait_vm(0));
+        barrier();
+        if (!grp) __builtin_amdgcn_s_waitcnt(wait_vm(0));
+        // (the last turn of the tile: group 1 stores its results before the
+        // barrier, while group 0 stores its own behind it)
+        mfmas(!(grp && s == nk - 1));
+        gs = 1 - gs;
+      }
+      const Bf16Epilogue<MODE, OUT_BF16> epi(p, m.e, m.row0, m.rows);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         if (i < mb) {
+          const int li = lane() & 15, q = lane() >> 4, r = 16 * mb * wm + 16 * i + li;
+          const float sc = (MODE == DGRAD || MODE == GDGRAD) && r < m.rows ? row_scale(p.scale, p.map, (int64_t)m.row0 + r, p.a_rows * p.div) : 1.0f;
 #pragma unroll
-          for (int n = 0; n < 8; ++n) acc[i][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[n], fa[i], acc[i][n], 0, 0, 0);
+          for (int pb = 0; pb < (MODE == GATED ? 2 : 4); ++pb) {
+            const uint32_t n = m.nt * NW + (MODE == GATED ? 64 : 128) * wn + 32 * pb + 8 * q;
+            const f32x4 x = acc[i][2 * pb], y = acc[i][2 * pb + 1];
+            const f32x4 x1 = acc[i][MODE == GATED ? 2 * pb + 4 : 0], y1 = acc[i][MODE == GATED ? 2 * pb + 5 : 0];
+            const float z[8] = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
+            const float z1[8] = {x1[0], x1[1], x1[2], x1[3], y1[0], y1[1], y1[2], y1[3]};
+            epi.template put<8>(r, n, sc, z, z1);
+            __builtin_amdgcn_sched_barrier(0);
+          }
         }
       }
-      __builtin_amdgcn_s_setprio(0);
-    };
-    for (uint32_t s = 0; s < nk; ++s) {
-      if (s == nk - 1) cur = bind();
-      reads(0);
-#pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        load_a(t, 1 - gs);
-        load_b(t, 1 - gs);
-      }
-      advance();
-      barrier();
-      mfmas();
-      barrier();
-      reads(1);
-      if (grp) __builtin_amdgcn_s_waitcnt(wait_vm(0));
-      barrier();
-      mfmas();
-      if (!grp) __builtin_amdgcn_s_waitcnt(wait_vm(0));
-      barrier();
-      gs = 1 - gs;
+      if (grp) barrier();
     }
-    const Bf16Epilogue<MODE, OUT_BF16> epi(p, m.e, m.row0, m.rows);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      if (i < mb) {
-        const int li = lane() & 15, q = lane() >> 4, r = 16 * mb * wm + 16 * i + li;
-        const float sc = (MODE == DGRAD || MODE == GDGRAD) && r < m.rows ? row_scale(p.scale, p.map, (int64_t)m.row0 + r, p.a_rows * p.div) : 1.0f;
-#pragma unroll
-        for (int pb = 0; pb < (MODE == GATED ? 2 : 4); ++pb) {
-          const uint32_t n = m.nt * NW + (MODE == GATED ? 64 : 128) * wn + 32 * pb + 8 * q;
-          const f32x4 x = acc[i][2 * pb], y = acc[i][2 * pb + 1];
-          const f32x4 x1 = acc[i][MODE == GATED ? 2 * pb + 4 : 0], y1 = acc[i][MODE == GATED ? 2 * pb + 5 : 0];
-          const float z[8] = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
-          const float z1[8] = {x1[0], x1[1], x1[2], x1[3], y1[0], y1[1], y1[2], y1[3]};
-          epi.template put<8>(r, n, sc, z, z1);
-          __builtin_amdgcn_sched_barrier(0);
-        }
-      }
-    }
+    if (!grp) barrier();
+    __builtin_amdgcn_s_waitcnt(wait_vm(0));   // (no load into this workgroup's LDS outlives it)
+    __syncthreads();
   }
-  if (!grp) barrier();
-  __builtin_amdgcn_s_waitcnt(wait_vm(0));   // (no load into this workgroup's LDS outlives it)
 }
 
 static int cu_count() {
@@ -357,9 +381,8 @@ static int launch_bf16(const Bf16Args& p, void* stream, const char* name) {
   const int cus = cu_count() / 8 * 8 < 8 ? 8 : cu_count() / 8 * 8;
   int cap = 8;   // log2 of a tile's most rows
   while (cap > 6 && ((p.M >> cap) + (p.M < p.E ? p.M : p.E)) * nt < cus) --cap;
-  const uint32_t gsz = (uint32_t)(t16::GM * nt), magic = gsz <= 1 ? 0xFFFFFFFFu : (uint32_t)(((uint64_t)1 << 32) / gsz);
   MOE4_REQUIRE(((p.M >> cap) + p.E) * nt < ((int64_t)1 << 31), MOE4_EINVAL, std::string(name) + ": too large");
-  hipLaunchKernelGGL((k_bf16_tile<MODE, OUT_BF16>), dim3((unsigned)cus), dim3(NT), 0, as_stream(stream), p, cap, (uint32_t)nt, gsz, magic);
+  hipLaunchKernelGGL((k_bf16_tile<MODE, OUT_BF16>), dim3((unsigned)cus), dim3(NT), 0, as_stream(stream), p, cap, (uint32_t)nt);
   return check_launch(name);
 }
 
