@@ -9,6 +9,7 @@ namespace t16 {
 constexpr int NT = 512;                      // eight waves of 64 x 128, 4 x 2
 constexpr int TM = 256, TN = 256, BK = 64;   // tile, contraction slab
 constexpr int HALF = 256 * BK * 2, STAGE = 2 * HALF, RING = 2 * STAGE;   // two slabs
+constexpr int MAX_E = 2048;                  // experts (their offsets are kept in LDS)
 constexpr uint32_t OOB = 0x80000000u;        // past every descriptor: zeros arrive
 typedef __attribute__((address_space(3))) uint8_t* lds_u8;
 typedef short s16x4 __attribute__((ext_vector_type(4)));
@@ -44,4 +45,8 @@ __device__ __forceinline__ void load_lds4(const u32x4& rs, uint32_t lds, uint32_
 }
 
 }  // namespace t16
+
+// Workgroups of the persistent kernels: the current device's CUs, a multiple of 8.
+int tile_grid();
+
 }  // namespace moe4

@@ -14,7 +14,6 @@ template <int N>
 using Int = std::integral_constant<int, N>;
 
 namespace t16 {
-constexpr int MAX_E = 2048;
 constexpr int GM = 4;            // m-tiles of a group (see tile order)
 }  // namespace t16
 
@@ -361,14 +360,14 @@ __global__ void __launch_bounds__(t16::NT, 1) k_bf16_tile(Bf16Args p, int cap, u
   }
 }
 
-static int cu_count() {
+int tile_grid() {
   static int n[64] = {0};
   int dev = 0;
   if (hipGetDevice(&dev) != hipSuccess || dev < 0 || dev >= 64) return 256;
   if (n[dev] == 0) {
     int v = 0;
     if (hipDeviceGetAttribute(&v, hipDeviceAttributeMultiprocessorCount, dev) != hipSuccess || v <= 0) v = 256;
-    n[dev] = v;
+    n[dev] = v < 8 ? 8 : v / 8 * 8;
   }
   return n[dev];
 }
@@ -378,7 +377,7 @@ static int launch_bf16(const Bf16Args& p, void* stream, const char* name) {
   using namespace t16;
   constexpr int NW = MODE == GATED ? TN / 2 : TN;
   const int64_t nt = (p.N + NW - 1) / NW;
-  const int cus = cu_count() / 8 * 8 < 8 ? 8 : cu_count() / 8 * 8;
+  const int cus = tile_grid();
   int cap = 8;   // log2 of a tile's most rows
   while (cap > 6 && ((p.M >> cap) + (p.M < p.E ? p.M : p.E)) * nt < cus) --cap;
   MOE4_REQUIRE(((p.M >> cap) + p.E) * nt < ((int64_t)1 << 31), MOE4_EINVAL, std::string(name) + ": too large");

@@ -1,84 +1,301 @@
 // Weight gradients of the BF16 expert products (gfx950): per expert
 // dw = dy^T a over its rows (v_mfma_f32_16x16x32_bf16, float32 accumulation),
 // and the column sums of dy for the bias.
-#include "bf16_gemm.h"
+#include "bf16_tile.h"
 
 namespace moe4 {
 
 static __device__ uint32_t g_dev_err;
 uint32_t take_dev_err_gemm_bf16_wgrad() { return take_device_word(&g_dev_err); }
 
-namespace b16w {
-constexpr int BN = 64, BK = 64, BR = 32, LD = BR + 8;
+// A tile of an expert's gradient: n-tile nt (of dy's columns), k-tile kt (of a's).
+struct WTile {
+  int32_t e, nt, kt, unused;
+};
+
+// The tiled products' structure (gemm_bf16.hip) with the rows as the
+// contraction: a slab is 64 rows of both operands, 512 bytes of each, read
+// transposed from LDS.  With a map each wave makes its eight rows' offsets of a
+// slab from eight scalar loads.  order: the experts are visited in steps of
+// `order` (coprime to E), so that popular and rare ones, whose tiles multiply
+// and store in different proportions, run side by side.
+__global__ void __launch_bounds__(t16::NT, 1) k_bf16_wgrad(Bf16Wgrad p, uint32_t n_nt, uint32_t n_kt, uint32_t order) {
+  using namespace t16;
+  __shared__ __attribute__((aligned(16))) uint8_t ring[RING];
+  __shared__ __attribute__((aligned(16))) WTile s_tile[NT];   // this workgroup's next tiles
+  __shared__ int32_t s_off[MAX_E + 1];                   // the experts' first rows, clamped
+  const int tid = threadIdx.x, l = tid & 63, li = l & 15, q = l >> 4;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6), wm = w >> 1, wn = w & 1, grp = w >> 2;
+  const uint32_t lds0 = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_u8)ring);
+  const int E = p.E;
+  const int32_t M = (int32_t)p.M;
+  for (int e = tid; e <= E; e += NT) {
+    const int32_t o = p.off[e];
+    s_off[e] = o < 0 ? 0 : (o < M ? o : M);
+  }
+  __syncthreads();
+  const uint32_t per_e = n_nt * n_kt, total = per_e * E, xcd = blockIdx.x % 8, stride = gridDim.x / 8;
+  const uint32_t chunk = total >= 16 * per_e ? per_e : (total + gridDim.x - 1) / gridDim.x;
+  const uint32_t N = (uint32_t)p.N, K = (uint32_t)p.K, ldd = N * 2, lda = K * 2;
+  auto lane = [&]() __attribute__((always_inline)) {   // (kept from the optimiser, as in gemm_bf16.hip)
+    int x = l;
+    asm volatile("" : "+v"(x));
+    return x;
+  };
+  auto rows_of = [&](int e) __attribute__((always_inline)) {
+    const int32_t n = s_off[e + 1] - s_off[e];
+    return n > 0 ? n : 0;
+  };
+
+  // ------------------------------------------------------------- load stream
+  uint32_t ln = 0, n_my = 0;
+  int32_t lr = 0, lr1 = 0;           // the next slab's first row, the expert's last
+  u32x4 rd, ra;
+  uint32_t vod[4], voa[4];
+  int32_t md[8], ma[8];              // the next slab's map entries of this wave's rows
+  auto tile = [&](uint32_t i) __attribute__((always_inline)) {
+    const WTile x = s_tile[i];
+    return WTile{__builtin_amdgcn_readfirstlane(x.e), __builtin_amdgcn_readfirstlane(x.nt), __builtin_amdgcn_readfirstlane(x.kt), 0};
+  };
+  auto chunk_of = [&](int t, int l) __attribute__((always_inline)) { return (uint32_t)(l & 31) ^ (4 * ((2 * t + (l >> 5)) & 3)); };
+  auto fetch = [&](int32_t r) __attribute__((always_inline)) {   // entries of rows r ..
+#pragma unroll
+    for (int x = 0; x < 8; ++x) {
+      const int32_t i = r + x < M ? r + x : M - 1;
+      if (p.dy_map) md[x] = ld_const(p.dy_map, i);
+      if (p.a_map) ma[x] = ld_const(p.a_map, i);
+    }
+  };
+  // a mapped operand's offsets of this wave's rows of the slab from row r on
+  auto gather = [&](uint32_t (&vo)[4], const int32_t (&m)[8], int32_t r, uint32_t rows, uint32_t ld, uint32_t c0, uint32_t cols) __attribute__((always_inline)) {
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      uint32_t o[2];
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const int x = 2 * t + h;
+        const uint32_t row = udiv_magic((uint32_t)m[x], p.div, p.magic);
+        const bool in = r + x < lr1, ok = m[x] >= 0 && row < rows;
+        if (in && !ok) atomicOr(&g_dev_err, MOE4_DEVERR_INDEX);
+        o[h] = in && ok ? row * ld : OOB;
+      }
+      const uint32_t c = c0 + 8 * chunk_of(t, l);
+      vo[t] = c < cols ? (l < 32 ? o[0] : o[1]) + 2 * c : OOB;
+    }
+  };
+  uint32_t n0 = 0, k0 = 0;
+  auto set_rows = [&]() __attribute__((always_inline)) {   // the operands at slab lr
+    const int32_t left = lr1 - lr, r = lr + 8 * w;
+    if (p.dy_map) gather(vod, md, r, (uint32_t)p.dy_rows, ldd, n0, N);
+    else rd = rsrc4(p.dy + (int64_t)lr * p.N, left > 0 ? (uint64_t)left * ldd : 0);
+    if (p.a_map) gather(voa, ma, r, (uint32_t)p.a_rows, lda, k0, K);
+    else ra = rsrc4(p.a + (int64_t)lr * p.K, left > 0 ? (uint64_t)left * lda : 0);
+    fetch(r + BK);
+  };
+  // the loads go on with tile ln, passing over those of experts without rows
+  auto bind = [&]() __attribute__((always_inline)) {
+    WTile x{0, 0, 0, 0};
+    while (ln < n_my) {
+      x = tile(ln);
+      if (__builtin_amdgcn_readfirstlane(rows_of(x.e)) > 0) break;
+      ++ln;
+    }
+    if (ln >= n_my) {   // (descriptors of nothing: every slab has as many loads)
+      rd = rsrc4(p.dy, 0);
+      ra = rd;
+      lr = lr1 = -1;
+      return;
+    }
+    ++ln;
+    const int l = lane();
+    lr = __builtin_amdgcn_readfirstlane(s_off[x.e]);
+    lr1 = __builtin_amdgcn_readfirstlane(s_off[x.e + 1]);
+    n0 = x.nt * TM;
+    k0 = x.kt * TN;
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      const uint32_t c = chunk_of(t, l), k = 8 * w + 2 * t + (l >> 5);
+      if (!p.dy_map) vod[t] = n0 + 8 * c < N ? k * ldd + 2 * n0 + 16 * c : OOB;
+      if (!p.a_map) voa[t] = k0 + 8 * c < K ? k * lda + 2 * k0 + 16 * c : OOB;
+    }
+    if (p.dy_map) rd = rsrc4(p.dy, (uint64_t)p.dy_rows * ldd);
+    if (p.a_map) ra = rsrc4(p.a, (uint64_t)p.a_rows * lda);
+    fetch(lr + 8 * w);
+    set_rows();
+  };
+  auto loads = [&](uint32_t stage) __attribute__((always_inline)) {
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      load_lds(rd, lds0 + stage * STAGE + (4 * w + t) * 1024, vod[t], 0);
+      load_lds(ra, lds0 + stage * STAGE + HALF + (4 * w + t) * 1024, voa[t], 0);
+    }
+  };
+  auto advance = [&]() __attribute__((always_inline)) {
+    if (lr < 0) return;
+    lr += BK;
+    if (lr < lr1) set_rows();
+  };
+
+  // --------------------------------------------------------------- fragments
+  uint32_t lb[4];          // the lane's offset for each pair of B's blocks
+  {
+    const int j = li >> 2, s = li & 3;
+#pragma unroll
+    for (int pb = 0; pb < 4; ++pb) lb[pb] = HALF + (8 * q + j) * 512 + 16 * (16 * wn + 4 * (pb ^ j) + s);
+  }
+  typedef __attribute__((address_space(3))) s16x4* lp;
+  auto read_tr = [&](bf16x8& f, uint32_t at) __attribute__((always_inline)) {
+    const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)(lds_u8)(ring + at));
+    const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)(lds_u8)(ring + at + 2048));
+    f = __builtin_bit_cast(bf16x8, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
+  };
+  auto barrier = [&]() __attribute__((always_inline)) {
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_waitcnt(WAIT_LGKM0);
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+    asm volatile("" ::: "memory");
+  };
+
+  for (uint32_t j0 = 0;; j0 += NT) {
+    {
+      const uint32_t J = (j0 + tid) * stride + blockIdx.x / 8, c = J / chunk, t = (c * 8 + xcd) * chunk + (J - c * chunk);
+      WTile x{0, 0, 0, 0};
+      if (t < total) {
+        const uint32_t i = t / per_e, r = t - i * per_e;
+        x.e = (int32_t)((uint64_t)i * order % (uint32_t)E);
+        x.nt = r / n_kt;
+        x.kt = r - x.nt * n_kt;
+      }
+      s_tile[tid] = x;
+      n_my = __syncthreads_count(t < total);
+    }
+    if (n_my == 0) break;
+    ln = 0;
+    bind();
+    loads(0);
+    advance();
+    bool fresh = lr >= lr1;   // the next slab to load is a new tile's
+    __builtin_amdgcn_s_waitcnt(wait_vm(0));
+    barrier();
+    if (grp) barrier();
+    uint32_t gs = 0;       // the slab's place in the ring
+    for (uint32_t ct = 0; ct < n_my; ++ct) {
+      const WTile m = tile(ct);
+      const int32_t rows = __builtin_amdgcn_readfirstlane(rows_of(m.e));
+      const uint32_t nk = ((uint32_t)rows + BK - 1) / BK;
+      if (nk == 0 && (p.beta != 0.0f || !p.zero_empty)) continue;
+      const uint32_t tn = N - m.nt * TM < TM ? N - m.nt * TM : TM;
+      const int mb = (int)((tn + 63) / 64);   // blocks of 16 of a wave
+      f32x4 acc[4][8];
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int n = 0; n < 8; ++n) acc[i][n] = f32x4{};
+      uint32_t ao[4];   // and for A's blocks: chunks 2 mb wm + 2 i and + 1 of the row
+      {
+        const int x = lane() & 15, q = lane() >> 4, j = x >> 2, s = x & 3;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) ao[i] = (8 * q + j) * 512 + 8 * (s & 1) + 16 * ((2 * mb * wm + 2 * i + (s >> 1)) ^ (4 * j));
+      }
+      bf16x8 fa[4], fb[8];
+      auto reads = [&](int h) __attribute__((always_inline)) {
+        const uint32_t st = gs * STAGE + 16384 * h;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          read_tr(fb[i], st + lb[i >> 1] + 8 * (i & 1));
+          if (i < 4) read_tr(fa[i], st + ao[i]);
+        }
+      };
+      auto mfmas = [&](bool bar) __attribute__((always_inline)) {
+        __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+        for (int i = 3; i >= 0; --i) {
+          if (i < mb) {
+#pragma unroll
+            for (int n = 0; n < (i ? 8 : 4); ++n) acc[i][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[n], fa[i], acc[i][n], 0, 0, 0);
+          }
+        }
+        if (bar) barrier();
+#pragma unroll
+        for (int n = 4; n < 8; ++n) acc[0][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[n], fa[0], acc[0][n], 0, 0, 0);
+        __builtin_amdgcn_s_setprio(0);
+      };
+      for (uint32_t s = 0; s < nk; ++s) {
+        if (fresh) bind();
+        reads(0);
+        loads(1 - gs);
+        advance();
+        fresh = lr >= lr1;
+        barrier();
+        mfmas(true);
+        reads(1);
+        if (grp) __builtin_amdgcn_s_waitcnt(wait_vm(0));
+        barrier();
+        if (!grp) __builtin_amdgcn_s_waitcnt(wait_vm(0));
+        mfmas(!(grp && s == nk - 1));
+        gs = 1 - gs;
+      }
+      const int64_t row0 = (int64_t)m.e * p.N + (int64_t)m.nt * TM;
+      const __amdgpu_buffer_rsrc_t rc = make_rsrc(p.dw + row0 * p.K, (uint64_t)tn * K * 4);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (i < mb) {
+          const int li = lane() & 15, q = lane() >> 4;
+          const uint32_t r = 16 * mb * wm + 16 * i + li;
+#pragma unroll
+          for (int pb = 0; pb < 4; ++pb) {
+            const uint32_t k = m.kt * TN + 128 * wn + 32 * pb + 8 * q, o = k < K ? r * K + k : PAST;
+            const f32x4 x = acc[i][2 * pb], y = acc[i][2 * pb + 1];
+            float z[8] = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
+            if (p.beta != 0.0f) {
+              float v[8];
+              load_f32<8>(rc, o, v);
+#pragma unroll
+              for (int n = 0; n < 8; ++n) z[n] = v[n] + z[n];
+            }
+            store_f32<8>(rc, o, z);
+          }
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      }
+      if (grp && nk) barrier();
+    }
+    if (!grp) barrier();
+    __builtin_amdgcn_s_waitcnt(wait_vm(0));   // (no load into this workgroup's LDS outlives it)
+    __syncthreads();
+  }
 }
 
-__global__ void __launch_bounds__(256) k_wgrad_bf16(Bf16Wgrad p) {
-  using namespace b16w;
-  __shared__ __attribute__((aligned(16))) uint16_t as[BN * LD], bs[BK * LD];
-  const int e = blockIdx.z;
-  const int tid = threadIdx.x, l = tid & 63, li = l & 15, q = l >> 4, w = tid >> 6;
-  const int64_t n0 = (int64_t)blockIdx.y * BN, k0 = (int64_t)blockIdx.x * BK;
+// db: 64 columns of one expert per workgroup, eight a thread; thread row y sums
+// rows y, y + 128, ... in order, then the 128 sums are added in order.
+__global__ void __launch_bounds__(1024) k_bias_grad_bf16(Bf16Wgrad p) {
+  __shared__ float s[128][65];
+  const int e = blockIdx.y, cx = threadIdx.x & 7, y = threadIdx.x >> 3;
+  const int64_t n = (int64_t)blockIdx.x * 64 + 8 * cx;
   int64_t r0 = p.off[e], r1 = p.off[e + 1];
   r0 = r0 < 0 ? 0 : r0;
   r1 = r1 < p.M ? r1 : p.M;
   if (r0 >= r1 && (p.beta != 0.0f || !p.zero_empty)) return;
-  f32x4 acc[4];
+  float v[8] = {};
+  if (n < p.N)
+    for (int64_t r = r0 + y; r < r1; r += 128) {
+      const int64_t rd = mapped_row(p.dy_map, r, p.div, p.magic, p.dy_rows, &g_dev_err);
+      if (rd < 0) continue;
+      const u32x4 q = *reinterpret_cast<const u32x4*>(p.dy + rd * p.N + n);
+      const float sc = row_scale(p.db_scale, p.dy_map, r, p.dy_rows * p.div);
 #pragma unroll
-  for (int b = 0; b < 4; ++b) acc[b] = f32x4{};
-  for (int64_t r = r0; r < r1; r += BR) {
-    __syncthreads();
-    const int64_t row = r + tid / 8;
-    const int c = 8 * (tid % 8);
-    u32x4 v = {}, x = {};
-    if (row < r1) {
-      const int64_t rd = mapped_row(p.dy_map, row, p.div, p.magic, p.dy_rows, &g_dev_err);
-      const int64_t ra = mapped_row(p.a_map, row, p.div, p.magic, p.a_rows, &g_dev_err);
-      if (rd >= 0 && n0 + c < p.N) v = *reinterpret_cast<const u32x4*>(p.dy + rd * p.N + n0 + c);
-      if (ra >= 0 && k0 + c < p.K) x = *reinterpret_cast<const u32x4*>(p.a + ra * p.K + k0 + c);
+      for (int i = 0; i < 8; ++i) v[i] = v[i] + sc * bf16_bits_to_f32((i & 1) ? q[i / 2] >> 16 : q[i / 2] & 0xFFFFu);
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      as[(c + i) * LD + tid / 8] = (uint16_t)(v[i / 2] >> (16 * (i & 1)));
-      bs[(c + i) * LD + tid / 8] = (uint16_t)(x[i / 2] >> (16 * (i & 1)));
-    }
-    __syncthreads();
-    const bf16x8 fa = *reinterpret_cast<const bf16x8*>(as + (16 * w + li) * LD + 8 * q);
-#pragma unroll
-    for (int b = 0; b < 4; ++b) {
-      const bf16x8 fb = *reinterpret_cast<const bf16x8*>(bs + (16 * b + li) * LD + 8 * q);
-      acc[b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb, fa, acc[b], 0, 0, 0);
-    }
-  }
-  const int64_t n = n0 + 16 * w + li;
-  if (n >= p.N) return;
-#pragma unroll
-  for (int b = 0; b < 4; ++b) {
-    const int64_t k = k0 + 16 * b + 4 * q;
-    if (k >= p.K) continue;
-    float* d = p.dw + ((int64_t)e * p.N + n) * p.K + k;
-    f32x4 v = acc[b];
-    if (p.beta != 0.0f) v = *reinterpret_cast<const f32x4*>(d) + v;
-    *reinterpret_cast<f32x4*>(d) = v;
-  }
-}
-
-// db: one wave per 64 columns of one expert, its rows in order.
-__global__ void __launch_bounds__(64) k_bias_grad_bf16(Bf16Wgrad p) {
-  const int e = blockIdx.y;
-  const int64_t n = (int64_t)blockIdx.x * 64 + threadIdx.x;
-  int64_t r0 = p.off[e], r1 = p.off[e + 1];
-  r0 = r0 < 0 ? 0 : r0;
-  r1 = r1 < p.M ? r1 : p.M;
-  if (n >= p.N || (r0 >= r1 && (p.beta != 0.0f || !p.zero_empty))) return;
-  float s = 0.0f;
-  for (int64_t r = r0; r < r1; ++r) {
-    const int64_t rd = mapped_row(p.dy_map, r, p.div, p.magic, p.dy_rows, &g_dev_err);
-    if (rd < 0) continue;
-    const float v = bf16_bits_to_f32(p.dy[rd * p.N + n]);
-    s = s + row_scale(p.db_scale, p.dy_map, r, p.dy_rows * p.div) * v;
-  }
-  float* d = p.db + (int64_t)e * p.N + n;
-  *d = p.beta != 0.0f ? *d + s : s;
+  for (int i = 0; i < 8; ++i) s[y][8 * cx + i] = v[i];
+  __syncthreads();
+  const int64_t c = (int64_t)blockIdx.x * 64 + threadIdx.x;
+  if (threadIdx.x >= 64 || c >= p.N) return;
+  float t = 0.0f;
+  for (int i = 0; i < 128; ++i) t = t + s[i][threadIdx.x];
+  float* d = p.db + (int64_t)e * p.N + c;
+  *d = p.beta != 0.0f ? *d + t : t;
 }
 
 }  // namespace moe4
@@ -110,8 +327,20 @@ extern "C" int moe_grouped_gemm_bf16_wgrad(const uint16_t* dy, int64_t dy_rows, 
   const Bf16Wgrad p{dy, a, dy_map, a_map, expert_off, db_scale, dw, db, dy_rows, a_rows, M_total, N, K, (uint32_t)map_div, magic, E, beta,
                     (flags & MOE4_WGRAD_SKIP_EMPTY) == 0};
   hipStream_t st = as_stream(stream);
-  const int64_t nx = (K + 63) / 64, ny = (N + 63) / 64;
-  hipLaunchKernelGGL(k_wgrad_bf16, dim3((unsigned)nx, (unsigned)ny, (unsigned)E), dim3(256), 0, st, p);
-  if (db) hipLaunchKernelGGL(k_bias_grad_bf16, dim3((unsigned)ny, (unsigned)E), dim3(64), 0, st, p);
+  const int64_t nt = (N + t16::TM - 1) / t16::TM, kt = (K + t16::TN - 1) / t16::TN;
+  MOE4_REQUIRE(nt * kt * E < ((int64_t)1 << 31), MOE4_EINVAL, s + ": too large");
+  // a step through the experts near the golden section of E, coprime to it
+  uint32_t order = (uint32_t)(0.618 * E);
+  const auto gcd = [](uint32_t a, uint32_t b) {
+    while (b) {
+      const uint32_t c = a % b;
+      a = b;
+      b = c;
+    }
+    return a;
+  };
+  while (order < 1 || gcd(order, (uint32_t)E) != 1) ++order;
+  hipLaunchKernelGGL(k_bf16_wgrad, dim3((unsigned)tile_grid()), dim3(t16::NT), 0, st, p, (uint32_t)nt, (uint32_t)kt, order);
+  if (db) hipLaunchKernelGGL(k_bias_grad_bf16, dim3((unsigned)((N + 63) / 64), (unsigned)E), dim3(1024), 0, st, p);
   return check_launch(s.c_str());
 }
