@@ -30,6 +30,10 @@ __global__ void __launch_bounds__(t16::NT, 1) k_bf16_tile(Bf16Args p, int cap, u
   using namespace t16;
   constexpr bool TR = MODE == DGRAD || MODE == GDGRAD;   // w's columns are the product's: read transposed
   constexpr int NW = MODE == GATED ? TN / 2 : TN;        // the tile's columns
+  // Column of block n, lane quarter q, value v of a wave's 128: with float32
+  // results 16 n + 4 q + v, with bf16 ones 32 (n / 2) + 8 q + 4 (n % 2) + v, so
+  // that four lanes store 64 consecutive bytes of a row either way.
+  constexpr bool PAIR = OUT_BF16;
   __shared__ __attribute__((aligned(16))) uint8_t ring[RING];
   __shared__ __attribute__((aligned(16))) Tile s_tile[NT];   // this workgroup's next tiles
   __shared__ int32_t s_off[MAX_E + 1];                   // the experts' first rows, clamped
@@ -105,7 +109,8 @@ __global__ void __launch_bounds__(t16::NT, 1) k_bf16_tile(Bf16Args p, int cap, u
   // + 8 t + l / 8, slot l % 8; so has B, or with TR k rows 8 w + 2 t + l / 32, slot l % 32
   auto ca = [&](int t, int l) __attribute__((always_inline)) { return (uint32_t)(l & 7) ^ (4 * (t & 1) + (l >> 4)); };
   auto cb = [&](int t, int l) __attribute__((always_inline)) {
-    return TR ? (uint32_t)(l & 31) ^ (4 * ((2 * t + (l >> 5)) & 3)) : (uint32_t)(l & 7) ^ (2 * (t & 3) + ((l >> 4) & 1));
+    if (TR) return (uint32_t)(l & 31) ^ (4 * ((2 * t + (l >> 5)) & 3)) ^ (PAIR ? 0 : 2 * (w & 1));
+    return (uint32_t)(l & 7) ^ (PAIR ? 2 * (t & 3) + ((l >> 4) & 1) : 4 * (t & 1) + (l >> 4));
   };
   auto tile = [&](uint32_t i) __attribute__((always_inline)) {
     const Tile x = s_tile[i];
@@ -200,28 +205,35 @@ __global__ void __launch_bounds__(t16::NT, 1) k_bf16_tile(Bf16Args p, int cap, u
   };
 
   // --------------------------------------------------------------- fragments
-  uint32_t lb[4];    // the lane's offset for each pair of column blocks (!TR: for each half of the slab)
+  // Swizzles (through the chunk that each lane loads): a row's 16-byte chunk c
+  // sits at c ^ x(row) such that the 16 lanes (transposed reads of 32 bytes a row:
+  // 32 lanes) of a fragment read hit different banks.
+  uint32_t lb[4];    // lane offsets of B's fragments: !TR one for each half of the slab, TR PAIR for each pair of blocks, TR one
   uint32_t la[2];    // A: for each half of the slab
   if (TR) {
     const int j = li >> 2, s = li & 3;
+    if (PAIR) {
 #pragma unroll
-    for (int pb = 0; pb < 4; ++pb) lb[pb] = HALF + (8 * q + j) * 512 + 16 * (16 * wn + 4 * (pb ^ j) + s);
+      for (int pb = 0; pb < 4; ++pb) lb[pb] = HALF + (8 * q + j) * 512 + 16 * (16 * wn + 4 * (pb ^ j) + s);
+    } else {
+      lb[0] = HALF + (8 * q + j) * 512 + 16 * (16 * wn + ((s >> 1) ^ (4 * j) ^ (2 * (q & 1)))) + 8 * (s & 1);
+    }
   } else {
 #pragma unroll
-    for (int h = 0; h < 2; ++h) lb[h] = HALF + (128 * wn + 8 * (li >> 2) + (li & 3)) * 128 + 16 * ((4 * h + q) ^ (li >> 1));
+    for (int h = 0; h < 2; ++h) lb[h] = HALF + (128 * wn + (PAIR ? 8 * (li >> 2) + (li & 3) : li)) * 128 + 16 * ((4 * h + q) ^ (li >> 1));
   }
   auto frag_a = [&](bf16x8& f, int i, int h, uint32_t st) __attribute__((always_inline)) {
     f = *reinterpret_cast<const bf16x8*>(ring + st + la[h] + 2048 * i);
   };
   auto frag_b = [&](bf16x8& f, int i, int h, uint32_t st) __attribute__((always_inline)) {
-    const int pb = i >> 1, b = i & 1;
     if (TR) {
       typedef __attribute__((address_space(3))) s16x4* lp;
-      const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)(lds_u8)(ring + st + lb[pb] + 16384 * h + 8 * b));
-      const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)(lds_u8)(ring + st + lb[pb] + 16384 * h + 8 * b + 2048));
+      const uint32_t at = PAIR ? st + lb[i >> 1] + 8 * (i & 1) : (st + lb[0]) ^ (32 * i);
+      const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)(lds_u8)(ring + at + 16384 * h));
+      const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)(lds_u8)(ring + at + 16384 * h + 2048));
       f = __builtin_bit_cast(bf16x8, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
     } else {
-      f = *reinterpret_cast<const bf16x8*>(ring + st + lb[h] + 4096 * pb + 512 * b);
+      f = *reinterpret_cast<const bf16x8*>(ring + st + lb[h] + (PAIR ? 4096 * (i >> 1) + 512 * (i & 1) : 2048 * i));
     }
   };
   auto barrier = [&]() __attribute__((always_inline)) {
@@ -340,15 +352,24 @@ __global__ void __launch_bounds__(t16::NT, 1) k_bf16_tile(Bf16Args p, int cap, u
         if (i < mb) {
           const int li = lane() & 15, q = lane() >> 4, r = 16 * mb * wm + 16 * i + li;
           const float sc = (MODE == DGRAD || MODE == GDGRAD) && r < m.rows ? row_scale(p.scale, p.map, (int64_t)m.row0 + r, p.a_rows * p.div) : 1.0f;
+          if (PAIR) {
 #pragma unroll
-          for (int pb = 0; pb < (MODE == GATED ? 2 : 4); ++pb) {
-            const uint32_t n = m.nt * NW + (MODE == GATED ? 64 : 128) * wn + 32 * pb + 8 * q;
-            const f32x4 x = acc[i][2 * pb], y = acc[i][2 * pb + 1];
-            const f32x4 x1 = acc[i][MODE == GATED ? 2 * pb + 4 : 0], y1 = acc[i][MODE == GATED ? 2 * pb + 5 : 0];
-            const float z[8] = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
-            const float z1[8] = {x1[0], x1[1], x1[2], x1[3], y1[0], y1[1], y1[2], y1[3]};
-            epi.template put<8>(r, n, sc, z, z1);
-            __builtin_amdgcn_sched_barrier(0);
+            for (int pb = 0; pb < (MODE == GATED ? 2 : 4); ++pb) {
+              const uint32_t n = m.nt * NW + (MODE == GATED ? 64 : 128) * wn + 32 * pb + 8 * q;
+              const f32x4 x = acc[i][2 * pb], y = acc[i][2 * pb + 1];
+              const f32x4 x1 = acc[i][MODE == GATED ? 2 * pb + 4 : 0], y1 = acc[i][MODE == GATED ? 2 * pb + 5 : 0];
+              const float z[8] = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
+              const float z1[8] = {x1[0], x1[1], x1[2], x1[3], y1[0], y1[1], y1[2], y1[3]};
+              epi.template put<8>(r, n, sc, z, z1);
+              __builtin_amdgcn_sched_barrier(0);
+            }
+          } else {
+#pragma unroll
+            for (int n = 0; n < 8; ++n) {
+              const float z[4] = {acc[i][n][0], acc[i][n][1], acc[i][n][2], acc[i][n][3]};
+              epi.template put<4>(r, m.nt * NW + 128 * wn + 16 * n + 4 * q, sc, z, z);
+              __builtin_amdgcn_sched_barrier(0);
+            }
           }
         }
       }

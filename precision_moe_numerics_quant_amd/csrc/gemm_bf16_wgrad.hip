@@ -8,15 +8,15 @@ namespace moe4 {
 static __device__ uint32_t g_dev_err;
 uint32_t take_dev_err_gemm_bf16_wgrad() { return take_device_word(&g_dev_err); }
 
-// A tile of an expert's gradient: n-tile nt (of dy's columns), k-tile kt (of a's).
+// A tile of an expert's gradient: n-tile nt (of dy's columns), k-tile kt (of a's;
+// at = nt 2^16 + kt), the expert's rows.
 struct WTile {
-  int32_t e, nt, kt, unused;
+  int32_t e, at, row0, rows;
 };
 
 // The tiled products' structure (gemm_bf16.hip) with the rows as the
 // contraction: a slab is 64 rows of both operands, 512 bytes of each, read
-// transposed from LDS.  With a map each wave makes its eight rows' offsets of a
-// slab from eight scalar loads.  order: the experts are visited in steps of
+// transposed from LDS.  A map's entries come a slab ahead, each lane's four.  order: the experts are visited in steps of
 // `order` (coprime to E), so that popular and rare ones, whose tiles multiply
 // and store in different proportions, run side by side.
 __global__ void __launch_bounds__(t16::NT, 1) k_bf16_wgrad(Bf16Wgrad p, uint32_t n_nt, uint32_t n_kt, uint32_t order) {
@@ -42,85 +42,79 @@ __global__ void __launch_bounds__(t16::NT, 1) k_bf16_wgrad(Bf16Wgrad p, uint32_t
     asm volatile("" : "+v"(x));
     return x;
   };
-  auto rows_of = [&](int e) __attribute__((always_inline)) {
-    const int32_t n = s_off[e + 1] - s_off[e];
-    return n > 0 ? n : 0;
-  };
 
   // ------------------------------------------------------------- load stream
   uint32_t ln = 0, n_my = 0;
-  int32_t lr = 0, lr1 = 0;           // the next slab's first row, the expert's last
+  int32_t lr = 0, left = 0;          // the next slab's first row in its expert, the expert's rows from there
   u32x4 rd, ra;
-  uint32_t vod[4], voa[4];
-  int32_t md[8], ma[8];              // the next slab's map entries of this wave's rows
+  __amdgpu_buffer_rsrc_t rmd = make_rsrc(p.off, 0), rma = rmd;   // the expert's map entries
+  uint32_t vod[4], voa[4], cd[4], ca[4];   // offsets; with a map those of the columns
+  uint32_t md[4], ma[4];             // the next slab's map entries
   auto tile = [&](uint32_t i) __attribute__((always_inline)) {
     const WTile x = s_tile[i];
-    return WTile{__builtin_amdgcn_readfirstlane(x.e), __builtin_amdgcn_readfirstlane(x.nt), __builtin_amdgcn_readfirstlane(x.kt), 0};
+    return WTile{__builtin_amdgcn_readfirstlane(x.e), __builtin_amdgcn_readfirstlane(x.at), __builtin_amdgcn_readfirstlane(x.row0),
+                 __builtin_amdgcn_readfirstlane(x.rows)};
   };
-  auto chunk_of = [&](int t, int l) __attribute__((always_inline)) { return (uint32_t)(l & 31) ^ (4 * ((2 * t + (l >> 5)) & 3)); };
-  auto fetch = [&](int32_t r) __attribute__((always_inline)) {   // entries of rows r ..
+  // the chunk (16 bytes) that lands in this lane's slot l % 32 of load t, row 8 w + 2 t + l / 32 of the slab
+  auto chunk_of = [&](int t, int l) __attribute__((always_inline)) { return (uint32_t)(l & 31) ^ (4 * ((2 * t + (l >> 5)) & 3)) ^ (2 * (w & 1)); };
+  auto fetch = [&](uint32_t (&m)[4], const __amdgpu_buffer_rsrc_t& rs, int32_t r) __attribute__((always_inline)) {   // entries of the slab at row r
 #pragma unroll
-    for (int x = 0; x < 8; ++x) {
-      const int32_t i = r + x < M ? r + x : M - 1;
-      if (p.dy_map) md[x] = ld_const(p.dy_map, i);
-      if (p.a_map) ma[x] = ld_const(p.a_map, i);
-    }
+    for (int t = 0; t < 4; ++t) m[t] = __builtin_amdgcn_raw_buffer_load_b32(rs, 4 * (r + 8 * w + 2 * t + (l >> 5)), 0, 0);
   };
-  // a mapped operand's offsets of this wave's rows of the slab from row r on
-  auto gather = [&](uint32_t (&vo)[4], const int32_t (&m)[8], int32_t r, uint32_t rows, uint32_t ld, uint32_t c0, uint32_t cols) __attribute__((always_inline)) {
+  // a mapped operand's offsets for the next slab
+  auto gather = [&](uint32_t (&vo)[4], const uint32_t (&m)[4], const uint32_t (&c)[4], uint32_t rows, uint32_t ld) __attribute__((always_inline)) {
+    bool bad = false;
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
-      uint32_t o[2];
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const int x = 2 * t + h;
-        const uint32_t row = udiv_magic((uint32_t)m[x], p.div, p.magic);
-        const bool in = r + x < lr1, ok = m[x] >= 0 && row < rows;
-        if (in && !ok) atomicOr(&g_dev_err, MOE4_DEVERR_INDEX);
-        o[h] = in && ok ? row * ld : OOB;
-      }
-      const uint32_t c = c0 + 8 * chunk_of(t, l);
-      vo[t] = c < cols ? (l < 32 ? o[0] : o[1]) + 2 * c : OOB;
+      const uint32_t row = udiv_magic(m[t], p.div, p.magic);
+      const bool in = 8 * w + 2 * t + (l >> 5) < left, ok = (int32_t)m[t] >= 0 && row < rows;
+      bad |= in && !ok;
+      vo[t] = in && ok ? row * ld + c[t] : OOB;
     }
+    if (__any(bad) && l == 0) atomicOr(&g_dev_err, MOE4_DEVERR_INDEX);
   };
-  uint32_t n0 = 0, k0 = 0;
-  auto set_rows = [&]() __attribute__((always_inline)) {   // the operands at slab lr
-    const int32_t left = lr1 - lr, r = lr + 8 * w;
-    if (p.dy_map) gather(vod, md, r, (uint32_t)p.dy_rows, ldd, n0, N);
-    else rd = rsrc4(p.dy + (int64_t)lr * p.N, left > 0 ? (uint64_t)left * ldd : 0);
-    if (p.a_map) gather(voa, ma, r, (uint32_t)p.a_rows, lda, k0, K);
-    else ra = rsrc4(p.a + (int64_t)lr * p.K, left > 0 ? (uint64_t)left * lda : 0);
-    fetch(r + BK);
+  auto set_rows = [&]() __attribute__((always_inline)) {   // the mapped operands at the next slab
+    if (p.dy_map) {
+      gather(vod, md, cd, (uint32_t)p.dy_rows, ldd);
+      fetch(md, rmd, lr + BK);
+    }
+    if (p.a_map) {
+      gather(voa, ma, ca, (uint32_t)p.a_rows, lda);
+      fetch(ma, rma, lr + BK);
+    }
   };
   // the loads go on with tile ln, passing over those of experts without rows
   auto bind = [&]() __attribute__((always_inline)) {
     WTile x{0, 0, 0, 0};
-    while (ln < n_my) {
-      x = tile(ln);
-      if (__builtin_amdgcn_readfirstlane(rows_of(x.e)) > 0) break;
-      ++ln;
+    while (ln < n_my && (x = tile(ln++)).rows == 0) {
     }
-    if (ln >= n_my) {   // (descriptors of nothing: every slab has as many loads)
+    lr = 0;
+    left = x.rows;
+    if (left == 0) {   // (descriptors of nothing: every slab has as many loads)
       rd = rsrc4(p.dy, 0);
       ra = rd;
-      lr = lr1 = -1;
       return;
     }
-    ++ln;
     const int l = lane();
-    lr = __builtin_amdgcn_readfirstlane(s_off[x.e]);
-    lr1 = __builtin_amdgcn_readfirstlane(s_off[x.e + 1]);
-    n0 = x.nt * TM;
-    k0 = x.kt * TN;
+    const uint32_t n0 = (uint32_t)(x.at >> 16) * TM, k0 = (uint32_t)(x.at & 0xFFFF) * TN;
+    rd = p.dy_map ? rsrc4(p.dy, (uint64_t)p.dy_rows * ldd) : rsrc4(p.dy + (int64_t)x.row0 * p.N, (uint64_t)left * ldd);
+    ra = p.a_map ? rsrc4(p.a, (uint64_t)p.a_rows * lda) : rsrc4(p.a + (int64_t)x.row0 * p.K, (uint64_t)left * lda);
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
       const uint32_t c = chunk_of(t, l), k = 8 * w + 2 * t + (l >> 5);
-      if (!p.dy_map) vod[t] = n0 + 8 * c < N ? k * ldd + 2 * n0 + 16 * c : OOB;
-      if (!p.a_map) voa[t] = k0 + 8 * c < K ? k * lda + 2 * k0 + 16 * c : OOB;
+      cd[t] = n0 + 8 * c < N ? 2 * n0 + 16 * c : OOB;
+      ca[t] = k0 + 8 * c < K ? 2 * k0 + 16 * c : OOB;
+      vod[t] = k * ldd + cd[t];
+      voa[t] = k * lda + ca[t];
     }
-    if (p.dy_map) rd = rsrc4(p.dy, (uint64_t)p.dy_rows * ldd);
-    if (p.a_map) ra = rsrc4(p.a, (uint64_t)p.a_rows * lda);
-    fetch(lr + 8 * w);
+    if (p.dy_map) {
+      rmd = make_rsrc(p.dy_map + x.row0, (uint64_t)left * 4);
+      fetch(md, rmd, 0);
+    }
+    if (p.a_map) {
+      rma = make_rsrc(p.a_map + x.row0, (uint64_t)left * 4);
+      fetch(ma, rma, 0);
+    }
     set_rows();
   };
   auto loads = [&](uint32_t stage) __attribute__((always_inline)) {
@@ -130,19 +124,21 @@ __global__ void __launch_bounds__(t16::NT, 1) k_bf16_wgrad(Bf16Wgrad p, uint32_t
       load_lds(ra, lds0 + stage * STAGE + HALF + (4 * w + t) * 1024, voa[t], 0);
     }
   };
+  auto step = [&](u32x4& rs, uint32_t ld) __attribute__((always_inline)) {
+    const uint64_t base = ((uint64_t)rs[1] << 32 | rs[0]) + BK * ld;
+    rs = rsrc4(reinterpret_cast<const void*>(base), (uint64_t)left * ld);
+  };
   auto advance = [&]() __attribute__((always_inline)) {
-    if (lr < 0) return;
     lr += BK;
-    if (lr < lr1) set_rows();
+    left = left > BK ? left - BK : 0;
+    if (!p.dy_map) step(rd, ldd);
+    if (!p.a_map) step(ra, lda);
+    if (left) set_rows();
   };
 
   // --------------------------------------------------------------- fragments
-  uint32_t lb[4];          // the lane's offset for each pair of B's blocks
-  {
-    const int j = li >> 2, s = li & 3;
-#pragma unroll
-    for (int pb = 0; pb < 4; ++pb) lb[pb] = HALF + (8 * q + j) * 512 + 16 * (16 * wn + 4 * (pb ^ j) + s);
-  }
+  // (swizzle and columns as in gemm_bf16.hip's float32 results)
+  const uint32_t lb = HALF + (8 * q + (li >> 2)) * 512 + 16 * (16 * wn + (((li & 3) >> 1) ^ (4 * (li >> 2)) ^ (2 * (q & 1)))) + 8 * (li & 1);
   typedef __attribute__((address_space(3))) s16x4* lp;
   auto read_tr = [&](bf16x8& f, uint32_t at) __attribute__((always_inline)) {
     const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)(lds_u8)(ring + at));
@@ -164,8 +160,10 @@ __global__ void __launch_bounds__(t16::NT, 1) k_bf16_wgrad(Bf16Wgrad p, uint32_t
       if (t < total) {
         const uint32_t i = t / per_e, r = t - i * per_e;
         x.e = (int32_t)((uint64_t)i * order % (uint32_t)E);
-        x.nt = r / n_kt;
-        x.kt = r - x.nt * n_kt;
+        const uint32_t nt = r / n_kt;
+        x.at = (int32_t)(nt << 16 | (r - nt * n_kt));
+        x.row0 = s_off[x.e];
+        x.rows = s_off[x.e + 1] > x.row0 ? s_off[x.e + 1] - x.row0 : 0;
       }
       s_tile[tid] = x;
       n_my = __syncthreads_count(t < total);
@@ -175,17 +173,15 @@ __global__ void __launch_bounds__(t16::NT, 1) k_bf16_wgrad(Bf16Wgrad p, uint32_t
     bind();
     loads(0);
     advance();
-    bool fresh = lr >= lr1;   // the next slab to load is a new tile's
     __builtin_amdgcn_s_waitcnt(wait_vm(0));
     barrier();
     if (grp) barrier();
     uint32_t gs = 0;       // the slab's place in the ring
     for (uint32_t ct = 0; ct < n_my; ++ct) {
       const WTile m = tile(ct);
-      const int32_t rows = __builtin_amdgcn_readfirstlane(rows_of(m.e));
-      const uint32_t nk = ((uint32_t)rows + BK - 1) / BK;
+      const uint32_t nt = (uint32_t)(m.at >> 16), kt = (uint32_t)(m.at & 0xFFFF), nk = ((uint32_t)m.rows + BK - 1) / BK;
       if (nk == 0 && (p.beta != 0.0f || !p.zero_empty)) continue;
-      const uint32_t tn = N - m.nt * TM < TM ? N - m.nt * TM : TM;
+      const uint32_t tn = N - nt * TM < TM ? N - nt * TM : TM;
       const int mb = (int)((tn + 63) / 64);   // blocks of 16 of a wave
       f32x4 acc[4][8];
 #pragma unroll
@@ -196,14 +192,14 @@ __global__ void __launch_bounds__(t16::NT, 1) k_bf16_wgrad(Bf16Wgrad p, uint32_t
       {
         const int x = lane() & 15, q = lane() >> 4, j = x >> 2, s = x & 3;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) ao[i] = (8 * q + j) * 512 + 8 * (s & 1) + 16 * ((2 * mb * wm + 2 * i + (s >> 1)) ^ (4 * j));
+        for (int i = 0; i < 4; ++i) ao[i] = (8 * q + j) * 512 + 8 * (s & 1) + 16 * ((2 * mb * wm + 2 * i + (s >> 1)) ^ (4 * j) ^ (2 * (q & 1)));
       }
       bf16x8 fa[4], fb[8];
       auto reads = [&](int h) __attribute__((always_inline)) {
         const uint32_t st = gs * STAGE + 16384 * h;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          read_tr(fb[i], st + lb[i >> 1] + 8 * (i & 1));
+          read_tr(fb[i], (st + lb) ^ (32 * i));
           if (i < 4) read_tr(fa[i], st + ao[i]);
         }
       };
@@ -222,11 +218,10 @@ __global__ void __launch_bounds__(t16::NT, 1) k_bf16_wgrad(Bf16Wgrad p, uint32_t
         __builtin_amdgcn_s_setprio(0);
       };
       for (uint32_t s = 0; s < nk; ++s) {
-        if (fresh) bind();
+        if (left == 0) bind();
         reads(0);
         loads(1 - gs);
         advance();
-        fresh = lr >= lr1;
         barrier();
         mfmas(true);
         reads(1);
@@ -236,7 +231,7 @@ __global__ void __launch_bounds__(t16::NT, 1) k_bf16_wgrad(Bf16Wgrad p, uint32_t
         mfmas(!(grp && s == nk - 1));
         gs = 1 - gs;
       }
-      const int64_t row0 = (int64_t)m.e * p.N + (int64_t)m.nt * TM;
+      const int64_t row0 = (int64_t)m.e * p.N + (int64_t)nt * TM;
       const __amdgpu_buffer_rsrc_t rc = make_rsrc(p.dw + row0 * p.K, (uint64_t)tn * K * 4);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -244,17 +239,16 @@ __global__ void __launch_bounds__(t16::NT, 1) k_bf16_wgrad(Bf16Wgrad p, uint32_t
           const int li = lane() & 15, q = lane() >> 4;
           const uint32_t r = 16 * mb * wm + 16 * i + li;
 #pragma unroll
-          for (int pb = 0; pb < 4; ++pb) {
-            const uint32_t k = m.kt * TN + 128 * wn + 32 * pb + 8 * q, o = k < K ? r * K + k : PAST;
-            const f32x4 x = acc[i][2 * pb], y = acc[i][2 * pb + 1];
-            float z[8] = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
+          for (int n = 0; n < 8; ++n) {
+            const uint32_t k = kt * TN + 128 * wn + 16 * n + 4 * q, o = k < K ? r * K + k : PAST;
+            float z[4] = {acc[i][n][0], acc[i][n][1], acc[i][n][2], acc[i][n][3]};
             if (p.beta != 0.0f) {
-              float v[8];
-              load_f32<8>(rc, o, v);
+              float v[4];
+              load_f32<4>(rc, o, v);
 #pragma unroll
-              for (int n = 0; n < 8; ++n) z[n] = v[n] + z[n];
+              for (int x = 0; x < 4; ++x) z[x] = v[x] + z[x];
             }
-            store_f32<8>(rc, o, z);
+            store_f32<4>(rc, o, z);
           }
           __builtin_amdgcn_sched_barrier(0);
         }
