@@ -381,6 +381,123 @@ __global__ void __launch_bounds__(t16::NT, 1) k_bf16_tile(Bf16Args p, int cap, u
   }
 }
 
+// ----------------------------------------------------------------- few rows
+// With a handful of rows per expert the cost is streaming each active
+// expert's weights once, through registers: the weights take the MFMA's M side,
+// the rows its N side, 16 at a time.  A workgroup takes 16 WB weight rows of
+// one expert (GATED: half of them gate rows, half the up rows of the same
+// columns) and up to 64 of its rows; its four waves take every fourth 64 values
+// of K (whole lines of a weight row, two steps of 32) and join their sums
+// through LDS in wave order.  A wave requests the weights of two such pieces
+// ahead of those it multiplies; the rows come from L2.
+namespace b16r {
+constexpr int NWV = 4, NT = 64 * NWV, PASSES = 4, TR = 16 * PASSES, NU = 2;
+}
+
+// Grid: n_nt weight-row blocks x (slots for the experts' first TR rows, then
+// slots for the rest).  first: the number of those slots: E (slot = expert) or,
+// with fewer rows than experts, M (slot = number among the experts with rows).
+template <int MODE, bool OUT_BF16, int WB>
+__global__ void __launch_bounds__(b16r::NT) k_bf16_rows(Bf16Args p, uint32_t n_nt, int64_t first) {
+  using namespace b16r;
+  constexpr int HB = MODE == GATED ? WB / 2 : WB;   // blocks of output columns
+  __shared__ f32x4 red[NWV][WB][64];
+  const int64_t slot = blockIdx.x / n_nt;
+  int e = (int)slot;
+  int64_t mt = 0;
+  if (slot >= first) {
+    if (!nth_item(p.off, p.E, slot - first, [](int m) { return (int64_t)(m > TR ? (m - 1) / TR : 0); }, e, mt)) return;
+    ++mt;
+  } else if (first < p.E) {
+    if (!nth_item(p.off, p.E, slot, [](int m) { return (int64_t)(m > 0); }, e, mt)) return;
+  }
+  const uint32_t N = (uint32_t)p.N, K = (uint32_t)p.K, KB = K * 2, n0 = (blockIdx.x % n_nt) * 16 * HB;
+  const int64_t r0 = (int64_t)p.off[e] + mt * TR, re = (int64_t)p.off[e + 1] < p.M ? (int64_t)p.off[e + 1] : p.M;
+  if (r0 < 0 || r0 >= re) return;
+  const int rows = re - r0 < TR ? (int)(re - r0) : TR;
+  const int l = threadIdx.x & 63, li = l & 15, q = l >> 4;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int np = (rows + 15) / 16;
+  const int nw = MODE == GATED ? 2 : 1;
+  const __amdgpu_buffer_rsrc_t rw = make_rsrc(p.w + (int64_t)e * nw * p.N * p.K, (uint64_t)nw * N * KB);
+  const __amdgpu_buffer_rsrc_t ra = p.map ? make_rsrc(p.a, (uint64_t)p.a_rows * KB) : make_rsrc(p.a + r0 * p.K, (uint64_t)rows * KB);
+  uint32_t wo[WB], ao[PASSES];
+#pragma unroll
+  for (int b = 0; b < WB; ++b) {
+    const uint32_t n = n0 + 16 * (b % HB) + li;
+    wo[b] = n < N ? (n + (b / HB) * N) * KB + 16 * q : t16::OOB;
+  }
+#pragma unroll
+  for (int s = 0; s < PASSES; ++s) {
+    const int r = 16 * s + li;
+    ao[s] = t16::OOB;
+    if (r < rows) {
+      const int64_t row = p.map ? mapped_row(p.map, r0 + r, p.div, p.magic, p.a_rows, &g_dev_err) : r;
+      if (row >= 0) ao[s] = (uint32_t)row * KB + 16 * q;
+    }
+  }
+  // step h (32 values) of this wave's piece i: K chunk 8 (4 i + w) + 4 h + q
+  auto at = [&](uint32_t o, uint32_t i, int h) { return 8 * (NWV * i + w) + 4 * h + q < K / 8 ? o + 128 * (NWV * i + w) + 64 * h : t16::OOB; };
+  const uint32_t np64 = (K + 63) / 64, mine = np64 > (uint32_t)w ? (np64 - w + NWV - 1) / NWV : 0;
+  u32x4 wq[2][NU][2][WB];
+  f32x4 acc[PASSES][WB];
+#pragma unroll
+  for (int s = 0; s < PASSES; ++s)
+#pragma unroll
+    for (int b = 0; b < WB; ++b) acc[s][b] = f32x4{};
+  auto weights = [&](u32x4 (&x)[NU][2][WB], uint32_t i) {   // (pieces past the wave's share: zeros)
+#pragma unroll
+    for (int u = 0; u < NU; ++u)
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int b = 0; b < WB; ++b) x[u][h][b] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(rw, at(wo[b], i + u, h), 0, 0));
+  };
+  auto multiply = [&](u32x4 (&x)[NU][2][WB], uint32_t i) {
+#pragma unroll
+    for (int s = 0; s < PASSES; ++s) {
+      if (s < np) {
+        u32x4 a[NU][2];
+#pragma unroll
+        for (int u = 0; u < NU; ++u)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) a[u][h] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(ra, at(ao[s], i + u, h), 0, 0));
+#pragma unroll
+        for (int u = 0; u < NU; ++u)
+#pragma unroll
+          for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int b = 0; b < WB; ++b)
+              acc[s][b] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, x[u][h][b]), __builtin_bit_cast(bf16x8, a[u][h]), acc[s][b], 0, 0, 0);
+      }
+    }
+  };
+  weights(wq[0], 0);
+  for (uint32_t i = 0; i < mine; i += 2 * NU) {
+    weights(wq[1], i + NU);
+    multiply(wq[0], i);
+    weights(wq[0], i + 2 * NU);
+    multiply(wq[1], i + NU);
+  }
+  const Bf16Epilogue<MODE, OUT_BF16> epi(p, e, r0, rows);
+#pragma unroll
+  for (int s = 0; s < PASSES; ++s) {
+    if (s < np) {
+      if (s) __syncthreads();   // (the last pass's sums have been read)
+#pragma unroll
+      for (int b = 0; b < WB; ++b) red[w][b][l] = acc[s][b];
+      __syncthreads();
+      // wave b joins column block b: lane (li, q) holds row li of the pass, four consecutive columns
+      for (int b = w; b < HB; b += NWV) {
+        const f32x4 x = ((red[0][b][l] + red[1][b][l]) + red[2][b][l]) + red[3][b][l];
+        const f32x4 y = MODE == GATED ? ((red[0][b + HB][l] + red[1][b + HB][l]) + red[2][b + HB][l]) + red[3][b + HB][l] : x;
+        const float z[4] = {x[0], x[1], x[2], x[3]}, z1[4] = {y[0], y[1], y[2], y[3]};
+        epi.template put<4>(16 * s + li, n0 + 16 * b + 4 * q, 1.0f, z, z1);
+      }
+    }
+  }
+}
+
 int tile_grid() {
   static int n[64] = {0};
   int dev = 0;
@@ -393,10 +510,28 @@ int tile_grid() {
   return n[dev];
 }
 
+// Whether a forward product goes to the few-rows kernel.
+static bool few_rows(const Bf16Args& p) { return p.M <= 16 * (int64_t)p.E; }
+
+template <int MODE, bool OUT_BF16, int WB>
+static int launch_rows(const Bf16Args& p, hipStream_t stream, const char* name) {
+  using namespace b16r;
+  constexpr int HB = MODE == GATED ? WB / 2 : WB;
+  const int64_t first = p.M < p.E ? p.M : p.E, nt = (p.N + 16 * HB - 1) / (16 * HB), slots = first + p.M / TR;
+  MOE4_REQUIRE(grid_fits(nt * slots, NT), MOE4_EINVAL, std::string(name) + ": too large");
+  hipLaunchKernelGGL((k_bf16_rows<MODE, OUT_BF16, WB>), dim3((unsigned)(nt * slots)), dim3(NT), 0, stream, p, (uint32_t)nt, first);
+  return check_launch(name);
+}
+
 template <int MODE, bool OUT_BF16>
 static int launch_bf16(const Bf16Args& p, void* stream, const char* name) {
   using namespace t16;
   constexpr int NW = MODE == GATED ? TN / 2 : TN;
+  if ((MODE == FWD || MODE == GATED) && few_rows(p)) {
+    constexpr int RM = MODE == GATED ? GATED : FWD;
+    const int64_t wide = (p.N * (MODE == GATED ? 2 : 1) + 63) / 64 * (p.M < p.E ? p.M : p.E);
+    return wide >= 1024 ? launch_rows<RM, OUT_BF16, 4>(p, as_stream(stream), name) : launch_rows<RM, OUT_BF16, 2>(p, as_stream(stream), name);
+  }
   const int64_t nt = (p.N + NW - 1) / NW;
   const int cus = tile_grid();
   int cap = 8;   // log2 of a tile's most rows

@@ -41,34 +41,6 @@ constexpr int KB = 128;           // K per step: lane (li, q) holds k = 128 s + 
 constexpr int PASSES = 4, TR = 16 * PASSES;
 }  // namespace m4s
 
-// The expert and the tile in it of item idx, the experts holding count(rows)
-// items each, in order; false past the last.  Lane l counts the experts
-// [l P, (l + 1) P), so all the offsets are in flight at once.
-template <typename Count>
-__device__ inline bool nth_item(const int32_t* __restrict__ off, int E, int64_t idx, Count count, int& e_out, int64_t& i_out) {
-  const int l = threadIdx.x & 63, P = (E + 63) / 64;
-  const int e0 = l * P, e1 = e0 + P < E ? e0 + P : E;
-  int64_t mine = 0;
-  for (int e = e0; e < e1; ++e) mine += count(off[e + 1] - off[e]);
-  int64_t inc = mine;
-#pragma unroll
-  for (int o = 1; o < 64; o <<= 1) {
-    const int64_t y = __shfl_up(inc, o, 64);
-    if (l >= o) inc += y;
-  }
-  int64_t rest = idx - (inc - mine);  // the item's number among this lane's
-  const unsigned long long hit = __ballot(rest >= 0 && rest < mine);
-  if (hit == 0) return false;
-  int e = e0;
-  if (rest >= 0 && rest < mine) {
-    for (int64_t n; rest >= (n = count(off[e + 1] - off[e])); ++e) rest -= n;
-  }
-  const int src = __ffsll((long long)hit) - 1;
-  e_out = __builtin_amdgcn_readfirstlane(__shfl(e, src, 64));
-  i_out = __builtin_amdgcn_readfirstlane(__shfl((int)rest, src, 64));
-  return true;
-}
-
 // Grid: n_nt weight-row blocks x (slots for the experts' first TR rows, then
 // slots for the rest).  first: the number of those slots: E (slot = expert) or,
 // with fewer rows than experts, M_total (slot = number among the experts with
