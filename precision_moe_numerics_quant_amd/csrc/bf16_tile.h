@@ -44,6 +44,17 @@ __device__ __forceinline__ void load_lds4(const u32x4& rs, uint32_t lds, uint32_
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(lds), "v"(off), "s"(rs) : "memory");
 }
 
+// Waits until all of this wave's memory operations but the `newer` latest have
+// completed (fewer may be let through).
+__device__ __forceinline__ void wait_but(int newer) {
+  __builtin_amdgcn_sched_barrier(0);
+  if (newer >= 48) __builtin_amdgcn_s_waitcnt(wait_vm(48));
+  else if (newer >= 32) __builtin_amdgcn_s_waitcnt(wait_vm(32));
+  else if (newer >= 16) __builtin_amdgcn_s_waitcnt(wait_vm(16));
+  else if (newer >= 8) __builtin_amdgcn_s_waitcnt(wait_vm(8));
+  else __builtin_amdgcn_s_waitcnt(wait_vm(0));
+}
+
 }  // namespace t16
 
 // Workgroups of the persistent kernels: the current device's CUs, a multiple of 8.

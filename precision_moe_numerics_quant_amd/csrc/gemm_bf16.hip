@@ -204,6 +204,17 @@ __global__ void __launch_bounds__(t16::NT, 1) k_bf16_tile(Bf16Args p, int cap, u
     }
   };
 
+  // the next slab of the stream into a slot of the ring
+  auto issue = [&](uint32_t stage) __attribute__((always_inline)) {
+    if (ls == nk) bind();
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      load_a(t, stage);
+      load_b(t, stage);
+    }
+    advance();
+  };
+
   // --------------------------------------------------------------- fragments
   // Swizzles (through the chunk that each lane loads): a row's 16-byte chunk c
   // sits at c ^ x(row) such that the 16 lanes (transposed reads of 32 bytes a row:
@@ -272,13 +283,8 @@ __global__ void __launch_bounds__(t16::NT, 1) k_bf16_tile(Bf16Args p, int cap, u
     ln = 0;
     fetch_map(0);
     __builtin_amdgcn_s_waitcnt(wait_vm(0));
-    bind();
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      load_a(t, 0);
-      load_b(t, 0);
-    }
-    advance();
+    ls = nk;
+    issue(0);
     __builtin_amdgcn_s_waitcnt(wait_vm(0));
     barrier();
     // The two groups of waves take turns: one runs the MFMAs of half a slab
@@ -286,6 +292,7 @@ __global__ void __launch_bounds__(t16::NT, 1) k_bf16_tile(Bf16Args p, int cap, u
     // slab after, a barrier between the turns.  Group 1 is a turn behind.
     if (grp) barrier();
     uint32_t gs = 0;       // the slab's place in the ring
+    int stored = -1;       // memory operations of the last epilogue, at least (-1: there was none)
     for (uint32_t ct = 0; ct < n_my; ++ct) {
       const Tile m = tile(ct);
       const int mb = (m.rows + 63) / 64;   // blocks of 16 rows of a wave
@@ -327,25 +334,27 @@ __global__ void __launch_bounds__(t16::NT, 1) k_bf16_tile(Bf16Args p, int cap, u
       for (uint32_t s = 0; s < nk; ++s) {
         // the next slab's loads must have landed before the end of group 1's
         // second reading turn, which is group 0's second turn at the MFMAs
-        if (s == nk - 1) bind();
+        // (in a tile's first slab they are older than the last tile's results,
+        // which need not have been stored by then)
         reads(0);
-#pragma unroll
-        for (int t = 0; t < 4; ++t) {
-          load_a(t, 1 - gs);
-          load_b(t, 1 - gs);
+        if (stored < 0) {
+          issue(1 - gs);
+          stored = 0;
         }
-        advance();
         barrier();
         mfmas(true);
         reads(1);
-        if (grp) __builtin_amdgcn_s_waitcnt(wait_vm(0));
+        if (grp) wait_but(stored);
         barrier();
-        if (!grp) __builtin_amdgcn_s_waitcnt(wait_vm(0));
+        if (!grp) wait_but(stored);
+        stored = -1;
         // (the last turn of the tile: group 1 stores its results before the
         // barrier, while group 0 stores its own behind it)
         mfmas(!(grp && s == nk - 1));
         gs = 1 - gs;
       }
+      issue(1 - gs);
+      stored = (MODE == GATED ? (p.aux ? 6 : 2) : MODE == GDGRAD || !OUT_BF16 ? 8 : 4) * mb;
       const Bf16Epilogue<MODE, OUT_BF16> epi(p, m.e, m.row0, m.rows);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {

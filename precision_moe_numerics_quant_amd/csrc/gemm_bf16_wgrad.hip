@@ -16,7 +16,8 @@ struct WTile {
 
 // The tiled products' structure (gemm_bf16.hip) with the rows as the
 // contraction: a slab is 64 rows of both operands, 512 bytes of each, read
-// transposed from LDS.  A map's entries come a slab ahead, each lane's four.  order: the experts are visited in steps of
+// transposed from LDS.  A map's entries come through LDS, those of eight slabs at a
+// time.  order: the experts are visited in steps of
 // `order` (coprime to E), so that popular and rare ones, whose tiles multiply
 // and store in different proportions, run side by side.
 __global__ void __launch_bounds__(t16::NT, 1) k_bf16_wgrad(Bf16Wgrad p, uint32_t n_nt, uint32_t n_kt, uint32_t order) {
@@ -24,9 +25,11 @@ __global__ void __launch_bounds__(t16::NT, 1) k_bf16_wgrad(Bf16Wgrad p, uint32_t
   __shared__ __attribute__((aligned(16))) uint8_t ring[RING];
   __shared__ __attribute__((aligned(16))) WTile s_tile[NT];   // this workgroup's next tiles
   __shared__ int32_t s_off[MAX_E + 1];                   // the experts' first rows, clamped
+  __shared__ __attribute__((aligned(16))) uint32_t s_map[2][2][8][64];   // map entries: operand, half of them, wave, slab and row
   const int tid = threadIdx.x, l = tid & 63, li = l & 15, q = l >> 4;
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6), wm = w >> 1, wn = w & 1, grp = w >> 2;
   const uint32_t lds0 = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_u8)ring);
+  const uint32_t ldsm = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_u8)(uint8_t*)s_map);
   const int E = p.E;
   const int32_t M = (int32_t)p.M;
   for (int e = tid; e <= E; e += NT) {
@@ -47,9 +50,8 @@ __global__ void __launch_bounds__(t16::NT, 1) k_bf16_wgrad(Bf16Wgrad p, uint32_t
   uint32_t ln = 0, n_my = 0;
   int32_t lr = 0, left = 0;          // the next slab's first row in its expert, the expert's rows from there
   u32x4 rd, ra;
-  __amdgpu_buffer_rsrc_t rmd = make_rsrc(p.off, 0), rma = rmd;   // the expert's map entries
   uint32_t vod[4], voa[4], cd[4], ca[4];   // offsets; with a map those of the columns
-  uint32_t md[4], ma[4];             // the next slab's map entries
+  uint32_t batch = 0;                // eight slabs' map entries that have been taken up
   auto tile = [&](uint32_t i) __attribute__((always_inline)) {
     const WTile x = s_tile[i];
     return WTile{__builtin_amdgcn_readfirstlane(x.e), __builtin_amdgcn_readfirstlane(x.at), __builtin_amdgcn_readfirstlane(x.row0),
@@ -57,12 +59,21 @@ __global__ void __launch_bounds__(t16::NT, 1) k_bf16_wgrad(Bf16Wgrad p, uint32_t
   };
   // the chunk (16 bytes) that lands in this lane's slot l % 32 of load t, row 8 w + 2 t + l / 32 of the slab
   auto chunk_of = [&](int t, int l) __attribute__((always_inline)) { return (uint32_t)(l & 31) ^ (4 * ((2 * t + (l >> 5)) & 3)) ^ (2 * (w & 1)); };
-  auto fetch = [&](uint32_t (&m)[4], const __amdgpu_buffer_rsrc_t& rs, int32_t r) __attribute__((always_inline)) {   // entries of the slab at row r
-#pragma unroll
-    for (int t = 0; t < 4; ++t) m[t] = __builtin_amdgcn_raw_buffer_load_b32(rs, 4 * (r + 8 * w + 2 * t + (l >> 5)), 0, 0);
+  // requests the map entries of the eight slabs from row r of the expert's rows
+  // (row0 .., n of them) on: this wave's rows 8 w + 2 t + h of slab s to s 8 + h 4 + t
+  auto fetch = [&](int32_t row0, int32_t n, int32_t r) __attribute__((always_inline)) {
+    const int x = lane();
+    const uint32_t o = 4 * (r + BK * (x >> 3) + 8 * w + 2 * (x & 3) + ((x >> 2) & 1));
+    __builtin_amdgcn_s_waitcnt(WAIT_LGKM0);   // (the entries there have been read)
+    const uint32_t to = ldsm + ((batch & 1) * 8 + w) * 256;
+    if (p.dy_map) load_lds4(rsrc4(p.dy_map + row0, (uint64_t)n * 4), to, o);
+    if (p.a_map) load_lds4(rsrc4(p.a_map + row0, (uint64_t)n * 4), to + 4096, o);
+    ++batch;
   };
   // a mapped operand's offsets for the next slab
-  auto gather = [&](uint32_t (&vo)[4], const uint32_t (&m)[4], const uint32_t (&c)[4], uint32_t rows, uint32_t ld) __attribute__((always_inline)) {
+  auto gather = [&](uint32_t (&vo)[4], int op, const uint32_t (&c)[4], uint32_t rows, uint32_t ld) __attribute__((always_inline)) {
+    // (the half being read is the one not being filled)
+    const u32x4 m = *reinterpret_cast<const u32x4*>(&s_map[op][batch & 1][w][8 * ((lr / BK) & 7) + 4 * (l >> 5)]);
     bool bad = false;
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
@@ -73,21 +84,34 @@ __global__ void __launch_bounds__(t16::NT, 1) k_bf16_wgrad(Bf16Wgrad p, uint32_t
     }
     if (__any(bad) && l == 0) atomicOr(&g_dev_err, MOE4_DEVERR_INDEX);
   };
-  auto set_rows = [&]() __attribute__((always_inline)) {   // the mapped operands at the next slab
-    if (p.dy_map) {
-      gather(vod, md, cd, (uint32_t)p.dy_rows, ldd);
-      fetch(md, rmd, lr + BK);
+  WTile lt{0, 0, 0, 0};              // the tile being loaded
+  const bool mapped = p.dy_map || p.a_map;
+  auto skip = [&](uint32_t i) __attribute__((always_inline)) {   // the first tile from i on that has rows
+    WTile x{0, 0, 0, 0};
+    while (i < n_my && (x = tile(i)).rows == 0) ++i;
+    ln = i;
+    return x;
+  };
+  // the mapped operands at the next slab; with its first of eight the next
+  // eight are requested: this tile's, or the next tile's first
+  auto set_rows = [&]() __attribute__((always_inline)) {
+    if (((lr / BK) & 7) == 0) {
+      if (left > 8 * BK) {
+        fetch(lt.row0, lt.rows, lr + 8 * BK);
+      } else {
+        const uint32_t keep = ln;
+        const WTile x = skip(ln);
+        fetch(x.row0, x.rows, 0);
+        ln = keep;
+      }
     }
-    if (p.a_map) {
-      gather(voa, ma, ca, (uint32_t)p.a_rows, lda);
-      fetch(ma, rma, lr + BK);
-    }
+    if (p.dy_map) gather(vod, 0, cd, (uint32_t)p.dy_rows, ldd);
+    if (p.a_map) gather(voa, 1, ca, (uint32_t)p.a_rows, lda);
   };
   // the loads go on with tile ln, passing over those of experts without rows
   auto bind = [&]() __attribute__((always_inline)) {
-    WTile x{0, 0, 0, 0};
-    while (ln < n_my && (x = tile(ln++)).rows == 0) {
-    }
+    const WTile x = lt = skip(ln);
+    ++ln;
     lr = 0;
     left = x.rows;
     if (left == 0) {   // (descriptors of nothing: every slab has as many loads)
@@ -107,33 +131,24 @@ __global__ void __launch_bounds__(t16::NT, 1) k_bf16_wgrad(Bf16Wgrad p, uint32_t
       vod[t] = k * ldd + cd[t];
       voa[t] = k * lda + ca[t];
     }
-    if (p.dy_map) {
-      rmd = make_rsrc(p.dy_map + x.row0, (uint64_t)left * 4);
-      fetch(md, rmd, 0);
-    }
-    if (p.a_map) {
-      rma = make_rsrc(p.a_map + x.row0, (uint64_t)left * 4);
-      fetch(ma, rma, 0);
-    }
-    set_rows();
-  };
-  auto loads = [&](uint32_t stage) __attribute__((always_inline)) {
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      load_lds(rd, lds0 + stage * STAGE + (4 * w + t) * 1024, vod[t], 0);
-      load_lds(ra, lds0 + stage * STAGE + HALF + (4 * w + t) * 1024, voa[t], 0);
-    }
   };
   auto step = [&](u32x4& rs, uint32_t ld) __attribute__((always_inline)) {
     const uint64_t base = ((uint64_t)rs[1] << 32 | rs[0]) + BK * ld;
     rs = rsrc4(reinterpret_cast<const void*>(base), (uint64_t)left * ld);
   };
-  auto advance = [&]() __attribute__((always_inline)) {
+  // the next slab of the stream into a slot of the ring
+  auto issue = [&](uint32_t stage) __attribute__((always_inline)) {
+    if (left == 0) bind();
+    if (mapped && left) set_rows();
+#pragma unroll
+    for (int t = 0; t < 4; ++t) {
+      load_lds(rd, lds0 + stage * STAGE + (4 * w + t) * 1024, vod[t], 0);
+      load_lds(ra, lds0 + stage * STAGE + HALF + (4 * w + t) * 1024, voa[t], 0);
+    }
     lr += BK;
     left = left > BK ? left - BK : 0;
     if (!p.dy_map) step(rd, ldd);
     if (!p.a_map) step(ra, lda);
-    if (left) set_rows();
   };
 
   // --------------------------------------------------------------- fragments
@@ -170,13 +185,18 @@ __global__ void __launch_bounds__(t16::NT, 1) k_bf16_wgrad(Bf16Wgrad p, uint32_t
     }
     if (n_my == 0) break;
     ln = 0;
-    bind();
-    loads(0);
-    advance();
+    left = 0;
+    if (mapped) {
+      const WTile x = skip(0);
+      fetch(x.row0, x.rows, 0);
+      __builtin_amdgcn_s_waitcnt(wait_vm(0));
+    }
+    issue(0);
     __builtin_amdgcn_s_waitcnt(wait_vm(0));
     barrier();
     if (grp) barrier();
     uint32_t gs = 0;       // the slab's place in the ring
+    int stored = -1;       // memory operations of the last epilogue, at least (-1: there was none)
     for (uint32_t ct = 0; ct < n_my; ++ct) {
       const WTile m = tile(ct);
       const uint32_t nt = (uint32_t)(m.at >> 16), kt = (uint32_t)(m.at & 0xFFFF), nk = ((uint32_t)m.rows + BK - 1) / BK;
@@ -218,18 +238,24 @@ __global__ void __launch_bounds__(t16::NT, 1) k_bf16_wgrad(Bf16Wgrad p, uint32_t
         __builtin_amdgcn_s_setprio(0);
       };
       for (uint32_t s = 0; s < nk; ++s) {
-        if (left == 0) bind();
         reads(0);
-        loads(1 - gs);
-        advance();
+        if (stored < 0) {
+          issue(1 - gs);
+          stored = 0;
+        }
         barrier();
         mfmas(true);
         reads(1);
-        if (grp) __builtin_amdgcn_s_waitcnt(wait_vm(0));
+        if (grp) wait_but(stored);
         barrier();
-        if (!grp) __builtin_amdgcn_s_waitcnt(wait_vm(0));
+        if (!grp) wait_but(stored);
+        stored = -1;
         mfmas(!(grp && s == nk - 1));
         gs = 1 - gs;
+      }
+      if (nk) {
+        issue(1 - gs);
+        stored = 8 * mb;
       }
       const int64_t row0 = (int64_t)m.e * p.N + (int64_t)nt * TM;
       const __amdgpu_buffer_rsrc_t rc = make_rsrc(p.dw + row0 * p.K, (uint64_t)tn * K * 4);
