@@ -52,6 +52,7 @@ __device__ __forceinline__ void wait_but(int newer) {
   else if (newer >= 32) __builtin_amdgcn_s_waitcnt(wait_vm(32));
   else if (newer >= 16) __builtin_amdgcn_s_waitcnt(wait_vm(16));
   else if (newer >= 8) __builtin_amdgcn_s_waitcnt(wait_vm(8));
+  else if (newer >= 4) __builtin_amdgcn_s_waitcnt(wait_vm(4));
   else __builtin_amdgcn_s_waitcnt(wait_vm(0));
 }
 

@@ -99,7 +99,7 @@ __global__ void __launch_bounds__(t16::NT, 1) k_bf16_tile(Bf16Args p, int cap, u
   const uint32_t ldb = TR ? N * 2 : KB;                     // bytes of a row of w
 
   // ------------------------------------------------------------- load stream
-  // It runs a slab ahead; the map entries of the tile after the one being
+  // It runs two slabs ahead; the map entries of the tile after the one being
   // loaded are fetched a tile ahead.  Past the last tile it goes on with
   // descriptors of nothing, so that every slab has as many loads.
   uint32_t ln = 0, n_my = 0, ls = 0;   // the next tile to load, this batch's tiles, slab
@@ -121,26 +121,28 @@ __global__ void __launch_bounds__(t16::NT, 1) k_bf16_tile(Bf16Args p, int cap, u
     if (!p.map || i >= n_my) return;
     const Tile x = tile(i);
     __builtin_amdgcn_s_waitcnt(WAIT_LGKM0);   // (the entries there have been read)
-    load_lds4(rsrc4(p.map + x.row0, (uint64_t)x.rows * 4), ldsm, 4 * (32 * w + lane()));
+    load_lds4(rsrc4(p.map + x.row0, (uint64_t)x.rows * 4), ldsm, 4 * (16 * ((x.rows + 63) / 64) * (w >> 1) + 32 * (w & 1) + lane()));
   };
   // the loads go on with tile ln (its map entries have landed: they are older
-  // than a slab that has been waited for)
+  // than a slab that has been waited for, unless tiles have but one)
   auto bind = [&]() __attribute__((always_inline)) {
     ls = 0;
+    if (p.map && nk == 1) __builtin_amdgcn_s_waitcnt(wait_vm(0));
     if (ln >= n_my) {
       ra = rsrc4(p.a, 0);
       rb = ra;
       return;
     }
     const Tile m = tile(ln);
-    const int l = lane();
+    const int l = lane(), mb = (m.rows + 63) / 64;
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
-      const int r = 32 * w + 8 * t + (l >> 3);
+      // row x of a wave row's 64 in LDS is row 16 mb wm + x of the tile
+      const int x = 32 * (w & 1) + 8 * t + (l >> 3), r = 16 * mb * (w >> 1) + x;
       uint32_t row = (uint32_t)r;
-      bool ok = r < m.rows;
+      bool ok = x < 16 * mb && r < m.rows;
       if (p.map && ok) {
-        const int32_t i = s_map[r + 32 * w];
+        const int32_t i = s_map[64 * w + 8 * t + (l >> 3)];
         row = udiv_magic((uint32_t)i, p.div, p.magic);
         ok = i >= 0 && row < (uint32_t)p.a_rows;
         if (!ok) atomicOr(&g_dev_err, MOE4_DEVERR_INDEX);
@@ -204,17 +206,6 @@ __global__ void __launch_bounds__(t16::NT, 1) k_bf16_tile(Bf16Args p, int cap, u
     }
   };
 
-  // the next slab of the stream into a slot of the ring
-  auto issue = [&](uint32_t stage) __attribute__((always_inline)) {
-    if (ls == nk) bind();
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      load_a(t, stage);
-      load_b(t, stage);
-    }
-    advance();
-  };
-
   // --------------------------------------------------------------- fragments
   // Swizzles (through the chunk that each lane loads): a row's 16-byte chunk c
   // sits at c ^ x(row) such that the 16 lanes (transposed reads of 32 bytes a row:
@@ -233,6 +224,8 @@ __global__ void __launch_bounds__(t16::NT, 1) k_bf16_tile(Bf16Args p, int cap, u
 #pragma unroll
     for (int h = 0; h < 2; ++h) lb[h] = HALF + (128 * wn + (PAIR ? 8 * (li >> 2) + (li & 3) : li)) * 128 + 16 * ((4 * h + q) ^ (li >> 1));
   }
+#pragma unroll
+  for (int h = 0; h < 2; ++h) la[h] = (64 * wm + li) * 128 + 16 * ((4 * h + q) ^ (li >> 1));
   auto frag_a = [&](bf16x8& f, int i, int h, uint32_t st) __attribute__((always_inline)) {
     f = *reinterpret_cast<const bf16x8*>(ring + st + la[h] + 2048 * i);
   };
@@ -283,16 +276,28 @@ __global__ void __launch_bounds__(t16::NT, 1) k_bf16_tile(Bf16Args p, int cap, u
     ln = 0;
     fetch_map(0);
     __builtin_amdgcn_s_waitcnt(wait_vm(0));
-    ls = nk;
-    issue(0);
-    __builtin_amdgcn_s_waitcnt(wait_vm(0));
+    for (int s = 0; s < 2; ++s) {   // slabs 0 and 1
+      if (s == 0 || ls == nk) bind();
+#pragma unroll
+      for (int t = 0; t < 4; ++t) {
+        load_a(t, s);
+        load_b(t, s);
+      }
+      advance();
+    }
+    __builtin_amdgcn_s_waitcnt(wait_vm(8));
     barrier();
     // The two groups of waves take turns: one runs the MFMAs of half a slab
-    // while the other reads its fragments of the next half and requests the
-    // slab after, a barrier between the turns.  Group 1 is a turn behind.
+    // while the other reads its fragments of the next half, a barrier between
+    // the turns; group 1 is a turn behind.  A slab's place in the ring is filled
+    // again as it is read to its end: the rows of A that only group 0 reads,
+    // by group 0, from its second turn at the MFMAs on, the rest from group 1's
+    // second turn on.  The loads go between the MFMAs: eight of them at once
+    // keep the memory pipeline busy for as long as a turn lasts, and a reading
+    // turn would last longer than the other group's MFMAs.
     if (grp) barrier();
     uint32_t gs = 0;       // the slab's place in the ring
-    int stored = -1;       // memory operations of the last epilogue, at least (-1: there was none)
+    int stored = 0;        // memory operations of the last epilogue, at least
     for (uint32_t ct = 0; ct < n_my; ++ct) {
       const Tile m = tile(ct);
       const int mb = (m.rows + 63) / 64;   // blocks of 16 rows of a wave
@@ -301,11 +306,6 @@ __global__ void __launch_bounds__(t16::NT, 1) k_bf16_tile(Bf16Args p, int cap, u
       for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int n = 0; n < 8; ++n) acc[i][n] = f32x4{};
-      {
-        const int li = lane() & 15, q = lane() >> 4;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) la[h] = (16 * mb * wm + li) * 128 + 16 * ((4 * h + q) ^ (li >> 1));
-      }
       bf16x8 fa[4], fb[8];
       auto reads = [&](int h) __attribute__((always_inline)) {
         const uint32_t st = gs * STAGE;
@@ -315,9 +315,10 @@ __global__ void __launch_bounds__(t16::NT, 1) k_bf16_tile(Bf16Args p, int cap, u
           if (i < 4) frag_a(fa[i], i, h, st);
         }
       };
-      // the turn's barrier comes four MFMAs before its end: the other group's
-      // first ones then follow without a gap
-      auto mfmas = [&](bool bar) __attribute__((always_inline)) {
+      // A turn at the MFMAs, with the loads that `load` makes in its four gaps.
+      // Its barrier comes four MFMAs before its end: the other group's first
+      // ones then follow without a gap.
+      auto mfmas = [&](auto load, auto hand_over) __attribute__((always_inline)) {
         __builtin_amdgcn_s_setprio(1);
 #pragma unroll
         for (int i = 3; i >= 0; --i) {
@@ -325,35 +326,47 @@ __global__ void __launch_bounds__(t16::NT, 1) k_bf16_tile(Bf16Args p, int cap, u
 #pragma unroll
             for (int n = 0; n < (i ? 8 : 4); ++n) acc[i][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[n], fa[i], acc[i][n], 0, 0, 0);
           }
+          load(3 - i);
         }
-        if (bar) barrier();
+        hand_over();
 #pragma unroll
         for (int n = 4; n < 8; ++n) acc[0][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[n], fa[0], acc[0][n], 0, 0, 0);
         __builtin_amdgcn_s_setprio(0);
       };
+      // group 0: B of the next slab, in its first turn; group 1: half its share
+      // of it while it reads (both before a tile's results are stored, so in the
+      // tile's first slab they have been made)
+      auto late = [&]() __attribute__((always_inline)) {
+#pragma unroll
+        for (int t = 0; t < 4; ++t)
+          if (!grp || t >= 2) load_b(t, 1 - gs);
+        advance();
+      };
       for (uint32_t s = 0; s < nk; ++s) {
-        // the next slab's loads must have landed before the end of group 1's
-        // second reading turn, which is group 0's second turn at the MFMAs
-        // (in a tile's first slab they are older than the last tile's results,
-        // which need not have been stored by then)
         reads(0);
-        if (stored < 0) {
-          issue(1 - gs);
-          stored = 0;
-        }
+        if (grp && s) late();
         barrier();
-        mfmas(true);
+        mfmas([&](int t) __attribute__((always_inline)) { if (!grp && s) load_b(t, 1 - gs); }, barrier);
+        if (!grp && s) advance();
         reads(1);
-        if (grp) wait_but(stored);
+        if (ls == nk) bind();
+        if (grp) wait_but(stored);   // (the next slab; the last tile's results need not have been stored)
         barrier();
-        if (!grp) wait_but(stored);
-        stored = -1;
-        // (the last turn of the tile: group 1 stores its results before the
-        // barrier, while group 0 stores its own behind it)
-        mfmas(!(grp && s == nk - 1));
+        mfmas(
+            [&](int t) __attribute__((always_inline)) {
+              load_a(t, gs);
+              if (grp && t < 2) load_b(t, gs);
+            },
+            [&]() __attribute__((always_inline)) {
+              if (!grp) wait_but(stored + 4);
+              // (a tile's last turn: group 1 stores its results before the
+              // barrier, while group 0 stores its own behind it)
+              if (!(grp && s == nk - 1)) barrier();
+            });
+        stored = 0;
         gs = 1 - gs;
       }
-      issue(1 - gs);
+      late();
       stored = (MODE == GATED ? (p.aux ? 6 : 2) : MODE == GDGRAD || !OUT_BF16 ? 8 : 4) * mb;
       const Bf16Epilogue<MODE, OUT_BF16> epi(p, m.e, m.row0, m.rows);
 #pragma unroll
