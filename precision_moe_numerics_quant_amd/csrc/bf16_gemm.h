@@ -121,12 +121,13 @@ __device__ inline void store_bf16(const __amdgpu_buffer_rsrc_t& rs, uint32_t o, 
   else
     __builtin_amdgcn_raw_buffer_store_b64(u32x2{bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3])}, rs, o * 2, 0, 0);
 }
-template <int W>
+constexpr int NT_STORE = 2;   // (a store's cache policy: passed on to memory rather than kept)
+template <int W, int POLICY = 0>
 __device__ inline void store_f32(const __amdgpu_buffer_rsrc_t& rs, uint32_t o, const float (&v)[W]) {
 #pragma unroll
   for (int i = 0; i < W; i += 4)
     __builtin_amdgcn_raw_buffer_store_b128(u32x4{__float_as_uint(v[i]), __float_as_uint(v[i + 1]), __float_as_uint(v[i + 2]), __float_as_uint(v[i + 3])},
-                                           rs, (o + i) * 4, 0, 0);
+                                           rs, (o + i) * 4, 0, POLICY);
 }
 
 // A tile's epilogue: descriptors that start with its first row and end with its

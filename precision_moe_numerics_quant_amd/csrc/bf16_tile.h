@@ -44,6 +44,25 @@ __device__ __forceinline__ void load_lds4(const u32x4& rs, uint32_t lds, uint32_
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds" ::"s"(lds), "v"(off), "s"(rs) : "memory");
 }
 
+// Results to store: x and y are two blocks, lane 16 q + i holding W values of row
+// i from column W q on.  Afterwards x is row l / 8 and y row 8 + l / 8 of lane l,
+// columns W (l % 4) on of the first block for l % 8 < 4, else of the second: a store
+// then takes whole lines, eight of 128 bytes, each from consecutive lanes.
+// (Stored as they were, 64 bytes of a row from lanes 16 apart, results pass the
+// memory pipeline far more slowly: see the weight gradient.)
+template <int W>
+__device__ __forceinline__ void store_order(float (&x)[W], float (&y)[W], int l) {
+  const bool hi = l & 8;
+  const int from = 4 * (16 * (l & 3) + 8 * ((l >> 2) & 1) + (l >> 3));
+#pragma unroll
+  for (int v = 0; v < W; ++v) {
+    const int s = __float_as_int(hi ? x[v] : y[v]);
+    const float r = __int_as_float(__builtin_amdgcn_update_dpp(s, s, 0x128, 0xF, 0xF, false));   // (lane i ^ 8's)
+    x[v] = __int_as_float(__builtin_amdgcn_ds_bpermute(from, __float_as_int(hi ? r : x[v])));
+    y[v] = __int_as_float(__builtin_amdgcn_ds_bpermute(from, __float_as_int(hi ? y[v] : r)));
+  }
+}
+
 // Waits until all of this wave's memory operations but the `newer` latest have
 // completed (fewer may be let through).
 __device__ __forceinline__ void wait_but(int newer) {

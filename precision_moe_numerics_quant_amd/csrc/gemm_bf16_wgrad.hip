@@ -8,35 +8,45 @@ namespace moe4 {
 static __device__ uint32_t g_dev_err;
 uint32_t take_dev_err_gemm_bf16_wgrad() { return take_device_word(&g_dev_err); }
 
+namespace wg {
+constexpr int NT = 256;                   // four waves of 64 x 128, 2 x 2
+constexpr int TM = 128, TN = 256, BK = 32;   // tile (of dy's and of a's columns), rows of a slab
+constexpr int HALF = BK * TM * 2, STAGE = HALF + BK * TN * 2, NS = 3;   // dy's part of a slab, a slab, the ring's slabs
+constexpr int NL = 6;                     // a wave's loads of a slab: two of dy, four of a
+constexpr int LIST = 128;                 // tiles listed at a time
+}  // namespace wg
+
 // A tile of an expert's gradient: n-tile nt (of dy's columns), k-tile kt (of a's;
 // at = nt 2^16 + kt), the expert's rows.
 struct WTile {
   int32_t e, at, row0, rows;
 };
 
-// The tiled products' structure (gemm_bf16.hip) with the rows as the
-// contraction: a slab is 64 rows of both operands, 512 bytes of each, read
-// transposed from LDS.  A map's entries come through LDS, those of eight slabs at a
-// time.  order: the experts are visited in steps of
-// `order` (coprime to E), so that popular and rare ones, whose tiles multiply
+// The rows are the contraction: a slab is 32 rows of both operands, read
+// transposed from LDS.  Two workgroups share a CU, so that one multiplies while
+// the other stores: a short contraction (a few hundred rows) writes its float32
+// tile in about the time that it takes to multiply.  A map's entries come through
+// LDS, those of eight slabs at a time.  order: the experts are visited in steps
+// of `order` (coprime to E), so that popular and rare ones, whose tiles multiply
 // and store in different proportions, run side by side.
-__global__ void __launch_bounds__(t16::NT, 1) k_bf16_wgrad(Bf16Wgrad p, uint32_t n_nt, uint32_t n_kt, uint32_t order) {
-  using namespace t16;
-  __shared__ __attribute__((aligned(16))) uint8_t ring[RING];
-  __shared__ __attribute__((aligned(16))) WTile s_tile[NT];   // this workgroup's next tiles
-  __shared__ int32_t s_off[MAX_E + 1];                   // the experts' first rows, clamped
-  __shared__ __attribute__((aligned(16))) uint32_t s_map[2][2][8][64];   // map entries: operand, half of them, wave, slab and row
+__global__ void __launch_bounds__(wg::NT, 2) k_bf16_wgrad(Bf16Wgrad p, uint32_t n_nt, uint32_t n_kt, uint32_t order) {
+  using namespace wg;
+  using t16::OOB;
+  using t16::lds_u8;
+  using t16::s16x4;
+  using t16::rsrc4;
+  using t16::load_lds;
+  using t16::load_lds4;
+  using t16::wait_vm;
+  __shared__ __attribute__((aligned(16))) uint8_t ring[NS * STAGE];
+  __shared__ __attribute__((aligned(16))) WTile s_tile[LIST];   // this workgroup's next tiles
+  __shared__ __attribute__((aligned(16))) uint32_t s_map[2][2][4][64];   // map entries: operand, half of them, wave, slab and row
   const int tid = threadIdx.x, l = tid & 63, li = l & 15, q = l >> 4;
-  const int w = __builtin_amdgcn_readfirstlane(tid >> 6), wm = w >> 1, wn = w & 1, grp = w >> 2;
+  const int w = __builtin_amdgcn_readfirstlane(tid >> 6), wm = w >> 1, wn = w & 1;
   const uint32_t lds0 = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_u8)ring);
   const uint32_t ldsm = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_u8)(uint8_t*)s_map);
   const int E = p.E;
   const int32_t M = (int32_t)p.M;
-  for (int e = tid; e <= E; e += NT) {
-    const int32_t o = p.off[e];
-    s_off[e] = o < 0 ? 0 : (o < M ? o : M);
-  }
-  __syncthreads();
   const uint32_t per_e = n_nt * n_kt, total = per_e * E, xcd = blockIdx.x % 8, stride = gridDim.x / 8;
   const uint32_t chunk = total >= 16 * per_e ? per_e : (total + gridDim.x - 1) / gridDim.x;
   const uint32_t N = (uint32_t)p.N, K = (uint32_t)p.K, ldd = N * 2, lda = K * 2;
@@ -47,42 +57,41 @@ __global__ void __launch_bounds__(t16::NT, 1) k_bf16_wgrad(Bf16Wgrad p, uint32_t
   };
 
   // ------------------------------------------------------------- load stream
+  // It runs two slabs ahead of the multiplication, through the tiles' ends.
   uint32_t ln = 0, n_my = 0;
   int32_t lr = 0, left = 0;          // the next slab's first row in its expert, the expert's rows from there
   u32x4 rd, ra;
-  uint32_t vod[4], voa[4], cd[4], ca[4];   // offsets; with a map those of the columns
+  uint32_t vod[2], voa[4], cd[2], ca[4];   // offsets; with a map those of the columns
   uint32_t batch = 0;                // eight slabs' map entries that have been taken up
   auto tile = [&](uint32_t i) __attribute__((always_inline)) {
     const WTile x = s_tile[i];
     return WTile{__builtin_amdgcn_readfirstlane(x.e), __builtin_amdgcn_readfirstlane(x.at), __builtin_amdgcn_readfirstlane(x.row0),
                  __builtin_amdgcn_readfirstlane(x.rows)};
   };
-  // the chunk (16 bytes) that lands in this lane's slot l % 32 of load t, row 8 w + 2 t + l / 32 of the slab
-  auto chunk_of = [&](int t, int l) __attribute__((always_inline)) { return (uint32_t)(l & 31) ^ (4 * ((2 * t + (l >> 5)) & 3)) ^ (2 * (w & 1)); };
+  // Rows 8 w .. 8 w + 7 of a slab are this wave's to load: dy's 8 w + 4 t + l / 16,
+  // a's 8 w + 2 t + l / 32; and the chunk (16 bytes) that lands in the lane's slot
+  auto row_d = [&](int t, int l) __attribute__((always_inline)) { return 4 * t + (l >> 4); };
+  auto row_a = [&](int t, int l) __attribute__((always_inline)) { return 2 * t + (l >> 5); };
+  auto chunk_d = [&](int t, int l) __attribute__((always_inline)) { return (uint32_t)(l & 15) ^ (4 * (l >> 4)) ^ (2 * (w & 1)); };
+  auto chunk_a = [&](int t, int l) __attribute__((always_inline)) { return (uint32_t)(l & 31) ^ (4 * (row_a(t, l) & 3)) ^ (2 * (w & 1)); };
   // requests the map entries of the eight slabs from row r of the expert's rows
-  // (row0 .., n of them) on: this wave's rows 8 w + 2 t + h of slab s to s 8 + h 4 + t
+  // (row0 .., n of them) on: this wave's of slab s to 8 s on, in the order in
+  // which a lane takes them (dy: row 4 t + g to 2 g + t, a: row 2 t + h to 4 h + t)
   auto fetch = [&](int32_t row0, int32_t n, int32_t r) __attribute__((always_inline)) {
     const int x = lane();
-    const uint32_t o = 4 * (r + BK * (x >> 3) + 8 * w + 2 * (x & 3) + ((x >> 2) & 1));
-    __builtin_amdgcn_s_waitcnt(WAIT_LGKM0);   // (the entries there have been read)
-    const uint32_t to = ldsm + ((batch & 1) * 8 + w) * 256;
-    if (p.dy_map) load_lds4(rsrc4(p.dy_map + row0, (uint64_t)n * 4), to, o);
-    if (p.a_map) load_lds4(rsrc4(p.a_map + row0, (uint64_t)n * 4), to + 4096, o);
+    const uint32_t o = 4 * (r + BK * (x >> 3) + 8 * w);
+    __builtin_amdgcn_s_waitcnt(t16::WAIT_LGKM0);   // (the entries there have been read)
+    const uint32_t to = ldsm + ((batch & 1) * 4 + w) * 256;
+    if (p.dy_map) load_lds4(rsrc4(p.dy_map + row0, (uint64_t)n * 4), to, o + 4 * (4 * (x & 1) + ((x >> 1) & 3)));
+    if (p.a_map) load_lds4(rsrc4(p.a_map + row0, (uint64_t)n * 4), to + 2048, o + 4 * (2 * (x & 3) + ((x >> 2) & 1)));
     ++batch;
   };
-  // a mapped operand's offsets for the next slab
-  auto gather = [&](uint32_t (&vo)[4], int op, const uint32_t (&c)[4], uint32_t rows, uint32_t ld) __attribute__((always_inline)) {
-    // (the half being read is the one not being filled)
-    const u32x4 m = *reinterpret_cast<const u32x4*>(&s_map[op][batch & 1][w][8 * ((lr / BK) & 7) + 4 * (l >> 5)]);
-    bool bad = false;
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      const uint32_t row = udiv_magic(m[t], p.div, p.magic);
-      const bool in = 8 * w + 2 * t + (l >> 5) < left, ok = (int32_t)m[t] >= 0 && row < rows;
-      bad |= in && !ok;
-      vo[t] = in && ok ? row * ld + c[t] : OOB;
-    }
-    if (__any(bad) && l == 0) atomicOr(&g_dev_err, MOE4_DEVERR_INDEX);
+  // a mapped row's offset; rows that do not exist are noted in bad
+  auto gather = [&](uint32_t m, bool in, uint32_t c, uint32_t rows, uint32_t ld, bool& bad) __attribute__((always_inline)) {
+    const uint32_t row = udiv_magic(m, p.div, p.magic);
+    const bool ok = (int32_t)m >= 0 && row < rows;
+    bad |= in && !ok;
+    return in && ok ? row * ld + c : OOB;
   };
   WTile lt{0, 0, 0, 0};              // the tile being loaded
   const bool mapped = p.dy_map || p.a_map;
@@ -105,13 +114,28 @@ __global__ void __launch_bounds__(t16::NT, 1) k_bf16_wgrad(Bf16Wgrad p, uint32_t
         ln = keep;
       }
     }
-    if (p.dy_map) gather(vod, 0, cd, (uint32_t)p.dy_rows, ldd);
-    if (p.a_map) gather(voa, 1, ca, (uint32_t)p.a_rows, lda);
+    // (the half being read is the one not being filled)
+    const uint32_t at = (batch & 1) * 256 + w * 64 + 8 * ((lr / BK) & 7);
+    bool bad = false;
+    if (p.dy_map) {
+      const u32x2 m = *reinterpret_cast<const u32x2*>(&s_map[0][0][0][0] + at + 2 * q);
+#pragma unroll
+      for (int t = 0; t < 2; ++t) vod[t] = gather(m[t], 8 * w + row_d(t, l) < left, cd[t], (uint32_t)p.dy_rows, ldd, bad);
+    }
+    if (p.a_map) {
+      const u32x4 m = *reinterpret_cast<const u32x4*>(&s_map[1][0][0][0] + at + 4 * (l >> 5));
+#pragma unroll
+      for (int t = 0; t < 4; ++t) voa[t] = gather(m[t], 8 * w + row_a(t, l) < left, ca[t], (uint32_t)p.a_rows, lda, bad);
+    }
+    if (__any(bad) && l == 0) atomicOr(&g_dev_err, MOE4_DEVERR_INDEX);
   };
   // the loads go on with tile ln, passing over those of experts without rows
   auto bind = [&]() __attribute__((always_inline)) {
     const WTile x = lt = skip(ln);
     ++ln;
+    // (its map entries were requested with the first slab of the tile before: with
+    // its only one, they have not been waited for)
+    if (mapped && lr <= BK && x.rows) __builtin_amdgcn_s_waitcnt(wait_vm(0));
     lr = 0;
     left = x.rows;
     if (left == 0) {   // (descriptors of nothing: every slab has as many loads)
@@ -125,26 +149,30 @@ __global__ void __launch_bounds__(t16::NT, 1) k_bf16_wgrad(Bf16Wgrad p, uint32_t
     ra = p.a_map ? rsrc4(p.a, (uint64_t)p.a_rows * lda) : rsrc4(p.a + (int64_t)x.row0 * p.K, (uint64_t)left * lda);
 #pragma unroll
     for (int t = 0; t < 4; ++t) {
-      const uint32_t c = chunk_of(t, l), k = 8 * w + 2 * t + (l >> 5);
-      cd[t] = n0 + 8 * c < N ? 2 * n0 + 16 * c : OOB;
-      ca[t] = k0 + 8 * c < K ? 2 * k0 + 16 * c : OOB;
-      vod[t] = k * ldd + cd[t];
-      voa[t] = k * lda + ca[t];
+      if (t < 2) {
+        const uint32_t c = n0 + 8 * chunk_d(t, l);
+        cd[t] = c < N ? 2 * c : OOB;
+        vod[t] = (8 * w + row_d(t, l)) * ldd + cd[t];
+      }
+      const uint32_t c = k0 + 8 * chunk_a(t, l);
+      ca[t] = c < K ? 2 * c : OOB;
+      voa[t] = (8 * w + row_a(t, l)) * lda + ca[t];
     }
   };
   auto step = [&](u32x4& rs, uint32_t ld) __attribute__((always_inline)) {
     const uint64_t base = ((uint64_t)rs[1] << 32 | rs[0]) + BK * ld;
     rs = rsrc4(reinterpret_cast<const void*>(base), (uint64_t)left * ld);
   };
-  // the next slab of the stream into a slot of the ring
-  auto issue = [&](uint32_t stage) __attribute__((always_inline)) {
+  // the next slab: its rows, its loads one at a time, and on
+  auto ready = [&]() __attribute__((always_inline)) {
     if (left == 0) bind();
     if (mapped && left) set_rows();
-#pragma unroll
-    for (int t = 0; t < 4; ++t) {
-      load_lds(rd, lds0 + stage * STAGE + (4 * w + t) * 1024, vod[t], 0);
-      load_lds(ra, lds0 + stage * STAGE + HALF + (4 * w + t) * 1024, voa[t], 0);
-    }
+  };
+  auto load = [&](int t, uint32_t st) __attribute__((always_inline)) {
+    if (t < 2) load_lds(rd, lds0 + st + (2 * w + t) * 1024, vod[t & 1], 0);
+    else load_lds(ra, lds0 + st + HALF + (4 * w + t - 2) * 1024, voa[(t - 2) & 3], 0);
+  };
+  auto advance = [&]() __attribute__((always_inline)) {
     lr += BK;
     left = left > BK ? left - BK : 0;
     if (!p.dy_map) step(rd, ldd);
@@ -152,37 +180,38 @@ __global__ void __launch_bounds__(t16::NT, 1) k_bf16_wgrad(Bf16Wgrad p, uint32_t
   };
 
   // --------------------------------------------------------------- fragments
-  // (swizzle and columns as in gemm_bf16.hip's float32 results)
-  const uint32_t lb = HALF + (8 * q + (li >> 2)) * 512 + 16 * (16 * wn + (((li & 3) >> 1) ^ (4 * (li >> 2)) ^ (2 * (q & 1)))) + 8 * (li & 1);
+  // A transposed read takes 4 rows x 32 bytes from each 16 lanes.  The 16-byte
+  // chunk c of row r sits at c ^ 4 (r % 4) ^ 2 (r / 8 % 2): 32 lanes hit every bank once.
+  const uint32_t sw = (4 * (li >> 2)) ^ (2 * (q & 1)), fr = 8 * q + (li >> 2);
+  const uint32_t lb = HALF + fr * 512 + 16 * (16 * wn + (((li & 3) >> 1) ^ sw)) + 8 * (li & 1);
   typedef __attribute__((address_space(3))) s16x4* lp;
-  auto read_tr = [&](bf16x8& f, uint32_t at) __attribute__((always_inline)) {
+  auto read_tr = [&](bf16x8& f, uint32_t at, uint32_t four_rows) __attribute__((always_inline)) {
     const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)(lds_u8)(ring + at));
-    const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)(lds_u8)(ring + at + 2048));
+    const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)(lds_u8)(ring + at + four_rows));
     f = __builtin_bit_cast(bf16x8, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
   };
-  auto barrier = [&]() __attribute__((always_inline)) {
-    __builtin_amdgcn_sched_barrier(0);
-    __builtin_amdgcn_s_waitcnt(WAIT_LGKM0);
-    __builtin_amdgcn_s_barrier();
-    __builtin_amdgcn_sched_barrier(0);
-    asm volatile("" ::: "memory");
-  };
 
-  for (uint32_t j0 = 0;; j0 += NT) {
-    {
+  for (uint32_t j0 = 0;; j0 += LIST) {
+    if (tid < LIST) {
       const uint32_t J = (j0 + tid) * stride + blockIdx.x / 8, c = J / chunk, t = (c * 8 + xcd) * chunk + (J - c * chunk);
-      WTile x{0, 0, 0, 0};
+      WTile x{-1, 0, 0, 0};
       if (t < total) {
         const uint32_t i = t / per_e, r = t - i * per_e;
         x.e = (int32_t)((uint64_t)i * order % (uint32_t)E);
         const uint32_t nt = r / n_kt;
         x.at = (int32_t)(nt << 16 | (r - nt * n_kt));
-        x.row0 = s_off[x.e];
-        x.rows = s_off[x.e + 1] > x.row0 ? s_off[x.e + 1] - x.row0 : 0;
+        int32_t r0 = p.off[x.e], r1 = p.off[x.e + 1];
+        r0 = r0 < 0 ? 0 : (r0 < M ? r0 : M);
+        r1 = r1 < M ? r1 : M;
+        x.row0 = r0;
+        x.rows = r1 > r0 ? r1 - r0 : 0;
       }
       s_tile[tid] = x;
-      n_my = __syncthreads_count(t < total);
     }
+    __syncthreads();
+    n_my = 0;
+    for (uint32_t i = LIST; i; i >>= 1)   // (the tiles come first)
+      if (n_my + i <= LIST && __builtin_amdgcn_readfirstlane(s_tile[n_my + i - 1].e) >= 0) n_my += i;
     if (n_my == 0) break;
     ln = 0;
     left = 0;
@@ -191,97 +220,102 @@ __global__ void __launch_bounds__(t16::NT, 1) k_bf16_wgrad(Bf16Wgrad p, uint32_t
       fetch(x.row0, x.rows, 0);
       __builtin_amdgcn_s_waitcnt(wait_vm(0));
     }
-    issue(0);
-    __builtin_amdgcn_s_waitcnt(wait_vm(0));
-    barrier();
-    if (grp) barrier();
-    uint32_t gs = 0;       // the slab's place in the ring
-    int stored = -1;       // memory operations of the last epilogue, at least (-1: there was none)
+    for (int s = 0; s < 2; ++s) {
+      ready();
+#pragma unroll
+      for (int t = 0; t < NL; ++t) load(t, s * STAGE);
+      advance();
+    }
+    uint32_t gs = 0, st2 = 2 * STAGE;   // the slab's place in the ring, and that of the one two slabs on
+    int stored = 0;                     // memory operations of the last epilogue, at least
     for (uint32_t ct = 0; ct < n_my; ++ct) {
       const WTile m = tile(ct);
       const uint32_t nt = (uint32_t)(m.at >> 16), kt = (uint32_t)(m.at & 0xFFFF), nk = ((uint32_t)m.rows + BK - 1) / BK;
       if (nk == 0 && (p.beta != 0.0f || !p.zero_empty)) continue;
       const uint32_t tn = N - nt * TM < TM ? N - nt * TM : TM;
-      const int mb = (int)((tn + 63) / 64);   // blocks of 16 of a wave
+      const int mb = (int)((tn + 31) / 32);   // blocks of 16 of a wave
       f32x4 acc[4][8];
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int n = 0; n < 8; ++n) acc[i][n] = f32x4{};
-      uint32_t ao[4];   // and for A's blocks: chunks 2 mb wm + 2 i and + 1 of the row
+      uint32_t ao[4];   // dy's blocks: chunks 2 mb wm + 2 i and + 1 of the row
       {
         const int x = lane() & 15, q = lane() >> 4, j = x >> 2, s = x & 3;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) ao[i] = (8 * q + j) * 512 + 8 * (s & 1) + 16 * ((2 * mb * wm + 2 * i + (s >> 1)) ^ (4 * j) ^ (2 * (q & 1)));
+        for (int i = 0; i < 4; ++i) ao[i] = (8 * q + j) * 256 + 8 * (s & 1) + 16 * ((2 * mb * wm + 2 * i + (s >> 1)) ^ (4 * j) ^ (2 * (q & 1)));
       }
-      bf16x8 fa[4], fb[8];
-      auto reads = [&](int h) __attribute__((always_inline)) {
-        const uint32_t st = gs * STAGE + 16384 * h;
+      for (uint32_t s = 0; s < nk; ++s) {
+        // This slab has landed: newer are the next one's loads and, in a tile's
+        // first two, the last tile's stores.  Past the barrier so have the other
+        // waves' loads, and the slab before has been read.
+        __builtin_amdgcn_sched_barrier(0);
+        if (s >= 2 || stored < 8) __builtin_amdgcn_s_waitcnt(wait_vm(NL));
+        else if (stored >= 32) __builtin_amdgcn_s_waitcnt(wait_vm(NL + 32));
+        else if (stored >= 16) __builtin_amdgcn_s_waitcnt(wait_vm(NL + 16));
+        else __builtin_amdgcn_s_waitcnt(wait_vm(NL + 8));
+        __builtin_amdgcn_s_barrier();
+        __builtin_amdgcn_sched_barrier(0);
+        asm volatile("" ::: "memory");
+        bf16x8 fa[4], fb[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-          read_tr(fb[i], (st + lb) ^ (32 * i));
-          if (i < 4) read_tr(fa[i], st + ao[i]);
+          read_tr(fb[i], (gs + lb) ^ (32 * i), 2048);
+          if (i < 4) read_tr(fa[i], gs + ao[i], 1024);
         }
-      };
-      auto mfmas = [&](bool bar) __attribute__((always_inline)) {
+        ready();
         __builtin_amdgcn_s_setprio(1);
 #pragma unroll
-        for (int i = 3; i >= 0; --i) {
+        for (int i = 0; i < 4; ++i) {
           if (i < mb) {
 #pragma unroll
-            for (int n = 0; n < (i ? 8 : 4); ++n) acc[i][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[n], fa[i], acc[i][n], 0, 0, 0);
+            for (int n = 0; n < 8; ++n) {
+              acc[i][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[n], fa[i], acc[i][n], 0, 0, 0);
+            }
           }
+          load(i, st2);
+          if (i >= 2) load(i + 2, st2);
         }
-        if (bar) barrier();
-#pragma unroll
-        for (int n = 4; n < 8; ++n) acc[0][n] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(fb[n], fa[0], acc[0][n], 0, 0, 0);
         __builtin_amdgcn_s_setprio(0);
-      };
-      for (uint32_t s = 0; s < nk; ++s) {
-        reads(0);
-        if (stored < 0) {
-          issue(1 - gs);
-          stored = 0;
-        }
-        barrier();
-        mfmas(true);
-        reads(1);
-        if (grp) wait_but(stored);
-        barrier();
-        if (!grp) wait_but(stored);
-        stored = -1;
-        mfmas(!(grp && s == nk - 1));
-        gs = 1 - gs;
+        advance();
+        st2 = gs;
+        gs = gs == (NS - 1) * STAGE ? 0 : gs + STAGE;
       }
-      if (nk) {
-        issue(1 - gs);
-        stored = 8 * mb;
-      }
+      if (nk) stored = 8 * mb;
       const int64_t row0 = (int64_t)m.e * p.N + (int64_t)nt * TM;
       const __amdgpu_buffer_rsrc_t rc = make_rsrc(p.dw + row0 * p.K, (uint64_t)tn * K * 4);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         if (i < mb) {
-          const int li = lane() & 15, q = lane() >> 4;
-          const uint32_t r = 16 * mb * wm + 16 * i + li;
+          const int l = lane();
+          const uint32_t r = 16 * mb * wm + 16 * i + (l >> 3);
 #pragma unroll
-          for (int n = 0; n < 8; ++n) {
-            const uint32_t k = kt * TN + 128 * wn + 16 * n + 4 * q, o = k < K ? r * K + k : PAST;
-            float z[4] = {acc[i][n][0], acc[i][n][1], acc[i][n][2], acc[i][n][3]};
-            if (p.beta != 0.0f) {
-              float v[4];
-              load_f32<4>(rc, o, v);
+          for (int n = 0; n < 8; n += 2) {
+            const uint32_t k = kt * TN + 128 * wn + 16 * n + 4 * (l & 7), o = k < K ? r * K + k : PAST, o8 = k < K ? o + 8 * K : PAST;
+            float x[4], y[4];
 #pragma unroll
-              for (int x = 0; x < 4; ++x) z[x] = v[x] + z[x];
+            for (int v = 0; v < 4; ++v) {
+              x[v] = acc[i][n][v];
+              y[v] = acc[i][n + 1][v];
             }
-            store_f32<4>(rc, o, z);
+            t16::store_order(x, y, l);
+            if (p.beta != 0.0f) {
+              float a[4], b[4];
+              load_f32<4>(rc, o, a);
+              load_f32<4>(rc, o8, b);
+#pragma unroll
+              for (int v = 0; v < 4; ++v) {
+                x[v] = a[v] + x[v];
+                y[v] = b[v] + y[v];
+              }
+            }
+            store_f32<4, NT_STORE>(rc, o, x);
+            store_f32<4, NT_STORE>(rc, o8, y);
           }
           __builtin_amdgcn_sched_barrier(0);
         }
       }
-      if (grp && nk) barrier();
     }
-    if (!grp) barrier();
     __builtin_amdgcn_s_waitcnt(wait_vm(0));   // (no load into this workgroup's LDS outlives it)
     __syncthreads();
   }
@@ -347,7 +381,7 @@ extern "C" int moe_grouped_gemm_bf16_wgrad(const uint16_t* dy, int64_t dy_rows, 
   const Bf16Wgrad p{dy, a, dy_map, a_map, expert_off, db_scale, dw, db, dy_rows, a_rows, M_total, N, K, (uint32_t)map_div, magic, E, beta,
                     (flags & MOE4_WGRAD_SKIP_EMPTY) == 0};
   hipStream_t st = as_stream(stream);
-  const int64_t nt = (N + t16::TM - 1) / t16::TM, kt = (K + t16::TN - 1) / t16::TN;
+  const int64_t nt = (N + wg::TM - 1) / wg::TM, kt = (K + wg::TN - 1) / wg::TN;
   MOE4_REQUIRE(nt * kt * E < ((int64_t)1 << 31), MOE4_EINVAL, s + ": too large");
   // a step through the experts near the golden section of E, coprime to it
   uint32_t order = (uint32_t)(0.618 * E);
@@ -360,7 +394,7 @@ extern "C" int moe_grouped_gemm_bf16_wgrad(const uint16_t* dy, int64_t dy_rows, 
     return a;
   };
   while (order < 1 || gcd(order, (uint32_t)E) != 1) ++order;
-  hipLaunchKernelGGL(k_bf16_wgrad, dim3((unsigned)tile_grid()), dim3(t16::NT), 0, st, p, (uint32_t)nt, (uint32_t)kt, order);
+  hipLaunchKernelGGL(k_bf16_wgrad, dim3(2 * (unsigned)tile_grid()), dim3(wg::NT), 0, st, p, (uint32_t)nt, (uint32_t)kt, order);
   if (db) hipLaunchKernelGGL(k_bias_grad_bf16, dim3((unsigned)((N + 63) / 64), (unsigned)E), dim3(1024), 0, st, p);
   return check_launch(s.c_str());
 }
