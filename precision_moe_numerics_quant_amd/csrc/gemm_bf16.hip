@@ -31,8 +31,8 @@ __global__ void __launch_bounds__(t16::NT, 1) k_bf16_tile(Bf16Args p, int cap, u
   constexpr bool TR = MODE == DGRAD || MODE == GDGRAD;   // w's columns are the product's: read transposed
   constexpr int NW = MODE == GATED ? TN / 2 : TN;        // the tile's columns
   // Column of block n, lane quarter q, value v of a wave's 128: with float32
-  // results 16 n + 4 q + v, with bf16 ones 32 (n / 2) + 8 q + 4 (n % 2) + v, so
-  // that four lanes store 64 consecutive bytes of a row either way.
+  // results 16 n + 4 q + v, with bf16 ones 32 (n / 2) + 8 q + 4 (n % 2) + v: four
+  // lanes have 64 consecutive bytes of a row either way (see store_order).
   constexpr bool PAIR = OUT_BF16;
   __shared__ __attribute__((aligned(16))) uint8_t ring[RING];
   __shared__ __attribute__((aligned(16))) Tile s_tile[NT];   // this workgroup's next tiles
@@ -368,30 +368,35 @@ __global__ void __launch_bounds__(t16::NT, 1) k_bf16_tile(Bf16Args p, int cap, u
       }
       late();
       stored = (MODE == GATED ? (p.aux ? 6 : 2) : MODE == GDGRAD || !OUT_BF16 ? 8 : 4) * mb;
-      const Bf16Epilogue<MODE, OUT_BF16> epi(p, m.e, m.row0, m.rows);
+      const Bf16Epilogue<MODE, OUT_BF16, NT_STORE> epi(p, m.e, m.row0, m.rows);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         if (i < mb) {
-          const int li = lane() & 15, q = lane() >> 4, r = 16 * mb * wm + 16 * i + li;
-          const float sc = (MODE == DGRAD || MODE == GDGRAD) && r < m.rows ? row_scale(p.scale, p.map, (int64_t)m.row0 + r, p.a_rows * p.div) : 1.0f;
-          if (PAIR) {
+          const int l = lane(), r = 16 * mb * wm + 16 * i + (l >> 3);
+          auto scale = [&](int r) __attribute__((always_inline)) {
+            return (MODE == DGRAD || MODE == GDGRAD) && r < m.rows ? row_scale(p.scale, p.map, (int64_t)m.row0 + r, p.a_rows * p.div) : 1.0f;
+          };
+          const float s0 = scale(r), s1 = scale(r + 8);
+          constexpr int W = PAIR ? 8 : 4;   // values of a lane
+          const uint32_t n0 = m.nt * NW + (MODE == GATED ? 64 : 128) * wn + W * (l & 7);
 #pragma unroll
-            for (int pb = 0; pb < (MODE == GATED ? 2 : 4); ++pb) {
-              const uint32_t n = m.nt * NW + (MODE == GATED ? 64 : 128) * wn + 32 * pb + 8 * q;
-              const f32x4 x = acc[i][2 * pb], y = acc[i][2 * pb + 1];
-              const f32x4 x1 = acc[i][MODE == GATED ? 2 * pb + 4 : 0], y1 = acc[i][MODE == GATED ? 2 * pb + 5 : 0];
-              const float z[8] = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
-              const float z1[8] = {x1[0], x1[1], x1[2], x1[3], y1[0], y1[1], y1[2], y1[3]};
-              epi.template put<8>(r, n, sc, z, z1);
-              __builtin_amdgcn_sched_barrier(0);
-            }
-          } else {
+          for (int b = 0; b < (MODE == GATED ? 4 : 8); b += W / 2) {
+            float x[W], y[W], x1[W], y1[W];
 #pragma unroll
-            for (int n = 0; n < 8; ++n) {
-              const float z[4] = {acc[i][n][0], acc[i][n][1], acc[i][n][2], acc[i][n][3]};
-              epi.template put<4>(r, m.nt * NW + 128 * wn + 16 * n + 4 * q, sc, z, z);
-              __builtin_amdgcn_sched_barrier(0);
+            for (int v = 0; v < W; ++v) {
+              x[v] = acc[i][b + v / 4][v % 4];
+              y[v] = acc[i][b + W / 4 + v / 4][v % 4];
+              if (MODE == GATED) {
+                x1[v] = acc[i][(b + 4 + v / 4) % 8][v % 4];
+                y1[v] = acc[i][(b + 4 + W / 4 + v / 4) % 8][v % 4];
+              }
             }
+            store_order(x, y, l);
+            if (MODE == GATED) store_order(x1, y1, l);
+            epi.template put<W>(r, n0 + 16 * b, s0, x, x1);
+            __builtin_amdgcn_sched_barrier(0);
+            epi.template put<W>(r + 8, n0 + 16 * b, s1, y, y1);
+            __builtin_amdgcn_sched_barrier(0);
           }
         }
       }
@@ -501,7 +506,7 @@ __global__ void __launch_bounds__(b16r::NT) k_bf16_rows(Bf16Args p, uint32_t n_n
     weights(wq[0], i + 2 * NU);
     multiply(wq[1], i + NU);
   }
-  const Bf16Epilogue<MODE, OUT_BF16> epi(p, e, r0, rows);
+  const Bf16Epilogue<MODE, OUT_BF16, 0> epi(p, e, r0, rows);
 #pragma unroll
   for (int s = 0; s < PASSES; ++s) {
     if (s < np) {
