@@ -864,11 +864,15 @@ int moe_gated_gemm_bf16_dgrad(const uint16_t* dy, int64_t dy_rows, const int32_t
  * (map_div for both); dw [E, N, K], db [E, N] (or NULL) float32.  beta 0 or 1.
  * Experts without rows: zeros, or with MOE4_WGRAD_SKIP_EMPTY in flags (or beta
  * = 1) left as they are.
+ * ws: moe_grouped_gemm_bf16_wgrad_ws_bytes(E, M_total, N, K) bytes, 16-byte aligned
+ * (0 unless few experts have many rows: then the sums of slices of their rows,
+ * joined in order); calls in flight at the same time need workspaces of their own.
  */
 int moe_grouped_gemm_bf16_wgrad(const uint16_t* dy, int64_t dy_rows, const int32_t* dy_map, const uint16_t* a,
                                 int64_t a_rows, const int32_t* a_map, int32_t map_div, const int32_t* expert_off,
                                 int32_t E, int64_t M_total, int64_t N, int64_t K, float* dw, float beta, int flags,
-                                const float* db_scale, float* db, void* stream);
+                                const float* db_scale, float* db, void* ws, size_t ws_bytes, void* stream);
+size_t moe_grouped_gemm_bf16_wgrad_ws_bytes(int32_t E, int64_t M_total, int64_t N, int64_t K);
 
 /*
  * moe_combine_dropout - moe_combine, dropout and residual in one pass:

@@ -116,7 +116,9 @@ _SIGS = {
     "moe_gated_gemm_bf16_dgrad": (_int, [_c_void_p, _i64, _c_void_p, _i32, _c_void_p, _c_void_p, _c_void_p, _i32, _i64,
                                          _i64, _i64, _int, _c_void_p, _c_void_p, _c_void_p, _c_void_p]),
     "moe_grouped_gemm_bf16_wgrad": (_int, [_c_void_p, _i64, _c_void_p, _c_void_p, _i64, _c_void_p, _i32, _c_void_p, _i32,
-                                           _i64, _i64, _i64, _c_void_p, _f32, _int, _c_void_p, _c_void_p, _c_void_p]),
+                                           _i64, _i64, _i64, _c_void_p, _f32, _int, _c_void_p, _c_void_p, _c_void_p, _size,
+                                           _c_void_p]),
+    "moe_grouped_gemm_bf16_wgrad_ws_bytes": (_size, [_i32, _i64, _i64, _i64]),
     "moe_combine_dropout": (_int, [_c_void_p, _c_void_p, _c_void_p, _i64, _i32, _i64, _f64, _u64, _u32, _c_void_p,
                                    _c_void_p, _c_void_p]),
     "moe_dropout_backward": (_int, [_c_void_p, _i64, _i64, _f64, _u64, _u32, _c_void_p, _c_void_p]),
@@ -768,8 +770,9 @@ def moe_grouped_gemm_bf16_wgrad(dy, a, expert_off, dy_map=None, a_map=None, map_
     elif bias_grad:
         db = _empty((max(E, 0), N), torch.float32, dy)
     _row_scale(db_scale, dy, dy_map, map_div, "db_scale")
+    ws = _ws(lib().moe_grouped_gemm_bf16_wgrad_ws_bytes(E, M, N, K), dy)
     _run("moe_grouped_gemm_bf16_wgrad", dy, dy, dy.shape[0], dy_map, a, a.shape[0], a_map, map_div, expert_off, E, M, N, K, dw,
-         float(beta), WGRAD_SKIP_EMPTY if skip_empty else 0, db_scale, db)
+         float(beta), WGRAD_SKIP_EMPTY if skip_empty else 0, db_scale, db, ws, ws.numel())
     return dw, db
 
 

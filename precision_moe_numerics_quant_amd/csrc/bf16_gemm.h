@@ -274,6 +274,8 @@ struct Bf16Wgrad {
   int E;
   float beta;
   bool zero_empty;
+  int slices, db_slices;             // of each expert's rows (1: dw and db themselves are written)
+  float *dw_part, *db_part;          // the slices' sums [E, slices, N, K] and [E, db_slices, N]
 };
 
 }  // namespace moe4

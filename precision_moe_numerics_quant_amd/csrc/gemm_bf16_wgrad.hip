@@ -14,10 +14,30 @@ constexpr int TM = 128, TN = 256, BK = 32;   // tile (of dy's and of a's columns
 constexpr int HALF = BK * TM * 2, STAGE = HALF + BK * TN * 2, NS = 3;   // dy's part of a slab, a slab, the ring's slabs
 constexpr int NL = 6;                     // a wave's loads of a slab: two of dy, four of a
 constexpr int LIST = 128;                 // tiles listed at a time
+constexpr int SLOTS = 512;                // workgroups at a time: two on each of 256 CUs
 }  // namespace wg
 
-// A tile of an expert's gradient: n-tile nt (of dy's columns), k-tile kt (of a's;
-// at = nt 2^16 + kt), the expert's rows.
+// Slice i of n rows: whole slabs, as even as they get; rows r .. r + m - 1.
+struct Slice {
+  int32_t r, m;
+  __device__ Slice(int32_t n, int i, int slices) {
+    const int64_t slabs = (n + wg::BK - 1) / wg::BK;
+    r = (int32_t)(slabs * i / slices) * wg::BK;
+    const int64_t end = slabs * (i + 1) / slices * wg::BK;
+    m = (int32_t)(end < n ? end : n) - r;
+  }
+};
+
+// An expert's first row and its rows, from offsets that need not be sound.
+__device__ inline int2 expert_rows(const int32_t* off, int e, int64_t M) {
+  int32_t r0 = off[e], r1 = off[e + 1];
+  r0 = r0 < 0 ? 0 : (r0 < (int32_t)M ? r0 : (int32_t)M);
+  r1 = r1 < (int32_t)M ? r1 : (int32_t)M;
+  return make_int2(r0, r1 > r0 ? r1 - r0 : 0);
+}
+
+// A tile of a slice's sum: n-tile nt (of dy's columns), k-tile kt (of a's; at = nt
+// 2^16 + kt), the slice's rows; e: its number, slices e + slice.
 struct WTile {
   int32_t e, at, row0, rows;
 };
@@ -45,8 +65,10 @@ __global__ void __launch_bounds__(wg::NT, 2) k_bf16_wgrad(Bf16Wgrad p, uint32_t 
   const int w = __builtin_amdgcn_readfirstlane(tid >> 6), wm = w >> 1, wn = w & 1;
   const uint32_t lds0 = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_u8)ring);
   const uint32_t ldsm = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_u8)(uint8_t*)s_map);
-  const int E = p.E;
-  const int32_t M = (int32_t)p.M;
+  const int E = p.E * p.slices;      // (of here on: the slices)
+  float* const dw = p.slices > 1 ? p.dw_part : p.dw;
+  const float beta = p.slices > 1 ? 0.0f : p.beta;
+  const bool zero_empty = p.slices == 1 && p.zero_empty && beta == 0.0f;
   const uint32_t per_e = n_nt * n_kt, total = per_e * E, xcd = blockIdx.x % 8, stride = gridDim.x / 8;
   const uint32_t chunk = total >= 16 * per_e ? per_e : (total + gridDim.x - 1) / gridDim.x;
   const uint32_t N = (uint32_t)p.N, K = (uint32_t)p.K, ldd = N * 2, lda = K * 2;
@@ -200,11 +222,11 @@ __global__ void __launch_bounds__(wg::NT, 2) k_bf16_wgrad(Bf16Wgrad p, uint32_t 
         x.e = (int32_t)((uint64_t)i * order % (uint32_t)E);
         const uint32_t nt = r / n_kt;
         x.at = (int32_t)(nt << 16 | (r - nt * n_kt));
-        int32_t r0 = p.off[x.e], r1 = p.off[x.e + 1];
-        r0 = r0 < 0 ? 0 : (r0 < M ? r0 : M);
-        r1 = r1 < M ? r1 : M;
-        x.row0 = r0;
-        x.rows = r1 > r0 ? r1 - r0 : 0;
+        const int e = x.e / p.slices;
+        const int2 m = expert_rows(p.off, e, p.M);
+        const Slice sl(m.y, x.e - e * p.slices, p.slices);
+        x.row0 = m.x + sl.r;
+        x.rows = sl.m;
       }
       s_tile[tid] = x;
     }
@@ -231,7 +253,7 @@ __global__ void __launch_bounds__(wg::NT, 2) k_bf16_wgrad(Bf16Wgrad p, uint32_t 
     for (uint32_t ct = 0; ct < n_my; ++ct) {
       const WTile m = tile(ct);
       const uint32_t nt = (uint32_t)(m.at >> 16), kt = (uint32_t)(m.at & 0xFFFF), nk = ((uint32_t)m.rows + BK - 1) / BK;
-      if (nk == 0 && (p.beta != 0.0f || !p.zero_empty)) continue;
+      if (nk == 0 && !zero_empty) continue;
       const uint32_t tn = N - nt * TM < TM ? N - nt * TM : TM;
       const int mb = (int)((tn + 31) / 32);   // blocks of 16 of a wave
       f32x4 acc[4][8];
@@ -283,7 +305,7 @@ __global__ void __launch_bounds__(wg::NT, 2) k_bf16_wgrad(Bf16Wgrad p, uint32_t 
       }
       if (nk) stored = 8 * mb;
       const int64_t row0 = (int64_t)m.e * p.N + (int64_t)nt * TM;
-      const __amdgpu_buffer_rsrc_t rc = make_rsrc(p.dw + row0 * p.K, (uint64_t)tn * K * 4);
+      const __amdgpu_buffer_rsrc_t rc = make_rsrc(dw + row0 * p.K, (uint64_t)tn * K * 4);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         if (i < mb) {
@@ -299,7 +321,7 @@ __global__ void __launch_bounds__(wg::NT, 2) k_bf16_wgrad(Bf16Wgrad p, uint32_t 
               y[v] = acc[i][n + 1][v];
             }
             t16::store_order(x, y, l);
-            if (p.beta != 0.0f) {
+            if (beta != 0.0f) {
               float a[4], b[4];
               load_f32<4>(rc, o, a);
               load_f32<4>(rc, o8, b);
@@ -321,16 +343,18 @@ __global__ void __launch_bounds__(wg::NT, 2) k_bf16_wgrad(Bf16Wgrad p, uint32_t 
   }
 }
 
-// db: 64 columns of one expert per workgroup, eight a thread; thread row y sums
-// rows y, y + 128, ... in order, then the 128 sums are added in order.
+// db: 64 columns of one slice of an expert's rows per workgroup, eight a thread;
+// thread row y sums rows y, y + 128, ... in order, then the 128 sums are added in
+// order.
 __global__ void __launch_bounds__(1024) k_bias_grad_bf16(Bf16Wgrad p) {
   __shared__ float s[128][65];
-  const int e = blockIdx.y, cx = threadIdx.x & 7, y = threadIdx.x >> 3;
+  const int e = blockIdx.y / p.db_slices, i = blockIdx.y - e * p.db_slices, cx = threadIdx.x & 7, y = threadIdx.x >> 3;
   const int64_t n = (int64_t)blockIdx.x * 64 + 8 * cx;
-  int64_t r0 = p.off[e], r1 = p.off[e + 1];
-  r0 = r0 < 0 ? 0 : r0;
-  r1 = r1 < p.M ? r1 : p.M;
-  if (r0 >= r1 && (p.beta != 0.0f || !p.zero_empty)) return;
+  const int2 m = expert_rows(p.off, e, p.M);
+  const Slice sl(m.y, i, p.db_slices);
+  const int64_t r0 = m.x + (int64_t)sl.r, r1 = r0 + sl.m;
+  const bool part = p.db_slices > 1;
+  if (sl.m == 0 && (part || p.beta != 0.0f || !p.zero_empty)) return;
   float v[8] = {};
   if (n < p.N)
     for (int64_t r = r0 + y; r < r1; r += 128) {
@@ -348,7 +372,21 @@ __global__ void __launch_bounds__(1024) k_bias_grad_bf16(Bf16Wgrad p) {
   if (threadIdx.x >= 64 || c >= p.N) return;
   float t = 0.0f;
   for (int i = 0; i < 128; ++i) t = t + s[i][threadIdx.x];
-  float* d = p.db + (int64_t)e * p.N + c;
+  float* d = part ? p.db_part + (int64_t)blockIdx.y * p.N + c : p.db + (int64_t)e * p.N + c;
+  *d = !part && p.beta != 0.0f ? *d + t : t;
+}
+
+// The slices' sums [E, slices, L] joined in their order: dst [E, L] (L % 4 == 0).
+__global__ void __launch_bounds__(256) k_wgrad_join(Bf16Wgrad p, const float* part, int slices, float* dst, int64_t L) {
+  const int e = blockIdx.y;
+  const int64_t i = 4 * ((int64_t)blockIdx.x * 256 + threadIdx.x);
+  const int32_t n = expert_rows(p.off, e, p.M).y;
+  if (i >= L || (n == 0 && (p.beta != 0.0f || !p.zero_empty))) return;
+  f32x4* d = reinterpret_cast<f32x4*>(dst + e * L + i);
+  const f32x4* s = reinterpret_cast<const f32x4*>(part + (int64_t)e * slices * L + i);
+  f32x4 t = {};
+  for (int k = 0; k < slices; ++k)
+    if (Slice(n, k, slices).m) t = t + s[k * (L / 4)];
   *d = p.beta != 0.0f ? *d + t : t;
 }
 
@@ -356,10 +394,34 @@ __global__ void __launch_bounds__(1024) k_bias_grad_bf16(Bf16Wgrad p) {
 
 using namespace moe4;
 
+// Slices of each expert's rows: as many as give every workgroup slot one tile (a
+// tile's rows cannot be shared otherwise), of at least 256 rows on average.  16384 rows
+// of 1536 x 4096, 192 tiles on 512 slots: one slice 327 us,
+// two 229 us with the join (five, two tiles a slot: 240 us).
+static int wgrad_slices(int64_t items, int32_t E, int64_t M) {
+  int64_t n = wg::SLOTS / items;
+  n = n < M / E / 256 ? n : M / E / 256;
+  return n < 1 ? 1 : (n < 32 ? (int)n : 32);
+}
+static int dw_slices(int32_t E, int64_t M, int64_t N, int64_t K) {
+  return wgrad_slices((N + wg::TM - 1) / wg::TM * ((K + wg::TN - 1) / wg::TN) * E, E, M);
+}
+static int db_slices(int32_t E, int64_t M, int64_t N) { return wgrad_slices((N + 63) / 64 * E, E, M); }
+static size_t dw_part_bytes(int32_t E, int64_t M, int64_t N, int64_t K) {
+  const int n = dw_slices(E, M, N, K);
+  return n > 1 ? (size_t)n * E * N * K * 4 : 0;
+}
+
+extern "C" size_t moe_grouped_gemm_bf16_wgrad_ws_bytes(int32_t E, int64_t M_total, int64_t N, int64_t K) {
+  if (E < 1 || M_total < 0 || N < 1 || K < 1) return 0;
+  const int n = db_slices(E, M_total, N);
+  return dw_part_bytes(E, M_total, N, K) + (n > 1 ? (size_t)n * E * N * 4 : 0);
+}
+
 extern "C" int moe_grouped_gemm_bf16_wgrad(const uint16_t* dy, int64_t dy_rows, const int32_t* dy_map, const uint16_t* a, int64_t a_rows,
                                            const int32_t* a_map, int32_t map_div, const int32_t* expert_off, int32_t E, int64_t M_total,
                                            int64_t N, int64_t K, float* dw, float beta, int flags, const float* db_scale, float* db,
-                                           void* stream) {
+                                           void* ws, size_t ws_bytes, void* stream) {
   const std::string s("moe_grouped_gemm_bf16_wgrad");
   MOE4_REQUIRE(E >= 1 && E <= 2048 && M_total >= 0 && N > 0 && K > 0 && N % 8 == 0 && K % 8 == 0, MOE4_EINVAL,
                s + ": need 1 <= E <= 2048 and widths that are multiples of 8");
@@ -377,14 +439,20 @@ extern "C" int moe_grouped_gemm_bf16_wgrad(const uint16_t* dy, int64_t dy_rows, 
   MOE4_REQUIRE(db || !db_scale, MOE4_EINVAL, s + ": db_scale needs db");
   MOE4_REQUIRE(aligned16(dy) && aligned16(a) && aligned16(dw) && aligned16(db) && aligned4(db_scale) && aligned4(dy_map) && aligned4(a_map),
                MOE4_EALIGN, s + ": misaligned pointer");
+  const size_t need = moe_grouped_gemm_bf16_wgrad_ws_bytes(E, M_total, N, K), dw_bytes = dw_part_bytes(E, M_total, N, K);
+  MOE4_REQUIRE(need == 0 || (ws && ws_bytes >= need), MOE4_EWORKSPACE, s + ": workspace of moe_grouped_gemm_bf16_wgrad_ws_bytes() bytes required");
+  MOE4_REQUIRE(need == 0 || aligned16(ws), MOE4_EALIGN, s + ": ws must be 16-byte aligned");
   const uint32_t magic = map_div <= 1 ? 0xFFFFFFFFu : (uint32_t)(((uint64_t)1 << 32) / (uint32_t)map_div);
   const Bf16Wgrad p{dy, a, dy_map, a_map, expert_off, db_scale, dw, db, dy_rows, a_rows, M_total, N, K, (uint32_t)map_div, magic, E, beta,
-                    (flags & MOE4_WGRAD_SKIP_EMPTY) == 0};
+                    (flags & MOE4_WGRAD_SKIP_EMPTY) == 0, dw_slices(E, M_total, N, K), db_slices(E, M_total, N), static_cast<float*>(ws),
+                    reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + dw_bytes)};
   hipStream_t st = as_stream(stream);
   const int64_t nt = (N + wg::TM - 1) / wg::TM, kt = (K + wg::TN - 1) / wg::TN;
   MOE4_REQUIRE(nt * kt * E < ((int64_t)1 << 31), MOE4_EINVAL, s + ": too large");
-  // a step through the experts near the golden section of E, coprime to it
-  uint32_t order = (uint32_t)(0.618 * E);
+  // a step through the experts (their slices) near the golden section of their
+  // number, coprime to it
+  const uint32_t V = (uint32_t)(E * p.slices);
+  uint32_t order = (uint32_t)(0.618 * V);
   const auto gcd = [](uint32_t a, uint32_t b) {
     while (b) {
       const uint32_t c = a % b;
@@ -393,8 +461,15 @@ extern "C" int moe_grouped_gemm_bf16_wgrad(const uint16_t* dy, int64_t dy_rows, 
     }
     return a;
   };
-  while (order < 1 || gcd(order, (uint32_t)E) != 1) ++order;
+  while (order < 1 || gcd(order, V) != 1) ++order;
   hipLaunchKernelGGL(k_bf16_wgrad, dim3(2 * (unsigned)tile_grid()), dim3(wg::NT), 0, st, p, (uint32_t)nt, (uint32_t)kt, order);
-  if (db) hipLaunchKernelGGL(k_bias_grad_bf16, dim3((unsigned)((N + 63) / 64), (unsigned)E), dim3(1024), 0, st, p);
+  const auto join = [&](const float* part, int slices, float* dst, int64_t L) {
+    if (slices > 1) hipLaunchKernelGGL(k_wgrad_join, dim3((unsigned)((L + 1023) / 1024), (unsigned)E), dim3(256), 0, st, p, part, slices, dst, L);
+  };
+  join(p.dw_part, p.slices, dw, N * K);
+  if (db) {
+    hipLaunchKernelGGL(k_bias_grad_bf16, dim3((unsigned)((N + 63) / 64), (unsigned)(E * p.db_slices)), dim3(1024), 0, st, p);
+    join(p.db_part, p.db_slices, db, N);
+  }
   return check_launch(s.c_str());
 }

@@ -9,7 +9,7 @@ from test_capi_exports import _lib
 v = ctypes.c_void_p
 i64, i32, f32, f64 = ctypes.c_int64, ctypes.c_int32, ctypes.c_float, ctypes.c_double
 P, O = v(4096), v(0)         # an aligned address that no refused call touches; NULL
-EINVAL, EALIGN = -1, -2
+EINVAL, EALIGN, EWS = -1, -2, -3
 
 
 def call(name, *args):
@@ -72,13 +72,14 @@ def test_gated_dgrad_needs_gu():
     assert gated_dgrad({**DEF, "pre": O}) == EINVAL
 
 
-W = dict(dy=P, dyr=8, dym=O, a=P, ar=8, am=O, div=1, off=P, E=2, M=8, N=64, K=64, dw=P, beta=0.0, flags=0, sc=O, db=O)
+W = dict(dy=P, dyr=8, dym=O, a=P, ar=8, am=O, div=1, off=P, E=2, M=8, N=64, K=64, dw=P, beta=0.0, flags=0, sc=O, db=O, ws=O, wsb=0)
 
 
 def wgrad(**kw):
     d = {**W, **kw}
     return call("moe_grouped_gemm_bf16_wgrad", d["dy"], i64(d["dyr"]), d["dym"], d["a"], i64(d["ar"]), d["am"], i32(d["div"]), d["off"],
-                i32(d["E"]), i64(d["M"]), i64(d["N"]), i64(d["K"]), d["dw"], f32(d["beta"]), d["flags"], d["sc"], d["db"], O)
+                i32(d["E"]), i64(d["M"]), i64(d["N"]), i64(d["K"]), d["dw"], f32(d["beta"]), d["flags"], d["sc"], d["db"], d["ws"],
+                ctypes.c_size_t(d["wsb"]), O)
 
 
 @pytest.mark.parametrize("kw,rc", [
@@ -86,7 +87,8 @@ def wgrad(**kw):
     (dict(ar=9), EINVAL), (dict(N=1 << 17, K=1 << 12), EINVAL), (dict(beta=0.5), EINVAL), (dict(flags=2), EINVAL), (dict(dw=O), EINVAL), (dict(off=O), EINVAL),
     (dict(dy=O), EINVAL), (dict(a=O), EINVAL), (dict(dym=P, div=0), EINVAL), (dict(am=P, ar=0), EINVAL), (dict(dym=P, dyr=1 << 24), EINVAL),
     (dict(am=P, ar=1 << 24), EINVAL), (dict(sc=P), EINVAL), (dict(dw=v(4104)), EALIGN), (dict(db=v(4104)), EALIGN), (dict(dy=v(4104)), EALIGN),
-    (dict(am=v(4098)), EALIGN)])
+    (dict(am=v(4098)), EALIGN), (dict(M=4096, dyr=4096, ar=4096), EWS), (dict(M=4096, dyr=4096, ar=4096, ws=P, wsb=1000), EWS),
+    (dict(M=4096, dyr=4096, ar=4096, ws=v(4104), wsb=1 << 20), EALIGN)])
 def test_wgrad_refusals(kw, rc):
     assert wgrad(**kw) == rc
 

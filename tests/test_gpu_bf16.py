@@ -158,6 +158,40 @@ def test_wgrad(N, K, name, maps):
     check(np64(db), 2 * b, 2 * z_err(rows + 2, bmag), False, "db twice")
 
 
+@pytest.mark.parametrize("mapped", [False, True])
+@pytest.mark.parametrize("m_list,N,K", [
+    ([2000], 136, 264),                # one expert: seven slices, the last with a part of a slab
+    ([1500, 0, 40, 900], 64, 72),      # two: none of the empty expert's, one slab each of the small one's
+    ([4100, 20], 200, 1000),           # eight, most of the second expert's empty
+    ([513], 8, 8),                     # two
+    ([300, 299], 520, 24)])            # one
+def test_wgrad_slices(m_list, N, K, mapped):
+    """Few experts with many rows: slices of the rows, joined; twice over, with a bias gradient and without."""
+    c = Case(m_list, N, K, N + K + 5, mapped=mapped, div=3, lead=5, tail=3)
+    m = c.gpu_map()
+    dy, tdy = c.bf(c.rows, N)
+    a, ta = c.bf(c.M, K)
+    gy = c.gather(dy)
+    off = c.gpu_off()
+    want, mag = ob.wgrad(gy, a, c.off)
+    b, bmag = np.zeros((c.E, N)), np.zeros((c.E, N))
+    for e, r0, r1 in ob.groups(c.off):
+        b[e], bmag[e] = gy[r0:r1].sum(0), np.abs(gy[r0:r1]).sum(0)
+    dw, db = m4.moe_grouped_gemm_bf16_wgrad(tdy, ta, off, m, map_div=c.div, bias_grad=True)
+    check(np64(dw), want, z_err(max(m_list), mag), False, "dw")
+    check(np64(db), b, z_err(max(m_list), bmag), False, "db")
+    assert torch.equal(dw, m4.moe_grouped_gemm_bf16_wgrad(tdy, ta, off, m, map_div=c.div)[0])
+    m4.moe_grouped_gemm_bf16_wgrad(tdy, ta, off, m, map_div=c.div, dw=dw, beta=1.0, db=db)
+    check(np64(dw), 2 * want, 2 * z_err(max(m_list) + 1, mag), False, "dw twice")
+    check(np64(db), 2 * b, 2 * z_err(max(m_list) + 1, bmag), False, "db twice")
+    if 0 in m_list:
+        dw.fill_(7.0)
+        m4.moe_grouped_gemm_bf16_wgrad(tdy, ta, off, m, map_div=c.div, dw=dw, skip_empty=True)
+        e = m_list.index(0)
+        assert bool((dw[e] == 7.0).all())
+        check(np64(dw[e + 1:]), want[e + 1:], z_err(max(m_list), mag[e + 1:]), False, "dw beside an empty expert")
+
+
 def test_wgrad_empty_experts():
     """Zeros, or with skip_empty (and when accumulating) left as they are."""
     c = Case([0, 40, 0], 72, 40, 5)
