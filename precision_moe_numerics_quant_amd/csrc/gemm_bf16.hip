@@ -537,8 +537,21 @@ int tile_grid() {
   return n[dev];
 }
 
-// Whether a forward product goes to the few-rows kernel.
-static bool few_rows(const Bf16Args& p) { return p.M <= 16 * (int64_t)p.E; }
+// Whether a forward product goes to the few-rows kernel: where the tiles of the
+// experts that can have rows are fewer than the CUs, the tiled kernel leaves CUs idle and
+// pays a ring's start for each; but the few-rows kernel multiplies a quarter as
+// fast, so only up to 16 rows times tile columns a CU.  Both, few rows / tiled:
+//   one of 1536 x 4096, 128 rows     12 column tiles    29.8 / 57.8 us
+//   one of 4096 x 1536, 256 rows     16                 22.5 / 26.8
+//   8 experts of 4096 x 4096, 32 and 64 rows each, 128  52.5 / 74.4, 67.5 / 76.5; 128 rows 129 / 89
+//   4 of 1024 x 512 (gated), 128 and 200 rows each, 32  12.3 / 15.3, 23.3 / 15.7
+//   1, 4 and 8 tokens of 8 of 384 experts of 1024 x 4096 (gated), 64, 248, 472   27.6 / 58.5, 98.8 / 104.9, 186 / 177
+// With more tiles the two are alike for even loads (384 experts of 4096 x 1024, 8
+// rows each 584 / 656, 16 rows 665 / 676) and the tiled one far ahead for uneven ones
+// (8 and 16 rows on average, weights falling by rank: 236 / 168, 369 / 209).
+static bool few_rows(const Bf16Args& p, int64_t n_nt, int cus) {
+  return n_nt * (p.M < p.E ? p.M : p.E) < cus && p.M * n_nt <= 16 * cus;
+}
 
 template <int MODE, bool OUT_BF16, int WB>
 static int launch_rows(const Bf16Args& p, hipStream_t stream, const char* name) {
@@ -554,13 +567,16 @@ template <int MODE, bool OUT_BF16>
 static int launch_bf16(const Bf16Args& p, void* stream, const char* name) {
   using namespace t16;
   constexpr int NW = MODE == GATED ? TN / 2 : TN;
-  if ((MODE == FWD || MODE == GATED) && few_rows(p)) {
-    constexpr int RM = MODE == GATED ? GATED : FWD;
-    const int64_t wide = (p.N * (MODE == GATED ? 2 : 1) + 63) / 64 * (p.M < p.E ? p.M : p.E);
-    return wide >= 1024 ? launch_rows<RM, OUT_BF16, 4>(p, as_stream(stream), name) : launch_rows<RM, OUT_BF16, 2>(p, as_stream(stream), name);
-  }
   const int64_t nt = (p.N + NW - 1) / NW;
   const int cus = tile_grid();
+  if ((MODE == FWD || MODE == GATED) && few_rows(p, nt, cus)) {
+    constexpr int RM = MODE == GATED ? GATED : FWD;
+    // 64 weight rows a workgroup where two of them come to each CU, else 32: 8
+    // experts of 4096 x 4096 with 8 rows (512 workgroups) 45.9 / 58.1 us, one token of
+    // 384 gated experts of 1024 x 4096 (256) 36.4 / 27.6 us
+    const int64_t wide = (p.N * (MODE == GATED ? 2 : 1) + 63) / 64 * (p.M < p.E ? p.M : p.E);
+    return wide >= 2 * cus ? launch_rows<RM, OUT_BF16, 4>(p, as_stream(stream), name) : launch_rows<RM, OUT_BF16, 2>(p, as_stream(stream), name);
+  }
   int cap = 8;   // log2 of a tile's most rows
   while (cap > 6 && ((p.M >> cap) + (p.M < p.E ? p.M : p.E)) * nt < cus) --cap;
   MOE4_REQUIRE(((p.M >> cap) + p.E) * nt < ((int64_t)1 << 31), MOE4_EINVAL, std::string(name) + ": too large");

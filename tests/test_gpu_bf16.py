@@ -16,7 +16,9 @@ if torch.cuda.is_available():
     import precision_moe_numerics_quant_amd as m4
 
 M_LISTS = {"one": [1], "few": [3, 0, 1, 17], "odd": [65, 0, 0, 129, 1, 64, 255, 2], "dense": [300], "big": [0, 700, 31, 0],
-           "many": [(5 * i) % 13 if i % 3 else 0 for i in range(150)]}
+           "many": [(5 * i) % 13 if i % 3 else 0 for i in range(150)],
+           # forward products take the tiled kernel with these two, whatever the sizes
+           "tall": [5, 0, 2300, 64, 1, 1900, 130, 0], "crowd": [(7 * i) % 11 for i in range(300)]}
 SIZES = [(8, 8), (72, 40), (136, 64), (264, 520), (520, 264), (40, 1096)]
 
 
