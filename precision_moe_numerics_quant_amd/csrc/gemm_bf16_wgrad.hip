@@ -37,7 +37,7 @@ __device__ inline int2 expert_rows(const int32_t* off, int e, int64_t M) {
 }
 
 // A tile of a slice's sum: n-tile nt (of dy's columns), k-tile kt (of a's; at = nt
-// 2^16 + kt), the slice's rows; e: its number, slices e + slice.
+// 2^16 + kt), the slice's rows; e: its number, slices e + slice (-1: no tile).
 struct WTile {
   int32_t e, at, row0, rows;
 };
@@ -46,10 +46,15 @@ struct WTile {
 // transposed from LDS.  Two workgroups share a CU, so that one multiplies while
 // the other stores: a short contraction (a few hundred rows) writes its float32
 // tile in about the time that it takes to multiply.  A map's entries come through
-// LDS, those of eight slabs at a time.  order: the experts are visited in steps
-// of `order` (coprime to E), so that popular and rare ones, whose tiles multiply
-// and store in different proportions, run side by side.
-__global__ void __launch_bounds__(wg::NT, 2) k_bf16_wgrad(Bf16Wgrad p, uint32_t n_nt, uint32_t n_kt, uint32_t order) {
+// LDS, those of eight slabs at a time.
+// Order: the experts by falling number of rows, their tiles dealt to the workgroups
+// from first to last, then from last to first, and so on, so that everyone gets as
+// much to multiply; every second workgroup of an XCD (they share a CU) takes its own from
+// the end, so that the experts with many rows are multiplied while those with few
+// or none are stored.  (16384 tokens, 8 of 384 experts by weights that fall with
+// rank, 4096 x 1024: experts visited in mixed order, each on one XCD, 2565 us, by
+// falling rows 2076, half of the workgroups from the end 1960.)
+__global__ void __launch_bounds__(wg::NT, 2) k_bf16_wgrad(Bf16Wgrad p, uint32_t n_nt, uint32_t n_kt) {
   using namespace wg;
   using t16::OOB;
   using t16::lds_u8;
@@ -69,8 +74,10 @@ __global__ void __launch_bounds__(wg::NT, 2) k_bf16_wgrad(Bf16Wgrad p, uint32_t 
   float* const dw = p.slices > 1 ? p.dw_part : p.dw;
   const float beta = p.slices > 1 ? 0.0f : p.beta;
   const bool zero_empty = p.slices == 1 && p.zero_empty && beta == 0.0f;
-  const uint32_t per_e = n_nt * n_kt, total = per_e * E, xcd = blockIdx.x % 8, stride = gridDim.x / 8;
-  const uint32_t chunk = total >= 16 * per_e ? per_e : (total + gridDim.x - 1) / gridDim.x;
+  const uint32_t per_e = n_nt * n_kt, total = per_e * E;
+  // neighbours in the order of tiles share operands: they are on one XCD
+  const uint32_t G = gridDim.x, pos = blockIdx.x % 8 * (G / 8) + blockIdx.x / 8, rounds = (total + G - 1) / G;
+  const bool back = blockIdx.x / 8 % 2;
   const uint32_t N = (uint32_t)p.N, K = (uint32_t)p.K, ldd = N * 2, lda = K * 2;
   auto lane = [&]() __attribute__((always_inline)) {   // (kept from the optimiser, as in gemm_bf16.hip)
     int x = l;
@@ -213,28 +220,53 @@ __global__ void __launch_bounds__(wg::NT, 2) k_bf16_wgrad(Bf16Wgrad p, uint32_t 
     f = __builtin_bit_cast(bf16x8, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
   };
 
-  for (uint32_t j0 = 0;; j0 += LIST) {
-    if (tid < LIST) {
-      const uint32_t J = (j0 + tid) * stride + blockIdx.x / 8, c = J / chunk, t = (c * 8 + xcd) * chunk + (J - c * chunk);
-      WTile x{-1, 0, 0, 0};
-      if (t < total) {
-        const uint32_t i = t / per_e, r = t - i * per_e;
-        x.e = (int32_t)((uint64_t)i * order % (uint32_t)E);
-        const uint32_t nt = r / n_kt;
-        x.at = (int32_t)(nt << 16 | (r - nt * n_kt));
-        const int e = x.e / p.slices;
+  for (uint32_t j0 = 0; j0 < rounds; j0 += LIST) {
+    // the slices by falling rows (equal ones, and from 2^20 on, by number): a bitonic
+    // sort in the ring, which is free between lists
+    {
+      uint32_t* key = reinterpret_cast<uint32_t*>(ring);
+      auto rows_of = [&](int i) __attribute__((always_inline)) {
+        const int e = i / p.slices;
         const int2 m = expert_rows(p.off, e, p.M);
-        const Slice sl(m.y, x.e - e * p.slices, p.slices);
-        x.row0 = m.x + sl.r;
-        x.rows = sl.m;
+        const Slice s(m.y, i - e * p.slices, p.slices);
+        return make_int2(m.x + s.r, s.m);
+      };
+      int n = 1;
+      while (n < E) n *= 2;
+      for (int i = tid; i < n; i += NT) {
+        const int m = i < E ? rows_of(i).y : 0;
+        key[i] = i < E ? (uint32_t)(m < 0xFFFFF ? m : 0xFFFFF) << 12 | (uint32_t)(4095 - i) : 0;
       }
-      s_tile[tid] = x;
+      for (int k = 2; k <= n; k *= 2) {
+        for (int j = k / 2; j; j /= 2) {
+          __syncthreads();
+          for (int x = tid; x < n / 2; x += NT) {
+            const int i = 2 * x - (x & (j - 1));   // (the pair's lower index)
+            const uint32_t a = key[i], b = key[i + j];
+            if ((a < b) == ((i & k) == 0)) {
+              key[i] = b;
+              key[i + j] = a;
+            }
+          }
+        }
+      }
+      __syncthreads();
+      if (tid < LIST && j0 + tid < rounds) {
+        const uint32_t r = back ? rounds - 1 - (j0 + tid) : j0 + tid, t = r * G + (r & 1 ? G - 1 - pos : pos);
+        WTile x{-1, 0, 0, 0};
+        if (t < total) {
+          const uint32_t i = t / per_e, y = t - i * per_e, nt = y / n_kt;
+          x.e = 4095 - (int32_t)(key[i] & 4095);
+          x.at = (int32_t)(nt << 16 | (y - nt * n_kt));
+          const int2 m = rows_of(x.e);
+          x.row0 = m.x;
+          x.rows = m.y;
+        }
+        s_tile[tid] = x;
+      }
+      __syncthreads();
+      n_my = rounds - j0 < LIST ? rounds - j0 : LIST;
     }
-    __syncthreads();
-    n_my = 0;
-    for (uint32_t i = LIST; i; i >>= 1)   // (the tiles come first)
-      if (n_my + i <= LIST && __builtin_amdgcn_readfirstlane(s_tile[n_my + i - 1].e) >= 0) n_my += i;
-    if (n_my == 0) break;
     ln = 0;
     left = 0;
     if (mapped) {
@@ -253,7 +285,7 @@ __global__ void __launch_bounds__(wg::NT, 2) k_bf16_wgrad(Bf16Wgrad p, uint32_t 
     for (uint32_t ct = 0; ct < n_my; ++ct) {
       const WTile m = tile(ct);
       const uint32_t nt = (uint32_t)(m.at >> 16), kt = (uint32_t)(m.at & 0xFFFF), nk = ((uint32_t)m.rows + BK - 1) / BK;
-      if (nk == 0 && !zero_empty) continue;
+      if (nk == 0 && (!zero_empty || m.e < 0)) continue;
       const uint32_t tn = N - nt * TM < TM ? N - nt * TM : TM;
       const int mb = (int)((tn + 31) / 32);   // blocks of 16 of a wave
       f32x4 acc[4][8];
@@ -449,20 +481,7 @@ extern "C" int moe_grouped_gemm_bf16_wgrad(const uint16_t* dy, int64_t dy_rows, 
   hipStream_t st = as_stream(stream);
   const int64_t nt = (N + wg::TM - 1) / wg::TM, kt = (K + wg::TN - 1) / wg::TN;
   MOE4_REQUIRE(nt * kt * E < ((int64_t)1 << 31), MOE4_EINVAL, s + ": too large");
-  // a step through the experts (their slices) near the golden section of their
-  // number, coprime to it
-  const uint32_t V = (uint32_t)(E * p.slices);
-  uint32_t order = (uint32_t)(0.618 * V);
-  const auto gcd = [](uint32_t a, uint32_t b) {
-    while (b) {
-      const uint32_t c = a % b;
-      a = b;
-      b = c;
-    }
-    return a;
-  };
-  while (order < 1 || gcd(order, V) != 1) ++order;
-  hipLaunchKernelGGL(k_bf16_wgrad, dim3(2 * (unsigned)tile_grid()), dim3(wg::NT), 0, st, p, (uint32_t)nt, (uint32_t)kt, order);
+  hipLaunchKernelGGL(k_bf16_wgrad, dim3(2 * (unsigned)tile_grid()), dim3(wg::NT), 0, st, p, (uint32_t)nt, (uint32_t)kt);
   const auto join = [&](const float* part, int slices, float* dst, int64_t L) {
     if (slices > 1) hipLaunchKernelGGL(k_wgrad_join, dim3((unsigned)((L + 1023) / 1024), (unsigned)E), dim3(256), 0, st, p, part, slices, dst, L);
   };
