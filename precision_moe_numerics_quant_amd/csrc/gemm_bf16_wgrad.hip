@@ -21,10 +21,10 @@ constexpr int SLOTS = 512;                // workgroups at a time: two on each o
 struct Slice {
   int32_t r, m;
   __device__ Slice(int32_t n, int i, int slices) {
-    const int64_t slabs = (n + wg::BK - 1) / wg::BK;
-    r = (int32_t)(slabs * i / slices) * wg::BK;
-    const int64_t end = slabs * (i + 1) / slices * wg::BK;
-    m = (int32_t)(end < n ? end : n) - r;
+    const uint32_t slabs = ((uint32_t)n + wg::BK - 1) / wg::BK;   // (below 2^26, slices at most 32)
+    r = (int32_t)(slabs * i / slices * wg::BK);
+    const uint32_t end = slabs * (i + 1) / slices * wg::BK;
+    m = (int32_t)(end < (uint32_t)n ? end : (uint32_t)n) - r;
   }
 };
 
@@ -53,7 +53,8 @@ struct WTile {
 // the end, so that the experts with many rows are multiplied while those with few
 // or none are stored.  (16384 tokens, 8 of 384 experts by weights that fall with
 // rank, 4096 x 1024: experts visited in mixed order, each on one XCD, 2565 us, by
-// falling rows 2076, half of the workgroups from the end 1960.)
+// falling rows 2076, half of the workgroups from the end 1960; 192 tiles 242 us
+// where each CU first gets one, else 259.)
 __global__ void __launch_bounds__(wg::NT, 2) k_bf16_wgrad(Bf16Wgrad p, uint32_t n_nt, uint32_t n_kt) {
   using namespace wg;
   using t16::OOB;
@@ -75,9 +76,11 @@ __global__ void __launch_bounds__(wg::NT, 2) k_bf16_wgrad(Bf16Wgrad p, uint32_t 
   const float beta = p.slices > 1 ? 0.0f : p.beta;
   const bool zero_empty = p.slices == 1 && p.zero_empty && beta == 0.0f;
   const uint32_t per_e = n_nt * n_kt, total = per_e * E;
-  // neighbours in the order of tiles share operands: they are on one XCD
-  const uint32_t G = gridDim.x, pos = blockIdx.x % 8 * (G / 8) + blockIdx.x / 8, rounds = (total + G - 1) / G;
-  const bool back = blockIdx.x / 8 % 2;
+  // Neighbours in the order of tiles share operands: they are on one XCD, whose
+  // workgroups 2 i and 2 i + 1 share a CU (of a round that is not full each CU first
+  // gets one tile).
+  const uint32_t G = gridDim.x, xcd = blockIdx.x % 8, slot = blockIdx.x / 8, rounds = (total + G - 1) / G;
+  const bool back = slot % 2;
   const uint32_t N = (uint32_t)p.N, K = (uint32_t)p.K, ldd = N * 2, lda = K * 2;
   auto lane = [&]() __attribute__((always_inline)) {   // (kept from the optimiser, as in gemm_bf16.hip)
     int x = l;
@@ -252,12 +255,13 @@ __global__ void __launch_bounds__(wg::NT, 2) k_bf16_wgrad(Bf16Wgrad p, uint32_t 
       }
       __syncthreads();
       if (tid < LIST && j0 + tid < rounds) {
-        const uint32_t r = back ? rounds - 1 - (j0 + tid) : j0 + tid, t = r * G + (r & 1 ? G - 1 - pos : pos);
+        const uint32_t r = back ? rounds - 1 - (j0 + tid) : j0 + tid, n = total - r * G < G ? total - r * G : G;
+        const uint32_t share = (n + 7) / 8, at = n == G ? slot : slot / 2 + slot % 2 * (G / 16), y = xcd * share + at;
         WTile x{-1, 0, 0, 0};
-        if (t < total) {
-          const uint32_t i = t / per_e, y = t - i * per_e, nt = y / n_kt;
+        if (at < share && y < n) {
+          const uint32_t t = r * G + (r & 1 ? n - 1 - y : y), i = t / per_e, z = t - i * per_e, nt = z / n_kt;
           x.e = 4095 - (int32_t)(key[i] & 4095);
-          x.at = (int32_t)(nt << 16 | (y - nt * n_kt));
+          x.at = (int32_t)(nt << 16 | (z - nt * n_kt));
           const int2 m = rows_of(x.e);
           x.row0 = m.x;
           x.rows = m.y;
@@ -417,8 +421,11 @@ __global__ void __launch_bounds__(256) k_wgrad_join(Bf16Wgrad p, const float* pa
   f32x4* d = reinterpret_cast<f32x4*>(dst + e * L + i);
   const f32x4* s = reinterpret_cast<const f32x4*>(part + (int64_t)e * slices * L + i);
   f32x4 t = {};
-  for (int k = 0; k < slices; ++k)
-    if (Slice(n, k, slices).m) t = t + s[k * (L / 4)];
+#pragma unroll 4
+  for (int k = 0; k < slices; ++k) {
+    const f32x4 x = s[k * (L / 4)];   // (an empty slice's is not written, and not used)
+    if (Slice(n, k, slices).m) t = t + x;
+  }
   *d = p.beta != 0.0f ? *d + t : t;
 }
 
