@@ -6,7 +6,7 @@ import numpy as np
 import pytest
 import torch
 
-from bf16_helpers import L_ACT, U, Case, act_parts, bf, check, z_err
+from bf16_helpers import L_ACT, U, Case, act_parts, bf, check, offsets, z_err
 from gpu_helpers import to_np
 from oracle import bf16 as ob
 
@@ -261,7 +261,7 @@ def _operands(m_list, N, K, seed, **kw):
                c.bf(c.M, K)[1], c.gpu_off(), c.gpu_map())
 
 
-@pytest.mark.parametrize("m_list", [[5, 0, 70, 3], [300, 1], [1, 1, 1]])
+@pytest.mark.parametrize("m_list", [[5, 0, 70, 3], [300, 1], [1, 1, 1], [900, 0, 3500, 1]])
 def test_rows_of_no_expert(m_list):
     """Rows before the first expert's and behind the last one's: inputs there (NaN) are not read, outputs keep what they hold."""
     N, K = 136, 72
@@ -290,11 +290,12 @@ def test_rows_of_no_expert(m_list):
         assert (out[dead] == 3.0).all() and not (out[~dead] == 3.0).all()
 
 
-def test_values_that_are_not_finite():
+@pytest.mark.parametrize("last", [2, 4200])
+def test_values_that_are_not_finite(last):
     """A NaN or infinity in one row, or in one expert's weights, reaches that row's or expert's results and no other,
     also where K ends inside a tile's step."""
     N, K = 72, 40
-    c = Case([5, 33, 2], N, K, 9)
+    c = Case([5, 33, last], N, K, 9)
     a, ta = c.bf(c.M, K)
     w, tw = c.bf(c.E, N, K, std=0.3)
     _, tdy = c.bf(c.M, N)
@@ -341,7 +342,7 @@ def test_activation_limits():
             assert (d[9:14] == 1).all() and torch.equal(h[9:14], pre.float().cpu()[0, 9:14])
 
 
-@pytest.mark.parametrize("m_list", [[3, 2], [200, 100]])
+@pytest.mark.parametrize("m_list", [[3, 2], [200, 100], [3000, 1200]])
 def test_map_entries_out_of_range(m_list):
     """They count as rows of zeros (scale 0) and are reported."""
     N, K = 72, 40
@@ -375,10 +376,11 @@ def test_map_entries_out_of_range(m_list):
         m4.moe4_debug_check()
 
 
-def test_same_row_many_times():
+@pytest.mark.parametrize("m_list", [[40, 90], [4000, 100]])
+def test_same_row_many_times(m_list):
     """A map may name a row more than once."""
     N, K = 136, 264
-    c = Case([40, 90], N, K, 12, mapped=True, dup=True)
+    c = Case(m_list, N, K, 12, mapped=True, dup=True)
     a, ta = c.bf(c.rows, K)
     w, tw = c.bf(c.E, N, K, std=0.3)
     out, _ = m4.moe_grouped_gemm_bf16(ta, tw, c.gpu_off(), row_map=c.gpu_map(), map_div=c.div, out_dtype=torch.float32)
@@ -386,10 +388,10 @@ def test_same_row_many_times():
     assert torch.equal(out, flat)
 
 
+@pytest.mark.parametrize("rows", [50, 4200])
 @pytest.mark.parametrize("div", [1, 3, 7, 8, 1000])
-def test_map_divisors(div):
+def test_map_divisors(div, rows):
     N, K = 8, 16
-    rows = 50
     c = Case([rows], N, K, 13)
     a, ta = c.bf(rows, K)
     w, tw = c.bf(1, N, K)
@@ -399,10 +401,11 @@ def test_map_divisors(div):
     assert torch.equal(out, ref)
 
 
-def test_in_place():
+@pytest.mark.parametrize("m_list", [[5, 0, 70], [3000, 0, 1200]])
+def test_in_place(m_list):
     """residual and c, add and dx, gu and dgu may be one tensor."""
     N, K = 136, 72
-    c = Case([5, 0, 70], N, K, 14)
+    c = Case(m_list, N, K, 14)
     _, a = c.bf(c.M, K)
     _, w = c.bf(c.E, N, K, std=0.3)
     _, dy = c.bf(c.M, N)
@@ -437,7 +440,7 @@ def test_nothing_to_do():
     assert (out == 2).all()
 
 
-@pytest.mark.parametrize("m_list", [[2, 0, 1, 3], [130, 0, 260, 5]])
+@pytest.mark.parametrize("m_list", [[2, 0, 1, 3], [130, 0, 260, 5], [1100], [2000, 150]])
 def test_graph_replay_and_streams(m_list):
     """Captured once and replayed with eager calls between; two streams at once: the same bits."""
     N, K = 264, 136
@@ -466,6 +469,82 @@ def test_graph_replay_and_streams(m_list):
         _all_calls(c2, *ops2)
         torch.cuda.synchronize()
     m4.moe4_debug_check()
+
+
+def test_long_lists_of_tiles():
+    """2048 experts with a row or none, so many tiles that each workgroup lists them more than once; a row's
+    gradient is one exact product per element, its results sums of eight."""
+    E, W = 2048, 16648
+    rng = np.random.default_rng(31)
+    cnt = (rng.random(E) < 0.9).astype(np.int64)
+    off = torch.from_numpy(offsets(cnt).astype(np.int32)).cuda()
+    M = int(cnt.sum())
+    of = torch.from_numpy(np.flatnonzero(cnt)).cuda()
+    g = torch.Generator(device="cuda")
+    g.manual_seed(5)
+    a = torch.randn((M, 8), generator=g, device="cuda").bfloat16()
+    w = torch.randn((E, W, 8), generator=g, device="cuda").bfloat16()
+
+    def near(got, x, y):
+        """got = the sums over the last axis of x y, each term exact in float32."""
+        z = x.float() * y.float()
+        assert bool(((got.double() - z.double().sum(-1)).abs() <= 8 * 2.0 ** -23 * z.abs().double().sum(-1)).all())
+    out, _ = m4.moe_grouped_gemm_bf16(a, w, off, out_dtype=torch.float32)
+    near(out, w[of], a[:, None, :])
+    wt = w.transpose(1, 2).contiguous()
+    dx, _ = m4.moe_grouped_gemm_bf16_dgrad(a, wt, off, out_dtype=torch.float32)
+    near(dx, w[of], a[:, None, :])
+    dy = torch.randn((M, 8448), generator=g, device="cuda").bfloat16()
+    dw, _ = m4.moe_grouped_gemm_bf16_wgrad(dy, a, off)
+    assert torch.equal(dw[of], dy.float()[:, :, None] * a.float()[:, None, :])
+    assert not dw[torch.from_numpy(np.flatnonzero(cnt == 0)).cuda()].any()
+
+
+def test_offsets_past_32_bits():
+    """Operands and results of more than 2^32 bytes, the rows of the last expert behind them."""
+    M, W = 280000, 8208
+    g = torch.Generator(device="cuda")
+    g.manual_seed(6)
+    off = torch.tensor([0, 5, M - 300, M], dtype=torch.int32, device="cuda")
+    rows = torch.cat((torch.arange(0, 40), torch.arange(M - 320, M))).cuda()
+    e = (torch.searchsorted(off, rows.int(), right=True) - 1).long()
+    a = _ints((M, 8), 7)
+    w = _ints((3, W, 8), 8)
+    out, pre = m4.moe_grouped_gemm_bf16(a, w, off, act=m4.ACT_NONE, save_pre=True)
+    want = (w[e].float() * a[rows].float()[:, None, :]).sum(-1)        # integers up to 32: exact in every type
+    assert torch.equal(out[rows].float(), want) and torch.equal(pre[rows].float(), want)
+    del pre
+    big = out                                                        # [M, W]: 4.6 GB of small integers
+    v = _ints((3, 8, W), 9, -1, 2)
+
+    def product(x):
+        return torch.stack([x[i].double() @ v[e[i]].double().t() for i in range(len(rows))])
+    c, _ = m4.moe_grouped_gemm_bf16(big, v, off, out_dtype=torch.float32)
+    assert torch.equal(c[rows].double(), product(big[rows]))
+    dx, _ = m4.moe_grouped_gemm_bf16_dgrad(big, v.transpose(1, 2).contiguous(), off, out_dtype=torch.float32)
+    assert torch.equal(dx, c)
+    h, gu = m4.moe_gated_gemm_bf16(a, w.view(3, 2, W // 2, 8), off, act=m4.ACT_NONE)
+    assert torch.equal(gu.view(M, W), big)
+    dgu, hs = m4.moe_gated_gemm_bf16_dgrad(a, w.view(3, 2, W // 2, 8)[:, 0].transpose(1, 2).contiguous(), gu, off, act=m4.ACT_NONE)
+    assert torch.equal(hs, h)
+    dh = want[:, :W // 2]
+    assert torch.equal(dgu[rows, 0].float(), (dh * gu[rows, 1].float()).bfloat16().float())
+    del gu, dgu, hs, h
+    small = torch.zeros((M, 8), dtype=torch.bfloat16, device="cuda")   # (few rows count: their sums are exact)
+    small[rows] = a[rows]
+    dw, _ = m4.moe_grouped_gemm_bf16_wgrad(big, small, off)
+    for i in range(3):
+        r = rows[e == i]
+        assert torch.equal(dw[i].double(), big[r].double().t() @ small[r].double())
+
+
+def test_weight_gradient_past_32_bits():
+    E, N, K = 70, 4096, 4096
+    dy, a = _ints((3 * E, N), 10), _ints((3 * E, K), 11)
+    off = torch.arange(0, 3 * E + 1, 3, dtype=torch.int32, device="cuda")
+    dw, _ = m4.moe_grouped_gemm_bf16_wgrad(dy, a, off)
+    for e in (0, 33, E - 1):
+        assert torch.equal(dw[e], dy[3 * e:3 * e + 3].float().t() @ a[3 * e:3 * e + 3].float())
 
 
 def test_gated_gradient_against_differences():
