@@ -92,8 +92,7 @@ __device__ inline void act_of(const ActCoef& a, float x, float& f, float& df) {
 // the descriptor's base; PAST as the offset reads zeros and stores nothing.
 constexpr uint32_t PAST = 0x20000000u;   // (times 4 or 2 bytes: past 2^30, the largest descriptor here, and no wrap)
 template <int W>
-__device__ inline void load_bf16(const __amdgpu_buffer_rsrc_t& rs, uint32_t o, float (&v)[W]) {
-  uint32_t q[W / 2];
+__device__ inline void load_words(const __amdgpu_buffer_rsrc_t& rs, uint32_t o, uint32_t (&q)[W / 2]) {   // W bf16 values
   if (W == 8) {
     const auto x = __builtin_amdgcn_raw_buffer_load_b128(rs, o * 2, 0, 0);
     q[0] = x[0]; q[1] = x[1]; q[W / 2 - 2] = x[2]; q[W / 2 - 1] = x[3];
@@ -101,6 +100,9 @@ __device__ inline void load_bf16(const __amdgpu_buffer_rsrc_t& rs, uint32_t o, f
     const auto x = __builtin_amdgcn_raw_buffer_load_b64(rs, o * 2, 0, 0);
     q[0] = x[0]; q[1] = x[1];
   }
+}
+template <int W>
+__device__ inline void values_of(const uint32_t (&q)[W / 2], float (&v)[W]) {
 #pragma unroll
   for (int i = 0; i < W; ++i) v[i] = bf16_bits_to_f32((i & 1) ? q[i / 2] >> 16 : q[i / 2] & 0xFFFFu);
 }
@@ -160,14 +162,44 @@ struct Bf16Epilogue {
     const int64_t nb = p.N * (MODE == GATED ? 2 : 1);
     bias = make_rsrc(p.bias + e * nb, has_bias ? (uint64_t)nb * 4 : 0);
   }
+  // What the results of row r, columns n .. n + W - 1 need from memory: requested
+  // for several rows before the first is used.
   template <int W>
-  __device__ void add_store(uint32_t o, float (&q)[W]) const {
+  struct Need {
+    uint32_t in[W / 2], in1[MODE == GDGRAD ? W / 2 : 1], res16[OUT_BF16 ? W / 2 : 1];
+    float res[OUT_BF16 ? 1 : W];
+  };
+  template <int W>
+  struct Bias {
+    float b[W], b1[MODE == GATED ? W : 1];
+  };
+  template <int W>
+  __device__ void request(Need<W>& x, uint32_t r, uint32_t n) const {
+    const uint32_t o = n < N ? (MODE == GDGRAD ? 2 * r * N : r * N) + n : PAST;
+    if (MODE == GDGRAD) {
+      load_words<W>(in, o, x.in);
+      load_words<W>(in, n < N ? o + N : PAST, reinterpret_cast<uint32_t(&)[W / 2]>(x.in1));
+    }
+    if (MODE == DGRAD && has_in) load_words<W>(in, o, x.in);
+    if ((MODE == FWD || MODE == DGRAD) && has_res) {
+      if (OUT_BF16) load_words<W>(res, o, reinterpret_cast<uint32_t(&)[W / 2]>(x.res16));
+      else load_f32<W>(res, o, reinterpret_cast<float(&)[W]>(x.res));
+    }
+  }
+  template <int W>
+  __device__ void request(Bias<W>& x, uint32_t n) const {
+    if ((MODE == FWD || MODE == GATED) && has_bias) {
+      load_f32<W>(bias, n < N ? n : PAST, x.b);
+      if (MODE == GATED) load_f32<W>(bias, n < N ? n + N : PAST, reinterpret_cast<float(&)[W]>(x.b1));
+    }
+  }
+  template <int W>
+  __device__ void add_store(uint32_t o, float (&q)[W], const Need<W>& x) const {
     if (has_res) {
       float v[W];
-      if (OUT_BF16) load_bf16<W>(res, o, v);
-      else load_f32<W>(res, o, v);
+      if (OUT_BF16) values_of<W>(reinterpret_cast<const uint32_t(&)[W / 2]>(x.res16), v);
 #pragma unroll
-      for (int i = 0; i < W; ++i) q[i] = q[i] + v[i];
+      for (int i = 0; i < W; ++i) q[i] = q[i] + (OUT_BF16 ? v[i] : x.res[OUT_BF16 ? 0 : i]);
     }
     if (OUT_BF16) store_bf16<W, POLICY>(c, o, q);
     else store_f32<W, POLICY>(c, o, q);
@@ -175,18 +207,13 @@ struct Bf16Epilogue {
   // The W results z (GATED: z and z1) of row r of the tile, columns n .. n + W -
   // 1 (n >= N: nothing happens); s: the row's scale.
   template <int W>
-  __device__ void put(uint32_t r, uint32_t n, float s, const float (&z)[W], const float (&z1)[W]) const {
+  __device__ void put(uint32_t r, uint32_t n, float s, const float (&z)[W], const float (&z1)[W], const Need<W>& x, const Bias<W>& bs) const {
     const bool ok = n < N;
     const uint32_t o = ok ? r * N + n : PAST, o0 = ok ? 2 * r * N + n : PAST, o1 = ok ? o0 + N : PAST;
     float v[W], h[W], q[W], d;
     if (MODE == FWD) {
 #pragma unroll
-      for (int i = 0; i < W; ++i) q[i] = z[i];
-      if (has_bias) {
-        load_f32<W>(bias, ok ? n : PAST, v);
-#pragma unroll
-        for (int i = 0; i < W; ++i) q[i] = q[i] + v[i];
-      }
+      for (int i = 0; i < W; ++i) q[i] = has_bias ? z[i] + bs.b[i] : z[i];
       if (has_aux) store_bf16<W, POLICY>(aux, o, q);
       if (has_act) {
 #pragma unroll
@@ -195,21 +222,13 @@ struct Bf16Epilogue {
           q[i] = h[i];
         }
       }
-      add_store<W>(o, q);
+      add_store<W>(o, q, x);
     } else if (MODE == GATED) {
       float u[W];
 #pragma unroll
       for (int i = 0; i < W; ++i) {
-        q[i] = z[i];
-        u[i] = z1[i];
-      }
-      if (has_bias) {
-        load_f32<W>(bias, ok ? n : PAST, v);
-#pragma unroll
-        for (int i = 0; i < W; ++i) q[i] = q[i] + v[i];
-        load_f32<W>(bias, ok ? n + N : PAST, v);
-#pragma unroll
-        for (int i = 0; i < W; ++i) u[i] = u[i] + v[i];
+        q[i] = has_bias ? z[i] + bs.b[i] : z[i];
+        u[i] = has_bias ? z1[i] + bs.b1[MODE == GATED ? i : 0] : z1[i];
       }
       if (has_aux) {
         store_bf16<W, POLICY>(aux, o0, q);
@@ -227,7 +246,7 @@ struct Bf16Epilogue {
       for (int i = 0; i < W; ++i) q[i] = s * z[i];
       if (MODE == DGRAD) {
         if (has_in) {
-          load_bf16<W>(in, o, v);
+          values_of<W>(x.in, v);
 #pragma unroll
           for (int i = 0; i < W; ++i) {
             if (has_act) {
@@ -240,11 +259,11 @@ struct Bf16Epilogue {
           }
           if (has_aux) store_bf16<W, POLICY>(aux, o, h);
         }
-        add_store<W>(o, q);
+        add_store<W>(o, q, x);
       } else {
         float u[W];
-        load_bf16<W>(in, o0, v);
-        load_bf16<W>(in, o1, u);
+        values_of<W>(x.in, v);
+        values_of<W>(reinterpret_cast<const uint32_t(&)[W / 2]>(x.in1), u);
 #pragma unroll
         for (int i = 0; i < W; ++i) {
           float f = v[i];

@@ -368,7 +368,8 @@ __global__ void __launch_bounds__(t16::NT, 1) k_bf16_tile(Bf16Args p, int cap, u
       }
       late();
       stored = (MODE == GATED ? (p.aux ? 6 : 2) : MODE == GDGRAD || !OUT_BF16 ? 8 : 4) * mb;
-      const Bf16Epilogue<MODE, OUT_BF16, NT_STORE> epi(p, m.e, m.row0, m.rows);
+      typedef Bf16Epilogue<MODE, OUT_BF16, NT_STORE> Epi;
+      const Epi epi(p, m.e, m.row0, m.rows);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         if (i < mb) {
@@ -377,26 +378,39 @@ __global__ void __launch_bounds__(t16::NT, 1) k_bf16_tile(Bf16Args p, int cap, u
             return (MODE == DGRAD || MODE == GDGRAD) && r < m.rows ? row_scale(p.scale, p.map, (int64_t)m.row0 + r, p.a_rows * p.div) : 1.0f;
           };
           const float s0 = scale(r), s1 = scale(r + 8);
-          constexpr int W = PAIR ? 8 : 4;   // values of a lane
+          constexpr int W = PAIR ? 8 : 4, NB = MODE == GATED ? 4 : 8;   // values of a lane, blocks of columns
           const uint32_t n0 = m.nt * NW + (MODE == GATED ? 64 : 128) * wn + W * (l & 7);
+          constexpr int GB = 4;                 // (as many are requested at once as registers hold)
 #pragma unroll
-          for (int b = 0; b < (MODE == GATED ? 4 : 8); b += W / 2) {
-            float x[W], y[W], x1[W], y1[W];
+          for (int g = 0; g < NB; g += GB) {
+            typename Epi::template Need<W> need[GB / (W / 2)][2];
+            typename Epi::template Bias<W> bias[GB / (W / 2)];
 #pragma unroll
-            for (int v = 0; v < W; ++v) {
-              x[v] = acc[i][b + v / 4][v % 4];
-              y[v] = acc[i][b + W / 4 + v / 4][v % 4];
-              if (MODE == GATED) {
-                x1[v] = acc[i][(b + 4 + v / 4) % 8][v % 4];
-                y1[v] = acc[i][(b + 4 + W / 4 + v / 4) % 8][v % 4];
-              }
+            for (int b = g; b < g + GB; b += W / 2) {
+              epi.template request<W>(need[(b - g) / (W / 2)][0], r, n0 + 16 * b);
+              epi.template request<W>(need[(b - g) / (W / 2)][1], r + 8, n0 + 16 * b);
+              epi.template request<W>(bias[(b - g) / (W / 2)], n0 + 16 * b);
             }
-            store_order(x, y, l);
-            if (MODE == GATED) store_order(x1, y1, l);
-            epi.template put<W>(r, n0 + 16 * b, s0, x, x1);
             __builtin_amdgcn_sched_barrier(0);
-            epi.template put<W>(r + 8, n0 + 16 * b, s1, y, y1);
-            __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+            for (int b = g; b < g + GB; b += W / 2) {
+              float x[W], y[W], x1[W], y1[W];
+#pragma unroll
+              for (int v = 0; v < W; ++v) {
+                x[v] = acc[i][b + v / 4][v % 4];
+                y[v] = acc[i][b + W / 4 + v / 4][v % 4];
+                if (MODE == GATED) {
+                  x1[v] = acc[i][(b + 4 + v / 4) % 8][v % 4];
+                  y1[v] = acc[i][(b + 4 + W / 4 + v / 4) % 8][v % 4];
+                }
+              }
+              store_order(x, y, l);
+              if (MODE == GATED) store_order(x1, y1, l);
+              epi.template put<W>(r, n0 + 16 * b, s0, x, x1, need[(b - g) / (W / 2)][0], bias[(b - g) / (W / 2)]);
+              __builtin_amdgcn_sched_barrier(0);
+              epi.template put<W>(r + 8, n0 + 16 * b, s1, y, y1, need[(b - g) / (W / 2)][1], bias[(b - g) / (W / 2)]);
+              __builtin_amdgcn_sched_barrier(0);
+            }
           }
         }
       }
@@ -506,7 +520,8 @@ __global__ void __launch_bounds__(b16r::NT) k_bf16_rows(Bf16Args p, uint32_t n_n
     weights(wq[0], i + 2 * NU);
     multiply(wq[1], i + NU);
   }
-  const Bf16Epilogue<MODE, OUT_BF16, 0> epi(p, e, r0, rows);
+  typedef Bf16Epilogue<MODE, OUT_BF16, 0> Epi;
+  const Epi epi(p, e, r0, rows);
 #pragma unroll
   for (int s = 0; s < PASSES; ++s) {
     if (s < np) {
@@ -519,7 +534,12 @@ __global__ void __launch_bounds__(b16r::NT) k_bf16_rows(Bf16Args p, uint32_t n_n
         const f32x4 x = ((red[0][b][l] + red[1][b][l]) + red[2][b][l]) + red[3][b][l];
         const f32x4 y = MODE == GATED ? ((red[0][b + HB][l] + red[1][b + HB][l]) + red[2][b + HB][l]) + red[3][b + HB][l] : x;
         const float z[4] = {x[0], x[1], x[2], x[3]}, z1[4] = {y[0], y[1], y[2], y[3]};
-        epi.template put<4>(16 * s + li, n0 + 16 * b + 4 * q, 1.0f, z, z1);
+        const uint32_t n = n0 + 16 * b + 4 * q;
+        typename Epi::template Need<4> need;
+        typename Epi::template Bias<4> bias;
+        epi.template request<4>(need, 16 * s + li, n);
+        epi.template request<4>(bias, n);
+        epi.template put<4>(16 * s + li, n, 1.0f, z, z1, need, bias);
       }
     }
   }
