@@ -1,5 +1,5 @@
-// The tiled core of the BF16 expert products (gfx950): the ring in LDS, the
-// fragment reads and the direct loads.
+// Shared by the tiled BF16 expert products (gfx950): the ring in LDS, the direct
+// loads and their waits, the order of stores.
 #pragma once
 #include "bf16_gemm.h"
 
@@ -48,8 +48,7 @@ __device__ __forceinline__ void load_lds4(const u32x4& rs, uint32_t lds, uint32_
 // i from column W q on.  Afterwards x is row l / 8 and y row 8 + l / 8 of lane l,
 // columns W (l % 4) on of the first block for l % 8 < 4, else of the second: a store
 // then takes whole lines, eight of 128 bytes, each from consecutive lanes.
-// (Stored as they were, 64 bytes of a row from lanes 16 apart, results pass the
-// memory pipeline far more slowly: see the weight gradient.)
+// (Figures at the weight gradient.)
 template <int W>
 __device__ __forceinline__ void store_order(float (&x)[W], float (&y)[W], int l) {
   const bool hi = l & 8;

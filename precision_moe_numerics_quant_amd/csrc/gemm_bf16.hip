@@ -1,17 +1,12 @@
 // Expert-grouped BF16 products with their epilogues (gfx950): forward with
 // bias, activation and residual, the gated block, and their input gradients.
 // v_mfma_f32_16x16x32_bf16, float32 accumulation, each result rounded once.
-#include <type_traits>
-
 #include "bf16_tile.h"
 
 namespace moe4 {
 
 static __device__ uint32_t g_dev_err;
 uint32_t take_dev_err_gemm_bf16() { return take_device_word(&g_dev_err); }
-
-template <int N>
-using Int = std::integral_constant<int, N>;
 
 namespace t16 {
 constexpr int GM = 4;            // m-tiles of a group (see tile order)
@@ -24,6 +19,21 @@ struct Tile {
   uint32_t nt;
 };
 
+// The tiled products: tiles of 256 rows of one expert x 256 columns by eight waves
+// of 64 x 128, whose sums fill half of the registers.  A slab of 64 values of K
+// (whole 128-byte lines) is 64 KB, two of them a ring in LDS that direct loads fill
+// through the tiles' ends; FWD and GATED have K contiguous in both operands, DGRAD
+// and GDGRAD read w transposed from LDS.  Workgroups stay, one per CU, and find
+// their tiles from the offsets on the device.  Tiles of few rows issue no MFMAs for the
+// missing blocks of 16.
+// Bound: a slab is 2048 cycles of MFMA per SIMD; the LDS gives its fragments (192 KB)
+// and takes the next one in about 1500, so the reads of one half of the waves run
+// under the MFMAs of the other half, and loads go between MFMAs (eight at once took
+// a turn of 1250 cycles, not 780).  16384 x 4096 from 4096: 438 us, 1254 TFLOP/s
+// (zeros: 363; torch's library product 399), its input gradient in float32 459 us
+// (449); 131072 gated rows of eight experts (1024 from 4096) 1286 TFLOP/s, of 384 even ones
+// with 256 rows 1047, with 341 (a second tile of 85 costs four fifths of a full one)
+// 766; 10 rows each: the weights at 5.9 TB/s.
 // cap: log2 of a tile's most rows
 template <int MODE, bool OUT_BF16>
 __global__ void __launch_bounds__(t16::NT, 1) k_bf16_tile(Bf16Args p, int cap, uint32_t n_nt) {
@@ -430,7 +440,9 @@ __global__ void __launch_bounds__(t16::NT, 1) k_bf16_tile(Bf16Args p, int cap, u
 // columns) and up to 64 of its rows; its four waves take every fourth 64 values
 // of K (whole lines of a weight row, two steps of 32) and join their sums
 // through LDS in wave order.  A wave requests the weights of two such pieces
-// ahead of those it multiplies; the rows come from L2.
+// ahead of those it multiplies; the rows come from L2.  Bound: HBM.  One token of
+// eight gated experts (1024 from 4096), 134 MB: 28 us, 4.8 TB/s (6.2 is the most that
+// a plain read reaches here); one row through 4096 x 1536, 12.6 MB: 11 us.
 namespace b16r {
 constexpr int NWV = 4, NT = 64 * NWV, PASSES = 4, TR = 16 * PASSES, NU = 2;
 }
@@ -583,6 +595,26 @@ static int launch_rows(const Bf16Args& p, hipStream_t stream, const char* name) 
   return check_launch(name);
 }
 
+// log2 of a tile's most rows: 256, or 128 or 64 where few tiles leave CUs idle.  A slab
+// of a tile with b blocks of 64 rows takes about 28 + 9 b; the rounds of tiles are
+// those of even loads.  Input gradients, 256 rows / as chosen: 512 rows 4096 -> 1536 (64)
+// 92.1 / 68.1 us, 8 x 500 rows 2048 -> 1024 (64) 51.6 / 39.4, 8 x 200 rows 2048 -> 4096
+// (128) 54.1 / 47.0, 4096 rows 4096 -> 1536 (128) 95.5 / 76.8.
+static int tile_rows(const Bf16Args& p, int64_t n_nt, int cus) {
+  const int64_t e = p.M < p.E ? p.M : p.E, m = (p.M + e - 1) / e;
+  int best = 8;
+  int64_t least = 0;
+  for (int cap = 8; cap >= 6; --cap) {
+    const int64_t tiles = e * n_nt * ((m + (1 << cap) - 1) >> cap), b = ((m < (1 << cap) ? m : 1 << cap) + 63) / 64;
+    const int64_t t = (tiles + cus - 1) / cus * (28 + 9 * b);
+    if (cap == 8 || t < least) {
+      least = t;
+      best = cap;
+    }
+  }
+  return best;
+}
+
 template <int MODE, bool OUT_BF16>
 static int launch_bf16(const Bf16Args& p, void* stream, const char* name) {
   using namespace t16;
@@ -597,8 +629,7 @@ static int launch_bf16(const Bf16Args& p, void* stream, const char* name) {
     const int64_t wide = (p.N * (MODE == GATED ? 2 : 1) + 63) / 64 * (p.M < p.E ? p.M : p.E);
     return wide >= 2 * cus ? launch_rows<RM, OUT_BF16, 4>(p, as_stream(stream), name) : launch_rows<RM, OUT_BF16, 2>(p, as_stream(stream), name);
   }
-  int cap = 8;   // log2 of a tile's most rows
-  while (cap > 6 && ((p.M >> cap) + (p.M < p.E ? p.M : p.E)) * nt < cus) --cap;
+  const int cap = tile_rows(p, nt, cus);
   MOE4_REQUIRE(((p.M >> cap) + p.E) * nt < ((int64_t)1 << 31), MOE4_EINVAL, std::string(name) + ": too large");
   hipLaunchKernelGGL((k_bf16_tile<MODE, OUT_BF16>), dim3((unsigned)cus), dim3(NT), 0, as_stream(stream), p, cap, (uint32_t)nt);
   return check_launch(name);
