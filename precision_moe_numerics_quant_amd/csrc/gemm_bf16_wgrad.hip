@@ -21,9 +21,9 @@ constexpr int SLOTS = 512;                // workgroups at a time: two on each o
 struct Slice {
   int32_t r, m;
   __device__ Slice(int32_t n, int i, int slices) {
-    const uint32_t slabs = ((uint32_t)n + wg::BK - 1) / wg::BK;   // (below 2^26, slices at most 32)
-    r = (int32_t)(slabs * i / slices * wg::BK);
-    const uint32_t end = slabs * (i + 1) / slices * wg::BK;
+    const uint32_t slabs = ((uint32_t)n + wg::BK - 1) / wg::BK, each = slabs / slices, more = slabs - each * slices;
+    const uint32_t from = (each * i + ((uint32_t)i < more ? i : more)) * wg::BK, end = from + (each + ((uint32_t)i < more)) * wg::BK;
+    r = (int32_t)(from < (uint32_t)n ? from : (uint32_t)n);
     m = (int32_t)(end < (uint32_t)n ? end : (uint32_t)n) - r;
   }
 };
@@ -391,7 +391,7 @@ __global__ void __launch_bounds__(wg::NT, 2) k_bf16_wgrad(Bf16Wgrad p, uint32_t 
 
 // db: 64 columns of one slice of an expert's rows per workgroup, eight a thread;
 // thread row y sums rows y, y + 128, ... in order, then the 128 sums are added in
-// order.  Bound: the read of dy; 16384 x 1536, 21 slices: 10 us, 4.9 TB/s (one: 55).
+// order.  Bound: the read of dy; 16384 x 1536, 19 slices: 10 us, 4.9 TB/s (one: 55).
 __global__ void __launch_bounds__(1024) k_bias_grad_bf16(Bf16Wgrad p) {
   __shared__ float s[128][65];
   const int e = blockIdx.y / p.db_slices, i = blockIdx.y - e * p.db_slices, cx = threadIdx.x & 7, y = threadIdx.x >> 3;
@@ -444,19 +444,29 @@ __global__ void __launch_bounds__(256) k_wgrad_join(Bf16Wgrad p, const float* pa
 
 using namespace moe4;
 
-// Slices of each expert's rows: as many as give every workgroup slot one tile (a
-// tile's rows cannot be shared otherwise), of at least 256 rows on average.  16384 rows
-// of 1536 x 4096, 192 tiles on 512 slots: one slice 327 us,
-// two 229 us with the join (five, two tiles a slot: 240 us).
-static int wgrad_slices(int64_t items, int32_t E, int64_t M) {
-  int64_t n = wg::SLOTS / items;
-  n = n < M / E / 256 ? n : M / E / 256;
-  return n < 1 ? 1 : (n < 32 ? (int)n : 32);
+// Slices of each expert's rows, for tiles (items) that are fewer than the workgroups
+// at a time: where the estimate is least, in 25 ns: a slab's share, a launch to join, for
+// each slice its turn there and the bytes of its sums, twice.
+// 16384 rows of 1536 x 4096, 192 tiles: one slice 327 us, two 229 us with the join (five,
+// two tiles a workgroup: 240).  In all, at one slice per 256 rows / as chosen: 60000
+// rows of 128 x 256 (32 slices) 52 / 42 us, 8 x 2048 rows of 512 x 512 (8) 40 / 33.
+static int wgrad_slices(int64_t items, int32_t E, int64_t M, int64_t slab, int64_t sums) {
+  const int64_t slabs = (M / E + wg::BK - 1) / wg::BK, most = wg::SLOTS / items < 128 ? wg::SLOTS / items : 128;
+  int64_t least = slab * slabs;
+  int best = 1;
+  for (int64_t n = 2; n <= most && n <= slabs; ++n) {
+    const int64_t t = slab * ((slabs + n - 1) / n) + 320 + 10 * n + n * E * sums / 15625;
+    if (t < least) {
+      least = t;
+      best = (int)n;
+    }
+  }
+  return best;
 }
 static int dw_slices(int32_t E, int64_t M, int64_t N, int64_t K) {
-  return wgrad_slices((N + wg::TM - 1) / wg::TM * ((K + wg::TN - 1) / wg::TN) * E, E, M);
+  return wgrad_slices((N + wg::TM - 1) / wg::TM * ((K + wg::TN - 1) / wg::TN) * E, E, M, 36, N * K);
 }
-static int db_slices(int32_t E, int64_t M, int64_t N) { return wgrad_slices((N + 63) / 64 * E, E, M); }
+static int db_slices(int32_t E, int64_t M, int64_t N) { return wgrad_slices((N + 63) / 64 * E, E, M, 9, N); }
 static size_t dw_part_bytes(int32_t E, int64_t M, int64_t N, int64_t K) {
   const int n = dw_slices(E, M, N, K);
   return n > 1 ? (size_t)n * E * N * K * 4 : 0;

@@ -162,10 +162,10 @@ def test_wgrad(N, K, name, maps):
 
 @pytest.mark.parametrize("mapped", [False, True])
 @pytest.mark.parametrize("m_list,N,K", [
-    ([2000], 136, 264),                # one expert: seven slices, the last with a part of a slab
-    ([1500, 0, 40, 900], 64, 72),      # two: none of the empty expert's, one slab each of the small one's
-    ([4100, 20], 200, 1000),           # eight, most of the second expert's empty
-    ([513], 8, 8),                     # two
+    ([2000], 136, 264),                # one expert, the last slab a part of one
+    ([1500, 0, 40, 900], 64, 72),      # none of the empty expert's, a slab or none each of the small one's
+    ([4100, 20], 200, 1000),           # most of the second expert's empty
+    ([513], 8, 8), ([70000], 16, 24),  # few and many
     ([300, 299], 520, 24)])            # one
 def test_wgrad_slices(m_list, N, K, mapped):
     """Few experts with many rows: slices of the rows, joined; twice over, with a bias gradient and without."""
