@@ -214,7 +214,8 @@ def _ints(shape, seed, lo=-2, hi=3):
 
 
 @pytest.mark.parametrize("m_list,N,K", [([1000, 0, 513, 2, 77], 1040, 1000), ([4096], 544, 2056), ([9] * 300, 272, 776),
-                                        ([0, 256, 255, 257, 64, 65, 192, 193, 448], 512, 96)])
+                                        ([0, 256, 255, 257, 64, 65, 192, 193, 448], 512, 96),
+                                        ([300, 31, 290, 0, 33, 64, 257, 1] * 8, 1040, 1032)])
 def test_exact_sums(m_list, N, K):
     """Small integers: every sum is exact in float32, so each result is the integer, whatever the tiles and their order."""
     c = Case(m_list, N, K, 1, mapped=True)
@@ -241,6 +242,14 @@ def test_exact_sums(m_list, N, K):
     assert torch.equal(dw.double(), wantw)
     wantb = torch.stack([dy[a:b].double().sum(0) for a, b in zip(c.off[:-1], c.off[1:])])
     assert torch.equal(db.double(), wantb)
+    # dy gathered as well (its rows in another order), and added to what is there
+    order = torch.randperm(c.M, generator=torch.Generator().manual_seed(4)).cuda()
+    there = dy[order].contiguous()
+    at = torch.empty(c.M, dtype=torch.int32, device="cuda")
+    at[order] = torch.arange(c.M, dtype=torch.int32, device="cuda")
+    # (one divisor serves both maps: dy's entries are its rows times it)
+    dw2, _ = m4.moe_grouped_gemm_bf16_wgrad(there, x, off, dy_map=at * c.div, a_map=mp, map_div=c.div, dw=dw, beta=1.0)
+    assert dw2 is dw and torch.equal(dw.double(), 2 * wantw)
 
 
 def _all_calls(c, ta, tw, tw2, tdy, tgu, tpre, off, m, outs=None):
