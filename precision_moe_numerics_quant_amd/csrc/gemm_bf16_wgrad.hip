@@ -115,14 +115,18 @@ __global__ void __launch_bounds__(wg::NT, 2) k_bf16_wgrad(Bf16Wgrad p, uint32_t 
   auto chunk_a = [&](int t, int l) __attribute__((always_inline)) { return (uint32_t)(l & 31) ^ (4 * (row_a(t, l) & 3)) ^ (2 * (w & 1)); };
   // requests the map entries of the eight slabs from row r of the expert's rows
   // (row0 .., n of them) on: this wave's of slab s to 8 s on, in the order in
-  // which a lane takes them (dy: row 4 t + g to 2 g + t, a: row 2 t + h to 4 h + t)
+  // which a lane takes them (dy: row 4 t + g to 2 g + t, a: row 2 t + h to 4 h + t).
+  // (The descriptors start at row r: an offset from the slice's first row would
+  // pass a descriptor's 2^31 bytes at row 2^29.)
   auto fetch = [&](int32_t row0, int32_t n, int32_t r) __attribute__((always_inline)) {
     const int x = lane();
-    const uint32_t o = 4 * (r + BK * (x >> 3) + 8 * w);
+    const uint32_t o = 4 * (BK * (x >> 3) + 8 * w);
+    const int64_t at = (int64_t)row0 + r;
+    const uint64_t bytes = (uint64_t)(n - r) * 4;
     __builtin_amdgcn_s_waitcnt(t16::WAIT_LGKM0);   // (the entries there have been read)
     const uint32_t to = ldsm + ((batch & 1) * 4 + w) * 256;
-    if (p.dy_map) load_lds4(rsrc4(p.dy_map + row0, (uint64_t)n * 4), to, o + 4 * (4 * (x & 1) + ((x >> 1) & 3)));
-    if (p.a_map) load_lds4(rsrc4(p.a_map + row0, (uint64_t)n * 4), to + 2048, o + 4 * (2 * (x & 3) + ((x >> 2) & 1)));
+    if (p.dy_map) load_lds4(rsrc4(p.dy_map + at, bytes), to, o + 4 * (4 * (x & 1) + ((x >> 1) & 3)));
+    if (p.a_map) load_lds4(rsrc4(p.a_map + at, bytes), to + 2048, o + 4 * (2 * (x & 3) + ((x >> 2) & 1)));
     ++batch;
   };
   // a mapped row's offset; rows that do not exist are noted in bad

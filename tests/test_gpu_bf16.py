@@ -547,6 +547,21 @@ def test_offsets_past_32_bits():
         assert torch.equal(dw[i].double(), big[r].double().t() @ small[r].double())
 
 
+def test_wgrad_maps_past_2_31_bytes():
+    """One expert's maps of more than 2^31 bytes (2^29 rows, one slice): the entries behind them are the ones read.
+    All rows but the last are zeros; row 0, which an entry that is not read would name, is not."""
+    E, M, tail = 2048, (1 << 29) + 96, 160                             # (the tail starts before 2^29)
+    off = torch.full((E + 1,), M, dtype=torch.int32, device="cuda")
+    off[0] = 0
+    dy, a = _ints((64, 8), 12), _ints((64, 8), 13)
+    dy[0], a[0], dy[1] = 1, 1, 0
+    m = torch.ones(M, dtype=torch.int32, device="cuda")
+    m[-tail:] = 2 + torch.arange(tail, dtype=torch.int32, device="cuda") * 7 % 62
+    i = m[-tail:].long()
+    dw, _ = m4.moe_grouped_gemm_bf16_wgrad(dy, a, off, dy_map=m, a_map=m)
+    assert torch.equal(dw[0].double(), dy[i].double().t() @ a[i].double()) and not dw[1:].any()
+
+
 def test_weight_gradient_past_32_bits():
     E, N, K = 70, 4096, 4096
     dy, a = _ints((3 * E, N), 10), _ints((3 * E, K), 11)
