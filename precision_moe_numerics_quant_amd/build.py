@@ -10,12 +10,17 @@ float32 division is kept.
 The SiLU / SiLU' tables are constant data of the library: gen_act_tab.cpp,
 compiled and run on the host first, writes them as the initialiser that
 capi.hip includes (act_tab.inc, in the build directory).
+
+The linked code is checked for the wait states that inline assembly needs
+(wait_states.py) before it takes the library's place.
 """
 import os
 import shutil
 import subprocess
 import sys
 import tempfile
+
+from . import wait_states
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -56,6 +61,7 @@ def build(verbose=False, jobs=8):
         r = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
         if r.returncode != 0:
             raise RuntimeError("link failed:\n" + r.stdout)
+        wait_states.check(out_tmp)
         os.replace(out_tmp, LIB)
     finally:
         shutil.rmtree(tmp, ignore_errors=True)

@@ -34,7 +34,10 @@ __device__ __forceinline__ u32x4 rsrc4(const void* p, uint64_t bytes) {
 // before each LDS read; it has no output register, and its completion is waited
 // for by hand (wait_vm) before the barrier that hands the stage over.
 // (M0 is not in the clobber list, which does not take it; nothing else in these
-// kernels uses it.)
+// kernels uses it.  It needs the one wait state.  The scalar registers need five
+// behind a vector instruction that writes them, a lane read of a spilled
+// descriptor say; the compiler does not see to that here, and three more in each load cost
+// 1 to 3 %: the build checks the distance in the code it made, wait_states.py.)
 __device__ __forceinline__ void load_lds(const u32x4& rs, uint32_t lds, uint32_t off, uint32_t soff) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds" ::"s"(lds), "v"(off), "s"(rs), "s"(soff) : "memory");
 }
