@@ -69,6 +69,10 @@ __device__ inline float row_scale(const float* scale, const int32_t* map, int64_
 // the hardware's exp2 and reciprocal, whose relative error (|p| 2^-24 and 1 ulp)
 // is far below the half step of 2^-9 that rounding to bf16 costs.
 // Infinities: act(-inf) = -0, act(inf) = inf, act' = 0 and 1 there.
+// Below p = FAR t leaves float32's range before x t does (exp(-p) overflows at
+// -88.7: SiLU of -89 is -2e-37), and 1 + exp(-p) is exp(-p) to all bits: there t =
+// h^2 with h = exp(p / 2), a factor at a time.  Hardly any value is so far out, so the
+// values of one store are looked at together: a minimum each, one branch.
 struct ActCoef {
   float c1, c3;
   __host__ __device__ ActCoef(int act) : c1(act == MOE4_ACT_GELU ? 1.5957691216f : 1.0f), c3(act == MOE4_ACT_GELU ? 1.5957691216f * 0.044715f : 0.0f) {}
@@ -78,13 +82,30 @@ __device__ inline float sigmoid_of(float p) {
   if (EXACT) return 1.0f / (1.0f + expf(-p));
   return __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(p * -1.44269504f));
 }
-template <bool EXACT>
-__device__ inline void act_of(const ActCoef& a, float x, float& f, float& df) {
-  const float x2 = fminf(x * x, 1e30f);   // (x^2 past the range, times c3 = 0)
-  const float t = sigmoid_of<EXACT>(x * fmaf(a.c3, x2, a.c1)), s = t * (1.0f - t);
-  f = t == 0.0f ? -0.0f : x * t;
-  // (x s before p': x^2 alone may exceed the range where s x p' does not)
-  df = s == 0.0f ? t : fmaf(x * s, fmaf(3.0f * a.c3, x2, a.c1), t);
+constexpr float FAR = -80.0f;
+template <bool EXACT, int W>
+__device__ inline void act_of(const ActCoef& a, const float (&x)[W], float (&f)[W], float (&df)[W]) {
+  float least = 0.0f;
+#pragma unroll
+  for (int i = 0; i < W; ++i) {
+    const float x2 = fminf(x[i] * x[i], 1e30f);   // (x^2 past the range, times c3 = 0)
+    const float p = x[i] * fmaf(a.c3, x2, a.c1), t = sigmoid_of<EXACT>(p), s = t * (1.0f - t);
+    least = fminf(least, p);
+    f[i] = x[i] * t;
+    // (x s before p': x^2 alone may exceed the range where s x p' does not)
+    df[i] = s == 0.0f ? t : fmaf(x[i] * s, fmaf(3.0f * a.c3, x2, a.c1), t);
+  }
+  if (least < FAR) {
+#pragma unroll
+    for (int i = 0; i < W; ++i) {
+      const float x2 = fminf(x[i] * x[i], 1e30f), p = x[i] * fmaf(a.c3, x2, a.c1);
+      const float h = EXACT ? expf(0.5f * p) : __builtin_amdgcn_exp2f(p * 0.72134752f);
+      if (p < FAR) {
+        f[i] = h == 0.0f ? -0.0f : x[i] * h * h;
+        df[i] = h == 0.0f ? 0.0f : h * fmaf(x[i], fmaf(3.0f * a.c3, x2, a.c1), 1.0f) * h;
+      }
+    }
+  }
 }
 
 // ---------------------------------------------------------------- epilogues
@@ -193,6 +214,18 @@ struct Bf16Epilogue {
       if (MODE == GATED) load_f32<W>(bias, n < N ? n + N : PAST, reinterpret_cast<float(&)[W]>(x.b1));
     }
   }
+  template <bool EXACT, int W>
+  __device__ void act_or_none(const float (&x)[W], float (&f)[W], float (&df)[W]) const {
+    if (has_act) {
+      act_of<EXACT, W>(act, x, f, df);
+    } else {
+#pragma unroll
+      for (int i = 0; i < W; ++i) {
+        f[i] = x[i];
+        df[i] = 1.0f;
+      }
+    }
+  }
   template <int W>
   __device__ void add_store(uint32_t o, float (&q)[W], const Need<W>& x) const {
     if (has_res) {
@@ -210,19 +243,13 @@ struct Bf16Epilogue {
   __device__ void put(uint32_t r, uint32_t n, float s, const float (&z)[W], const float (&z1)[W], const Need<W>& x, const Bias<W>& bs) const {
     const bool ok = n < N;
     const uint32_t o = ok ? r * N + n : PAST, o0 = ok ? 2 * r * N + n : PAST, o1 = ok ? o0 + N : PAST;
-    float v[W], h[W], q[W], d;
+    float v[W], h[W], q[W], d[W];
     if (MODE == FWD) {
 #pragma unroll
       for (int i = 0; i < W; ++i) q[i] = has_bias ? z[i] + bs.b[i] : z[i];
       if (has_aux) store_bf16<W, POLICY>(aux, o, q);
-      if (has_act) {
-#pragma unroll
-        for (int i = 0; i < W; ++i) {
-          act_of<!OUT_BF16>(act, q[i], h[i], d);
-          q[i] = h[i];
-        }
-      }
-      add_store<W>(o, q, x);
+      act_or_none<!OUT_BF16, W>(q, h, d);
+      add_store<W>(o, h, x);
     } else if (MODE == GATED) {
       float u[W];
 #pragma unroll
@@ -234,12 +261,9 @@ struct Bf16Epilogue {
         store_bf16<W, POLICY>(aux, o0, q);
         store_bf16<W, POLICY>(aux, o1, u);
       }
+      act_or_none<false, W>(q, h, d);
 #pragma unroll
-      for (int i = 0; i < W; ++i) {
-        if (has_act) act_of<false>(act, q[i], h[i], d);
-        else h[i] = q[i];
-        h[i] = h[i] * u[i];
-      }
+      for (int i = 0; i < W; ++i) h[i] = h[i] * u[i];
       store_bf16<W, POLICY>(c, o, h);
     } else {
 #pragma unroll
@@ -247,14 +271,10 @@ struct Bf16Epilogue {
       if (MODE == DGRAD) {
         if (has_in) {
           values_of<W>(x.in, v);
+          act_or_none<!OUT_BF16, W>(v, h, d);
 #pragma unroll
           for (int i = 0; i < W; ++i) {
-            if (has_act) {
-              act_of<!OUT_BF16>(act, v[i], h[i], d);
-              q[i] = q[i] * d;
-            } else {
-              h[i] = v[i];
-            }
+            q[i] = q[i] * d[i];
             h[i] = s * h[i];
           }
           if (has_aux) store_bf16<W, POLICY>(aux, o, h);
@@ -264,13 +284,12 @@ struct Bf16Epilogue {
         float u[W];
         values_of<W>(x.in, v);
         values_of<W>(reinterpret_cast<const uint32_t(&)[W / 2]>(x.in1), u);
+        act_or_none<false, W>(v, h, d);
 #pragma unroll
         for (int i = 0; i < W; ++i) {
-          float f = v[i];
-          d = 1.0f;
-          if (has_act) act_of<false>(act, v[i], f, d);
+          const float f = h[i];
           h[i] = s * (f * u[i]);
-          v[i] = q[i] * u[i] * d;
+          v[i] = q[i] * u[i] * d[i];
           u[i] = q[i] * f;
         }
         if (has_aux) store_bf16<W, POLICY>(aux, o, h);

@@ -351,6 +351,60 @@ def test_activation_limits():
             assert (d[9:14] == 1).all() and torch.equal(h[9:14], pre.float().cpu()[0, 9:14])
 
 
+def _act_far(kind, x):
+    """act and act' where sigmoid(p) is near or below float32's smallest normal number (1 - t = 1 to far below a
+    unit there), and their errors' bound relative to them: p is off by three roundings and its product with log2 e
+    by two, |p| 5 U in the exponent; the exponential a unit (2 U) in each of two factors, their products 2 U, and
+    in act' the factor 1 + x p' another five."""
+    f, d = ob.act(kind, x)
+    p = x if kind == ob.SILU else ob._C * (x + 0.044715 * x ** 3)
+    return f, d, (5 * np.abs(p) + 12) * U
+
+
+def _far_check(got, want, rel, bf16, what):
+    """rel, a half step of the type, and half a unit of its subnormal numbers (2**-149, bf16 2**-133) after a
+    product of the same."""
+    got = got.double().cpu().numpy()
+    lim = np.abs(want) * (rel + (2.0 ** -8 if bf16 else U)) + 2.0 ** -149 + (2.0 ** -134 if bf16 else 0.0)
+    bad = ~(np.abs(got - want) <= lim)
+    assert not bad.any(), f"{what}: {int(bad.sum())} of {bad.size} off; first: {got[bad][0]} for {want[bad][0]}, bound {lim[bad][0]}"
+
+
+@pytest.mark.parametrize("M", [8, 300, 5000])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("act", [ob.SILU, ob.GELU])
+def test_activations_of_far_values(act, dt, M):
+    """Where the sigmoid leaves float32's range the activation itself does not: SiLU of -89 is -2e-37."""
+    K = 64
+    rng = np.random.default_rng(M)
+    x = np.where(rng.random((M, K)) < 0.5, rng.uniform(-110, -60, (M, K)), rng.uniform(-13, -7, (M, K)))
+    x, tx = bf(x)
+    tx = tx.cuda()
+    eye = torch.eye(K, dtype=torch.bfloat16, device="cuda")[None].contiguous()
+    off = torch.tensor([0, M], dtype=torch.int32, device="cuda")
+    f, d, rel = _act_far(act, x)
+    bf16 = dt == "bf16"
+    c, _ = m4.moe_grouped_gemm_bf16(tx, eye, off, act=act, out_dtype=dtype_of(dt))
+    _far_check(c, f, rel, bf16, "c")
+    ones = torch.zeros((M, K), dtype=torch.bfloat16, device="cuda")
+    ones[:, 0] = 1
+    w = torch.zeros((1, K, K), dtype=torch.bfloat16, device="cuda")
+    w[0, 0] = 1
+    dx, hs = m4.moe_grouped_gemm_bf16_dgrad(ones, w, off, pre=tx, act=act, out_dtype=dtype_of(dt))
+    _far_check(hs, f, rel, True, "hs")
+    _far_check(dx, d, rel, bf16, "dx")
+    if bf16:
+        h, _ = m4.moe_gated_gemm_bf16(tx, torch.stack((eye, eye), 1).view(1, 2, K, K), off, act=act)
+        # (the product with u = x: a rounding more, and a subnormal act(g)'s unit times |x|)
+        _far_check(h, f * x, rel + U + 110 * 2.0 ** -149 / np.maximum(np.abs(f * x), 2.0 ** -133), True, "h")
+        gu = torch.stack((tx, tx), 1).contiguous()
+        dgu, hs = m4.moe_gated_gemm_bf16_dgrad(ones, w, gu, off, act=act)
+        lost = 110 * 2.0 ** -149 / np.maximum(np.abs(f * x), 2.0 ** -133)
+        _far_check(hs, f * x, rel + U + lost, True, "gated hs")
+        _far_check(dgu[:, 0], d * x, rel + U + lost, True, "dg")
+        _far_check(dgu[:, 1], f, rel, True, "du")
+
+
 @pytest.mark.parametrize("m_list", [[3, 2], [200, 100], [3000, 1200]])
 def test_map_entries_out_of_range(m_list):
     """They count as rows of zeros (scale 0) and are reported."""
