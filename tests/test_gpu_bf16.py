@@ -194,6 +194,27 @@ def test_wgrad_slices(m_list, N, K, mapped):
         check(np64(dw[e + 1:]), want[e + 1:], z_err(max(m_list), mag[e + 1:]), False, "dw beside an empty expert")
 
 
+@pytest.mark.parametrize("mapped", [False, True])
+@pytest.mark.parametrize("m_list,N,K", [([5000], 72, 40), ([4100, 20], 200, 1000), ([3000, 0, 8000], 8, 16)])
+def test_bias_gradient_scaled_in_slices(m_list, N, K, mapped):
+    """db = the sum of db_scale dy where the rows are cut into slices."""
+    c = Case(m_list, N, K, N + K + 6, mapped=mapped, div=3, lead=5, tail=3)
+    # (more than the weight gradient's slices: those of the bias gradient too)
+    assert m4.lib().moe_grouped_gemm_bf16_wgrad_ws_bytes(c.E, c.M, N, K) % (c.E * N * K * 4) != 0
+    dy, tdy = c.bf(c.rows, N)
+    _, ta = c.bf(c.M, K)
+    s, ts = c.f32(c.rows * c.div)
+    terms = c.scale_of(s) * c.gather(dy)
+    b, bmag = np.zeros((c.E, N)), np.zeros((c.E, N))
+    for e, r0, r1 in ob.groups(c.off):
+        b[e], bmag[e] = terms[r0:r1].sum(0), np.abs(terms[r0:r1]).sum(0)
+    args = dict(dy_map=c.gpu_map(), map_div=c.div, db_scale=ts)
+    dw, db = m4.moe_grouped_gemm_bf16_wgrad(tdy, ta, c.gpu_off(), bias_grad=True, **args)
+    check(np64(db), b, z_err(max(m_list) + 1, bmag), False, "db")
+    m4.moe_grouped_gemm_bf16_wgrad(tdy, ta, c.gpu_off(), dw=dw, beta=1.0, db=db, **args)
+    check(np64(db), 2 * b, 2 * z_err(max(m_list) + 2, bmag), False, "db twice")
+
+
 def test_wgrad_empty_experts():
     """Zeros, or with skip_empty (and when accumulating) left as they are."""
     c = Case([0, 40, 0], 72, 40, 5)
@@ -437,6 +458,29 @@ def test_map_entries_out_of_range(m_list):
     assert torch.equal(dw, dwz)
     with pytest.raises(m4.Moe4DeviceError):
         m4.moe4_debug_check()
+
+
+@pytest.mark.parametrize("m_list", [[3, 2], [200, 100], [9000, 1200], [12000]])
+def test_dy_map_entries_out_of_range(m_list):
+    """In the weight and bias gradients their rows count as zeros, whatever scale they would have, and are reported."""
+    N, K = 72, 40
+    c = Case(m_list, N, K, 15, mapped=True)
+    dy, a = c.bf(c.rows, N)[1], c.bf(c.M, K)[1]
+    scale = c.f32(c.rows * c.div)[1]
+    off, m = c.gpu_off(), c.gpu_map()
+    out = [1, 3, 4]
+    bad = m.clone()
+    bad[1], bad[3], bad[4] = -1, c.rows * c.div, 2 ** 31 - 1
+    m4.moe4_debug_check()
+    dw, db = m4.moe_grouped_gemm_bf16_wgrad(dy, a, off, dy_map=bad, map_div=c.div, bias_grad=True, db_scale=scale)
+    with pytest.raises(m4.Moe4DeviceError):
+        m4.moe4_debug_check()
+    # the same sums with zeros in those rows of a, and as those entries' scale
+    a[out] = 0
+    scale[m[out].long()] = 0
+    dwz, dbz = m4.moe_grouped_gemm_bf16_wgrad(dy, a, off, dy_map=m, map_div=c.div, bias_grad=True, db_scale=scale)
+    m4.moe4_debug_check()
+    assert torch.equal(dw, dwz) and torch.equal(db, dbz)
 
 
 @pytest.mark.parametrize("m_list", [[40, 90], [4000, 100]])
