@@ -15,9 +15,10 @@ Zipf(1.1) expert bias; upstream gradient N(0, 1e-3); synthetic seeded inputs
 resident in HBM before the timed region.
 
 The same layer with an MXFP8 forward (the pages' higher-precision layers,
-and their full-MXFP8 baseline) and with an MXFP4 forward is timed on the same
-inputs afterwards and reported under `mxfp8_forward_variant` and
-`mxfp4_forward_variant`.
+and their full-MXFP8 baseline), with an MXFP4 forward and in BF16 (weights in
+bf16 from the start: nothing to quantise) is timed on the same inputs
+afterwards and reported under `mxfp8_forward_variant`, `mxfp4_forward_variant`
+and `bf16_variant`.
 
 Printed: one JSON line.  `value` is the step's grouped-GEMM work (6 GEMMs,
 2*M*N*K each, padding excluded) divided by the whole step time; the
@@ -316,11 +317,11 @@ def gpu_run(steps, warmup, layer_only=False):
     payload = combine_payload_bench(fw, c)
     small = small_configs_bench(inp, fw["wq"])
     del fw, bw
-    # the MXFP8- and MXFP4-forward variants of the same layer on the same inputs
-    def variant(forward, backward):
+    # the MXFP8- and MXFP4-forward variants of the same layer on the same inputs, and the layer in BF16
+    def variant(forward, backward, weights=(inp["w_up"], inp["w_down"]), **sr):
         def step_v(t=None):
-            fw = forward(inp["x"], inp["w_up"], inp["w_down"], inp["logits"], k, inp["bias"], timer=t, seed=synth.SR_SEED)
-            backward(fw, inp["dy"], seed=synth.SR_SEED, timer=t, skip_empty_dw=True)
+            fw = forward(inp["x"], *weights, inp["logits"], k, inp["bias"], timer=t, **sr)
+            backward(fw, inp["dy"], timer=t, skip_empty_dw=True, **sr)
         for _ in range(warmup):
             step_v()
         torch.cuda.synchronize()
@@ -339,7 +340,8 @@ def gpu_run(steps, warmup, layer_only=False):
                 per_v[name] = round(prev.elapsed_time(ev), 4)
             prev = ev
         return ms, per_v
-    variants = variant(layer.forward_mx, layer.backward_mx), variant(layer.forward_mx4, layer.backward_mx4)
+    variants = (variant(layer.forward_mx, layer.backward_mx, seed=synth.SR_SEED), variant(layer.forward_mx4, layer.backward_mx4, seed=synth.SR_SEED),
+                variant(layer.forward_bf16, layer.backward_bf16, (inp["w_up"].bfloat16(), inp["w_down"].bfloat16())))
     # last, since its memory pool makes the caching allocator's later large
     # allocations slow: the step replayed from one HIP graph
     graph_run = graph_steps(step, steps, ref_outputs)
@@ -777,17 +779,18 @@ def main():
                 "ms_per_step": round(ms, 3),
                 "value": round(step_gemm_flops / (ms * 1e-3) / 1e12, 2),
                 "fwd_gemm_tflops": {n: round(2.0 * c["T"] * c["k"] * c["d"] * c["F"] / (per_v[n] * 1e-3) / 1e12, 1)
-                                    for n in (f"F6 up GEMM ({fmt})", f"F8 down GEMM ({fmt})") if n in per_v},
+                                    for n in (f"F6 up GEMM ({fmt})", f"F6 up GEMM + activation ({fmt})", f"F8 down GEMM ({fmt})") if n in per_v},
                 "breakdown_ms": per_v,
             }
         out.update({
             "wgrad_zero_fill": zero_fill,
             "quantizer_microbench": quantizer_microbench(),
             # the same layer with an MXFP8 forward (the pages' higher-precision
-            # layers, and their full-MXFP8 baseline) and with an MXFP4 forward:
-            # whole step, and per call (ms)
+            # layers, and their full-MXFP8 baseline), with an MXFP4 forward and in
+            # BF16: whole step, and per call (ms)
             "mxfp8_forward_variant": variant(*variants[0], "MXFP8"),
             "mxfp4_forward_variant": variant(*variants[1], "MXFP4"),
+            "bf16_variant": variant(*variants[2], "BF16"),
             # the combine fed by the 8.25-bit payload the pages send back between GPUs
             "combine_payload_8p25": payload,
             # the small workloads: weight streaming (RL-shaped forward) and launch latency (tiny layer)
