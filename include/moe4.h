@@ -866,7 +866,7 @@ int moe_gated_gemm_bf16_dgrad(const uint16_t* dy, int64_t dy_rows, const int32_t
  * = 1) left as they are.
  * ws: moe_grouped_gemm_bf16_wgrad_ws_bytes(E, M_total, N, K) bytes, 16-byte aligned
  * (0 unless few experts have many rows: then the sums of slices of their rows,
- * joined in order); calls in flight at the same time need workspaces of their own.
+ * joined in order; 0 too for sizes that the call refuses); calls in flight at the same time need workspaces of their own.
  */
 int moe_grouped_gemm_bf16_wgrad(const uint16_t* dy, int64_t dy_rows, const int32_t* dy_map, const uint16_t* a,
                                 int64_t a_rows, const int32_t* a_map, int32_t map_div, const int32_t* expert_off,

@@ -476,8 +476,15 @@ static size_t dw_part_bytes(int32_t E, int64_t M, int64_t N, int64_t K) {
   return n > 1 ? (size_t)n * E * N * K * 4 : 0;
 }
 
+static bool wgrad_shape(int32_t E, int64_t M, int64_t N, int64_t K) {
+  return E >= 1 && E <= 2048 && M >= 0 && N > 0 && K > 0 && N % 8 == 0 && K % 8 == 0;
+}
+static bool wgrad_fits(int64_t M, int64_t N, int64_t K) {
+  return M < ((int64_t)1 << 31) && N < ((int64_t)1 << 20) && K < ((int64_t)1 << 20) && N * K < ((int64_t)1 << 29);
+}
+
 extern "C" size_t moe_grouped_gemm_bf16_wgrad_ws_bytes(int32_t E, int64_t M_total, int64_t N, int64_t K) {
-  if (E < 1 || M_total < 0 || N < 1 || K < 1) return 0;
+  if (!wgrad_shape(E, M_total, N, K) || !wgrad_fits(M_total, N, K)) return 0;   // (the call refuses these)
   const int n = db_slices(E, M_total, N);
   return dw_part_bytes(E, M_total, N, K) + (n > 1 ? (size_t)n * E * N * 4 : 0);
 }
@@ -487,10 +494,9 @@ extern "C" int moe_grouped_gemm_bf16_wgrad(const uint16_t* dy, int64_t dy_rows, 
                                            int64_t N, int64_t K, float* dw, float beta, int flags, const float* db_scale, float* db,
                                            void* ws, size_t ws_bytes, void* stream) {
   const std::string s("moe_grouped_gemm_bf16_wgrad");
-  MOE4_REQUIRE(E >= 1 && E <= 2048 && M_total >= 0 && N > 0 && K > 0 && N % 8 == 0 && K % 8 == 0, MOE4_EINVAL,
+  MOE4_REQUIRE(wgrad_shape(E, M_total, N, K), MOE4_EINVAL,
                s + ": need 1 <= E <= 2048 and widths that are multiples of 8");
-  MOE4_REQUIRE(M_total < ((int64_t)1 << 31) && dy_rows >= 0 && a_rows >= 0 && dy_rows < ((int64_t)1 << 31) && a_rows < ((int64_t)1 << 31) &&
-                   N < ((int64_t)1 << 20) && K < ((int64_t)1 << 20) && N * K < ((int64_t)1 << 29),
+  MOE4_REQUIRE(wgrad_fits(M_total, N, K) && dy_rows >= 0 && a_rows >= 0 && dy_rows < ((int64_t)1 << 31) && a_rows < ((int64_t)1 << 31),
                MOE4_EINVAL, s + ": rows must be below 2^31, widths below 2^20, each expert's matrix below 2 GiB");
   MOE4_REQUIRE((beta == 0.0f || beta == 1.0f) && (flags & ~MOE4_WGRAD_SKIP_EMPTY) == 0, MOE4_EINVAL, s + ": beta must be 0 or 1, flags known");
   MOE4_REQUIRE(expert_off && dw, MOE4_EINVAL, s + ": NULL pointer");

@@ -93,6 +93,28 @@ def test_wgrad_refusals(kw, rc):
     assert wgrad(**kw) == rc
 
 
+@pytest.mark.parametrize("E,M,N,K", [(1, 8, 1 << 39, 1 << 40), (128, 8, 1 << 62, 8), (2, 4096, 1 << 20, 64), (2, 4096, 1 << 17, 1 << 12), (2049, 8, 64, 64),
+                                     (0, 8, 64, 64), (2, -1, 64, 64), (2, 1 << 31, 64, 64), (2, 4096, 0, 64), (2, 4096, 64, -8), (2, 4096, 60, 64)])
+def test_wgrad_workspace_of_refused_sizes(E, M, N, K):
+    """0 for what the call refuses, however large (in a process of its own: the sizes' products may wrap to a divisor of 0)."""
+    import subprocess
+    import sys
+    from test_capi_exports import LIB
+    _lib()
+    code = ("import ctypes; f = ctypes.CDLL(%r).moe_grouped_gemm_bf16_wgrad_ws_bytes; f.restype = ctypes.c_size_t; "
+            "print(f(ctypes.c_int32(%d), ctypes.c_int64(%d), ctypes.c_int64(%d), ctypes.c_int64(%d)))" % (LIB, E, M, N, K))
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True)
+    assert r.returncode == 0 and r.stdout.strip() == "0", (r.returncode, r.stdout, r.stderr[-300:])
+
+
+def test_wgrad_workspace_of_served_sizes():
+    """Few experts with many rows need one, one that would not pay for its join does not."""
+    f = _lib().moe_grouped_gemm_bf16_wgrad_ws_bytes
+    f.restype = ctypes.c_size_t
+    size = lambda E, M, N, K: f(i32(E), i64(M), i64(N), i64(K))  # noqa: E731
+    assert size(1, 16384, 1536, 4096) >= 2 * 1536 * 4096 * 4 and size(2048, 16384, 1536, 4096) == 0 and size(1, 8, 64, 64) == 0
+
+
 def drop(yp=P, T=8, k=2, d=64, p=0.1, res=O, y=P):
     return call("moe_combine_dropout", yp, P, P, i64(T), i32(k), i64(d), f64(p), ctypes.c_uint64(1), ctypes.c_uint32(0), res, y, O)
 
