@@ -792,7 +792,9 @@ size_t moe_router_wgrad_dense_ws_bytes(int64_t T, int32_t E, int64_t d);
  *  - Exact products, float32 accumulation, one rounding of each result (of
  *    bf16 outputs, and none of float32 ones).  act: MOE4_ACT_NONE, MOE4_ACT_SILU
  *    (x sigmoid(x)) or MOE4_ACT_GELU (the tanh form, x sigmoid(2 sqrt(2/pi) (x +
- *    0.044715 x^3))); act(-infinity) = -0.
+ *    0.044715 x^3))), in float32 to a relative (3 |p| + 8) 2^-23, p the sigmoid's
+ *    argument, also where the sigmoid alone is below float32's range;
+ *    act(-infinity) = -0.
  *  - Every width is a multiple of 8 below 2^20, each expert's matrix below 1 GiB
  *    (wgrad: its float32 gradient below 2 GiB), a mapped operand below 2 GiB,
  *    M_total and the operands' rows below 2^31, E <= 2048.  Pointers 16-byte
@@ -880,7 +882,10 @@ size_t moe_grouped_gemm_bf16_wgrad_ws_bytes(int32_t E, int64_t M_total, int64_t 
  * acc moe_combine's float32 sum, q = round((1 - p) 65536) (ties to even).  keep(i)
  * is 1 iff the 16 random bits of element i, those of the stochastic rounding for
  * (seed, stream_id, i), are below q: the mask is never stored.  A dropped value
- * is 0 whatever acc holds; p = 1 drops all.  residual [T, d] bf16 or NULL (it
+ * is 0 whatever acc holds; p = 1 drops all.  The hash's key has 32 bits: about
+ * one pair of (seed, stream_id) in 2^32 has the same mask, and any two masks are one
+ * sequence of words in another order (element pairs related by an XOR of their
+ * indices).  residual [T, d] bf16 or NULL (it
  * may be y).  yp [T*k, d] float32, gates [T, k], inv_perm [T*k], y [T, d] bf16.
  * 1 <= k <= 16, d % 4 == 0, T * k < 2^31, 0 <= p <= 1.  Rows outside [0, T*k) are
  * clamped and reported (MOE4_DEVERR_INDEX).

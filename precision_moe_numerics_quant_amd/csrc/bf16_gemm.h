@@ -67,7 +67,7 @@ __device__ inline float row_scale(const float* scale, const int32_t* map, int64_
 // and c3 = 0.044715 c1.  act'(x) = t + x t (1 - t) p'.
 // EXACT (float32 results): exp and the division to within an ulp; otherwise
 // the hardware's exp2 and reciprocal, whose relative error (|p| 2^-24 and 1 ulp)
-// is far below the half step of 2^-9 that rounding to bf16 costs.
+// is far below the half step of 2^-8 that rounding to bf16 costs.
 // Infinities: act(-inf) = -0, act(inf) = inf, act' = 0 and 1 there.
 // Below p = FAR t leaves float32's range before x t does (exp(-p) overflows at
 // -88.7: SiLU of -89 is -2e-37), and 1 + exp(-p) is exp(-p) to all bits: there t =

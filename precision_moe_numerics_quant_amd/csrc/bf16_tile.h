@@ -7,13 +7,12 @@ namespace moe4 {
 namespace t16 {
 
 constexpr int NT = 512;                      // eight waves of 64 x 128, 4 x 2
-constexpr int TM = 256, TN = 256, BK = 64;   // tile, contraction slab
+constexpr int TN = 256, BK = 64;             // tile columns, contraction slab
 constexpr int HALF = 256 * BK * 2, STAGE = 2 * HALF, RING = 2 * STAGE;   // two slabs
 constexpr int MAX_E = 2048;                  // experts (their offsets are kept in LDS)
 constexpr uint32_t OOB = 0x80000000u;        // past every descriptor: zeros arrive
 typedef __attribute__((address_space(3))) uint8_t* lds_u8;
 typedef short s16x4 __attribute__((ext_vector_type(4)));
-typedef short s16x8 __attribute__((ext_vector_type(8)));
 
 // s_waitcnt immediates (vmcnt: bits 3:0 and 15:14; expcnt 6:4; lgkmcnt 11:8)
 constexpr int wait_vm(int n) { return (n & 15) | ((n >> 4) << 14) | (7 << 4) | (15 << 8); }

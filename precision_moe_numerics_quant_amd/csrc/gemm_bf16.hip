@@ -33,7 +33,7 @@ struct Tile {
 // (zeros: 363; torch's library product 399), its input gradient in float32 459 us
 // (449); 131072 gated rows of eight experts (1024 from 4096) 1286 TFLOP/s, of 384 even ones
 // with 256 rows 1047, with 341 (a second tile of 85 costs four fifths of a full one)
-// 766; 10 rows each: the weights at 5.9 TB/s.
+// 766; some 10 rows each, uneven: the weights at 4.7 TB/s.
 // cap: log2 of a tile's most rows
 template <int MODE, bool OUT_BF16>
 __global__ void __launch_bounds__(t16::NT, 1) k_bf16_tile(Bf16Args p, int cap, uint32_t n_nt) {
@@ -442,7 +442,7 @@ __global__ void __launch_bounds__(t16::NT, 1) k_bf16_tile(Bf16Args p, int cap, u
 // through LDS in wave order.  A wave requests the weights of two such pieces
 // ahead of those it multiplies; the rows come from L2.  Bound: HBM.  One token of
 // eight gated experts (1024 from 4096), 134 MB: 28 us, 4.8 TB/s (6.2 is the most that
-// a plain read reaches here); one row through 4096 x 1536, 12.6 MB: 11 us.
+// a plain read reaches here); one row through 4096 x 1536, 12.6 MB: 8 us.
 namespace b16r {
 constexpr int NWV = 4, NT = 64 * NWV, PASSES = 4, TR = 16 * PASSES, NU = 2;
 }
@@ -572,12 +572,16 @@ int tile_grid() {
 // Whether a forward product goes to the few-rows kernel: where the tiles of the
 // experts that can have rows are fewer than the CUs, the tiled kernel leaves CUs idle and
 // pays a ring's start for each; but the few-rows kernel multiplies a quarter as
-// fast, so only up to 16 rows times tile columns a CU.  Both, few rows / tiled:
-//   one of 1536 x 4096, 128 rows     12 column tiles    29.8 / 57.8 us
-//   one of 4096 x 1536, 256 rows     16                 22.5 / 26.8
-//   8 experts of 4096 x 4096, 32 and 64 rows each, 128  52.5 / 74.4, 67.5 / 76.5; 128 rows 129 / 89
-//   4 of 1024 x 512 (gated), 128 and 200 rows each, 32  12.3 / 15.3, 23.3 / 15.7
-//   1, 4 and 8 tokens of 8 of 384 experts of 1024 x 4096 (gated), 64, 248, 472   27.6 / 58.5, 98.8 / 104.9, 186 / 177
+// fast, so only up to 16 rows times tile columns a CU.  Both, few rows / tiled in
+// us (weights from memory, launches in one graph), by tiles as counted below:
+//   16   one of 4096 x 1536, 1 and 256 rows             7.8 / 35.4, 23.6 / 34.6
+//    6   one of 1536 x 4096, 128 rows                   27.0 / 73.8
+//   12   one of 1536 x 4096 (gated), 128 rows           29.8 / 74.9
+//   32   4 of 1024 x 512 (gated), 128 rows each         12.2 / 14.9; 200 (past the bound) 23.8 / 15.8
+//  128   8 of 4096 x 4096, 32 rows each                 66.3 / 89.2; 64 and 128 (past it) 79.5 / 92.5, 145 / 96
+//  256   16 of 4096 x 1024, 8 and 16 rows each          29.8 / 33.1, 31.6 / 33.1
+//   64 to 512   1, 2, 3, 4 and 8 tokens of 8 of 384 experts of 1024 x 4096 (gated)
+//               30.6 / 65.6, 55.7 / 86.5, 78.8 / 91.0, 103 / 102, 198 / 187
 // With more tiles the two are alike for even loads (384 experts of 4096 x 1024, 8
 // rows each 584 / 656, 16 rows 665 / 676) and the tiled one far ahead for uneven ones
 // (8 and 16 rows on average, weights falling by rank: 236 / 168, 369 / 209).

@@ -490,7 +490,10 @@ def forward_bf16(x, w_up, w_down, logits, k, bias=None, b_up=None, b_down=None, 
     shared: dict(w_up, w_down, and optionally b_up, b_down) of a shared expert, each with E = 1.
     y = residual + dropout(routed experts' output) + shared expert's output;
     residual [T, d] bf16 or None, dropout the probability (random words of (seed,
-    stream 16 * layer + 4)).  save: keep what the backward needs.
+    stream 16 * layer + 4)).  With a shared expert y is rounded to bf16 twice: the
+    combine writes it, and the shared output projection, whose residual has its
+    result's type, reads it back and adds; the backward's dx likewise.  save: keep
+    what the backward needs.
     The other arguments as in forward."""
     T, d = x.shape
     _tick(timer, None)
