@@ -478,7 +478,7 @@ def _down_dgrad_bf16(dy, w, pre, off, act, row_scale, row_map, map_div):
     """The pre-activations' gradient as [M, F] or [M, 2F], and the scaled activations."""
     if pre.dim() == 3:
         dpre, hs = moe_gated_gemm_bf16_dgrad(dy, w, pre, off, act, row_scale, row_map, map_div)
-        return dpre.view(pre.shape[0], -1), hs
+        return dpre.flatten(1), hs
     return moe_grouped_gemm_bf16_dgrad(dy, w, off, pre, act, row_scale, row_map, map_div)
 
 

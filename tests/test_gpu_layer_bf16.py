@@ -199,6 +199,22 @@ def test_layer_graph_replay(t):
         torch.cuda.synchronize()
 
 
+@pytest.mark.parametrize("gated", [True])
+def test_empty_batch(gated):
+    """No tokens: empty outputs, weight gradients of zeros."""
+    rng = np.random.default_rng(12)
+    x = torch.empty((0, D), dtype=torch.bfloat16, device="cuda")
+    w, sh = _gpu(_weights(rng, gated, E)), _gpu(_weights(rng, gated, 1))
+    fw = layer.forward_bf16(x, w["w_up"], w["w_down"], torch.empty((0, E), device="cuda"), K, b_up=w["b_up"], b_down=w["b_down"],
+                            shared=sh, residual=x, dropout=0.1)
+    bw = layer.backward_bf16(fw, x)
+    assert fw["y"].shape == (0, D) and bw["dx"].shape == (0, D) and bw["dlogits"].shape == (0, E)
+    for g, v in ((bw, w), (bw["shared"], sh)):
+        for n in ("w_up", "w_down", "b_up", "b_down"):
+            d = g["d" + n.replace("w_", "W_")]
+            assert d.shape == v[n].shape and not d.any(), n
+
+
 def test_single_token_without_saving():
     """Serving: nothing kept, and the backward refuses."""
     rng = np.random.default_rng(11)
