@@ -696,7 +696,7 @@ extern "C" int moe_grouped_gemm_bf16_dgrad(const uint16_t* dy, int64_t dy_rows, 
   const char* name = "moe_grouped_gemm_bf16_dgrad";
   const Bf16Args p{dy, row_map, w, expert_off, nullptr, row_scale, pre, add, dx, hs, dy_rows, M_total, K, N, (uint32_t)map_div, div_magic(map_div), E, act};
   MOE4_REQUIRE(dx_dtype == MOE4_F32 || dx_dtype == MOE4_BF16, MOE4_EINVAL, "moe_grouped_gemm_bf16_dgrad: dx_dtype must be F32 or BF16");
-  MOE4_REQUIRE(pre || (act == MOE4_ACT_NONE && !hs), MOE4_EINVAL, "moe_grouped_gemm_bf16_dgrad: an activation or hs needs pre");
+  MOE4_REQUIRE(pre || M_total == 0 || (act == MOE4_ACT_NONE && !hs), MOE4_EINVAL, "moe_grouped_gemm_bf16_dgrad: an activation or hs needs pre");
   if (const int rc = check_bf16(p, name)) return rc;
   if (M_total == 0) return MOE4_OK;
   return dx_dtype == MOE4_BF16 ? launch_bf16<DGRAD, true>(p, stream, name) : launch_bf16<DGRAD, false>(p, stream, name);

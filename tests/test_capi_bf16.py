@@ -68,6 +68,13 @@ def test_dgrad_refusals(kw, rc):
     assert dgrad({**DEF, **kw}) == rc
 
 
+@pytest.mark.parametrize("act", [0, 1, 2])
+def test_dgrad_of_no_rows(act):
+    """Empty tensors have no address: pre may be NULL where there are no rows, with an activation too."""
+    none = dict(M=0, rows=0, a=O, w=O, c=O, pre=O, act=act)
+    assert dgrad({**DEF, **none}) == 0 and gated_dgrad({**DEF, **none}) == 0
+
+
 def test_gated_dgrad_needs_gu():
     assert gated_dgrad({**DEF, "pre": O}) == EINVAL
 

@@ -199,7 +199,7 @@ def test_layer_graph_replay(t):
         torch.cuda.synchronize()
 
 
-@pytest.mark.parametrize("gated", [True])
+@pytest.mark.parametrize("gated", [True, False])
 def test_empty_batch(gated):
     """No tokens: empty outputs, weight gradients of zeros."""
     rng = np.random.default_rng(12)
